@@ -13,9 +13,9 @@ operations in 32 bits) and the library's own:
 
 Layouts.  4-bit codes: u = q + 8 for q in [-7, 7], in blocks of 16 columns x
 64 rows of 512 bytes, block (n / 16, k / 64); inside a block the 32-bit word
-4 * (4 * (n % 8) + k % 64 / 16) + k % 16 / 4 holds the element in its nibble
-4 * (k % 2) + 2 * (k % 4 / 2) + n % 16 / 8.  Scales: [n / 16][k / group][n % 8]
-[n % 16 / 8].  Cache codes: c + 128 for c in [-127, 127], [page][head][token]
+4 * (4 * (n % 8) + k % 32 / 8) + 2 * (k % 64 / 32) + k % 8 / 4 holds the
+element in its nibble 4 * (k % 2) + 2 * (k % 4 / 2) + n % 16 / 8.  Scales:
+[n / 16][k / group][n % 8][n % 16 / 8].  Cache codes: c + 128 for c in [-127, 127], [page][head][token]
 [dim], scales [page][head]; a page table row per sequence.
 """
 import math
@@ -253,7 +253,7 @@ def _plain_weights(s):
     nb, kb = words.shape[:2]
     shifts = torch.arange(0, 32, 4, dtype=torch.int32, device=words.device)
     u = ((words.unsqueeze(-1) >> shifts) & 15).to(torch.uint8)      # block n, block k, lane, word, nibble
-    u = u.view(nb, kb, 8, 4, 4, 2, 2, 2).permute(0, 7, 2, 1, 3, 4, 6, 5).reshape(nb * 16, kb * 64)[:n, :k]
+    u = u.view(nb, kb, 8, 4, 2, 2, 2, 2, 2).permute(0, 8, 2, 1, 4, 3, 5, 7, 6).reshape(nb * 16, kb * 64)[:n, :k]
     scale = s["scales"].float().permute(0, 3, 2, 1).reshape(nb * 16, -1)[:n]
     scale = scale.repeat_interleave(group, 1)[:, :k]
     return (u.float() - 8.0) * scale
@@ -374,7 +374,7 @@ def _exact_gemm_w4(s):
     x, out = s["X"].double(), []
     for block in range(s["words"].shape[0]):
         n = torch.arange(16, device="cuda")[:, None]
-        word = s["words"][block].view(-1)[k // 64 * 128 + 4 * (4 * (n % 8) + k % 64 // 16) + k % 16 // 4].long()
+        word = s["words"][block].view(-1)[k // 64 * 128 + 4 * (4 * (n % 8) + k % 32 // 8) + 2 * (k % 64 // 32) + k % 8 // 4].long()
         q = (word >> (4 * (4 * (k % 2) + 2 * (k % 4 // 2) + n // 8)) & 15) - 8
         w = q.double() * s["scales"][block][k // s["group"], n % 8, n // 8].double()
         out.append(x @ w.t())
