@@ -25,6 +25,7 @@ ERR_UNSUPPORTED_DEVICE = 5
 ERR_TIMEOUT = 6
 ERR_SCRATCH_LIMIT = 7
 ERR_BOUNDS = 8          # debug build only: an out-of-buffer access was caught and skipped
+ERR_INDEX = 9           # debug_status(): a page, position or row offset out of range was skipped
 
 # Every entry point include/gemm.h declares, with its ctypes signature.
 _i64, _vp, _int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
@@ -39,6 +40,16 @@ SIGNATURES = {
     "gemm_launch_count": (_i64, []),
     "gemm_selftest_bounded_wait": (_int, [_i64, _vp]),
     "gemm_tf32_noalloc": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp]),
+    # operands held in few bits (lowbit.py)
+    "gemm_w4_sizes": (_int, [_i64, _i64, _int, _vp, _vp]),
+    "gemm_w4_quantize": (_int, [_vp, _i64, _int, _i64, _i64, _int, _vp, _vp, _vp]),
+    "gemm_w4_dequantize": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _i64, _int, _vp]),
+    "gemm_w4": (_int, [_vp, _i64, _int, _vp, _vp, _vp, _i64, _int, _i64, _i64, _i64, _int, _vp]),
+    "gemm_kv_append": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _int, _vp, _i64, _vp, _vp, _i64,
+                              _i64, _vp]),
+    "gemm_kv_read": (_int, [_vp, _vp, _vp, _int, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
+    "gemm_kv_attention": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _int, ctypes.c_int32,
+                                 ctypes.c_float, _int, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
 }
 
 _lock = threading.Lock()

@@ -10,6 +10,7 @@
 #include "gemm.h"
 #include "debug.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace {
 
@@ -446,6 +447,17 @@ int tc_product(const TcPlan& plan, const void* A, const void* B, float* C, int64
 
 void count_launch() { g_launches++; }
 
+void* scratch_alloc(int64_t bytes, cudaStream_t stream) {
+    DeviceState* st = nullptr;
+    void* p = nullptr;
+    if (device_state(&st) != GEMM_OK) return nullptr;
+    if (cudaMallocFromPoolAsync(&p, (size_t)bytes, st->pool, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    return p;
+}
+
 }  // namespace libgemm
 
 namespace {
@@ -531,6 +543,8 @@ const char* gemm_status_string(int status) {
     case GEMM_ERR_UNSUPPORTED_DEVICE: return "device is not compute capability 10.3 (sm_103a)";
     case GEMM_ERR_TIMEOUT: return "a bounded wait inside a kernel expired";
     case GEMM_ERR_BOUNDS: return "a kernel access outside its buffer was detected and skipped (debug build)";
+    case GEMM_ERR_INDEX:
+        return "a page number, position or row offset outside its range was met and skipped";
     case GEMM_ERR_SCRATCH_LIMIT:
         return "the product needs more scratch than the no-allocation entry point's static buffer";
     default: return "unknown status";
@@ -548,12 +562,14 @@ int gemm_debug_status(struct CUstream_st* stream_) {
         return GEMM_ERR_CUDA;
     // debug build: the bounds-check flags of every kernel (read and cleared)
     const unsigned bounds =
-        ffma_debug_flags() | ffma_small_debug_flags() | tc_debug_flags() | prep_debug_flags();
+        ffma_debug_flags() | ffma_small_debug_flags() | tc_debug_flags() | prep_debug_flags() |
+        w4_debug_flags() | kv_cache_debug_flags() | kv_attention_debug_flags();
     if (word == 0) return bounds ? GEMM_ERR_BOUNDS : GEMM_OK;
     const unsigned zero = 0;
     if (cudaMemcpy(st->err, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
         return GEMM_ERR_CUDA;
-    return GEMM_ERR_TIMEOUT;
+    if (word & kErrTimeout) return GEMM_ERR_TIMEOUT;
+    return bounds ? GEMM_ERR_BOUNDS : GEMM_ERR_INDEX;
 }
 
 int gemm_debug_build(void) { return kDebugBuild ? 1 : 0; }

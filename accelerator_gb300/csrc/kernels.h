@@ -184,7 +184,62 @@ cudaError_t launch_fill_zero(float* C, int64_t n, cudaStream_t stream);
 cudaError_t launch_scale(float* C, int64_t n, float beta, cudaStream_t stream);
 cudaError_t launch_wait_selftest(unsigned* err, uint64_t limit_ns, cudaStream_t stream);
 
+// ---- operands held in few bits (w4.cu, kv_cache.cu, kv_attention.cu) ----
+enum class ElemType { kF32 = 0, kBF16 = 1, kF16 = 2 };   // as enum gemm_type
+unsigned w4_debug_flags();
+unsigned kv_cache_debug_flags();
+unsigned kv_attention_debug_flags();
+// Work units of a launch are counted in the grid's x; the callers keep
+// (K / 128) * (N / 64) and (N / 16) * (M / 8) within it.
+cudaError_t launch_w4_quantize(const void* B, int64_t ldb, ElemType type, int64_t K, int64_t N,
+                               int group, void* codes, void* scales, cudaStream_t stream);
+cudaError_t launch_w4_dequantize(const void* codes, const void* scales, int64_t K, int64_t N,
+                                 int group, void* B, int64_t ldb, ElemType type,
+                                 cudaStream_t stream);
+cudaError_t launch_w4_gemm(const void* X, int64_t ldx, ElemType x_type, const void* codes,
+                           const void* scales, void* C, int64_t ldc, ElemType c_type, int64_t M,
+                           int64_t K, int64_t N, int group, cudaStream_t stream);
+
+// The paged cache as the kernels see it (layout in gemm.h).
+struct KvView {
+    uint8_t *k, *v;
+    float *ks, *vs;
+    int64_t pages;
+    int heads, page_log2, dim;
+};
+// A batch: page table, row offsets and each sequence's first position (append,
+// read) or length (attention).
+struct KvBatch {
+    const int32_t *table, *starts, *at;
+    int64_t width, rows;
+    int sequences;
+};
+// Rows x heads x dim elements with strides (in elements).
+struct KvRows {
+    void* p;
+    int64_t row, head;
+};
+cudaError_t launch_kv_append(const KvView& c, const KvRows& K, const KvRows& V, ElemType type,
+                             const KvBatch& b, unsigned* err, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvView& c, void* K, void* V, ElemType type, const KvBatch& b,
+                           unsigned* err, cudaStream_t stream);
+// Attention in two launches when the tokens are split over CTAs: partial
+// results go to scratch (plan.scratch_bytes) and a second launch joins them.
+struct KvPlan {
+    int64_t units;        // upper bound of the row tiles of the batch
+    int splits;
+    int64_t scratch_bytes;
+};
+KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, int num_sms);
+cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& O, ElemType type,
+                                int q_heads, float scale, bool causal, int64_t window,
+                                const KvBatch& b, const KvPlan& plan, void* scratch,
+                                unsigned* err, int* launches, cudaStream_t stream);
+
 // ---- host-side hooks of the C ABI (api.cu) ----
+// Stream-ordered scratch from the current device's pool; nullptr if none is
+// to be had.  Freed with cudaFreeAsync on the same stream.
+void* scratch_alloc(int64_t bytes, cudaStream_t stream);
 // Per-device set-up of the library (device check, kernel attributes, error
 // word); returns a gemm_status code.
 int device_setup(int* num_sms, unsigned** err);

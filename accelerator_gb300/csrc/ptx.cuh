@@ -12,7 +12,7 @@
 namespace libgemm {
 
 // Bits of the per-device error word that kernels set (never cleared by a kernel).
-enum : unsigned { kErrTimeout = 1u };
+enum : unsigned { kErrTimeout = 1u, kErrIndex = 2u };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

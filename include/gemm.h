@@ -99,10 +99,14 @@ enum gemm_status {
                                         stopped early and its output is not valid */
     GEMM_ERR_SCRATCH_LIMIT = 7,      /* gemm_tf32_noalloc: the product needs more scratch
                                         than GEMM_NOALLOC_SCRATCH_BYTES */
-    GEMM_ERR_BOUNDS = 8              /* debug build only (gemm_debug_build() == 1): a kernel
+    GEMM_ERR_BOUNDS = 8,             /* debug build only (gemm_debug_build() == 1): a kernel
                                         computed a global-memory access outside the buffer
                                         it belongs to; the access was skipped and the
                                         output is not valid */
+    GEMM_ERR_INDEX = 9               /* reported by gemm_debug_status(): a kernel met a page
+                                        number, a position or a row offset outside the cache,
+                                        the page table or the rows of its call; it skipped
+                                        that part, whose output is not valid */
 };
 
 /*
@@ -156,10 +160,11 @@ GEMM_API const char* gemm_status_string(int status);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's error
- * word, which kernels set when a bounded wait expires, and, in the debug
- * build, the bounds-check flags.  Returns GEMM_OK, GEMM_ERR_TIMEOUT,
- * GEMM_ERR_BOUNDS (debug build; a timeout is reported first when both
- * happened), or GEMM_ERR_CUDA if the synchronisation itself failed.
+ * word, which kernels set when a bounded wait expires or an index that they
+ * read is out of range, and, in the debug build, the bounds-check flags.
+ * Returns GEMM_OK, GEMM_ERR_TIMEOUT, GEMM_ERR_BOUNDS (debug build),
+ * GEMM_ERR_INDEX (the first of these where several happened), or
+ * GEMM_ERR_CUDA if the synchronisation itself failed.
  */
 GEMM_API int gemm_debug_status(struct CUstream_st* stream);
 
@@ -244,6 +249,160 @@ GEMM_API int gemm_selftest_bounded_wait(int64_t timeout_ns, struct CUstream_st* 
 
 GEMM_API int gemm_tf32_noalloc(const float* A, const float* B, float* C, int64_t M, int64_t K,
                                int64_t N, struct CUstream_st* stream);
+
+/*
+ * ---- operands held in few bits ------------------------------------------
+ *
+ * The products of a decoding step, in which one operand is kept in 4 or 8
+ * bits with scales: C = X*W with a 4-bit W for a few rows X, and attention
+ * (two products with a softmax between them) over a paged cache of 8-bit
+ * keys and values.  The rules above hold: device pointers, asynchronous on
+ * `stream`, status codes, nothing enqueued on an error, scratch from the
+ * library's stream-ordered pool, safe under stream capture after the first
+ * call on a device.  Indices that live in device memory (page numbers,
+ * positions, row offsets) are checked by the kernels: one outside its range
+ * is skipped and reported by gemm_debug_status() as GEMM_ERR_INDEX.
+ */
+
+/* Element types of the 16- and 32-bit operands. */
+enum gemm_type { GEMM_TYPE_F32 = 0, GEMM_TYPE_BF16 = 1, GEMM_TYPE_F16 = 2 };
+
+/*
+ * 4-bit weights.  W stands for the K x N matrix q_kn * s_gn, q in [-7, 7],
+ * with one bfloat16 scale s for each column n and each `group` consecutive
+ * rows g = k / group (group: 32, 64 or 128; the last group may be short).
+ * C_mn = sum over k of X_mk * q_kn * s_(k/group)n.
+ *
+ * Layout.  Codes: u = q + 8, in blocks of 16 columns x 64 rows of 512 bytes;
+ * block (n / 16, k / 64) is number (n / 16) * ceil(K / 64) + k / 64.  In a
+ * block, the 32-bit word 4 * (4 * (n % 8) + k % 32 / 8) + 2 * (k % 64 / 32)
+ * + k % 8 / 4 holds the element in bits 4i .. 4i + 3 with i = 4 * (k % 2) +
+ * 2 * (k % 4 / 2) + n % 16 / 8: what one lane of a warp needs for a matrix
+ * instruction is one 16-byte load.  Scales: element
+ * (((n / 16) * ceil(K / group) + k / group) * 8 + n % 8) * 2 + n % 16 / 8.
+ * gemm_w4_quantize writes q = 0 and s = 0 where the blocks reach past K or N.
+ */
+
+/* Bytes of the codes and of the scales of a K x N matrix (both 0 when K or N
+ * is 0); GEMM_ERR_INVALID_ARG for a group that is not 32, 64 or 128 or sizes
+ * out of range. */
+GEMM_API int gemm_w4_sizes(int64_t K, int64_t N, int group, int64_t* code_bytes,
+                           int64_t* scale_bytes);
+
+/*
+ * B (K x N, row stride ldb >= N elements, of `type`) to codes and scales:
+ * s = max|b| / 7 over the group's rows of the column, rounded to bfloat16,
+ * q = b / s rounded to the nearest integer (ties to even) and held to
+ * [-7, 7].  A group whose s is under 2^-126 becomes zeros; one that holds a
+ * NaN or an infinity gets s = NaN, so that every product with it is NaN.
+ * codes: 16-byte aligned; scales: 4-byte aligned.
+ */
+GEMM_API int gemm_w4_quantize(const void* B, int64_t ldb, int type, int64_t K, int64_t N,
+                              int group, void* codes, void* scales, struct CUstream_st* stream);
+
+/* The values q * s (formed in binary32, rounded once to `type`) into B. */
+GEMM_API int gemm_w4_dequantize(const void* codes, const void* scales, int64_t K, int64_t N,
+                                int group, void* B, int64_t ldb, int type,
+                                struct CUstream_st* stream);
+
+/*
+ * C = X*W.  X: M x K, row stride ldx elements, bfloat16 or binary16
+ * (x_type); C: M x N, row stride ldc, of x_type or float (c_type),
+ * overwritten, not overlapping the inputs.  Made for few rows: up to 8 rows
+ * read W once, and each further 32 read it again.  Products q * x are exact,
+ * summed in binary32 over a group (or a part of one) and scaled there; C is
+ * rounded once.  The order of the sums depends on the sizes alone.  K == 0
+ * gives 0.
+ */
+GEMM_API int gemm_w4(const void* X, int64_t ldx, int x_type, const void* codes,
+                     const void* scales, void* C, int64_t ldc, int c_type, int64_t M, int64_t K,
+                     int64_t N, int group, struct CUstream_st* stream);
+
+/*
+ * A paged cache of keys and values in 8 bits.  A page holds page_tokens
+ * consecutive tokens (16, 32, 64 or 128) of one sequence for every head;
+ * element d of token t, head h of page p is code (((p * heads + h) *
+ * page_tokens + t) * head_dim + d), an unsigned byte c + 128 with c in
+ * [-127, 127], and stands for c * scale[p * heads + h] (binary32 scales, one
+ * for the page's keys and one for its values, >= 0 or NaN).  head_dim: 64 or
+ * 128.  Codes are 16-byte aligned.  The caller owns all of it; a page needs
+ * no initial contents.
+ */
+typedef struct gemm_kv_cache {
+    void* k_codes;
+    void* v_codes;
+    float* k_scales;
+    float* v_scales;
+    int64_t pages;
+    int32_t heads, page_tokens, head_dim;
+} gemm_kv_cache;
+
+/*
+ * What the calls on a cache share: a batch of sequences with their rows of
+ * new tokens (or queries) one after another.
+ *   page_table  int32[sequences][table_width]: the page that holds a
+ *               sequence's tokens page_tokens * i ... in column i
+ *   starts      int32[sequences + 1]: sequence b's rows are starts[b] ..
+ *               starts[b + 1] - 1 (ascending; starts[0] = 0, the last one
+ *               = tokens); a sequence may have none
+ *   tokens      the number of rows; it and `sequences` are host values
+ * These arrays are on the device, 4-byte aligned.
+ */
+
+/*
+ * Writes new keys and values: row starts[b] + i becomes token first[b] + i of
+ * sequence b.  K and V: rows of heads x head_dim elements of `type`, element
+ * (row, h, d) at row * row_stride + h * head_stride + d (strides in
+ * elements, >= 0).  For each page, head and operand that gets new tokens,
+ *     s' = max(s, max|x| / 127)   (s = 0 if token 0 of the page is new)
+ * over its new elements x; new codes are x * (1 / s') rounded to the nearest
+ * integer (ties to even) and held to [-127, 127]; if s' > s the page's older
+ * codes c (its tokens before the first new one) become c * (s * (1 / s'))
+ * rounded alike.  Each of these steps is one binary32 operation.  With
+ * s' < 2^-126 they are all 0; a NaN or an infinity makes s' NaN, so that the
+ * page's tokens read as NaN for that head until its token 0 is written again.
+ * Tokens after the last new one are left as they are.  No page may belong to
+ * two of the sequences that are written in one call.
+ */
+GEMM_API int gemm_kv_append(const gemm_kv_cache* cache, const void* K, int64_t k_row_stride,
+                            int64_t k_head_stride, const void* V, int64_t v_row_stride,
+                            int64_t v_head_stride, int type, const int32_t* page_table,
+                            int64_t table_width, const int32_t* starts, const int32_t* first,
+                            int64_t tokens, int64_t sequences, struct CUstream_st* stream);
+
+/*
+ * Reads tokens back: rows starts[b] + i of K and V (dense, tokens x heads x
+ * head_dim, of `type`, 16-byte aligned) become the values of token
+ * first[b] + i of sequence b: c * s in binary32, rounded once.
+ */
+GEMM_API int gemm_kv_read(const gemm_kv_cache* cache, void* K, void* V, int type,
+                          const int32_t* page_table, int64_t table_width, const int32_t* starts,
+                          const int32_t* first, int64_t tokens, int64_t sequences,
+                          struct CUstream_st* stream);
+
+/*
+ * Attention of ragged queries over the cache.  Sequence b has lengths[b]
+ * tokens in the cache and T = starts[b + 1] - starts[b] queries, which stand
+ * at its last T positions: query i at p = lengths[b] - T + i.  For query
+ * head h (of q_heads, a multiple of the cache's heads; it reads head
+ * h / (q_heads / heads))
+ *     O = sum over j of softmax_j(scale * Q . K_j) V_j
+ * over the tokens 0 <= j < lengths[b], with causal != 0 only j <= p, and with
+ * window > 0 (causal only) only j > p - window.  A query that sees no token
+ * (p < 0, or an empty cache) gets 0.  Q and O: rows of q_heads x head_dim
+ * elements of `type` (bfloat16 or binary16), strides as above; O must not
+ * overlap the inputs.  Softmax statistics and sums are binary32; the weights
+ * enter the second product as binary16 relative to the row's largest, O is
+ * rounded once.  The order of the sums depends on the sizes, the
+ * lengths and the page table's width alone.
+ */
+GEMM_API int gemm_kv_attention(const gemm_kv_cache* cache, const void* Q, int64_t q_row_stride,
+                               int64_t q_head_stride, void* O, int64_t o_row_stride,
+                               int64_t o_head_stride, int type, int32_t q_heads, float scale,
+                               int causal, int64_t window, const int32_t* page_table,
+                               int64_t table_width, const int32_t* starts,
+                               const int32_t* lengths, int64_t tokens, int64_t sequences,
+                               struct CUstream_st* stream);
 
 #ifdef __cplusplus
 }
