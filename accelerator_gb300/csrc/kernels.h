@@ -190,7 +190,7 @@ unsigned w4_debug_flags();
 unsigned kv_cache_debug_flags();
 unsigned kv_attention_debug_flags();
 // Work units of a launch are counted in the grid's x; the callers keep
-// (K / 128) * (N / 64) and (N / 16) * (M / 8) within it.
+// (K / 128) * (N / 64) and 8 * (N / 32) * (M / 8) within it.
 cudaError_t launch_w4_quantize(const void* B, int64_t ldb, ElemType type, int64_t K, int64_t N,
                                int group, void* codes, void* scales, cudaStream_t stream);
 cudaError_t launch_w4_dequantize(const void* codes, const void* scales, int64_t K, int64_t N,
@@ -198,7 +198,7 @@ cudaError_t launch_w4_dequantize(const void* codes, const void* scales, int64_t 
                                  cudaStream_t stream);
 cudaError_t launch_w4_gemm(const void* X, int64_t ldx, ElemType x_type, const void* codes,
                            const void* scales, void* C, int64_t ldc, ElemType c_type, int64_t M,
-                           int64_t K, int64_t N, int group, cudaStream_t stream);
+                           int64_t K, int64_t N, int group, int num_sms, cudaStream_t stream);
 
 // The paged cache as the kernels see it (layout in gemm.h).
 struct KvView {

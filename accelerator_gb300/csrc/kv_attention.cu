@@ -6,6 +6,8 @@
 // onto the score and its value scale onto p_j, and the codes themselves enter
 // both products exactly, as binary16 integers.  The query heads that share a
 // cache head, and the queries of a sequence, are the rows of one tile.
+#include <type_traits>
+
 #include "kernels.h"
 #include "lowbit.cuh"
 
@@ -65,9 +67,9 @@ struct Tile {
         seq = last_not_above(a.b.sequences, u, [&](int i) { return starts.at(i) * a.share / kRows + i; });
         row0 = starts.at(seq);
         const int64_t count = starts.at(seq + 1) - row0;
-        if (!starts.good(seq) || (u == 0 && (__ldg(a.b.starts) != 0 || __ldg(a.b.starts + a.b.sequences) != a.b.rows))) {
+        if (!starts.whole(u == 0, seq)) {
             if (report) atomicOr(a.err, kErrIndex);
-            if (!starts.good(seq)) return false;
+            return false;
         }
         nrows = count * a.share;
         r0 = (u - row0 * a.share / kRows - seq) * kRows;

@@ -1,10 +1,13 @@
 // kv_cache.cu -- writing keys and values into the paged 8-bit cache and
 // reading them back (layouts and rules in gemm.h).
 //
-// A page's codes of one head share one scale, so what is written together is
-// a page: one CTA takes the new tokens of one (sequence, page, head) of the
-// keys or the values.  Sequences and pages are found from the row offsets on
-// the device; a launch has one unit for each page that could be touched.
+// A page's codes of one head share one scale, so the unit of both directions
+// is the part of one (sequence, page, head) of the keys or the values that a
+// call touches: one CTA.  Sequences and pages are found from the row offsets
+// on the device; a launch has one unit for each page that could be touched.
+// Both are bound by memory: every thread has all of its loads in flight, 8
+// elements each, before it uses the first, and the new elements stay in
+// registers between the search for their largest and the rounding.
 #include "kernels.h"
 #include "lowbit.cuh"
 
@@ -12,135 +15,197 @@ namespace libgemm {
 namespace {
 
 constexpr float kTiny = 1.1754943508222875e-38f;   // 2^-126
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint8_t code_of(float x, float inv) {
-    const float c = fminf(fmaxf(rintf(__fmul_rn(x, inv)), -127.0f), 127.0f);
-    return (uint8_t)((int)c + 128);
+// The part of a page that a unit of a launch is about.
+struct Part {
+    int64_t row0;      // the batch row of the sequence's first token
+    int64_t row;       // the batch row of the first token of the part
+    int64_t page;
+    int begin, end;    // its tokens in the page
+};
+
+// Sequence q's pages are units floor(starts[q] / P) + 2q + j: T rows touch at
+// most floor(T / P) + 2 pages, which is how far apart these are.
+__device__ __forceinline__ bool find_part(const KvView& c, const KvBatch& b, int64_t u, unsigned* err, Part& part) {
+    const bool report = threadIdx.x == 0 && blockIdx.y == 0;
+    const Starts starts{b.starts, b.sequences, b.rows};
+    const int log2 = c.page_log2, P = 1 << log2;
+    const int q = last_not_above(b.sequences, u, [&](int i) { return (starts.at(i) >> log2) + 2 * (int64_t)i; });
+    const int64_t row0 = starts.at(q), count = starts.at(q + 1) - row0, first = __ldg(b.at + q);
+    if (!starts.whole(u == 0, q) || (count > 0 && (first < 0 || first + count > (b.width << log2)))) {
+        if (report) atomicOr(err, kErrIndex);
+        return false;
+    }
+    const int64_t blk = (first >> log2) + u - (row0 >> log2) - 2 * (int64_t)q, lo = blk << log2;
+    if (count == 0 || lo >= first + count) return false;
+    part.begin = (int)(first > lo ? first - lo : 0);
+    part.end = (int)(first + count - lo < P ? first + count - lo : P);
+    part.row = row0 + lo + part.begin - first;
+    part.page = __ldg(b.table + q * b.width + blk);
+    if (part.page < 0 || part.page >= c.pages) {
+        if (report) atomicOr(err, kErrIndex);
+        return false;
+    }
+    return true;
 }
 
-template <typename T>
+__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
+    return (uint32_t)((int)a + 128) | (uint32_t)((int)b + 128) << 8 | (uint32_t)((int)c + 128) << 16 |
+           (uint32_t)((int)d + 128) << 24;
+}
+__device__ __forceinline__ float code_of(float x, float inv) {
+    return fminf(fmaxf(rintf(__fmul_rn(x, inv)), -127.0f), 127.0f);
+}
+// Byte i of a word of codes as c, exactly: u in the low fraction bits of 2^23.
+__device__ __forceinline__ float value_of(uint32_t w, int i) {
+    return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | i)) - 8388736.0f;
+}
+
+// UNITS groups of 8 elements a thread: a page's elements / 8 / kThreads.
+template <typename T, int UNITS>
 __global__ void __launch_bounds__(kThreads)
-    kv_append_kernel(KvView c, KvRows K, KvRows V, KvBatch b, unsigned* err) {
-    __shared__ uint32_t s_top;
-    const int P = 1 << c.page_log2, tid = threadIdx.x;
-    const int h = blockIdx.y >> 1;
+    kv_append_kernel(KvView c, KvRows K, KvRows V, bool vec, KvBatch b, unsigned* err) {
+    __shared__ uint32_t s_top[kThreads / 32];
+    const int tid = threadIdx.x, h = blockIdx.y >> 1;
     const bool values = blockIdx.y & 1;
     const KvRows& src = values ? V : K;
     uint8_t* codes = values ? c.v : c.k;
     float* scales = values ? c.vs : c.ks;
-    const Starts starts{b.starts, b.sequences, b.rows};
-    const int64_t u = blockIdx.x;
-    // Sequence q's pages are units floor(starts[q] / P) + 2q + j: T rows touch
-    // at most floor(T / P) + 2 pages, which is how far apart these are.
-    const int q = last_not_above(b.sequences, u, [&](int i) { return (starts.at(i) >> c.page_log2) + 2 * (int64_t)i; });
-    const int64_t row0 = starts.at(q), count = starts.at(q + 1) - row0;
-    const bool report = tid == 0 && blockIdx.y == 0;
-    if (!starts.good(q)) {
-        if (report) atomicOr(err, kErrIndex);
-        return;
-    }
-    const int64_t first = __ldg(b.at + q), j = u - (row0 >> c.page_log2) - 2 * (int64_t)q;
-    if (count == 0) return;
-    if (first < 0 || first + count > (b.width << c.page_log2)) {
-        if (report) atomicOr(err, kErrIndex);
-        return;
-    }
-    const int64_t blk = (first >> c.page_log2) + j, lo = blk << c.page_log2;
-    if (lo >= first + count) return;
-    const int64_t page = __ldg(b.table + q * b.width + blk);
-    if (page < 0 || page >= c.pages) {
-        if (report) atomicOr(err, kErrIndex);
-        return;
-    }
-    const int begin = (int)(first > lo ? first - lo : 0);                    // first new token of the page
-    const int end = (int)(first + count - lo < P ? first + count - lo : P);
-    const T* x = static_cast<const T*>(src.p) + (row0 + lo + begin - first) * src.row + h * src.head;
+    Part part;
+    if (!find_part(c, b, blockIdx.x, err, part)) return;
+    const int per_row = c.dim / 8, n = (part.end - part.begin) * per_row;
+    const T* x = static_cast<const T*>(src.p) + part.row * src.row + h * src.head;
     [[maybe_unused]] const int64_t x_bytes =
         ((b.rows - 1) * src.row + (c.heads - 1) * src.head + c.dim) * (int64_t)sizeof(T);
     [[maybe_unused]] const int64_t code_bytes = c.pages * c.heads * ((int64_t)c.dim << c.page_log2);
-    const int dim = c.dim, n = (end - begin) * dim;
-    uint32_t m = 0;
-    for (int i = tid; i < n; i += kThreads) {
-        const T* p = x + i / dim * src.row + i % dim;
-        if (GEMM_DBG_OK(p, src.p, x_bytes, sizeof(T))) m = max(m, __float_as_uint(to_float(*p)) & 0x7FFFFFFFu);
-    }
-    if (tid == 0) s_top = 0;
-    __syncthreads();
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (tid % 32 == 0) atomicMax(&s_top, m);
-    __syncthreads();
-    m = s_top;
-    float* sp = scales + page * c.heads + h;
+    float* sp = scales + part.page * c.heads + h;
     if (!GEMM_DBG_OK(sp, scales, c.pages * c.heads * 4, 4)) return;
-    const float before = begin > 0 ? *sp : 0.0f;
-    float s = fmaxf(before, __fdiv_rn(__uint_as_float(m), 127.0f));
+    const float before = part.begin > 0 ? *sp : 0.0f;
+
+    Eight<T> held[UNITS] = {};
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+        const int e = tid + i * kThreads;
+        if (i * kThreads >= n) break;
+        const T* p = x + (int64_t)(e / per_row) * src.row + e % per_row * 8;
+        if (e < n && GEMM_DBG_OK(p, src.p, x_bytes, 8 * sizeof(T))) held[i] = load_eight(p, vec);
+    }
+    uint32_t m = 0;   // magnitudes compare as their bits; from 0x7F800000 on they are not finite
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+        if (i * kThreads >= n) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(held[i].at(j)) & 0x7FFFFFFFu);
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (tid % 32 == 0) s_top[tid / 32] = m;
+    __syncthreads();   // also: every thread has read the old scale
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) m = max(m, s_top[i]);
+    const float s = fmaxf(before, __fdiv_rn(__uint_as_float(m), 127.0f));
     const bool bad = m >= 0x7F800000u || before != before;
     const float inv = bad || s < kTiny ? 0.0f : __fdiv_rn(1.0f, s);
-    __syncthreads();   // every thread has read the old scale
     if (tid == 0) *sp = bad ? __uint_as_float(0x7FC00000u) : s;
-    uint8_t* out = codes + ((page * c.heads + h) << c.page_log2) * dim;
-    for (int i = tid; i < n; i += kThreads) {
-        const T* p = x + i / dim * src.row + i % dim;
-        uint8_t* o = out + begin * dim + i;
-        if (GEMM_DBG_OK(p, src.p, x_bytes, sizeof(T)) && GEMM_DBG_OK(o, codes, code_bytes, 1))
-            *o = bad ? 128 : code_of(to_float(*p), inv);
+    uint8_t* out = codes + ((part.page * c.heads + h) << c.page_log2) * c.dim;
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+        const int e = tid + i * kThreads;
+        uint8_t* o = out + part.begin * c.dim + e * 8;
+        if (e >= n || !GEMM_DBG_OK(o, codes, code_bytes, 8)) break;
+        float q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = bad ? 0.0f : code_of(held[i].at(j), inv);
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_codes(q[0], q[1], q[2], q[3]), pack_codes(q[4], q[5], q[6], q[7]));
     }
-    if (!bad && before < s) {
+    if (!bad && before < s) {   // the scale grew: the page's older codes follow
         const float r = __fmul_rn(before, inv);
-        for (int i = tid; i < begin * dim; i += kThreads)
-            if (GEMM_DBG_OK(out + i, codes, code_bytes, 1)) out[i] = (uint8_t)((int)rintf(__fmul_rn((float)((int)out[i] - 128), r)) + 128);
+        for (int e = tid; e < part.begin * per_row; e += kThreads) {
+            uint2* o = reinterpret_cast<uint2*>(out) + e;
+            if (!GEMM_DBG_OK(o, codes, code_bytes, 8)) continue;
+            const uint2 w = *o;
+            float q[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = rintf(__fmul_rn(value_of(j < 4 ? w.x : w.y, j & 3), r));
+            *o = make_uint2(pack_codes(q[0], q[1], q[2], q[3]), pack_codes(q[4], q[5], q[6], q[7]));
+        }
     }
 }
 
-// Each thread turns 16 codes of one row and head into values.
-template <typename T>
-__global__ void __launch_bounds__(256)
+template <typename T, int UNITS>
+__global__ void __launch_bounds__(kThreads)
     kv_read_kernel(KvView c, T* __restrict__ K, T* __restrict__ V, KvBatch b, unsigned* err) {
-    const int chunks = c.dim / 16;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t per_row = (int64_t)c.heads * chunks;
-    if (i >= b.rows * per_row) return;
-    const int64_t row = i / per_row;
-    const int rest = (int)(i - row * per_row), h = rest / chunks, d = rest % chunks * 16;
-    const Starts starts{b.starts, b.sequences, b.rows};
-    const int q = last_not_above(b.sequences, row, [&](int j) { return starts.at(j); });
-    const int64_t pos = (int64_t)__ldg(b.at + q) + row - starts.at(q), blk = pos >> c.page_log2;
-    bool ok = starts.good(q) && row >= starts.at(q) && row < starts.at(q + 1) && pos >= 0 && blk < b.width;
-    const int64_t page = ok ? __ldg(b.table + q * b.width + blk) : -1;
-    ok = ok && page >= 0 && page < c.pages;
-    if (!ok) {
-        atomicOr(err, kErrIndex);
-        return;
-    }
-    const int64_t ph = page * c.heads + h;
-    const int64_t from = ((ph << c.page_log2) + (pos & ((1 << c.page_log2) - 1))) * c.dim + d;
-    const int64_t to = (row * c.heads + h) * c.dim + d;
+    const int tid = threadIdx.x, h = blockIdx.y >> 1;
+    const bool values = blockIdx.y & 1;
+    Part part;
+    if (!find_part(c, b, blockIdx.x, err, part)) return;
+    const uint8_t* codes = values ? c.v : c.k;
+    const float* scales = values ? c.vs : c.ks;
+    T* out = values ? V : K;
+    const int per_row = c.dim / 8, n = (part.end - part.begin) * per_row;
+    const int64_t ph = part.page * c.heads + h;
+    const uint8_t* from = codes + ((ph << c.page_log2) + part.begin) * c.dim;
+    T* to = out + (part.row * c.heads + h) * c.dim;
     [[maybe_unused]] const int64_t code_bytes = c.pages * c.heads * ((int64_t)c.dim << c.page_log2);
     [[maybe_unused]] const int64_t out_bytes = b.rows * c.heads * c.dim * (int64_t)sizeof(T);
+    if (!GEMM_DBG_OK(scales + ph, scales, c.pages * c.heads * 4, 4)) return;
+    const float s = scales[ph];
+    uint2 held[UNITS] = {};
 #pragma unroll
-    for (int o = 0; o < 2; ++o) {
-        const uint8_t* codes = o ? c.v : c.k;
-        T* out = (o ? V : K) + to;
-        const float s = __ldg((o ? c.vs : c.ks) + ph);
-        if (!GEMM_DBG_OK(codes + from, codes, code_bytes, 16) || !GEMM_DBG_OK(out, o ? V : K, out_bytes, 16 * sizeof(T))) continue;
-        const uint4 w = *reinterpret_cast<const uint4*>(codes + from);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        float v[16];
+    for (int i = 0; i < UNITS; ++i) {
+        const int e = tid + i * kThreads;
+        if (e < n && GEMM_DBG_OK(from + e * 8, codes, code_bytes, 8)) held[i] = *(reinterpret_cast<const uint2*>(from) + e);
+    }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = __fmul_rn((float)((int)((ws[e / 4] >> (8 * (e % 4))) & 255u) - 128), s);
+    for (int i = 0; i < UNITS; ++i) {
+        const int e = tid + i * kThreads;
+        T* o = to + (int64_t)(e / per_row) * c.heads * c.dim + e % per_row * 8;
+        if (e >= n || !GEMM_DBG_OK(o, out, out_bytes, 8 * sizeof(T))) break;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(value_of(j < 4 ? held[i].x : held[i].y, j & 3), s);
         if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                reinterpret_cast<float4*>(out)[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
         } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                reinterpret_cast<uint4*>(out)[e] =
-                    make_uint4(pack2<T>(v[8 * e], v[8 * e + 1]), pack2<T>(v[8 * e + 2], v[8 * e + 3]),
-                               pack2<T>(v[8 * e + 4], v[8 * e + 5]), pack2<T>(v[8 * e + 6], v[8 * e + 7]));
+            *reinterpret_cast<uint4*>(o) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
+                                                      pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
         }
     }
+}
+
+dim3 grid_of(const KvView& c, const KvBatch& b) {
+    return dim3((unsigned)((b.rows >> c.page_log2) + 2 * (int64_t)b.sequences), (unsigned)(2 * c.heads));
+}
+
+// Calls f with the number of groups of 8 elements that a thread holds.
+template <typename F>
+void with_units(const KvView& c, F f) {
+    const int units = (c.dim << c.page_log2) / (8 * kThreads);
+    if (units <= 1) f(std::integral_constant<int, 1>());
+    else if (units == 2) f(std::integral_constant<int, 2>());
+    else if (units == 4) f(std::integral_constant<int, 4>());
+    else f(std::integral_constant<int, 8>());
+}
+
+template <typename T>
+void append(const KvView& c, const KvRows& K, const KvRows& V, const KvBatch& b, unsigned* err, cudaStream_t stream) {
+    auto by16 = [](const KvRows& r) {
+        const int64_t es = sizeof(T);
+        return (reinterpret_cast<uintptr_t>(r.p) & 15u) == 0 && r.row * es % 16 == 0 && r.head * es % 16 == 0;
+    };
+    const bool vec = by16(K) && by16(V);
+    with_units(c, [&](auto units) {
+        kv_append_kernel<T, decltype(units)::value><<<grid_of(c, b), kThreads, 0, stream>>>(c, K, V, vec, b, err);
+    });
+}
+
+template <typename T>
+void read(const KvView& c, void* K, void* V, const KvBatch& b, unsigned* err, cudaStream_t stream) {
+    with_units(c, [&](auto units) {
+        kv_read_kernel<T, decltype(units)::value>
+            <<<grid_of(c, b), kThreads, 0, stream>>>(c, static_cast<T*>(K), static_cast<T*>(V), b, err);
+    });
 }
 
 }  // namespace
@@ -149,22 +214,17 @@ LIBGEMM_DEBUG_READER(kv_cache_debug_flags)
 
 cudaError_t launch_kv_append(const KvView& c, const KvRows& K, const KvRows& V, ElemType type,
                              const KvBatch& b, unsigned* err, cudaStream_t stream) {
-    const dim3 grid((unsigned)((b.rows >> c.page_log2) + 2 * (int64_t)b.sequences), (unsigned)(2 * c.heads));
-    if (type == ElemType::kF32) kv_append_kernel<float><<<grid, kThreads, 0, stream>>>(c, K, V, b, err);
-    else if (type == ElemType::kBF16) kv_append_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(c, K, V, b, err);
-    else kv_append_kernel<__half><<<grid, kThreads, 0, stream>>>(c, K, V, b, err);
+    if (type == ElemType::kF32) append<float>(c, K, V, b, err, stream);
+    else if (type == ElemType::kBF16) append<__nv_bfloat16>(c, K, V, b, err, stream);
+    else append<__half>(c, K, V, b, err, stream);
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const KvView& c, void* K, void* V, ElemType type, const KvBatch& b,
                            unsigned* err, cudaStream_t stream) {
-    const unsigned grid = (unsigned)((b.rows * c.heads * (c.dim / 16) + 255) / 256);
-    if (type == ElemType::kF32)
-        kv_read_kernel<float><<<grid, 256, 0, stream>>>(c, static_cast<float*>(K), static_cast<float*>(V), b, err);
-    else if (type == ElemType::kBF16)
-        kv_read_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(c, static_cast<__nv_bfloat16*>(K), static_cast<__nv_bfloat16*>(V), b, err);
-    else
-        kv_read_kernel<__half><<<grid, 256, 0, stream>>>(c, static_cast<__half*>(K), static_cast<__half*>(V), b, err);
+    if (type == ElemType::kF32) read<float>(c, K, V, b, err, stream);
+    else if (type == ElemType::kBF16) read<__nv_bfloat16>(c, K, V, b, err, stream);
+    else read<__half>(c, K, V, b, err, stream);
     return cudaGetLastError();
 }
 

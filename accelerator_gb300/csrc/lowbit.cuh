@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <type_traits>
 
 #include "debug.cuh"
 #include "ptx.cuh"
@@ -83,15 +84,54 @@ __device__ __forceinline__ uint32_t halves_from_biased(uint32_t x) {
 __device__ __forceinline__ uint32_t codes01(uint32_t w) { return halves_from_biased(__byte_perm(w, 0x64646464u, 0x4140)); }
 __device__ __forceinline__ uint32_t codes23(uint32_t w) { return halves_from_biased(__byte_perm(w, 0x64646464u, 0x4342)); }
 
+// Eight neighbours as the 16 or 32 bytes that hold them.
+template <typename T>
+struct Eight {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ float at(int i) const {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else if constexpr (std::is_same<T, __half>::value)
+            return __half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (16 * (i & 1)))));
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+};
+template <typename T>
+__device__ __forceinline__ Eight<T> load_eight(const T* p, bool vec) {
+    Eight<T> e;
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) e.v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    } else if constexpr (sizeof(T) == 4) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = p[i];
+        e.v[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        e.v[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+        e.v[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    return e;
+}
+
 // The largest b in [0, n) with value(b) <= x, for a non-decreasing value();
-// 0 if there is none.
+// 0 if there is none.  The lanes of a warp look at 32 places at once: a chain
+// of two loads for a thousand sequences where halving has ten.
 template <typename F>
 __device__ __forceinline__ int last_not_above(int n, int64_t x, F value) {
+    const int lane = threadIdx.x % 32;
     int lo = 0, hi = n;   // value(lo) <= x (or lo = 0), value(hi) > x (or hi = n)
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (value(mid) <= x) lo = mid;
-        else hi = mid;
+        const int step = (hi - lo + 31) / 32;
+        const int64_t at = lo + (int64_t)lane * step;
+        const unsigned below = __ballot_sync(0xFFFFFFFFu, at < hi && value((int)at) <= x);
+        const int k = max(__popc(below) - 1, 0);
+        lo += k * step;
+        hi = min(hi, lo + step);
     }
     return lo;
 }
@@ -111,6 +151,10 @@ struct Starts {
     __device__ __forceinline__ bool good(int b) const {
         const int64_t s = __ldg(p + b), e = __ldg(p + b + 1);
         return s >= 0 && s <= e && e <= rows;
+    }
+    // good(b), and with `ends` (one unit of a launch) the offsets begin at 0 and end at `rows`.
+    __device__ __forceinline__ bool whole(bool ends, int b) const {
+        return good(b) && (!ends || (__ldg(p) == 0 && __ldg(p + n) == rows));
     }
 };
 

@@ -134,7 +134,7 @@ int gemm_w4(const void* X, int64_t ldx, int x_type, const void* codes, const voi
     if ((x_type != GEMM_TYPE_BF16 && x_type != GEMM_TYPE_F16) || (c_type != GEMM_TYPE_F32 && c_type != x_type))
         return GEMM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return GEMM_OK;
-    if (ldx > kElemMax / M || ldc > kElemMax / M || ((N + 15) / 16) * ((M + 7) / 8) > kIndexMax)
+    if (ldx > kElemMax / M || ldc > kElemMax / M || ((N + 31) / 32) * ((M + 7) / 8) > kIndexMax / 8)
         return GEMM_ERR_INVALID_ARG;
     if (!C || (K > 0 && (!X || !codes || !scales))) return GEMM_ERR_INVALID_ARG;
     const int64_t ces = type_size(c_type);
@@ -147,7 +147,7 @@ int gemm_w4(const void* X, int64_t ldx, int x_type, const void* codes, const voi
     const int rc = device_setup(&sms, &err);
     if (rc != GEMM_OK) return rc;
     if (launch_w4_gemm(X, ldx, static_cast<ElemType>(x_type), codes, scales, C, ldc,
-                       static_cast<ElemType>(c_type), M, K, N, group, stream) != cudaSuccess)
+                       static_cast<ElemType>(c_type), M, K, N, group, sms, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
     count_launch();
     return GEMM_OK;
@@ -199,7 +199,7 @@ int gemm_kv_read(const gemm_kv_cache* cache, void* K, void* V, int type, const i
     const int64_t bytes = tokens * v.heads * v.dim * type_size(type);
     if (overlaps_cache(v, K, bytes) || overlaps_cache(v, V, bytes) || overlap(K, bytes, V, bytes))
         return GEMM_ERR_INVALID_ARG;
-    if (tokens * v.heads * (v.dim / 16) / 256 >= kIndexMax) return GEMM_ERR_INVALID_ARG;
+    if ((tokens >> v.page_log2) + 2 * sequences > kIndexMax) return GEMM_ERR_INVALID_ARG;
     int sms = 0;
     unsigned* err = nullptr;
     rc = device_setup(&sms, &err);

@@ -24,48 +24,69 @@ struct W4 {
     __host__ __device__ int64_t nb() const { return (N + 15) / 16; }
 };
 
-// ---- quantise ----------------------------------------------------------------
-// One CTA takes 128 rows x 64 columns (a whole number of groups and blocks):
-// the tile goes through shared memory as floats, a thread finds the largest
-// magnitude of 32 rows of one column, and each thread packs words of 8 codes.
+// Both conversions take tiles of 128 rows x 64 columns, a whole number of
+// groups and blocks, with 256 threads of 32 elements each.
 constexpr int kQRows = 128, kQCols = 64, kQThreads = 256;
 
+__device__ __forceinline__ void tile_at(const W4& w, int64_t& k0, int64_t& n0) {
+    const int64_t across = (w.N + kQCols - 1) / kQCols;
+    k0 = blockIdx.x / across * kQRows;
+    n0 = blockIdx.x % across * kQCols;
+}
+
+// ---- quantise ----------------------------------------------------------------
+// A thread holds four neighbouring rows of eight columns, all loaded before
+// the first is used.  The largest magnitude of a column goes over four lanes
+// by shuffles and over two warps through shared memory (a group of 32 rows);
+// a word of codes is four rows of two columns eight apart, so a thread and its
+// neighbour make half of it each and swap; the words leave in 16-byte pieces
+// by way of shared memory.
 template <typename T>
 __global__ void __launch_bounds__(kQThreads)
-    w4_quantize_kernel(const T* __restrict__ B, int64_t ldb, W4 w) {
-    __shared__ float tile[kQRows][kQCols + 1];
-    __shared__ uint32_t top[4][kQCols];
-    __shared__ float scale[4][kQCols];
-    const int64_t across = (w.N + kQCols - 1) / kQCols;
-    const int64_t k0 = blockIdx.x / across * kQRows, n0 = blockIdx.x % across * kQCols;
-    const int tid = threadIdx.x;
+    w4_quantize_kernel(const T* __restrict__ B, int64_t ldb, bool vec, W4 w) {
+    __shared__ uint32_t top[kQThreads / 32][kQCols];
+    __shared__ float scale[4][kQCols], inverse[4][kQCols];
+    __shared__ __align__(16) uint32_t words[4 * 296];   // [16 columns][64 rows][128 words], spread over the banks
+    int64_t k0, n0;
+    tile_at(w, k0, n0);
+    const int tid = threadIdx.x, c8 = tid % 8, r = tid / 8;
     [[maybe_unused]] const int64_t b_bytes = ((w.K - 1) * ldb + w.N) * (int64_t)sizeof(T);
-    for (int i = tid; i < kQRows * kQCols; i += kQThreads) {
-        const int r = i / kQCols, c = i % kQCols;
-        const T* p = B + (k0 + r) * ldb + n0 + c;
-        tile[r][c] = k0 + r < w.K && n0 + c < w.N && GEMM_DBG_OK(p, B, b_bytes, sizeof(T))
-                         ? to_float(*p) : 0.0f;
+    Eight<T> x[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t k = k0 + 4 * r + i, n = n0 + 8 * c8;
+        const T* p = B + k * ldb + n;
+        if (k >= w.K || n >= w.N) continue;
+        if (n + 8 <= w.N) {
+            if (GEMM_DBG_OK(p, B, b_bytes, 8 * sizeof(T))) x[i] = load_eight(p, vec);
+        } else {
+            T part[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) part[j] = n + j < w.N && GEMM_DBG_OK(p + j, B, b_bytes, sizeof(T)) ? p[j] : from_float<T>(0.0f);
+            x[i] = load_eight(part, false);
+        }
     }
-    __syncthreads();
-    {
-        const int c = tid % kQCols, part = tid / kQCols;
-        uint32_t m = 0;   // magnitudes compare as their bits; above 0x7F800000 is NaN
-        for (int r = 0; r < 32; ++r)
-            m = max(m, __float_as_uint(tile[part * 32 + r][c]) & 0x7FFFFFFFu);
-        top[part][c] = m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {   // magnitudes compare as their bits; from 0x7F800000 on they are not finite
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(x[i].at(j)) & 0x7FFFFFFFu);
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+        if (tid % 32 < 8) top[tid / 32][8 * c8 + j] = m;
     }
     __syncthreads();
     {
         const int c = tid % kQCols, part = tid / kQCols, per = w.group / 32;
         uint32_t m = 0;
-        for (int i = 0; i < per; ++i) m = max(m, top[part / per * per + i][c]);
-        const bool bad = m >= 0x7F800000u;
+        for (int i = 0; i < 2 * per; ++i) m = max(m, top[part / per * per * 2 + i][c]);
         const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(m), 7.0f));
         float s = __bfloat162float(sb);
         uint16_t bits = __bfloat16_as_ushort(sb);
-        if (bad) s = 0.0f, bits = 0x7FC0;   // NaN; the codes are 0
+        if (m >= 0x7F800000u) s = 0.0f, bits = 0x7FC0;   // NaN; the codes are 0
         else if (s < kTiny) s = 0.0f, bits = 0;
         scale[part][c] = s;
+        inverse[part][c] = s == 0.0f ? 0.0f : __fdiv_rn(1.0f, s);
         const int64_t g = (k0 + part * 32) / w.group, n = n0 + c;
         if (part % per == 0 && k0 + part * 32 < w.K && n < w.nb() * 16) {
             uint16_t* p = w.scales + ((n / 16 * w.groups + g) * 8 + n % 8) * 2 + n % 16 / 8;
@@ -73,66 +94,107 @@ __global__ void __launch_bounds__(kQThreads)
         }
     }
     __syncthreads();
-    for (int i = tid; i < (kQRows / 64) * (kQCols / 16) * 128; i += kQThreads) {
-        const int word = i % 128, kbl = i / 128 % (kQRows / 64), nbl = i / 128 / (kQRows / 64);
-        const int lane = word / 4, j = word % 4, g = lane / 4, t = lane % 4;
-        const int64_t nb = n0 / 16 + nbl, kb = k0 / 64 + kbl;
-        if (nb >= w.nb() || kb >= w.kb) continue;
+    // b / s rounded to the nearest integer: the quotient has to be the
+    // correctly rounded one, for b / s is often halfway between two integers.
+    // From t = b * (1 / s) the residual b - t * s (exact in one fused
+    // multiply-add) gives it (Markstein 1990) as long as nothing underflows,
+    // which needs s above about 2^-100; below, the division itself.  |b / s|
+    // stays under 7.04, as s is at most 2^-8 below max|b| / 7.
+    uint32_t mine[8];
+    const int hi = c8 & 1, part = r / 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float s = scale[part][8 * c8 + j], inv = inverse[part][8 * c8 + j];
         uint32_t v = 0;
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-            const int hi = b & 1, e = (b >> 2) + 2 * ((b >> 1) & 1);
-            const int r = kbl * 64 + 32 * (j >> 1) + 8 * t + 4 * (j & 1) + e, c = nbl * 16 + 8 * hi + g;
-            const float s = scale[r / 32][c];
-            const float q = s == 0.0f ? 0.0f : fminf(fmaxf(rintf(__fdiv_rn(tile[r][c], s)), -7.0f), 7.0f);
-            v |= (uint32_t)((int)q + 8) << (4 * b);
+        for (int i = 0; i < 4; ++i) {
+            const float b = x[i].at(j);
+            const float t = __fmul_rn(b, inv);
+            float q = __fmaf_rn(__fmaf_rn(-t, s, b), inv, t);
+            if (s < 7.9e-31f && s > 0.0f) q = __fdiv_rn(b, s);
+            // 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low bits
+            const uint32_t u = __float_as_uint(__fadd_rn(q, 12582912.0f)) + 8u;
+            v |= (u & 15u) << (4 * (4 * (i & 1) + 2 * (i >> 1)));
         }
-        uint32_t* p = w.codes + (nb * w.kb + kb) * 128 + word;
-        if (GEMM_DBG_OK(p, w.codes, w.nb() * w.kb * 512, 4)) *p = v;
+        mine[j] = (s == 0.0f ? 0x08080808u : v) << (4 * hi);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {   // the even thread keeps columns 0-3 of 8, the odd one 4-7
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, hi ? mine[j] : mine[j + 4], 1);
+        const uint32_t word = (hi ? mine[j + 4] : mine[j]) | got;
+        const int g = j + 4 * hi, t = (r >> 1) & 3, at = 4 * (4 * g + t) + 2 * ((r >> 3) & 1) + (r & 1);
+        words[c8 / 2 * 296 + r / 16 * 144 + at + 16 * (at >> 6)] = word;
+    }
+    __syncthreads();
+    {
+        const int nbl = tid / 64, kbl = tid / 32 % 2, at = tid % 32 * 4;
+        const int64_t nb = n0 / 16 + nbl, kb = k0 / 64 + kbl;
+        uint32_t* p = w.codes + (nb * w.kb + kb) * 128 + at;
+        if (nb < w.nb() && kb < w.kb && GEMM_DBG_OK(p, w.codes, w.nb() * w.kb * 512, 16))
+            *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&words[nbl * 296 + kbl * 144 + at + 16 * (at >> 6)]);
     }
 }
 
 // ---- dequantise --------------------------------------------------------------
+// A warp takes a block, a thread its 16 bytes; the values pass through a
+// tile in shared memory whose pieces of eight columns are permuted by the row
+// (piece ^ row / 8), so that neither side meets itself in a bank.
 template <typename T>
 __global__ void __launch_bounds__(kQThreads)
-    w4_dequantize_kernel(W4 w, T* __restrict__ B, int64_t ldb) {
-    __shared__ float tile[kQRows][kQCols + 1];
-    const int64_t across = (w.N + kQCols - 1) / kQCols;
-    const int64_t k0 = blockIdx.x / across * kQRows, n0 = blockIdx.x % across * kQCols;
+    w4_dequantize_kernel(W4 w, T* __restrict__ B, int64_t ldb, bool vec) {
+    __shared__ __align__(16) T tile[kQRows][kQCols];
+    int64_t k0, n0;
+    tile_at(w, k0, n0);
     const int tid = threadIdx.x;
-    for (int i = tid; i < (kQRows / 64) * (kQCols / 16) * 128; i += kQThreads) {
-        const int word = i % 128, kbl = i / 128 % (kQRows / 64), nbl = i / 128 / (kQRows / 64);
-        const int lane = word / 4, j = word % 4, g = lane / 4, t = lane % 4;
+    {
+        const int nbl = tid / 64, kbl = tid / 32 % 2, lane = tid % 32, g = lane / 4, t = lane % 4;
         const int64_t nb = n0 / 16 + nbl, kb = k0 / 64 + kbl;
-        if (nb >= w.nb() || kb >= w.kb) continue;
-        const uint32_t* p = w.codes + (nb * w.kb + kb) * 128 + word;
-        if (!GEMM_DBG_OK(p, w.codes, w.nb() * w.kb * 512, 4)) continue;
-        const uint32_t v = *p;
-        const int64_t k = kb * 64 + 32 * (j >> 1);
-        uint32_t s2 = 0;   // the scales of columns g and g + 8
-        if (k < w.K) {
-            const uint16_t* sp = w.scales + ((nb * w.groups + k / w.group) * 8 + g) * 2;
-            if (GEMM_DBG_OK(sp, w.scales, w.nb() * w.groups * 32, 4)) s2 = *reinterpret_cast<const uint32_t*>(sp);
-        }
+        const uint4* p = reinterpret_cast<const uint4*>(w.codes + (nb * w.kb + kb) * 128) + lane;
+        if (nb < w.nb() && kb < w.kb && GEMM_DBG_OK(p, w.codes, w.nb() * w.kb * 512, 16)) {
+            const uint4 v = __ldg(p);
+            const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-            const int hi = b & 1, e = (b >> 2) + 2 * ((b >> 1) & 1);
-            const float s = __uint_as_float(hi ? s2 & 0xFFFF0000u : s2 << 16);
-            tile[kbl * 64 + 32 * (j >> 1) + 8 * t + 4 * (j & 1) + e][nbl * 16 + 8 * hi + g] =
-                __fmul_rn((float)((int)((v >> (4 * b)) & 15u) - 8), s);
+            for (int j = 0; j < 4; ++j) {
+                const int64_t k = kb * 64 + 32 * (j >> 1);
+                const uint16_t* sp = w.scales + ((nb * w.groups + k / w.group) * 8 + g) * 2;
+                uint32_t s2 = 0;   // the scales of columns g and g + 8
+                if (k < w.K && GEMM_DBG_OK(sp, w.scales, w.nb() * w.groups * 32, 4))
+                    s2 = __ldg(reinterpret_cast<const uint32_t*>(sp));
+                const int row = kbl * 64 + 32 * (j >> 1) + 8 * t + 4 * (j & 1);
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    const int hi = b & 1, e = (b >> 2) + 2 * ((b >> 1) & 1);
+                    const float s = __uint_as_float(hi ? s2 & 0xFFFF0000u : s2 << 16);
+                    const float q = __uint_as_float(((ws[j] >> (4 * b)) & 15u) | 0x4B000000u) - 8388616.0f;
+                    tile[row + e][8 * ((2 * nbl + hi) ^ (row / 8 & 7)) + g] = from_float<T>(__fmul_rn(q, s));
+                }
+            }
         }
     }
     __syncthreads();
     [[maybe_unused]] const int64_t b_bytes = ((w.K - 1) * ldb + w.N) * (int64_t)sizeof(T);
-    for (int i = tid; i < kQRows * kQCols; i += kQThreads) {
-        const int r = i / kQCols, c = i % kQCols;
-        T* p = B + (k0 + r) * ldb + n0 + c;
-        if (k0 + r < w.K && n0 + c < w.N && GEMM_DBG_OK(p, B, b_bytes, sizeof(T))) *p = from_float<T>(tile[r][c]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = tid / 8 + 32 * i, c8 = tid % 8;
+        const int64_t k = k0 + row, n = n0 + 8 * c8;
+        if (k >= w.K) break;
+        const T* from = &tile[row][8 * (c8 ^ (row / 8 & 7))];
+        T* to = B + k * ldb + n;
+        if (vec && n + 8 <= w.N) {
+            if (!GEMM_DBG_OK(to, B, b_bytes, 8 * sizeof(T))) continue;
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T) / 2; ++j) reinterpret_cast<uint4*>(to)[j] = reinterpret_cast<const uint4*>(from)[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (n + j < w.N && GEMM_DBG_OK(to + j, B, b_bytes, sizeof(T))) to[j] = from[j];
+        }
     }
 }
 
 // ---- the product -------------------------------------------------------------
 constexpr int kPWarps = 8;
+constexpr int kAhead = 4;       // blocks of 64 rows whose codes a warp has in flight
 
 // Four nibble pairs of a word as pairs of T holding q, exactly.
 template <typename T>
@@ -168,84 +230,158 @@ template <typename T, bool VEC>
 __device__ __forceinline__ uint4 load_x8(const T* row, int64_t k, int64_t K, bool live) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (!live || k >= K) return v;
-    if (VEC && k + 8 <= K) return *reinterpret_cast<const uint4*>(row + k);
+    if (VEC && k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
     uint32_t r[4] = {0, 0, 0, 0};
     const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (k + i < K) r[i / 2] |= (uint32_t)p[k + i] << (16 * (i & 1));
+        if (k + i < K) r[i / 2] |= (uint32_t)__ldg(p + k + i) << (16 * (i & 1));
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// One CTA computes 16 columns of C for 8*MT rows: its warps take the blocks
-// of 64 rows of W in turn and add their sums up at the end, in warp order.
-template <typename T, typename U, int MT, bool VEC>
-__global__ void __launch_bounds__(kPWarps * 32)
+__device__ __forceinline__ uint4 load_once(const uint4* p) {   // streamed past L1, which is for X
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// A cluster of CTAs computes 32 * WN columns of C for 8 * MT rows: each CTA a
+// range of the blocks of 64 rows of W, in which each of its warps takes every
+// WK-th block of 32 columns (two blocks of 16, so that a part of X that is
+// loaded serves both).  The sums are added up over the warps, then over the
+// cluster's CTAs through distributed shared memory, always in that order.
+template <typename T, typename U, int MT, int WN, bool HALF, bool VEC>
+__global__ void __launch_bounds__(kPWarps * 32, MT <= 2 ? 2 : 1)
     w4_gemm_kernel(const T* __restrict__ X, int64_t ldx, W4 w, U* __restrict__ C, int64_t ldc,
-                   int64_t M) {
-    __shared__ float part[kPWarps][MT * 8][17];
+                   int64_t M, int splits, int64_t tiles_n) {
+    constexpr int WK = kPWarps / WN, kCols = 32 * WN, kRows = 8 * MT;
+    __shared__ float part[WK][kRows][kCols + 4];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const int64_t nb = blockIdx.x % w.nb(), m0 = blockIdx.x / w.nb() * (8 * MT);
-    [[maybe_unused]] const int64_t x_bytes = ((M - 1) * ldx + w.K) * (int64_t)sizeof(T);
-    float total[MT][4] = {};
-    const bool by_half = w.group == 32;   // scaled after each half block, or each block
-    for (int kb = warp; kb < w.kb; kb += kPWarps) {
-        const uint4* cp = reinterpret_cast<const uint4*>(w.codes + (nb * w.kb + kb) * 128) + lane;
-        uint4 q = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-        if (GEMM_DBG_OK(cp, w.codes, w.nb() * w.kb * 512, 16)) q = __ldcs(cp);
-        const uint32_t words[4] = {q.x, q.y, q.z, q.w};
-        float acc[MT][4] = {};
+    const int wn = warp % WN, wk = warp / WN;
+    const int rank = blockIdx.x % splits;
+    const int64_t tile = blockIdx.x / splits, m0 = tile / tiles_n * kRows;
+    const int64_t nb0 = (tile % tiles_n) * (2 * WN) + 2 * wn;
+    const int per = (w.kb + splits - 1) / splits;
+    const int kb0 = rank * per, kb1 = min(w.kb, kb0 + per);
+    [[maybe_unused]] const int64_t code_bytes = w.nb() * w.kb * 512, scale_bytes = w.nb() * w.groups * 32;
+
+    const uint4* codes[2];
+    const uint16_t* scales[2];
+    bool live[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t k = (int64_t)kb * 64 + 32 * h;
-            uint32_t a0[4], a1[4];
-            unpack8<T>(words[2 * h], a0);
-            unpack8<T>(words[2 * h + 1], a1);
+    for (int b = 0; b < 2; ++b) {
+        live[b] = nb0 + b < w.nb();
+        codes[b] = reinterpret_cast<const uint4*>(w.codes + (live[b] ? nb0 + b : 0) * w.kb * 128) + lane;
+        scales[b] = w.scales + (live[b] ? nb0 + b : 0) * w.groups * 16 + 2 * g;
+    }
+    const T* rows[MT];
+    bool row_live[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int64_t row = m0 + 8 * m + g;
-                const uint4 x = load_x8<T, VEC>(X + row * ldx, k + 8 * t, w.K, row < M);
-                mma_16816<T>(acc[m], a0[0], a0[1], a0[2], a0[3], x.x, x.y);
-                mma_16816<T>(acc[m], a1[0], a1[1], a1[2], a1[3], x.z, x.w);
+    for (int m = 0; m < MT; ++m) {
+        row_live[m] = m0 + 8 * m + g < M;
+        rows[m] = X + (row_live[m] ? m0 + 8 * m + g : 0) * ldx;
+    }
+    uint4 q[kAhead][2];
+    uint32_t s2[kAhead][2][HALF ? 2 : 1];
+    auto fetch = [&](int slot, int kb) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            q[slot][b] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+            if (kb < kb1 && live[b] && GEMM_DBG_OK(codes[b] + (int64_t)kb * 32, w.codes, code_bytes, 16))
+                q[slot][b] = load_once(codes[b] + (int64_t)kb * 32);
+#pragma unroll
+            for (int h = 0; h < (HALF ? 2 : 1); ++h) {
+                const int64_t k = (int64_t)kb * 64 + 32 * h;
+                const uint16_t* sp = scales[b] + (HALF ? k / 32 : k / w.group) * 16;
+                s2[slot][b][h] = 0;
+                if (kb < kb1 && live[b] && k < w.K && GEMM_DBG_OK(sp, w.scales, scale_bytes, 4))
+                    s2[slot][b][h] = __ldg(reinterpret_cast<const uint32_t*>(sp));
             }
-            if (by_half || h == 1) {
-                uint32_t s2 = 0;
-                const int64_t kk = by_half ? k : (int64_t)kb * 64;
-                if (kk < w.K) {
-                    const uint16_t* sp = w.scales + ((nb * w.groups + kk / w.group) * 8 + g) * 2;
-                    if (GEMM_DBG_OK(sp, w.scales, w.nb() * w.groups * 32, 4))
-                        s2 = __ldg(reinterpret_cast<const uint32_t*>(sp));
-                }
-                const float lo = __uint_as_float(s2 << 16), hi = __uint_as_float(s2 & 0xFFFF0000u);
+        }
+    };
+    float total[2][MT][4] = {};
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    total[m][0] = fmaf(acc[m][0], lo, total[m][0]);
-                    total[m][1] = fmaf(acc[m][1], lo, total[m][1]);
-                    total[m][2] = fmaf(acc[m][2], hi, total[m][2]);
-                    total[m][3] = fmaf(acc[m][3], hi, total[m][3]);
-                    acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
+    for (int p = 0; p < kAhead; ++p) fetch(p, kb0 + wk + p * WK);
+    for (int kb = kb0 + wk; kb < kb1; kb += kAhead * WK) {
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) {
+            const int at = kb + p * WK;
+            if (at >= kb1) break;
+            uint4 x[2][MT];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    x[h][m] = load_x8<T, VEC>(rows[m], (int64_t)at * 64 + 32 * h + 8 * t, w.K, row_live[m]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint32_t words[4] = {q[p][b].x, q[p][b].y, q[p][b].z, q[p][b].w};
+                float acc[MT][4] = {};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a0[4], a1[4];
+                    unpack8<T>(words[2 * h], a0);
+                    unpack8<T>(words[2 * h + 1], a1);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        mma_16816<T>(acc[m], a0[0], a0[1], a0[2], a0[3], x[h][m].x, x[h][m].y);
+                        mma_16816<T>(acc[m], a1[0], a1[1], a1[2], a1[3], x[h][m].z, x[h][m].w);
+                    }
+                    if (HALF || h == 1) {
+                        const uint32_t s = s2[p][b][HALF ? h : 0];
+                        const float lo = __uint_as_float(s << 16), hi = __uint_as_float(s & 0xFFFF0000u);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            total[b][m][0] = fmaf(acc[m][0], lo, total[b][m][0]);
+                            total[b][m][1] = fmaf(acc[m][1], lo, total[b][m][1]);
+                            total[b][m][2] = fmaf(acc[m][2], hi, total[b][m][2]);
+                            total[b][m][3] = fmaf(acc[m][3], hi, total[b][m][3]);
+                            acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
+                        }
+                    }
                 }
             }
+            fetch(p, at + kAhead * WK);
         }
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        part[warp][8 * m + 2 * t][g] = total[m][0];
-        part[warp][8 * m + 2 * t + 1][g] = total[m][1];
-        part[warp][8 * m + 2 * t][g + 8] = total[m][2];
-        part[warp][8 * m + 2 * t + 1][g + 8] = total[m][3];
-    }
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                part[wk][8 * m + 2 * t + (e & 1)][32 * wn + 16 * b + 8 * (e >> 1) + g] = total[b][m][e];
     __syncthreads();
     [[maybe_unused]] const int64_t c_bytes = ((M - 1) * ldc + w.N) * (int64_t)sizeof(U);
-    for (int i = threadIdx.x; i < MT * 8 * 16; i += kPWarps * 32) {
-        const int r = i / 16, c = i % 16;
-        const int64_t row = m0 + r, col = nb * 16 + c;
-        if (row >= M || col >= w.N) continue;
-        float v = part[0][r][c];
-#pragma unroll
-        for (int p = 1; p < kPWarps; ++p) v += part[p][r][c];
+    auto store = [&](int i, float v) {
+        const int64_t row = m0 + i / kCols, col = (nb0 - 2 * wn) * 16 + i % kCols;
+        if (row >= M || col >= w.N) return;
         U* dst = C + row * ldc + col;
         if (GEMM_DBG_OK(dst, C, c_bytes, sizeof(U))) *dst = from_float<U>(v);
+    };
+    for (int i = threadIdx.x; i < kRows * kCols; i += kPWarps * 32) {
+        float v = part[0][i / kCols][i % kCols];
+#pragma unroll
+        for (int p = 1; p < WK; ++p) v += part[p][i / kCols][i % kCols];
+        if (splits == 1) store(i, v);
+        else part[0][i / kCols][i % kCols] = v;
     }
+    if (splits == 1) return;
+    cluster_sync();
+    const int share = (kRows * kCols + splits - 1) / splits;
+    for (int i = rank * share + threadIdx.x; i < min(kRows * kCols, (rank + 1) * share); i += kPWarps * 32) {
+        const uint32_t at = smem_u32(&part[0][i / kCols][i % kCols]);
+        float v = ld_cluster_f32(mapa_shared(at, 0));
+        for (int p = 1; p < splits; ++p) v += ld_cluster_f32(mapa_shared(at, p));
+        store(i, v);
+    }
+    cluster_sync();   // no CTA leaves while another reads its sums
 }
 
 W4 view(const void* codes, const void* scales, int64_t K, int64_t N, int group) {
@@ -254,14 +390,43 @@ W4 view(const void* codes, const void* scales, int64_t K, int64_t N, int group) 
               (int)((K + 63) / 64), (int)((K + group - 1) / group)};
 }
 
+template <typename T, typename U, int MT, int WN, bool HALF, bool VEC>
+cudaError_t launch_product(const T* X, int64_t ldx, const W4& w, U* C, int64_t ldc, int64_t M,
+                           int num_sms, cudaStream_t stream) {
+    constexpr int WK = kPWarps / WN;
+    const int64_t tiles_n = (w.nb() + 2 * WN - 1) / (2 * WN), tiles = tiles_n * ((M + 8 * MT - 1) / (8 * MT));
+    // The blocks of rows are shared over a cluster until the CTAs fill the GPU
+    // twice, as long as every warp keeps two of them.
+    int splits = 1;
+    while (splits < 8 && tiles * splits < 2 * num_sms && w.kb >= 4 * splits * WK) splits *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * splits));
+    cfg.blockDim = dim3(kPWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, w4_gemm_kernel<T, U, MT, WN, HALF, VEC>, X, ldx, w, C, ldc, M, splits, tiles_n);
+}
+
+// More rows go with more columns to a CTA: X is read once for every tile of
+// columns, 2 * rows bytes beside each column's half byte of codes.
 template <typename T, typename U, bool VEC>
-void launch_product(const T* X, int64_t ldx, const W4& w, U* C, int64_t ldc, int64_t M,
-                    cudaStream_t stream) {
-    const int mt = M <= 8 ? 1 : M <= 16 ? 2 : 4;
-    const unsigned grid = (unsigned)(w.nb() * ((M + 8 * mt - 1) / (8 * mt)));
-    if (mt == 1) w4_gemm_kernel<T, U, 1, VEC><<<grid, kPWarps * 32, 0, stream>>>(X, ldx, w, C, ldc, M);
-    else if (mt == 2) w4_gemm_kernel<T, U, 2, VEC><<<grid, kPWarps * 32, 0, stream>>>(X, ldx, w, C, ldc, M);
-    else w4_gemm_kernel<T, U, 4, VEC><<<grid, kPWarps * 32, 0, stream>>>(X, ldx, w, C, ldc, M);
+cudaError_t launch_by_rows(const T* X, int64_t ldx, const W4& w, U* C, int64_t ldc, int64_t M,
+                           int num_sms, cudaStream_t stream) {
+    auto go = [&](auto mt, auto wn) {
+        constexpr int MT = decltype(mt)::value, WN = decltype(wn)::value;
+        return w.group == 32 ? launch_product<T, U, MT, WN, true, VEC>(X, ldx, w, C, ldc, M, num_sms, stream)
+                             : launch_product<T, U, MT, WN, false, VEC>(X, ldx, w, C, ldc, M, num_sms, stream);
+    };
+    using std::integral_constant;
+    if (M <= 2) return go(integral_constant<int, 1>(), integral_constant<int, 1>());
+    if (M <= 8) return go(integral_constant<int, 1>(), integral_constant<int, 2>());
+    if (M <= 16) return go(integral_constant<int, 2>(), integral_constant<int, 4>());
+    return go(integral_constant<int, 4>(), integral_constant<int, 4>());
 }
 
 }  // namespace
@@ -272,12 +437,14 @@ cudaError_t launch_w4_quantize(const void* B, int64_t ldb, ElemType type, int64_
                                int group, void* codes, void* scales, cudaStream_t stream) {
     const W4 w = view(codes, scales, K, N, group);
     const unsigned grid = (unsigned)(((K + kQRows - 1) / kQRows) * ((N + kQCols - 1) / kQCols));
+    const int64_t es = type == ElemType::kF32 ? 4 : 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(B) & 15u) == 0 && ldb * es % 16 == 0;
     if (type == ElemType::kF32)
-        w4_quantize_kernel<float><<<grid, kQThreads, 0, stream>>>(static_cast<const float*>(B), ldb, w);
+        w4_quantize_kernel<float><<<grid, kQThreads, 0, stream>>>(static_cast<const float*>(B), ldb, vec, w);
     else if (type == ElemType::kBF16)
-        w4_quantize_kernel<__nv_bfloat16><<<grid, kQThreads, 0, stream>>>(static_cast<const __nv_bfloat16*>(B), ldb, w);
+        w4_quantize_kernel<__nv_bfloat16><<<grid, kQThreads, 0, stream>>>(static_cast<const __nv_bfloat16*>(B), ldb, vec, w);
     else
-        w4_quantize_kernel<__half><<<grid, kQThreads, 0, stream>>>(static_cast<const __half*>(B), ldb, w);
+        w4_quantize_kernel<__half><<<grid, kQThreads, 0, stream>>>(static_cast<const __half*>(B), ldb, vec, w);
     return cudaGetLastError();
 }
 
@@ -286,34 +453,31 @@ cudaError_t launch_w4_dequantize(const void* codes, const void* scales, int64_t 
                                  cudaStream_t stream) {
     const W4 w = view(codes, scales, K, N, group);
     const unsigned grid = (unsigned)(((K + kQRows - 1) / kQRows) * ((N + kQCols - 1) / kQCols));
+    const int64_t es = type == ElemType::kF32 ? 4 : 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(B) & 15u) == 0 && ldb * es % 16 == 0;
     if (type == ElemType::kF32)
-        w4_dequantize_kernel<float><<<grid, kQThreads, 0, stream>>>(w, static_cast<float*>(B), ldb);
+        w4_dequantize_kernel<float><<<grid, kQThreads, 0, stream>>>(w, static_cast<float*>(B), ldb, vec);
     else if (type == ElemType::kBF16)
-        w4_dequantize_kernel<__nv_bfloat16><<<grid, kQThreads, 0, stream>>>(w, static_cast<__nv_bfloat16*>(B), ldb);
+        w4_dequantize_kernel<__nv_bfloat16><<<grid, kQThreads, 0, stream>>>(w, static_cast<__nv_bfloat16*>(B), ldb, vec);
     else
-        w4_dequantize_kernel<__half><<<grid, kQThreads, 0, stream>>>(w, static_cast<__half*>(B), ldb);
+        w4_dequantize_kernel<__half><<<grid, kQThreads, 0, stream>>>(w, static_cast<__half*>(B), ldb, vec);
     return cudaGetLastError();
 }
 
 cudaError_t launch_w4_gemm(const void* X, int64_t ldx, ElemType x_type, const void* codes,
                            const void* scales, void* C, int64_t ldc, ElemType c_type, int64_t M,
-                           int64_t K, int64_t N, int group, cudaStream_t stream) {
+                           int64_t K, int64_t N, int group, int num_sms, cudaStream_t stream) {
     const W4 w = view(codes, scales, K, N, group);
     const bool vec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && (ldx % 8 == 0 || M == 1);
     auto go = [&](auto x, auto c) {
         using T = decltype(x);
         using U = decltype(c);
-        if (vec) launch_product<T, U, true>(static_cast<const T*>(X), ldx, w, static_cast<U*>(C), ldc, M, stream);
-        else launch_product<T, U, false>(static_cast<const T*>(X), ldx, w, static_cast<U*>(C), ldc, M, stream);
+        return vec ? launch_by_rows<T, U, true>(static_cast<const T*>(X), ldx, w, static_cast<U*>(C), ldc, M, num_sms, stream)
+                   : launch_by_rows<T, U, false>(static_cast<const T*>(X), ldx, w, static_cast<U*>(C), ldc, M, num_sms, stream);
     };
-    if (x_type == ElemType::kBF16) {
-        if (c_type == ElemType::kF32) go(__nv_bfloat16(), float());
-        else go(__nv_bfloat16(), __nv_bfloat16());
-    } else {
-        if (c_type == ElemType::kF32) go(__half(), float());
-        else go(__half(), __half());
-    }
-    return cudaGetLastError();
+    if (x_type == ElemType::kBF16)
+        return c_type == ElemType::kF32 ? go(__nv_bfloat16(), float()) : go(__nv_bfloat16(), __nv_bfloat16());
+    return c_type == ElemType::kF32 ? go(__half(), float()) : go(__half(), __half());
 }
 
 }  // namespace libgemm

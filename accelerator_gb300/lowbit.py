@@ -35,9 +35,11 @@ class _CKvCache(ctypes.Structure):
                 ("page_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
-def _stream(stream) -> int:
+def _stream(stream, device):
+    """The address of `stream`, or of the current stream of `device` (asked for
+    by number: making a Stream object of it costs 3 us, a kernel's launch)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(device.index) or None
     return stream.cuda_stream or None
 
 
@@ -106,7 +108,7 @@ def w4_quantize(B, group=128, stream=None) -> W4Matrix:
     scales = _empty(scale_bytes // 2, torch.bfloat16, B.device, stream)
     W = W4Matrix(codes, scales, K, N, group)
     rc = binding.lib().gemm_w4_quantize(B.data_ptr() or None, ldb, _TYPES[B.dtype], K, N, group, *W._args,
-                                        _stream(stream))
+                                        _stream(stream, B.device))
     if rc != binding.OK:
         raise GemmError(rc, "gemm_w4_quantize")
     return W
@@ -123,7 +125,7 @@ def w4_dequantize(W: W4Matrix, out=None, dtype=torch.bfloat16, stream=None):
     if tuple(out.shape) != (W.K, W.N):
         raise ValueError(f"out has shape {tuple(out.shape)}, not {(W.K, W.N)}")
     rc = binding.lib().gemm_w4_dequantize(*W._args, W.K, W.N, W.group, out.data_ptr() or None, ldb,
-                                          _TYPES[out.dtype], _stream(stream))
+                                          _TYPES[out.dtype], _stream(stream, out.device))
     if rc != binding.OK:
         raise GemmError(rc, "gemm_w4_dequantize")
     return out
@@ -154,7 +156,7 @@ def gemm_w4(X, W: W4Matrix, C=None, dtype=None, stream=None):
             raise ValueError(f"C has shape {tuple(C.shape)}, not {(M, W.N)}")
     _need(C.dtype == xt or C.dtype == torch.float32, "C", "of X's type or float32")
     rc = binding.lib().gemm_w4(X.data_ptr() or None, ldx, _TYPES[xt], *W._args, C.data_ptr() or None, ldc,
-                               _TYPES[C.dtype], M, K, W.N, W.group, _stream(stream))
+                               _TYPES[C.dtype], M, K, W.N, W.group, _stream(stream, X.device))
     if rc != binding.OK:
         raise GemmError(rc, "gemm_w4")
     return C
@@ -227,7 +229,7 @@ def kv_append(cache: KvCache, K, V, page_table, starts, first, stream=None):
         raise ValueError(f"{K.shape[0]} keys and {V.shape[0]} values")
     rc = binding.lib().gemm_kv_append(cache._ref, K.data_ptr() or None, kr, kh, V.data_ptr() or None, vr, vh,
                                       _TYPES[K.dtype], page_table.data_ptr() or None, width, starts.data_ptr(),
-                                      first.data_ptr() or None, K.shape[0], sequences, _stream(stream))
+                                      first.data_ptr() or None, K.shape[0], sequences, _stream(stream, cache.device))
     if rc != binding.OK:
         raise GemmError(rc, "gemm_kv_append")
 
@@ -242,7 +244,7 @@ def kv_read(cache: KvCache, page_table, starts, first, tokens, dtype=torch.bfloa
     V = _empty((tokens, cache.heads, cache.head_dim), dtype, cache.device, stream)
     rc = binding.lib().gemm_kv_read(cache._ref, K.data_ptr() or None, V.data_ptr() or None, _TYPES[dtype],
                                     page_table.data_ptr() or None, width, starts.data_ptr(),
-                                    first.data_ptr() or None, tokens, sequences, _stream(stream))
+                                    first.data_ptr() or None, tokens, sequences, _stream(stream, cache.device))
     if rc != binding.OK:
         raise GemmError(rc, "gemm_kv_read")
     return K, V
@@ -269,7 +271,7 @@ def kv_attention(Q, cache: KvCache, page_table, starts, lengths, scale=None, cau
     rc = binding.lib().gemm_kv_attention(cache._ref, Q.data_ptr() or None, qr, qh, out.data_ptr() or None, orow, oh,
                                          _TYPES[Q.dtype], Q.shape[1], scale, causal, window,
                                          page_table.data_ptr() or None, width, starts.data_ptr(),
-                                         lengths.data_ptr() or None, Q.shape[0], sequences, _stream(stream))
+                                         lengths.data_ptr() or None, Q.shape[0], sequences, _stream(stream, cache.device))
     if rc != binding.OK:
         raise GemmError(rc, "gemm_kv_attention")
     return out
