@@ -77,7 +77,8 @@ int device_state(DeviceState** out) {
         } else if (major != 10 || minor != 3) {
             st.status = GEMM_ERR_UNSUPPORTED_DEVICE;
         } else if (cudaGetSymbolAddress(reinterpret_cast<void**>(&st.err), g_error_word) != cudaSuccess ||
-                   ffma_setup() != cudaSuccess || tc_setup() != cudaSuccess) {
+                   ffma_setup() != cudaSuccess || tc_setup() != cudaSuccess ||
+                   kv_attention_setup() != cudaSuccess) {
             st.status = GEMM_ERR_CUDA;
         } else if (!make_pool(dev, &st.pool)) {
             st.status = GEMM_ERR_CUDA;

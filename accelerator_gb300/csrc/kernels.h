@@ -223,13 +223,14 @@ cudaError_t launch_kv_append(const KvView& c, const KvRows& K, const KvRows& V, 
                              const KvBatch& b, unsigned* err, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvView& c, void* K, void* V, ElemType type, const KvBatch& b,
                            unsigned* err, cudaStream_t stream);
-// Attention in two launches when the tokens are split over CTAs: partial
-// results go to scratch (plan.scratch_bytes) and a second launch joins them.
+// Attention: `splits` CTAs share the tokens of a tile of rows, as a cluster
+// or, with scratch (plan.scratch_bytes), joined by a second launch.
 struct KvPlan {
     int64_t units;        // upper bound of the row tiles of the batch
     int splits;
     int64_t scratch_bytes;
 };
+cudaError_t kv_attention_setup();
 KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, int num_sms);
 cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& O, ElemType type,
                                 int q_heads, float scale, bool causal, int64_t window,

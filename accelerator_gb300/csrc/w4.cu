@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kQThreads)
 // ---- the product -------------------------------------------------------------
 constexpr int kPWarps = 8;
 constexpr int kAhead = 4;       // blocks of 64 rows whose codes a warp has in flight
+constexpr int resident(int mt) { return mt <= 2 ? 2 : 1; }   // CTAs of an SM
 
 // Four nibble pairs of a word as pairs of T holding q, exactly.
 template <typename T>
@@ -226,14 +227,10 @@ __device__ __forceinline__ void unpack8<__nv_bfloat16>(uint32_t w, uint32_t (&a)
 }
 
 // Eight neighbours x[k .. k + 7] of one row of X as four pairs; 0 past K.
-template <typename T, bool VEC>
-__device__ __forceinline__ uint4 load_x8(const T* row, int64_t k, int64_t K, bool live) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (!live || k >= K) return v;
-    if (VEC && k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+template <typename T>
+__device__ __noinline__ uint4 load_x8_edge(const T* row, int k, int K) {
     uint32_t r[4] = {0, 0, 0, 0};
     const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
-#pragma unroll
     for (int i = 0; i < 8; ++i)
         if (k + i < K) r[i / 2] |= (uint32_t)__ldg(p + k + i) << (16 * (i & 1));
     return make_uint4(r[0], r[1], r[2], r[3]);
@@ -257,7 +254,7 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 // loaded serves both).  The sums are added up over the warps, then over the
 // cluster's CTAs through distributed shared memory, always in that order.
 template <typename T, typename U, int MT, int WN, bool HALF, bool VEC>
-__global__ void __launch_bounds__(kPWarps * 32, MT <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(kPWarps * 32, resident(MT))
     w4_gemm_kernel(const T* __restrict__ X, int64_t ldx, W4 w, U* __restrict__ C, int64_t ldc,
                    int64_t M, int splits, int64_t tiles_n) {
     constexpr int WK = kPWarps / WN, kCols = 32 * WN, kRows = 8 * MT;
@@ -273,52 +270,67 @@ __global__ void __launch_bounds__(kPWarps * 32, MT <= 2 ? 2 : 1)
 
     const uint4* codes[2];
     const uint16_t* scales[2];
-    bool live[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        live[b] = nb0 + b < w.nb();
-        codes[b] = reinterpret_cast<const uint4*>(w.codes + (live[b] ? nb0 + b : 0) * w.kb * 128) + lane;
-        scales[b] = w.scales + (live[b] ? nb0 + b : 0) * w.groups * 16 + 2 * g;
+        // past the last column the last block again, whose sums are not stored
+        const int64_t nb = min(nb0 + b, w.nb() - 1);
+        codes[b] = reinterpret_cast<const uint4*>(w.codes + nb * w.kb * 128) + lane;
+        scales[b] = w.scales + nb * w.groups * 16 + 2 * g;
     }
-    const T* rows[MT];
-    bool row_live[MT];
+    const T* rows[MT];   // past the last row that row again, likewise
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        row_live[m] = m0 + 8 * m + g < M;
-        rows[m] = X + (row_live[m] ? m0 + 8 * m + g : 0) * ldx;
-    }
+    for (int m = 0; m < MT; ++m) rows[m] = X + min(m0 + 8 * m + g, M - 1) * ldx + 8 * t;
     uint4 q[kAhead][2];
     uint32_t s2[kAhead][2][HALF ? 2 : 1];
+    const int group_shift = w.group == 128 ? 1 : 0;   // blocks of a group
     auto fetch = [&](int slot, int kb) {
+        kb = min(kb, kb1 - 1);   // past the end the last block again, unused
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            q[slot][b] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-            if (kb < kb1 && live[b] && GEMM_DBG_OK(codes[b] + (int64_t)kb * 32, w.codes, code_bytes, 16))
-                q[slot][b] = load_once(codes[b] + (int64_t)kb * 32);
+            if (GEMM_DBG_OK(codes[b] + kb * 32, w.codes, code_bytes, 16)) q[slot][b] = load_once(codes[b] + kb * 32);
 #pragma unroll
             for (int h = 0; h < (HALF ? 2 : 1); ++h) {
-                const int64_t k = (int64_t)kb * 64 + 32 * h;
-                const uint16_t* sp = scales[b] + (HALF ? k / 32 : k / w.group) * 16;
-                s2[slot][b][h] = 0;
-                if (kb < kb1 && live[b] && k < w.K && GEMM_DBG_OK(sp, w.scales, scale_bytes, 4))
-                    s2[slot][b][h] = __ldg(reinterpret_cast<const uint32_t*>(sp));
+                // a last half block past K has X = 0: any scale of the column will do
+                const uint16_t* sp = scales[b] + (HALF ? min(2 * kb + h, w.groups - 1) : kb >> group_shift) * 16;
+                if (GEMM_DBG_OK(sp, w.scales, scale_bytes, 4)) s2[slot][b][h] = __ldg(reinterpret_cast<const uint32_t*>(sp));
             }
         }
     };
-    float total[2][MT][4] = {};
+    const int K = (int)w.K;
+    [[maybe_unused]] const int64_t x_bytes = ((M - 1) * ldx + w.K) * (int64_t)sizeof(T);
+    constexpr int kX = MT <= 2 ? 2 : 1;   // parts of X: with few rows the next block's are in flight too
+    uint4 x[kX][2][MT];
+    auto fetch_x = [&](int slot, int kb) {
+        kb = min(kb, kb1 - 1);
+        if (VEC && kb * 64 + 64 <= K) {
 #pragma unroll
-    for (int p = 0; p < kAhead; ++p) fetch(p, kb0 + wk + p * WK);
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const T* p = rows[m] + kb * 64 + 32 * h;
+                    if (GEMM_DBG_OK(p, X, x_bytes, 16)) x[slot][h][m] = __ldg(reinterpret_cast<const uint4*>(p));
+                }
+        } else {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    x[slot][h][m] = load_x8_edge(rows[m], kb * 64 + 32 * h, K - 8 * t);
+        }
+    };
+    float total[2][MT][4] = {};
+    if (kb0 + wk < kb1) {
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) fetch(p, kb0 + wk + p * WK);
+        if (kX == 2) fetch_x(0, kb0 + wk);
+    }
     for (int kb = kb0 + wk; kb < kb1; kb += kAhead * WK) {
 #pragma unroll
         for (int p = 0; p < kAhead; ++p) {
             const int at = kb + p * WK;
             if (at >= kb1) break;
-            uint4 x[2][MT];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    x[h][m] = load_x8<T, VEC>(rows[m], (int64_t)at * 64 + 32 * h + 8 * t, w.K, row_live[m]);
+            fetch_x((p + 1) % kX, kX == 2 ? at + WK : at);
+            const int xs = p % kX;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const uint32_t words[4] = {q[p][b].x, q[p][b].y, q[p][b].z, q[p][b].w};
@@ -330,8 +342,8 @@ __global__ void __launch_bounds__(kPWarps * 32, MT <= 2 ? 2 : 1)
                     unpack8<T>(words[2 * h + 1], a1);
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
-                        mma_16816<T>(acc[m], a0[0], a0[1], a0[2], a0[3], x[h][m].x, x[h][m].y);
-                        mma_16816<T>(acc[m], a1[0], a1[1], a1[2], a1[3], x[h][m].z, x[h][m].w);
+                        mma_16816<T>(acc[m], a0[0], a0[1], a0[2], a0[3], x[xs][h][m].x, x[xs][h][m].y);
+                        mma_16816<T>(acc[m], a1[0], a1[1], a1[2], a1[3], x[xs][h][m].z, x[xs][h][m].w);
                     }
                     if (HALF || h == 1) {
                         const uint32_t s = s2[p][b][HALF ? h : 0];
@@ -395,10 +407,17 @@ cudaError_t launch_product(const T* X, int64_t ldx, const W4& w, U* C, int64_t l
                            int num_sms, cudaStream_t stream) {
     constexpr int WK = kPWarps / WN;
     const int64_t tiles_n = (w.nb() + 2 * WN - 1) / (2 * WN), tiles = tiles_n * ((M + 8 * MT - 1) / (8 * MT));
-    // The blocks of rows are shared over a cluster until the CTAs fill the GPU
-    // twice, as long as every warp keeps two of them.
+    // The blocks of rows are shared over a cluster of the size for which the
+    // rounds of resident CTAs take least, a round costing the blocks of a warp
+    // and about five more to start and to add up.
+    const int64_t slots = (int64_t)num_sms * resident(MT);
     int splits = 1;
-    while (splits < 8 && tiles * splits < 2 * num_sms && w.kb >= 4 * splits * WK) splits *= 2;
+    int64_t least = INT64_MAX;
+    for (int s = 1; s <= 8 && (s == 1 || s * WK <= w.kb); ++s) {
+        const int64_t per = (w.kb + s - 1) / s;
+        const int64_t cost = (tiles * s + slots - 1) / slots * ((per + WK - 1) / WK + 5);
+        if (cost < least) least = cost, splits = s;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * splits));
     cfg.blockDim = dim3(kPWarps * 32);
