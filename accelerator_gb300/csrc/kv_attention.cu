@@ -14,7 +14,6 @@
 namespace libgemm {
 namespace {
 
-constexpr int kRows = 16;        // query rows of a tile (one m16 matrix instruction)
 constexpr int kWarps = 4;        // warps that compute; one more copies
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kSub = 16;         // tokens a warp takes at once
@@ -22,8 +21,10 @@ constexpr int kStep = kWarps * kSub;   // tokens of a stage
 constexpr int kMinSteps = 2;     // stages of a split, at least
 constexpr int kRingBytes = 96 * 1024;  // two CTAs of an SM keep 192 KB in flight
 constexpr int kMaxCluster = 8;
-constexpr float kNegInf = -INFINITY;
-constexpr float kPScale = 32768.0f;   // weights enter the second product times 2^15
+constexpr float kNegInf = -INFINITY, kLowest = -3.402823466e38f;
+// Weights enter the second product as binary16 times 2^15, under 2^16: the
+// maximum that they are relative to may lag behind by this much (in log2).
+constexpr float kPScale = 32768.0f, kLag = 0.9f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -39,60 +40,58 @@ struct AttnArgs {
     int q_heads, share;          // query heads, and how many read one cache head
     float scale_log2;            // scale * log2(e)
     int causal;
-    int64_t window;
+    int window;
     int splits;                  // CTAs that share a tile's tokens: a cluster, or with `partial` any number
     bool q_vec;                  // Q in 16-byte loads
-    float* partial;              // [unit][head][split] x (kRows x dim sums, then kRows x (max, sum))
+    float* partial;              // [unit][head][split] x (rows x dim sums, then rows x (max, sum))
     unsigned* err;
 };
 
-// The tile of a unit: its sequence and rows, and the tokens that it sees.
+// The tile of a unit: its sequence and rows, and the tokens that it sees
+// (token numbers fit 32 bits, as the lengths do).
 struct Tile {
     int seq;
     int64_t row0;                // first of the sequence's rows
     int64_t r0, nrows;           // first row (query, head pair) of the tile; rows of the sequence
-    int64_t len, p0;             // cached tokens; position of query 0
-    int64_t tok0;                // first token, a multiple of kStep
-    int64_t hi;                  // end of the tokens any row sees
+    int len, p0;                 // cached tokens; position of query 0
+    int tok0;                    // first token, a multiple of kStep
+    int hi;                      // end of the tokens any row sees
     int steps, per, active;      // steps in all, per split, splits that have any
 
-    __device__ __forceinline__ int64_t row_hi(const AttnArgs& a, int64_t r) const {
-        if (r >= nrows) return 0;
-        const int64_t p = p0 + r / a.share;
+    // Row r sees the tokens row_lo(r) .. row_hi(r) - 1; both grow with r.
+    __device__ __forceinline__ int row_hi(const AttnArgs& a, int64_t r) const {
+        const int p = p0 + (int)(r / a.share);
         if (p < 0) return 0;
         return a.causal ? p + 1 : len;
     }
-    __device__ __forceinline__ int64_t row_lo(const AttnArgs& a, int64_t r) const {
-        const int64_t p = p0 + r / a.share;
+    __device__ __forceinline__ int row_lo(const AttnArgs& a, int64_t r) const {
+        const int p = p0 + (int)(r / a.share);
         return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
     }
-    __device__ __forceinline__ bool find(const AttnArgs& a, int64_t u, bool report) {
+    __device__ __forceinline__ bool find(const AttnArgs& a, int64_t u, int rows, int step, bool report) {
         const Starts starts{a.b.starts, a.b.sequences, a.b.rows};
-        // Sequence q's tiles are units floor(starts[q] * share / 16) + q + j.
-        seq = last_not_above(a.b.sequences, u, [&](int i) { return starts.at(i) * a.share / kRows + i; });
+        // Sequence q's tiles are units floor(starts[q] * share / rows) + q + j.
+        seq = last_not_above(a.b.sequences, u, [&](int i) { return starts.at(i) * a.share / rows + i; });
         row0 = starts.at(seq);
-        const int64_t count = starts.at(seq + 1) - row0;
+        const int64_t count = starts.at(seq + 1) - row0, length = __ldg(a.b.at + seq);
         if (!starts.whole(u == 0, seq)) {
             if (report) atomicOr(a.err, kErrIndex);
             return false;
         }
         nrows = count * a.share;
-        r0 = (u - row0 * a.share / kRows - seq) * kRows;
+        r0 = (u - row0 * a.share / rows - seq) * rows;
         if (r0 < 0 || r0 >= nrows) return false;
-        len = __ldg(a.b.at + seq);
-        if (len < 0 || len > (a.b.width << a.c.page_log2)) {
+        len = (int)length;
+        if (length < 0 || length > (a.b.width << a.c.page_log2)) {
             if (report) atomicOr(a.err, kErrIndex);
             len = 0;
         }
-        p0 = len - count;
-        const int64_t last = r0 + kRows - 1 < nrows ? r0 + kRows - 1 : nrows - 1;
-        hi = row_hi(a, last);
-        tok0 = row_lo(a, r0) / kStep * kStep;
-        steps = hi > tok0 ? (int)((hi - tok0 + kStep - 1) / kStep) : 0;
-        per = (steps + a.splits - 1) / a.splits;
-        if (per < kMinSteps) per = kMinSteps;
-        active = (steps + per - 1) / per;
-        if (active < 1) active = 1;
+        p0 = len - (int)count;
+        hi = row_hi(a, (r0 + rows < nrows ? r0 + rows : nrows) - 1);
+        tok0 = row_lo(a, r0) / step * step;
+        steps = hi > tok0 ? (hi - tok0 + step - 1) / step : 0;
+        per = max(kMinSteps, (steps + a.splits - 1) / a.splits);
+        active = max(1, (steps + per - 1) / per);
         return true;
     }
 };
@@ -141,19 +140,29 @@ struct Ring {
     static constexpr int kBarsAt = kInfoAt + kStages * kWarps * (int)sizeof(SubInfo);
     static constexpr int kAbortAt = kBarsAt + 16 * kStages;
     static constexpr int kBytes = kAbortAt + 16;
-    // the joining of the warps reuses the ring: [warps][rows][D + 4] sums, maxima, sums of weights
-    static constexpr int kLd = D + 4;
-    static_assert(kWarps * kRows * (kLd + 2) * 4 <= kInfoAt, "");
 };
 
-// Few query rows: a tile of 16 rows over a share of its tokens.  One warp
+// The 8 x 8 binary16 matrix that a warp holds in fragments (lane 4 g + t has
+// row g, columns 2t and 2t + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Few query rows: a tile of 8 * NQ rows over a share of its tokens.  One warp
 // copies whole pages' parts into a ring of stages of 64 tokens (their codes
-// lie in one piece for a page and head), four take 16 tokens of each stage
-// with all rows.  Bound by reading the codes; at 64 sequences of up to 8192
-// tokens, 8 x 8 heads of 128, the ring's two CTAs per SM keep HBM busy.
-template <typename T, int D>
+// lie in one piece for a page and head), four take 16 tokens of each stage.
+// Both products have the tokens' side, of which there is much, as the 16-row
+// operand and the queries as its eight columns: S^T = K Q^T, then O^T = V^T
+// P^T, for which the weights are turned over in registers; a product of 16
+// query rows would be half empty for the usual eight or fewer heads to a key
+// head.  Bound by reading the codes.
+template <typename T, int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArgs a) {
     using R = Ring<D>;
+    constexpr int kRows = 8 * NQ, kLd = D + 4;
+    static_assert(kWarps * kRows * (kLd + 2) * 4 + 8 * kRows <= R::kInfoAt, "the joining reuses the ring");
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t ring = smem_u32(smem), bars = ring + R::kBarsAt;   // full[stages], empty[stages]
     SubInfo* info = reinterpret_cast<SubInfo*>(smem + R::kInfoAt);
@@ -164,10 +173,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
     const bool cluster = a.splits > 1 && !a.partial;
     Tile tile;
     // A cluster's CTAs have one tile: they leave here together or not at all.
-    if (!tile.find(a, u, threadIdx.x == 0 && h == 0 && split == 0) || (!cluster && split >= tile.active)) return;
+    if (!tile.find(a, u, kRows, kStep, threadIdx.x == 0 && h == 0 && split == 0) || (!cluster && split >= tile.active)) return;
     const int step_begin = min(tile.steps, split * tile.per);
     const int steps = min(tile.steps, step_begin + tile.per) - step_begin;
-    const int64_t tok_begin = tile.tok0 + (int64_t)step_begin * kStep;
+    const int tok_begin = tile.tok0 + step_begin * kStep;
     if (threadIdx.x == 0) {
         for (int s = 0; s < R::kStages; ++s) {
             mbar_init(bars + 8 * s, 1);
@@ -179,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
     __syncthreads();
 
     float* s_o = reinterpret_cast<float*>(smem);                     // [warps][rows][kLd]
-    float* s_m = s_o + kWarps * kRows * R::kLd;                      // [warps][rows]
+    float* s_m = s_o + kWarps * kRows * kLd;                      // [warps][rows]
     float* s_l = s_m + kWarps * kRows;
     if (warp == kWarps) {
         // ---- copies: lane i looks up 16 tokens, for 32 of them at a time ----
@@ -192,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         int stage = 0, issued = 0;
         for (int s = 0; s < steps; ++s) {
             if (s % 8 == 0) {
-                const int64_t tok = tok_begin + (int64_t)s * kStep + lane * kSub;
+                const int tok = tok_begin + s * kStep + lane * kSub;
                 bool live = tok < tile.hi;
                 const int64_t page = live ? __ldg(table + (tok >> log2)) : 0;
                 if (live && (page < 0 || page >= a.c.pages)) {
@@ -242,24 +251,23 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         __syncthreads();   // the ring is free
         __syncthreads();   // the warps' results are in it
     } else {
-        // Q rows g and g + 8 as A fragments.  A lane's part of a row is 16
+        // Query row 8n + g as the column g of B.  A lane's part of a row is 16
         // neighbours of each 64: its k of four instructions, in the order in
         // which its 16 bytes of a key row hold them.  bfloat16 rows are brought
         // to [1, 2) by a power of two (exact, but for elements under 2^-14 of the
         // row's largest, whose error stays under 2^-25 of it) to be binary16.
-        uint32_t qf[D / 16][4];
-        float row_scale[2];
-        int64_t row_lo[2], row_hi[2];
+        uint32_t qf[NQ][D / 16][2];
+        float row_scale[NQ][2];      // of the rows 8n + 2t, + 1, whose scores a lane gets
+        int row_lo[NQ][2], row_hi[NQ][2];
         [[maybe_unused]] const int64_t q_bytes =
             ((a.b.rows - 1) * a.Q.row + (a.q_heads - 1) * a.Q.head + D) * (int64_t)sizeof(T);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t r = tile.r0 + g + 8 * i;
+        for (int n = 0; n < NQ; ++n) {
+            const int64_t r = tile.r0 + 8 * n + g;
             const bool live = r < tile.nrows;
             const T* p = static_cast<const T*>(a.Q.p) + (tile.row0 + (live ? r / a.share : 0)) * a.Q.row +
                          (h * a.share + (live ? r % a.share : 0)) * a.Q.head;
             Eight<T> x[D / 64][2] = {};
-            float top = 0.0f;
 #pragma unroll
             for (int j = 0; j < D / 64; ++j)
 #pragma unroll
@@ -269,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                 }
             float up = 1.0f, down = 1.0f;
             if constexpr (!std::is_same<T, __half>::value) {
+                float top = 0.0f;
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j)
 #pragma unroll
@@ -282,28 +291,38 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                     down = __uint_as_float((uint32_t)(254 - k) << 23);   // 2^(127 - k)
                 }
             }
-            row_scale[i] = a.scale_log2 * up;
+            if (a.scale_log2 < 0.0f) down = -down;   // the scores' scale is positive from here on
 #pragma unroll
             for (int j = 0; j < D / 64; ++j)
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const Eight<T>& e = x[j][s / 2];
                     const int o = 4 * (s % 2);
-                    qf[4 * j + s][i] = pack2<__half>(e.at(o) * down, e.at(o + 1) * down);
-                    qf[4 * j + s][2 + i] = pack2<__half>(e.at(o + 2) * down, e.at(o + 3) * down);
+                    qf[n][4 * j + s][0] = pack2<__half>(e.at(o) * down, e.at(o + 1) * down);
+                    qf[n][4 * j + s][1] = pack2<__half>(e.at(o + 2) * down, e.at(o + 3) * down);
                 }
-            row_lo[i] = tile.row_lo(a, r);
-            row_hi[i] = tile.row_hi(a, r);
-        }
-        // tokens that every row of the tile sees (rows past the last one see none)
-        const int64_t full_lo = tile.row_lo(a, tile.r0 + kRows - 1);
-        const int64_t full_hi = tile.r0 + kRows <= tile.nrows ? tile.row_hi(a, tile.r0) : 0;
-
-        constexpr int NT = D / 8;      // column tiles of the output
-        float o[NT][4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-        float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f}, ref = 0.0f;
+            for (int i = 0; i < 2; ++i) {
+                row_scale[n][i] = fabsf(a.scale_log2) * __shfl_sync(0xFFFFFFFFu, up, 4 * (2 * t + i));
+                // rows past the last one see all: they are not stored
+                const int64_t rr = tile.r0 + 8 * n + 2 * t + i;
+                row_lo[n][i] = rr < tile.nrows ? tile.row_lo(a, rr) : 0;
+                row_hi[n][i] = rr < tile.nrows ? tile.row_hi(a, rr) : tile.hi;
+            }
+        }
+        // tokens that every row of the tile sees
+        const int full_lo = tile.row_lo(a, (tile.r0 + kRows < tile.nrows ? tile.r0 + kRows : tile.nrows) - 1);
+        const int full_hi = tile.row_hi(a, tile.r0);
+
+        constexpr int MT = D / 16;      // row tiles of O^T: row g of tile i is d = g * D / 8 + 2i, row g + 8 the next
+        float o[NQ][MT][4], m[NQ][2], l[NQ][2], ref = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
+            m[n][0] = m[n][1] = kLowest;
+            l[n][0] = l[n][1] = 0.0f;
+        }
 
         uint32_t phase = 0;
         int stage = 0;
@@ -312,23 +331,20 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
             const SubInfo in = info[stage * kWarps + warp];
             const uint32_t kat = ring + stage * R::kStageBytes + warp * kSub * D, vat = kat + kStep * D;
             if (in.live) {
-                const int64_t tok = tok_begin + (int64_t)s * kStep + warp * kSub;
-                float sc[2][4];
+                const int tok = tok_begin + s * kStep + warp * kSub;
+                // scores of tokens g and g + 8 for the rows 2t, 2t + 1
+                float sc[NQ][2][4] = {};
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    float part[2][4] = {};
+                for (int j = 0; j < D / 64; ++j) {
+                    const uint4 w0 = lds128(kat + g * D + 64 * j + 16 * t), w1 = lds128(kat + (g + 8) * D + 64 * j + 16 * t);
+                    const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                    for (int j = 0; j < D / 64; ++j) {
-                        const uint4 w = lds128(kat + (8 * n + g) * D + 64 * j + 16 * t);
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t a0 = codes01(lo[k]), a1 = codes01(hi[k]), a2 = codes23(lo[k]), a3 = codes23(hi[k]);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t(&f)[4] = qf[4 * j + k];
-                            mma_16816<__half>(part[k & 1], f[0], f[1], f[2], f[3], codes01(ws[k]), codes23(ws[k]));
-                        }
+                        for (int n = 0; n < NQ; ++n)
+                            mma_16816<__half>(sc[n][k & 1], a0, a1, a2, a3, qf[n][4 * j + k][0], qf[n][4 * j + k][1]);
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[n][e] = part[0][e] + part[1][e];
                 }
                 uint32_t vw[4][D / 32];
 #pragma unroll
@@ -342,74 +358,107 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                         vw[i][0] = w.x, vw[i][1] = w.y;
                     }
                 }
-                const bool all = tok >= full_lo && tok + kSub <= full_hi;
-                const float f0 = row_scale[0] * in.ks, f1 = row_scale[1] * in.ks;
+                float f[NQ][2];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = sc[n][e] * (e < 2 ? f0 : f1);
-                        if (!all) {
-                            const int64_t j = tok + 8 * n + 2 * t + (e & 1);
-                            if (j < row_lo[e >> 1] || j >= row_hi[e >> 1]) x = kNegInf;
-                        }
-                        sc[n][e] = x;
-                    }
-                float top[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    top[i] = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
-                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
-                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
-                }
-                // The sums so far are brought to a new maximum, or a new largest
-                // value scale, only when there is one.
-                if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1] || in.vs > ref)) {
-                    const float nref = fmaxf(ref, in.vs);
-                    const float grow = ref == nref ? 1.0f : ref / nref;   // ref = 0 at first: o is still 0
-                    float keep[2];
+                    for (int e = 0; e < 4; ++e) sc[n][0][e] += sc[n][1][e];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float nm = fmaxf(m[i], top[i]);
-                        keep[i] = exp2_approx(m[i] - (nm == kNegInf ? 0.0f : nm));
-                        m[i] = nm;
-                        l[i] *= keep[i];
-                        keep[i] *= grow;
+                        // a page of zeros has scale 0: above 0, so that a hidden token's -inf stays that
+                        f[n][i] = row_scale[n][i] * in.ks;
+                        if (f[n][i] < 1.1754943508222875e-38f) f[n][i] = 1.1754943508222875e-38f;
                     }
+                }
+                if (tok < full_lo || tok + kSub > full_hi) {
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = tok + g + 8 * (e >> 1);
+                            if (j < row_lo[n][e & 1] || j >= row_hi[n][e & 1]) sc[n][0][e] = kNegInf;
+                        }
+                    asm volatile("");   // a branch: few tokens come here
+                }
+                if (in.ks != in.ks) {   // a page that reads as NaN: for the rows that see it alone
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[n][0][e] = sc[n][0][e] == kNegInf ? kNegInf : in.ks;
+                        f[n][0] = f[n][1] = 1.0f;
+                    }
+                }
+                float w[NQ][4];
+                bool above = in.vs > ref;
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[n][e] = fmaf(sc[n][0][e], f[n][e & 1], -m[n][e & 1]);
+                        above |= w[n][e] > kLag;
+                    }
+                // The sums so far are brought to a new maximum, or a new largest
+                // value scale, only when one is passed.
+                if (__any_sync(0xFFFFFFFFu, above)) {
+                    const float nref = fmaxf(ref, in.vs);
+                    const float grow = ref == nref ? 1.0f : __fdividef(ref, nref);   // ref = 0 at first: o is still 0
                     ref = nref;
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        o[i][0] *= keep[0], o[i][1] *= keep[0];
-                        o[i][2] *= keep[1], o[i][3] *= keep[1];
+                    for (int n = 0; n < NQ; ++n) {
+                        float keep[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float top = fmaxf(fmaxf(sc[n][0][i], sc[n][0][2 + i]) * f[n][i], m[n][i]);
+                            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                            keep[i] = exp2_approx(m[n][i] - top);
+                            m[n][i] = top;
+                            l[n][i] *= keep[i];
+                            keep[i] *= grow;
+                        }
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            o[n][i][0] *= keep[0], o[n][i][1] *= keep[1];
+                            o[n][i][2] *= keep[0], o[n][i][3] *= keep[1];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[n][e] = fmaf(sc[n][0][e], f[n][e & 1], -m[n][e & 1]);
                     }
                 }
                 // A page's value scale relative to the largest so far, times 2^15:
-                // the weight is a binary16 of at most 2^15, normal down to 2^-29 of
-                // the largest possible.
-                const float f = ref == 0.0f && in.vs == 0.0f ? 0.0f : in.vs / ref * kPScale;
-                const float base[2] = {m[0] == kNegInf ? 0.0f : m[0], m[1] == kNegInf ? 0.0f : m[1]};
-                uint32_t pf[4];
+                // the weight is a binary16 under 2^16, normal down to 2^-29 of the
+                // largest possible.
+                const float fv = in.vs == 0.0f ? 0.0f : __fdividef(in.vs, ref) * kPScale;
+                uint32_t pf[NQ][2];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < NQ; ++n) {
                     float p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float x = sc[n][e];
-                        const float w = exp2_approx(x - base[e >> 1]);
-                        l[e >> 1] += w;
-                        p[e] = x == kNegInf ? 0.0f : w * f;   // where f is NaN, only a seen token's
+                        w[n][e] = exp2_approx(w[n][e]);
+                        p[e] = w[n][e] * fv;
                     }
-                    pf[2 * n] = pack2<__half>(p[0], p[1]);
-                    pf[2 * n + 1] = pack2<__half>(p[2], p[3]);
+                    if (fv != fv) {   // likewise
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[e] = sc[n][0][e] == kNegInf ? 0.0f : fv;
+                    }
+                    l[n][0] += w[n][0] + w[n][2];
+                    l[n][1] += w[n][1] + w[n][3];
+                    pf[n][0] = transpose8(pack2<__half>(p[0], p[1]));
+                    pf[n][1] = transpose8(pack2<__half>(p[2], p[3]));
                 }
 #pragma unroll
                 for (int e = 0; e < D / 32; ++e) {
                     const uint32_t a01 = __byte_perm(vw[0][e], vw[1][e], 0x5140), a23 = __byte_perm(vw[0][e], vw[1][e], 0x7362);
                     const uint32_t b01 = __byte_perm(vw[2][e], vw[3][e], 0x5140), b23 = __byte_perm(vw[2][e], vw[3][e], 0x7362);
-                    mma_16816<__half>(o[4 * e], pf[0], pf[1], pf[2], pf[3], codes01(a01), codes01(b01));
-                    mma_16816<__half>(o[4 * e + 1], pf[0], pf[1], pf[2], pf[3], codes23(a01), codes23(b01));
-                    mma_16816<__half>(o[4 * e + 2], pf[0], pf[1], pf[2], pf[3], codes01(a23), codes01(b23));
-                    mma_16816<__half>(o[4 * e + 3], pf[0], pf[1], pf[2], pf[3], codes23(a23), codes23(b23));
+                    const uint32_t f0[4] = {codes01(a01), codes23(a01), codes01(b01), codes23(b01)};
+                    const uint32_t f1[4] = {codes01(a23), codes23(a23), codes01(b23), codes23(b23)};
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        mma_16816<__half>(o[n][2 * e], f0[0], f0[1], f0[2], f0[3], pf[n][0], pf[n][1]);
+                        mma_16816<__half>(o[n][2 * e + 1], f1[0], f1[1], f1[2], f1[3], pf[n][0], pf[n][1]);
+                    }
                 }
             }
             __syncwarp();
@@ -421,17 +470,20 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         // Join the warps: each has a maximum, a sum and unnormalised outputs.
         const float unit = ref / kPScale;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-            if (t == 0) s_m[warp * kRows + g + 8 * i] = m[i], s_l[warp * kRows + g + 8 * i] = l[i];
-            float* row = s_o + (warp * kRows + g + 8 * i) * R::kLd;
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                row[2 * t * NT + n] = o[n][2 * i] * unit;
-                row[(2 * t + 1) * NT + n] = o[n][2 * i + 1] * unit;
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * n + 2 * t + i;
+                l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 4);
+                l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 8);
+                l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 16);
+                if (g == 0) s_m[warp * kRows + r] = m[n][i], s_l[warp * kRows + r] = l[n][i];
+                float4* row = reinterpret_cast<float4*>(s_o + (warp * kRows + r) * kLd + g * (D / 8));
+#pragma unroll
+                for (int e = 0; e < MT / 2; ++e)
+                    row[e] = make_float4(o[n][2 * e][i] * unit, o[n][2 * e][2 + i] * unit, o[n][2 * e + 1][i] * unit,
+                                         o[n][2 * e + 1][2 + i] * unit);
             }
-        }
         __syncthreads();
     }
 
@@ -445,19 +497,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         float top = s_m[r];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w * kRows + r]);
-        const float from = top == kNegInf ? 0.0f : top;
         float sum = 0.0f, acc = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2_approx(s_m[w * kRows + r] - from);
+            const float f = exp2_approx(s_m[w * kRows + r] - top);
             sum = fmaf(f, s_l[w * kRows + r], sum);
-            acc = fmaf(f, s_o[(w * kRows + r) * R::kLd + d], acc);
+            acc = fmaf(f, s_o[(w * kRows + r) * kLd + d], acc);
         }
         if (whole) {
             T* dst = out_row<T>(a, tile, h, tile.r0 + r) + d;
             if (GEMM_DBG_OK(dst, a.O.p, o_bytes, sizeof(T))) *dst = from_float<T>(sum == 0.0f ? 0.0f : acc / sum);
         } else if (cluster) {
-            s_o[r * R::kLd + d] = acc;   // warp 0's place: read by this thread alone so far
+            s_o[r * kLd + d] = acc;   // warp 0's place: read by this thread alone so far
             if (d == 0) {
                 float* ml = s_l + kWarps * kRows + 2 * r;
                 ml[0] = top, ml[1] = sum;
@@ -473,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
     const int share = (rows * D + a.splits - 1) / a.splits;
     for (int i = split * share + threadIdx.x; i < min(rows * D, (split + 1) * share); i += kThreads) {
         const int r = i / D, d = i % D;
-        const uint32_t ml = smem_u32(s_l + kWarps * kRows + 2 * r), at = smem_u32(s_o + r * R::kLd + d);
-        float tops[kMaxCluster], sums[kMaxCluster], accs[kMaxCluster], top = kNegInf;
+        const uint32_t ml = smem_u32(s_l + kWarps * kRows + 2 * r), at = smem_u32(s_o + r * kLd + d);
+        float tops[kMaxCluster], sums[kMaxCluster], accs[kMaxCluster], top = kLowest;
 #pragma unroll
         for (int s = 0; s < kMaxCluster; ++s) {
             if (s >= tile.active) break;
@@ -483,12 +534,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
             accs[s] = ld_cluster_f32(mapa_shared(at, s));
             top = fmaxf(top, tops[s]);
         }
-        const float from = top == kNegInf ? 0.0f : top;
         float sum = 0.0f, acc = 0.0f;
 #pragma unroll
         for (int s = 0; s < kMaxCluster; ++s) {
             if (s >= tile.active) break;
-            const float f = exp2_approx(tops[s] - from);
+            const float f = exp2_approx(tops[s] - top);
             sum = fmaf(f, sums[s], sum);
             acc = fmaf(f, accs[s], acc);
         }
@@ -500,26 +550,25 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
 
 // Joins the splits of one row of a tile, in order: four threads share an
 // output element's splits.
-template <typename T, int D>
+template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a) {
     __shared__ float s_acc[4][D], s_sum[4];
     const int64_t u = blockIdx.x;
     const int h = blockIdx.y, r = blockIdx.z, d = threadIdx.x % D, q = threadIdx.x / D;
     Tile tile;
-    if (!tile.find(a, u, false) || tile.active == 1 || tile.r0 + r >= tile.nrows) return;
+    if (!tile.find(a, u, kRows, kStep, false) || tile.active == 1 || tile.r0 + r >= tile.nrows) return;
     constexpr int64_t kSlot = kRows * (D + 2);
     const float* part = a.partial + (u * a.c.heads + h) * a.splits * kSlot;
     const float* ml = part + kRows * D + 2 * r;
-    float top = kNegInf;
+    float top = kLowest;
     for (int s = threadIdx.x % 32; s < tile.active; s += 32) top = fmaxf(top, ml[s * kSlot]);
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-    const float from = top == kNegInf ? 0.0f : top;
     const int share = (tile.active + 3) / 4, end = min(tile.active, (q + 1) * share);
     float sum = 0.0f, acc = 0.0f;
 #pragma unroll 4
     for (int s = q * share; s < end; ++s) {
-        const float f = exp2_approx(ml[s * kSlot] - from);
+        const float f = exp2_approx(ml[s * kSlot] - top);
         sum = fmaf(f, ml[s * kSlot + 1], sum);
         acc = fmaf(f, part[s * kSlot + r * D + d], acc);
     }
@@ -535,7 +584,7 @@ __global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a) {
     if (GEMM_DBG_OK(dst, a.O.p, o_bytes, sizeof(T))) *dst = from_float<T>(sum == 0.0f ? 0.0f : acc / sum);
 }
 
-template <typename T, int D>
+template <typename T, int D, int NQ>
 cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(plan.units * plan.splits), (unsigned)a.c.heads);
@@ -548,10 +597,10 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStr
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<T, D>, a);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<T, D, NQ>, a);
     *launches = 1;
     if (e == cudaSuccess && a.partial) {
-        kv_join_kernel<T, D><<<dim3((unsigned)plan.units, (unsigned)a.c.heads, kRows), 4 * D, 0, stream>>>(a);
+        kv_join_kernel<T, D, 8 * NQ><<<dim3((unsigned)plan.units, (unsigned)a.c.heads, 8 * NQ), 4 * D, 0, stream>>>(a);
         e = cudaGetLastError();
         *launches = 2;
     }
@@ -559,8 +608,17 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStr
 }
 
 template <typename T, int D>
+cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStream_t stream) {
+    return plan.rows == 8 ? launch<T, D, 1>(a, plan, launches, stream) : launch<T, D, 2>(a, plan, launches, stream);
+}
+
+template <typename T, int D>
 cudaError_t allow_smem() {
-    return cudaFuncSetAttribute(kv_attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes);
+    const cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<T, D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Ring<D>::kBytes);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(kv_attention_kernel<T, D, 2>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes);
 }
 
 }  // namespace
@@ -581,8 +639,10 @@ cudaError_t kv_attention_setup() {
 // sequences differ in length.  Fewer tiles over long sequences are shared over
 // one round of CTAs and joined by a second kernel.
 KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, int num_sms) {
-    const int64_t share = q_heads / c.heads, tiles = b.rows * share / kRows;
     KvPlan p;
+    const int64_t share = q_heads / c.heads;
+    p.rows = b.rows * share <= 8 * (int64_t)b.sequences ? 8 : 16;   // eight hold the rows of a sequence, or not
+    const int64_t tiles = b.rows * share / p.rows;
     p.units = tiles + b.sequences;
     int64_t longest = b.width << c.page_log2;
     if (window > 0 && window + 2 * kStep < longest) longest = window + 2 * kStep;
@@ -593,7 +653,7 @@ KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, i
     if (splits > most) splits = most;
     if (cluster && splits > kMaxCluster) splits = kMaxCluster;
     p.splits = (int)(splits < 1 ? 1 : splits);
-    p.scratch_bytes = p.splits > kMaxCluster ? p.units * c.heads * p.splits * (kRows * (c.dim + 2) * 4) : 0;
+    p.scratch_bytes = p.splits > kMaxCluster ? p.units * c.heads * p.splits * (p.rows * (c.dim + 2) * 4) : 0;
     return p;
 }
 
@@ -603,7 +663,7 @@ cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& 
                                 unsigned* err, int* launches, cudaStream_t stream) {
     const bool q_vec = (reinterpret_cast<uintptr_t>(Q.p) & 15u) == 0 && Q.row % 8 == 0 && Q.head % 8 == 0;
     const AttnArgs a{c, Q, O, b, q_heads, q_heads / c.heads, scale * 1.44269504088896341f, causal,
-                     window, plan.splits, q_vec, static_cast<float*>(scratch), err};
+                     (int)(window < INT32_MAX ? window : INT32_MAX), plan.splits, q_vec, static_cast<float*>(scratch), err};
     if (type == ElemType::kBF16)
         return c.dim == 128 ? launch<__nv_bfloat16, 128>(a, plan, launches, stream)
                             : launch<__nv_bfloat16, 64>(a, plan, launches, stream);

@@ -273,13 +273,16 @@ def test_nothing_beyond_the_mask_is_used(libgemm, new):
     again = lowbit.kv_attention(Q, pool.gpu, ints(pool.table), starts, ints(lengths))
     assert torch.equal(O, again)
     # tokens 96 .. 99 of sequence 0: only its last four queries see them
-    pool.gpu.v_scales[int(pool.table[0, 6])] = float("nan")
-    again = lowbit.kv_attention(Q, pool.gpu, ints(pool.table), starts, ints(lengths))
-    nan = torch.isnan(again).flatten(1)
-    hit = torch.zeros(2 * new, dtype=torch.bool, device="cuda")
-    hit[max(0, new - 4):new] = True
-    assert torch.equal(nan.all(1), hit) and torch.equal(nan.any(1), hit)
-    assert torch.equal(again[~hit], O[~hit])
+    for scales in (pool.gpu.v_scales, pool.gpu.k_scales):
+        kept = scales.clone()
+        scales[int(pool.table[0, 6])] = float("nan")
+        again = lowbit.kv_attention(Q, pool.gpu, ints(pool.table), starts, ints(lengths))
+        nan = torch.isnan(again).flatten(1)
+        hit = torch.zeros(2 * new, dtype=torch.bool, device="cuda")
+        hit[max(0, new - 4):new] = True
+        assert torch.equal(nan.all(1), hit) and torch.equal(nan.any(1), hit)
+        assert torch.equal(again[~hit], O[~hit])
+        scales.copy_(kept)
 
 
 @gpu
