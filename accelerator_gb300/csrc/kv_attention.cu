@@ -16,9 +16,9 @@ namespace {
 
 constexpr int kWarps = 4;        // warps that compute; one more copies
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kSub = 16;         // tokens a warp takes at once
-constexpr int kStep = kWarps * kSub;   // tokens of a stage
-constexpr int kMinSteps = 2;     // stages of a split, at least
+constexpr int kSub = 16;         // tokens of one product, all of one page
+constexpr int kSubs = 2;         // a warp takes this many times 16 tokens at once
+constexpr int kStep = kWarps * kSubs * kSub;   // tokens of a stage
 constexpr int kRingBytes = 96 * 1024;  // two CTAs of an SM keep 192 KB in flight
 constexpr int kMaxCluster = 8;
 constexpr float kNegInf = -INFINITY, kLowest = -3.402823466e38f;
@@ -37,7 +37,8 @@ struct AttnArgs {
     KvView c;
     KvRows Q, O;
     KvBatch b;
-    int q_heads, share;          // query heads, and how many read one cache head
+    int q_heads;
+    unsigned share;              // query heads that read one cache head; rows * share fits 31 bits
     float scale_log2;            // scale * log2(e)
     int causal;
     int window;
@@ -51,46 +52,46 @@ struct AttnArgs {
 // (token numbers fit 32 bits, as the lengths do).
 struct Tile {
     int seq;
-    int64_t row0;                // first of the sequence's rows
-    int64_t r0, nrows;           // first row (query, head pair) of the tile; rows of the sequence
+    int row0;                    // first of the sequence's rows
+    int r0, nrows;               // first row (query, head pair) of the tile; rows of the sequence
     int len, p0;                 // cached tokens; position of query 0
-    int tok0;                    // first token, a multiple of kStep
+    int tok0;                    // first token, a multiple of the step
     int hi;                      // end of the tokens any row sees
     int steps, per, active;      // steps in all, per split, splits that have any
 
     // Row r sees the tokens row_lo(r) .. row_hi(r) - 1; both grow with r.
-    __device__ __forceinline__ int row_hi(const AttnArgs& a, int64_t r) const {
-        const int p = p0 + (int)(r / a.share);
+    __device__ __forceinline__ int row_hi(const AttnArgs& a, int r) const {
+        const int p = p0 + (int)((unsigned)r / a.share);
         if (p < 0) return 0;
         return a.causal ? p + 1 : len;
     }
-    __device__ __forceinline__ int row_lo(const AttnArgs& a, int64_t r) const {
-        const int p = p0 + (int)(r / a.share);
+    __device__ __forceinline__ int row_lo(const AttnArgs& a, int r) const {
+        const int p = p0 + (int)((unsigned)r / a.share);
         return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
     }
-    __device__ __forceinline__ bool find(const AttnArgs& a, int64_t u, int rows, int step, bool report) {
+    __device__ __forceinline__ bool find(const AttnArgs& a, int u, int rows, int step, bool report) {
         const Starts starts{a.b.starts, a.b.sequences, a.b.rows};
         // Sequence q's tiles are units floor(starts[q] * share / rows) + q + j.
-        seq = last_not_above(a.b.sequences, u, [&](int i) { return starts.at(i) * a.share / rows + i; });
-        row0 = starts.at(seq);
-        const int64_t count = starts.at(seq + 1) - row0, length = __ldg(a.b.at + seq);
+        seq = last_not_above(a.b.sequences, u, [&](int i) { return (unsigned)starts.at(i) * a.share / rows + i; });
+        row0 = (int)starts.at(seq);
+        const int count = (int)starts.at(seq + 1) - row0, length = __ldg(a.b.at + seq);
         if (!starts.whole(u == 0, seq)) {
             if (report) atomicOr(a.err, kErrIndex);
             return false;
         }
-        nrows = count * a.share;
-        r0 = (u - row0 * a.share / rows - seq) * rows;
+        nrows = count * (int)a.share;
+        r0 = (u - (int)((unsigned)row0 * a.share / rows) - seq) * rows;
         if (r0 < 0 || r0 >= nrows) return false;
-        len = (int)length;
+        len = length;
         if (length < 0 || length > (a.b.width << a.c.page_log2)) {
             if (report) atomicOr(a.err, kErrIndex);
             len = 0;
         }
-        p0 = len - (int)count;
-        hi = row_hi(a, (r0 + rows < nrows ? r0 + rows : nrows) - 1);
+        p0 = len - count;
+        hi = row_hi(a, min(r0 + rows, nrows) - 1);
         tok0 = row_lo(a, r0) / step * step;
         steps = hi > tok0 ? (hi - tok0 + step - 1) / step : 0;
-        per = max(kMinSteps, (steps + a.splits - 1) / a.splits);
+        per = max(1, (steps + a.splits - 1) / a.splits);
         active = max(1, (steps + per - 1) / per);
         return true;
     }
@@ -98,8 +99,8 @@ struct Tile {
 
 // Where a row's results go.
 template <typename T>
-__device__ __forceinline__ T* out_row(const AttnArgs& a, const Tile& tile, int h, int64_t r) {
-    return static_cast<T*>(a.O.p) + (tile.row0 + r / a.share) * a.O.row + (h * a.share + r % a.share) * a.O.head;
+__device__ __forceinline__ T* out_row(const AttnArgs& a, const Tile& tile, int h, unsigned r) {
+    return static_cast<T*>(a.O.p) + (int64_t)(tile.row0 + r / a.share) * a.O.row + (int64_t)(h * a.share + r % a.share) * a.O.head;
 }
 
 // Untiled bulk copy into this CTA's shared memory, completing on `bar`.
@@ -134,10 +135,10 @@ struct SubInfo {
 template <int D>
 struct Ring {
     static constexpr int kStageBytes = 2 * kStep * D;
-    static constexpr int kStages = kRingBytes / kStageBytes;   // 6 for 128, 12 for 64
-    // [stages][keys, values][64][D], then SubInfo[stages][4], then the barriers
+    static constexpr int kStages = kRingBytes / kStageBytes;   // 3 for 128, 6 for 64
+    // [stages][keys, values][128][D], then SubInfo[stages][8], then the barriers
     static constexpr int kInfoAt = kStages * kStageBytes;
-    static constexpr int kBarsAt = kInfoAt + kStages * kWarps * (int)sizeof(SubInfo);
+    static constexpr int kBarsAt = kInfoAt + kStages * kWarps * kSubs * (int)sizeof(SubInfo);
     static constexpr int kAbortAt = kBarsAt + 16 * kStages;
     static constexpr int kBytes = kAbortAt + 16;
 };
@@ -151,8 +152,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 // Few query rows: a tile of 8 * NQ rows over a share of its tokens.  One warp
-// copies whole pages' parts into a ring of stages of 64 tokens (their codes
-// lie in one piece for a page and head), four take 16 tokens of each stage.
+// copies whole pages' parts into a ring of stages of 128 tokens (their codes
+// lie in one piece for a page and head), four take 32 tokens of each stage.
 // Both products have the tokens' side, of which there is much, as the 16-row
 // operand and the queries as its eight columns: S^T = K Q^T, then O^T = V^T
 // P^T, for which the weights are turned over in registers; a product of 16
@@ -168,8 +169,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
     SubInfo* info = reinterpret_cast<SubInfo*>(smem + R::kInfoAt);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + R::kAbortAt);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const int64_t u = blockIdx.x / a.splits;
-    const int h = blockIdx.y, split = blockIdx.x % a.splits;
+    const int u = blockIdx.x / a.splits, split = blockIdx.x % a.splits, h = blockIdx.y;
     const bool cluster = a.splits > 1 && !a.partial;
     Tile tile;
     // A cluster's CTAs have one tile: they leave here together or not at all.
@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
     float* s_m = s_o + kWarps * kRows * kLd;                      // [warps][rows]
     float* s_l = s_m + kWarps * kRows;
     if (warp == kWarps) {
-        // ---- copies: lane i looks up 16 tokens, for 32 of them at a time ----
+        // ---- copies: lane i looks up 16 tokens, those of four stages at a time ----
+        static_assert(kWarps * kSubs == 8, "");
         const int32_t* table = a.b.table + tile.seq * a.b.width;
         const int log2 = a.c.page_log2, chunk = min(kStep, 1 << log2);   // tokens of one copy
         [[maybe_unused]] const int64_t code_bytes = a.c.pages * a.c.heads * ((int64_t)D << log2);
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         uint32_t phase = 0;
         int stage = 0, issued = 0;
         for (int s = 0; s < steps; ++s) {
-            if (s % 8 == 0) {
+            if (s % 4 == 0) {
                 const int tok = tok_begin + s * kStep + lane * kSub;
                 bool live = tok < tile.hi;
                 const int64_t page = live ? __ldg(table + (tok >> log2)) : 0;
@@ -217,12 +218,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
             int ok = 1;
             if (lane == 0) ok = mbar_wait(bars + 8 * (R::kStages + stage), phase ^ 1u, abort_flag, a.err, kWaitLimitNs);
             if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
-            const int sub = lane - s % 8 * kWarps;   // this lane's part of the stage, if it has one
-            const bool here = sub >= 0 && sub < kWarps;
+            const int sub = lane - s % 4 * 8;   // this lane's part of the stage, if it has one
+            const bool here = sub >= 0 && sub < 8;
             // the first 16 tokens of a page's part fetch all of it
             bool copies = here && mine.live && sub * kSub % chunk == 0;
             if (copies) copies = GEMM_DBG_OK(a.c.k + from, a.c.k, code_bytes, chunk * D) && GEMM_DBG_OK(a.c.v + from, a.c.v, code_bytes, chunk * D);
-            if (here) info[stage * kWarps + sub] = mine;
+            if (here) info[stage * 8 + sub] = mine;
             const int parts = __popc(__ballot_sync(0xFFFFFFFFu, copies));
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, (uint32_t)(parts * 2 * chunk * D));
@@ -263,10 +264,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
             ((a.b.rows - 1) * a.Q.row + (a.q_heads - 1) * a.Q.head + D) * (int64_t)sizeof(T);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            const int64_t r = tile.r0 + 8 * n + g;
-            const bool live = r < tile.nrows;
-            const T* p = static_cast<const T*>(a.Q.p) + (tile.row0 + (live ? r / a.share : 0)) * a.Q.row +
-                         (h * a.share + (live ? r % a.share : 0)) * a.Q.head;
+            const unsigned r = tile.r0 + 8 * n + g;
+            const bool live = r < (unsigned)tile.nrows;
+            const T* p = static_cast<const T*>(a.Q.p) + (int64_t)(tile.row0 + (live ? r / a.share : 0)) * a.Q.row +
+                         (int64_t)(h * a.share + (live ? r % a.share : 0)) * a.Q.head;
             Eight<T> x[D / 64][2] = {};
 #pragma unroll
             for (int j = 0; j < D / 64; ++j)
@@ -305,13 +306,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
             for (int i = 0; i < 2; ++i) {
                 row_scale[n][i] = fabsf(a.scale_log2) * __shfl_sync(0xFFFFFFFFu, up, 4 * (2 * t + i));
                 // rows past the last one see all: they are not stored
-                const int64_t rr = tile.r0 + 8 * n + 2 * t + i;
+                const int rr = tile.r0 + 8 * n + 2 * t + i;
                 row_lo[n][i] = rr < tile.nrows ? tile.row_lo(a, rr) : 0;
                 row_hi[n][i] = rr < tile.nrows ? tile.row_hi(a, rr) : tile.hi;
             }
         }
         // tokens that every row of the tile sees
-        const int full_lo = tile.row_lo(a, (tile.r0 + kRows < tile.nrows ? tile.r0 + kRows : tile.nrows) - 1);
+        const int full_lo = tile.row_lo(a, min(tile.r0 + kRows, tile.nrows) - 1);
         const int full_hi = tile.row_hi(a, tile.r0);
 
         constexpr int MT = D / 16;      // row tiles of O^T: row g of tile i is d = g * D / 8 + 2i, row g + 8 the next
@@ -328,79 +329,77 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         int stage = 0;
         for (int s = 0; s < steps; ++s) {
             if (!mbar_wait(bars + 8 * stage, phase, abort_flag, a.err, kWaitLimitNs)) break;
-            const SubInfo in = info[stage * kWarps + warp];
-            const uint32_t kat = ring + stage * R::kStageBytes + warp * kSub * D, vat = kat + kStep * D;
-            if (in.live) {
-                const int tok = tok_begin + s * kStep + warp * kSub;
-                // scores of tokens g and g + 8 for the rows 2t, 2t + 1
-                float sc[NQ][2][4] = {};
+            const SubInfo* in = info + (stage * kWarps + warp) * kSubs;
+            const uint32_t kat = ring + stage * R::kStageBytes + warp * (kSubs * kSub * D), vat = kat + kStep * D;
+            const int tok = tok_begin + s * kStep + warp * (kSubs * kSub);
+            if (tok < tile.hi) {
+                // scores of tokens 16b + g and 16b + g + 8 for the rows 2t, 2t + 1
+                float sc[kSubs][NQ][4], f[kSubs][NQ][2];
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j) {
-                    const uint4 w0 = lds128(kat + g * D + 64 * j + 16 * t), w1 = lds128(kat + (g + 8) * D + 64 * j + 16 * t);
-                    const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
+                for (int b = 0; b < kSubs; ++b) {
+                    float part[NQ][2][4] = {};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t a0 = codes01(lo[k]), a1 = codes01(hi[k]), a2 = codes23(lo[k]), a3 = codes23(hi[k]);
+                    for (int j = 0; j < D / 64; ++j) {
+                        const uint32_t at = kat + (16 * b + g) * D + 64 * j + 16 * t;
+                        const uint4 w0 = lds128(at), w1 = lds128(at + 8 * D);
+                        const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t a0 = codes01(lo[k]), a1 = codes01(hi[k]), a2 = codes23(lo[k]), a3 = codes23(hi[k]);
+#pragma unroll
+                            for (int n = 0; n < NQ; ++n)
+                                mma_16816<__half>(part[n][k & 1], a0, a1, a2, a3, qf[n][4 * j + k][0], qf[n][4 * j + k][1]);
+                        }
+                    }
+                    const float ks = in[b].ks;
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[b][n][e] = part[n][0][e] + part[n][1][e];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            // a page of zeros has scale 0: above 0, so that a hidden token's -inf stays that
+                            f[b][n][i] = row_scale[n][i] * ks;
+                            if (f[b][n][i] < 1.1754943508222875e-38f) f[b][n][i] = 1.1754943508222875e-38f;
+                        }
+                    }
+                    // Tokens that some row does not see, pages that do not exist.
+                    const bool live = in[b].live != 0;
+                    if (tok + 16 * b < full_lo || tok + 16 * b + kSub > full_hi || !live) {
 #pragma unroll
                         for (int n = 0; n < NQ; ++n)
-                            mma_16816<__half>(sc[n][k & 1], a0, a1, a2, a3, qf[n][4 * j + k][0], qf[n][4 * j + k][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int j = tok + 16 * b + g + 8 * (e >> 1);
+                                if (j < row_lo[n][e & 1] || j >= row_hi[n][e & 1] || !live) sc[b][n][e] = kNegInf;
+                            }
+                        asm volatile("");   // a branch: few tokens come here
+                    }
+                    if (ks != ks) {   // a page that reads as NaN: for the rows that see it alone
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sc[b][n][e] = sc[b][n][e] == kNegInf ? kNegInf : ks;
+                            f[b][n][0] = f[b][n][1] = 1.0f;
+                        }
                     }
                 }
-                uint32_t vw[4][D / 32];
+                const float vs[2] = {in[0].vs, in[1].vs};
+                float w[kSubs][NQ][4];
+                bool above = fmaxf(vs[0], vs[1]) > ref;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t at = vat + (8 * (i >> 1) + 2 * t + (i & 1)) * D + g * (D / 8);
-                    if constexpr (D == 128) {
-                        const uint4 w = lds128(at);
-                        vw[i][0] = w.x, vw[i][1] = w.y, vw[i][2] = w.z, vw[i][3] = w.w;
-                    } else {
-                        const uint2 w = lds64(at);
-                        vw[i][0] = w.x, vw[i][1] = w.y;
-                    }
-                }
-                float f[NQ][2];
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[n][0][e] += sc[n][1][e];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        // a page of zeros has scale 0: above 0, so that a hidden token's -inf stays that
-                        f[n][i] = row_scale[n][i] * in.ks;
-                        if (f[n][i] < 1.1754943508222875e-38f) f[n][i] = 1.1754943508222875e-38f;
-                    }
-                }
-                if (tok < full_lo || tok + kSub > full_hi) {
+                for (int b = 0; b < kSubs; ++b)
 #pragma unroll
                     for (int n = 0; n < NQ; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int j = tok + g + 8 * (e >> 1);
-                            if (j < row_lo[n][e & 1] || j >= row_hi[n][e & 1]) sc[n][0][e] = kNegInf;
+                            w[b][n][e] = fmaf(sc[b][n][e], f[b][n][e & 1], -m[n][e & 1]);
+                            above |= w[b][n][e] > kLag;
                         }
-                    asm volatile("");   // a branch: few tokens come here
-                }
-                if (in.ks != in.ks) {   // a page that reads as NaN: for the rows that see it alone
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[n][0][e] = sc[n][0][e] == kNegInf ? kNegInf : in.ks;
-                        f[n][0] = f[n][1] = 1.0f;
-                    }
-                }
-                float w[NQ][4];
-                bool above = in.vs > ref;
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        w[n][e] = fmaf(sc[n][0][e], f[n][e & 1], -m[n][e & 1]);
-                        above |= w[n][e] > kLag;
-                    }
                 // The sums so far are brought to a new maximum, or a new largest
                 // value scale, only when one is passed.
                 if (__any_sync(0xFFFFFFFFu, above)) {
-                    const float nref = fmaxf(ref, in.vs);
+                    const float nref = fmaxf(ref, fmaxf(vs[0], vs[1]));
                     const float grow = ref == nref ? 1.0f : __fdividef(ref, nref);   // ref = 0 at first: o is still 0
                     ref = nref;
 #pragma unroll
@@ -408,10 +407,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                         float keep[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float top = fmaxf(fmaxf(sc[n][0][i], sc[n][0][2 + i]) * f[n][i], m[n][i]);
+                            float top = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]) * f[0][n][i],
+                                              fmaxf(sc[1][n][i], sc[1][n][2 + i]) * f[1][n][i]);
                             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
                             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-                            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                            top = fmaxf(fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16)), m[n][i]);
                             keep[i] = exp2_approx(m[n][i] - top);
                             m[n][i] = top;
                             l[n][i] *= keep[i];
@@ -423,41 +423,59 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                             o[n][i][2] *= keep[0], o[n][i][3] *= keep[1];
                         }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) w[n][e] = fmaf(sc[n][0][e], f[n][e & 1], -m[n][e & 1]);
+                        for (int b = 0; b < kSubs; ++b)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[b][n][e] = fmaf(sc[b][n][e], f[b][n][e & 1], -m[n][e & 1]);
                     }
                 }
-                // A page's value scale relative to the largest so far, times 2^15:
-                // the weight is a binary16 under 2^16, normal down to 2^-29 of the
-                // largest possible.
-                const float fv = in.vs == 0.0f ? 0.0f : __fdividef(in.vs, ref) * kPScale;
-                uint32_t pf[NQ][2];
+                const float inv_ref = ref == 0.0f ? 0.0f : __fdividef(kPScale, ref);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    float p[4];
+                for (int b = 0; b < kSubs; ++b) {
+                    uint32_t vw[4][D / 32];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        w[n][e] = exp2_approx(w[n][e]);
-                        p[e] = w[n][e] * fv;
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t at = vat + (16 * b + 8 * (i >> 1) + 2 * t + (i & 1)) * D + g * (D / 8);
+                        if constexpr (D == 128) {
+                            const uint4 x = lds128(at);
+                            vw[i][0] = x.x, vw[i][1] = x.y, vw[i][2] = x.z, vw[i][3] = x.w;
+                        } else {
+                            const uint2 x = lds64(at);
+                            vw[i][0] = x.x, vw[i][1] = x.y;
+                        }
                     }
-                    if (fv != fv) {   // likewise
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) p[e] = sc[n][0][e] == kNegInf ? 0.0f : fv;
-                    }
-                    l[n][0] += w[n][0] + w[n][2];
-                    l[n][1] += w[n][1] + w[n][3];
-                    pf[n][0] = transpose8(pack2<__half>(p[0], p[1]));
-                    pf[n][1] = transpose8(pack2<__half>(p[2], p[3]));
-                }
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) {
-                    const uint32_t a01 = __byte_perm(vw[0][e], vw[1][e], 0x5140), a23 = __byte_perm(vw[0][e], vw[1][e], 0x7362);
-                    const uint32_t b01 = __byte_perm(vw[2][e], vw[3][e], 0x5140), b23 = __byte_perm(vw[2][e], vw[3][e], 0x7362);
-                    const uint32_t f0[4] = {codes01(a01), codes23(a01), codes01(b01), codes23(b01)};
-                    const uint32_t f1[4] = {codes01(a23), codes23(a23), codes01(b23), codes23(b23)};
+                    // A page's value scale relative to the largest so far, times 2^15:
+                    // the weight is a binary16 under 2^16, normal down to 2^-29 of the
+                    // largest possible.
+                    const float fv = vs[b] * inv_ref;
+                    uint32_t pf[NQ][2];
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        mma_16816<__half>(o[n][2 * e], f0[0], f0[1], f0[2], f0[3], pf[n][0], pf[n][1]);
-                        mma_16816<__half>(o[n][2 * e + 1], f1[0], f1[1], f1[2], f1[3], pf[n][0], pf[n][1]);
+                        float p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            w[b][n][e] = exp2_approx(w[b][n][e]);
+                            p[e] = w[b][n][e] * fv;
+                        }
+                        if (fv != fv) {   // a page that reads as NaN, likewise
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) p[e] = sc[b][n][e] == kNegInf ? 0.0f : fv;
+                        }
+                        l[n][0] += w[b][n][0] + w[b][n][2];
+                        l[n][1] += w[b][n][1] + w[b][n][3];
+                        pf[n][0] = transpose8(pack2<__half>(p[0], p[1]));
+                        pf[n][1] = transpose8(pack2<__half>(p[2], p[3]));
+                    }
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) {
+                        const uint32_t a01 = __byte_perm(vw[0][e], vw[1][e], 0x5140), a23 = __byte_perm(vw[0][e], vw[1][e], 0x7362);
+                        const uint32_t b01 = __byte_perm(vw[2][e], vw[3][e], 0x5140), b23 = __byte_perm(vw[2][e], vw[3][e], 0x7362);
+                        const uint32_t f0[4] = {codes01(a01), codes23(a01), codes01(b01), codes23(b01)};
+                        const uint32_t f1[4] = {codes01(a23), codes23(a23), codes01(b23), codes23(b23)};
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            mma_16816<__half>(o[n][2 * e], f0[0], f0[1], f0[2], f0[3], pf[n][0], pf[n][1]);
+                            mma_16816<__half>(o[n][2 * e + 1], f1[0], f1[1], f1[2], f1[3], pf[n][0], pf[n][1]);
+                        }
                     }
                 }
             }
@@ -489,9 +507,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
 
     [[maybe_unused]] const int64_t o_bytes =
         ((a.b.rows - 1) * a.O.row + (a.q_heads - 1) * a.O.head + D) * (int64_t)sizeof(T);
-    const int rows = (int)(tile.nrows - tile.r0 < kRows ? tile.nrows - tile.r0 : kRows);
+    const int rows = min(tile.nrows - tile.r0, kRows);
     const bool whole = a.splits == 1 || (!cluster && tile.active == 1);
-    float* part = a.partial ? a.partial + ((u * a.c.heads + h) * a.splits + split) * (kRows * (D + 2)) : nullptr;
+    float* part = a.partial ? a.partial + (((int64_t)u * a.c.heads + h) * a.splits + split) * (kRows * (D + 2)) : nullptr;
     for (int i = threadIdx.x; i < rows * D; i += kThreads) {
         const int r = i / D, d = i % D;
         float top = s_m[r];
@@ -553,12 +571,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
 template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a) {
     __shared__ float s_acc[4][D], s_sum[4];
-    const int64_t u = blockIdx.x;
-    const int h = blockIdx.y, r = blockIdx.z, d = threadIdx.x % D, q = threadIdx.x / D;
+    const int u = blockIdx.x, h = blockIdx.y, r = blockIdx.z, d = threadIdx.x % D, q = threadIdx.x / D;
     Tile tile;
     if (!tile.find(a, u, kRows, kStep, false) || tile.active == 1 || tile.r0 + r >= tile.nrows) return;
     constexpr int64_t kSlot = kRows * (D + 2);
-    const float* part = a.partial + (u * a.c.heads + h) * a.splits * kSlot;
+    const float* part = a.partial + ((int64_t)u * a.c.heads + h) * a.splits * kSlot;
     const float* ml = part + kRows * D + 2 * r;
     float top = kLowest;
     for (int s = threadIdx.x % 32; s < tile.active; s += 32) top = fmaxf(top, ml[s * kSlot]);
@@ -647,7 +664,7 @@ KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, i
     int64_t longest = b.width << c.page_log2;
     if (window > 0 && window + 2 * kStep < longest) longest = window + 2 * kStep;
     const int64_t have = (tiles > b.sequences ? tiles : b.sequences) * c.heads, slots = 2 * (int64_t)num_sms;
-    const int64_t most = (longest + kStep * kMinSteps - 1) / (kStep * kMinSteps);
+    const int64_t most = (longest + kStep - 1) / kStep;
     const bool cluster = most <= 8 * kMaxCluster || have * kMaxCluster >= slots;
     int64_t splits = cluster ? (4 * slots + have - 1) / have : slots / have;
     if (splits > most) splits = most;
@@ -662,7 +679,7 @@ cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& 
                                 const KvBatch& b, const KvPlan& plan, void* scratch,
                                 unsigned* err, int* launches, cudaStream_t stream) {
     const bool q_vec = (reinterpret_cast<uintptr_t>(Q.p) & 15u) == 0 && Q.row % 8 == 0 && Q.head % 8 == 0;
-    const AttnArgs a{c, Q, O, b, q_heads, q_heads / c.heads, scale * 1.44269504088896341f, causal,
+    const AttnArgs a{c, Q, O, b, q_heads, (unsigned)(q_heads / c.heads), scale * 1.44269504088896341f, causal,
                      (int)(window < INT32_MAX ? window : INT32_MAX), plan.splits, q_vec, static_cast<float*>(scratch), err};
     if (type == ElemType::kBF16)
         return c.dim == 128 ? launch<__nv_bfloat16, 128>(a, plan, launches, stream)
