@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();   // also: every thread has read the old scale
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) m = max(m, s_top[i]);
-    const float s = fmaxf(before, __fdiv_rn(__uint_as_float(m), 127.0f));
+    const float s = fmaxf(before, __fmul_rn(__uint_as_float(m), 1.0f / 127.0f));
     const bool bad = m >= 0x7F800000u || before != before;
     const float inv = bad || s < kTiny ? 0.0f : __fdiv_rn(1.0f, s);
     if (tid == 0) *sp = bad ? __uint_as_float(0x7FC00000u) : s;

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kQThreads)
         const int c = tid % kQCols, part = tid / kQCols, per = w.group / 32;
         uint32_t m = 0;
         for (int i = 0; i < 2 * per; ++i) m = max(m, top[part / per * per * 2 + i][c]);
-        const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(m), 7.0f));
+        const __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(__uint_as_float(m), 1.0f / 7.0f));
         float s = __bfloat162float(sb);
         uint16_t bits = __bfloat16_as_ushort(sb);
         if (m >= 0x7F800000u) s = 0.0f, bits = 0x7FC0;   // NaN; the codes are 0

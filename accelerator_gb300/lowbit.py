@@ -99,7 +99,7 @@ def w4_sizes(K: int, N: int, group: int):
 
 def w4_quantize(B, group=128, stream=None) -> W4Matrix:
     """B (K x N; float32, bfloat16 or float16, dense rows) in 4 bits: for each
-    column and `group` rows s = max|b| / 7 in bfloat16 and q = round(b / s)."""
+    column and `group` rows s = max|b| * (1 / 7) in bfloat16 and q = round(b / s)."""
     ldb = _rows2(B, "B")
     _need(B.dtype in _TYPES, "B", "float32, bfloat16 or float16")
     K, N = B.shape

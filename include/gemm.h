@@ -291,8 +291,8 @@ GEMM_API int gemm_w4_sizes(int64_t K, int64_t N, int group, int64_t* code_bytes,
 
 /*
  * B (K x N, row stride ldb >= N elements, of `type`) to codes and scales:
- * s = max|b| / 7 over the group's rows of the column, rounded to bfloat16,
- * q = b / s rounded to the nearest integer (ties to even) and held to
+ * s = max|b| * (1 / 7) over the group's rows of the column (one binary32
+ * product with the binary32 1 / 7), rounded to bfloat16, q = b / s rounded to the nearest integer (ties to even) and held to
  * [-7, 7].  A group whose s is under 2^-126 becomes zeros; one that holds a
  * NaN or an infinity gets s = NaN, so that every product with it is NaN.
  * codes: 16-byte aligned; scales: 4-byte aligned.
@@ -354,7 +354,7 @@ typedef struct gemm_kv_cache {
  * sequence b.  K and V: rows of heads x head_dim elements of `type`, element
  * (row, h, d) at row * row_stride + h * head_stride + d (strides in
  * elements, >= 0).  For each page, head and operand that gets new tokens,
- *     s' = max(s, max|x| / 127)   (s = 0 if token 0 of the page is new)
+ *     s' = max(s, max|x| * (1 / 127))   (s = 0 if token 0 of the page is new)
  * over its new elements x; new codes are x * (1 / s') rounded to the nearest
  * integer (ties to even) and held to [-127, 127]; if s' > s the page's older
  * codes c (its tokens before the first new one) become c * (s * (1 / s'))

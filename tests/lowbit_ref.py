@@ -35,7 +35,7 @@ def w4_quantize(B, group):
         top = np.abs(part).max(0)
         bad = ~np.isfinite(part).all(0)
         with np.errstate(all="ignore"):
-            sg = bf16_round((np.where(bad, 0, top) / np.float32(7)).astype(np.float32))
+            sg = bf16_round((np.where(bad, 0, top) * (np.float32(1) / np.float32(7))).astype(np.float32))
             sg = np.where(sg < TINY, np.float32(0), sg)
             qg = np.clip(np.rint((part / sg).astype(np.float32)), -7, 7)
         q[g * group:(g + 1) * group] = np.where((sg == 0) | bad, 0, np.nan_to_num(qg)).astype(np.int8)
@@ -92,7 +92,7 @@ class Cache:
                         self.c[p, h, begin:end] = 0
                         self.s[p, h] = np.nan
                         continue
-                    s = max(before, f32(np.abs(v).max()) / f32(127))
+                    s = max(before, f32(np.abs(v).max()) * (f32(1) / f32(127)))
                     inv = f32(1) / s if s >= TINY else f32(0)
                     self.c[p, h, begin:end] = np.clip(np.rint(v * inv), -127, 127).astype(np.int64)
                     if before < s:
