@@ -564,7 +564,8 @@ int gemm_debug_status(struct CUstream_st* stream_) {
     // debug build: the bounds-check flags of every kernel (read and cleared)
     const unsigned bounds =
         ffma_debug_flags() | ffma_small_debug_flags() | tc_debug_flags() | prep_debug_flags() |
-        w4_debug_flags() | kv_cache_debug_flags() | kv_attention_debug_flags();
+        w4_debug_flags() | kv_cache_debug_flags() | kv_attention_debug_flags() |
+        kv_prompt_debug_flags();
     if (word == 0) return bounds ? GEMM_ERR_BOUNDS : GEMM_OK;
     const unsigned zero = 0;
     if (cudaMemcpy(st->err, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)

@@ -189,6 +189,7 @@ enum class ElemType { kF32 = 0, kBF16 = 1, kF16 = 2 };   // as enum gemm_type
 unsigned w4_debug_flags();
 unsigned kv_cache_debug_flags();
 unsigned kv_attention_debug_flags();
+unsigned kv_prompt_debug_flags();
 // Work units of a launch are counted in the grid's x; the callers keep
 // (K / 128) * (N / 64) and 8 * (N / 32) * (M / 8) within it.
 cudaError_t launch_w4_quantize(const void* B, int64_t ldb, ElemType type, int64_t K, int64_t N,
@@ -229,6 +230,7 @@ struct KvPlan {
     int rows;             // query rows of a tile
     int64_t units;        // upper bound of the row tiles of the batch
     int splits;
+    bool cluster;         // the splits of a tile are a cluster
     int64_t scratch_bytes;
 };
 cudaError_t kv_attention_setup();

@@ -6,10 +6,7 @@
 // onto the score and its value scale onto p_j, and the codes themselves enter
 // both products exactly, as binary16 integers.  The query heads that share a
 // cache head, and the queries of a sequence, are the rows of one tile.
-#include <type_traits>
-
-#include "kernels.h"
-#include "lowbit.cuh"
+#include "kv_attention.cuh"
 
 namespace libgemm {
 namespace {
@@ -21,88 +18,6 @@ constexpr int kSubs = 2;         // a warp takes this many times 16 tokens at on
 constexpr int kStep = kWarps * kSubs * kSub;   // tokens of a stage
 constexpr int kRingBytes = 96 * 1024;  // two CTAs of an SM keep 192 KB in flight
 constexpr int kMaxCluster = 8;
-constexpr float kNegInf = -INFINITY, kLowest = -3.402823466e38f;
-// Weights enter the second product as binary16 times 2^15, under 2^16: the
-// maximum that they are relative to may lag behind by this much (in log2).
-constexpr float kPScale = 32768.0f, kLag = 0.9f;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-struct AttnArgs {
-    KvView c;
-    KvRows Q, O;
-    KvBatch b;
-    int q_heads;
-    unsigned share;              // query heads that read one cache head; rows * share fits 31 bits
-    float scale_log2;            // scale * log2(e)
-    int causal;
-    int window;
-    int splits;                  // CTAs that share a tile's tokens: a cluster, or with `partial` any number
-    bool q_vec;                  // Q in 16-byte loads
-    float* partial;              // [unit][head][split] x (rows x dim sums, then rows x (max, sum))
-    unsigned* err;
-};
-
-// The tile of a unit: its sequence and rows, and the tokens that it sees
-// (token numbers fit 32 bits, as the lengths do).
-struct Tile {
-    int seq;
-    int row0;                    // first of the sequence's rows
-    int r0, nrows;               // first row (query, head pair) of the tile; rows of the sequence
-    int len, p0;                 // cached tokens; position of query 0
-    int tok0;                    // first token, a multiple of the step
-    int hi;                      // end of the tokens any row sees
-    int steps, per, active;      // steps in all, per split, splits that have any
-
-    // Row r sees the tokens row_lo(r) .. row_hi(r) - 1; both grow with r.
-    __device__ __forceinline__ int row_hi(const AttnArgs& a, int r) const {
-        const int p = p0 + (int)((unsigned)r / a.share);
-        if (p < 0) return 0;
-        return a.causal ? p + 1 : len;
-    }
-    __device__ __forceinline__ int row_lo(const AttnArgs& a, int r) const {
-        const int p = p0 + (int)((unsigned)r / a.share);
-        return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
-    }
-    __device__ __forceinline__ bool find(const AttnArgs& a, int u, int rows, int step, bool report) {
-        const Starts starts{a.b.starts, a.b.sequences, a.b.rows};
-        // Sequence q's tiles are units floor(starts[q] * share / rows) + q + j.
-        seq = last_not_above(a.b.sequences, u, [&](int i) { return (unsigned)starts.at(i) * a.share / rows + i; });
-        row0 = (int)starts.at(seq);
-        const int count = (int)starts.at(seq + 1) - row0, length = __ldg(a.b.at + seq);
-        if (!starts.whole(u == 0, seq)) {
-            if (report) atomicOr(a.err, kErrIndex);
-            return false;
-        }
-        nrows = count * (int)a.share;
-        r0 = (u - (int)((unsigned)row0 * a.share / rows) - seq) * rows;
-        if (r0 < 0 || r0 >= nrows) return false;
-        len = length;
-        if (length < 0 || length > (a.b.width << a.c.page_log2)) {
-            if (report) atomicOr(a.err, kErrIndex);
-            len = 0;
-        }
-        p0 = len - count;
-        hi = row_hi(a, min(r0 + rows, nrows) - 1);
-        tok0 = row_lo(a, r0) / step * step;
-        steps = hi > tok0 ? (hi - tok0 + step - 1) / step : 0;
-        per = max(1, (steps + a.splits - 1) / a.splits);
-        active = max(1, (steps + per - 1) / per);
-        return true;
-    }
-};
-
-// Where a row's results go.
-template <typename T>
-__device__ __forceinline__ T* out_row(const AttnArgs& a, const Tile& tile, int h, unsigned r) {
-    return static_cast<T*>(a.O.p) + (int64_t)(tile.row0 + r / a.share) * a.O.row + (int64_t)(h * a.share + r % a.share) * a.O.head;
-}
-
 // Untiled bulk copy into this CTA's shared memory, completing on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -328,7 +243,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         uint32_t phase = 0;
         int stage = 0;
         for (int s = 0; s < steps; ++s) {
-            if (!mbar_wait(bars + 8 * stage, phase, abort_flag, a.err, kWaitLimitNs)) break;
+            // the warp goes on or gives up together
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars + 8 * stage, phase, abort_flag, a.err, kWaitLimitNs))) break;
             const SubInfo* in = info + (stage * kWarps + warp) * kSubs;
             const uint32_t kat = ring + stage * R::kStageBytes + warp * (kSubs * kSub * D), vat = kat + kStep * D;
             const int tok = tok_begin + s * kStep + warp * (kSubs * kSub);
@@ -568,26 +484,26 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
 
 // Joins the splits of one row of a tile, in order: four threads share an
 // output element's splits.
-template <typename T, int D, int kRows>
-__global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a) {
+template <typename T, int D>
+__global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a, int rows, int step) {
     __shared__ float s_acc[4][D], s_sum[4];
     const int u = blockIdx.x, h = blockIdx.y, r = blockIdx.z, d = threadIdx.x % D, q = threadIdx.x / D;
     Tile tile;
-    if (!tile.find(a, u, kRows, kStep, false) || tile.active == 1 || tile.r0 + r >= tile.nrows) return;
-    constexpr int64_t kSlot = kRows * (D + 2);
-    const float* part = a.partial + ((int64_t)u * a.c.heads + h) * a.splits * kSlot;
-    const float* ml = part + kRows * D + 2 * r;
+    if (!tile.find(a, u, rows, step, false) || tile.active == 1 || tile.r0 + r >= tile.nrows) return;
+    const int64_t slot = (int64_t)rows * (D + 2);
+    const float* part = a.partial + ((int64_t)u * a.c.heads + h) * a.splits * slot;
+    const float* ml = part + rows * D + 2 * r;
     float top = kLowest;
-    for (int s = threadIdx.x % 32; s < tile.active; s += 32) top = fmaxf(top, ml[s * kSlot]);
+    for (int s = threadIdx.x % 32; s < tile.active; s += 32) top = fmaxf(top, ml[s * slot]);
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
     const int share = (tile.active + 3) / 4, end = min(tile.active, (q + 1) * share);
     float sum = 0.0f, acc = 0.0f;
 #pragma unroll 4
     for (int s = q * share; s < end; ++s) {
-        const float f = exp2_approx(ml[s * kSlot] - top);
-        sum = fmaf(f, ml[s * kSlot + 1], sum);
-        acc = fmaf(f, part[s * kSlot + r * D + d], acc);
+        const float f = exp2_approx(ml[s * slot] - top);
+        sum = fmaf(f, ml[s * slot + 1], sum);
+        acc = fmaf(f, part[s * slot + r * D + d], acc);
     }
     s_acc[q][d] = acc;
     if (d == 0) s_sum[q] = sum;
@@ -602,7 +518,7 @@ __global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a) {
 }
 
 template <typename T, int D, int NQ>
-cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStream_t stream) {
+cudaError_t launch(const AttnArgs& a, const KvPlan& plan, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(plan.units * plan.splits), (unsigned)a.c.heads);
     cfg.blockDim = dim3(kThreads);
@@ -614,19 +530,23 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStr
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<T, D, NQ>, a);
-    *launches = 1;
-    if (e == cudaSuccess && a.partial) {
-        kv_join_kernel<T, D, 8 * NQ><<<dim3((unsigned)plan.units, (unsigned)a.c.heads, 8 * NQ), 4 * D, 0, stream>>>(a);
-        e = cudaGetLastError();
-        *launches = 2;
-    }
-    return e;
+    return cudaLaunchKernelEx(&cfg, kv_attention_kernel<T, D, NQ>, a);
 }
 
 template <typename T, int D>
 cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStream_t stream) {
-    return plan.rows == 8 ? launch<T, D, 1>(a, plan, launches, stream) : launch<T, D, 2>(a, plan, launches, stream);
+    const ElemType type = std::is_same<T, __half>::value ? ElemType::kF16 : ElemType::kBF16;
+    cudaError_t e = plan.rows == 8    ? launch<T, D, 1>(a, plan, stream)
+                    : plan.rows == 16 ? launch<T, D, 2>(a, plan, stream)
+                                      : launch_kv_prompt(a, type, plan, stream);
+    *launches = 1;
+    if (e == cudaSuccess && a.partial) {
+        static_assert(kStep == 128, "both kernels count tokens in the same steps");
+        kv_join_kernel<T, D><<<dim3((unsigned)plan.units, (unsigned)a.c.heads, (unsigned)plan.rows), 4 * D, 0, stream>>>(a, plan.rows, kStep);
+        e = cudaGetLastError();
+        *launches = 2;
+    }
+    return e;
 }
 
 template <typename T, int D>
@@ -647,30 +567,46 @@ cudaError_t kv_attention_setup() {
     if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, 128>();
     if (e == cudaSuccess) e = allow_smem<__half, 64>();
     if (e == cudaSuccess) e = allow_smem<__half, 128>();
-    return e;
+    return e == cudaSuccess ? kv_prompt_setup() : e;
 }
 
-// Tiles of rows that fill an eighth of the GPU's CTA slots or more, or whose
+// How many rows a tile has follows from the rows of a sequence and cache head,
+// on average: up to 8 and 16 the kernel for few rows, beyond kPromptRows the one
+// on the tensor memory (whose 128-row products are then more than half full).
+//
+// Few rows: tiles that fill an eighth of the GPU's CTA slots or more, or whose
 // tokens are few, have their tokens shared over a cluster (joined through
-// distributed shared memory, no second launch): four rounds of CTAs, as
+// distributed shared memory, no second launch), two rounds of CTAs in all, as
 // sequences differ in length.  Fewer tiles over long sequences are shared over
-// one round of CTAs and joined by a second kernel.
+// one round of CTAs and joined by a second kernel.  Many rows: the tokens are
+// shared, and joined likewise, only if the tiles leave half the GPU idle.
+constexpr int64_t kPromptRows = 64;
+
 KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, int num_sms) {
     KvPlan p;
-    const int64_t share = q_heads / c.heads;
-    p.rows = b.rows * share <= 8 * (int64_t)b.sequences ? 8 : 16;   // eight hold the rows of a sequence, or not
-    const int64_t tiles = b.rows * share / p.rows;
+    const int64_t share = q_heads / c.heads, all = b.rows * share;
+    p.rows = all <= 8 * (int64_t)b.sequences    ? 8
+             : all <= kPromptRows * b.sequences ? 16
+                                                : 256;
+    const int64_t tiles = all / p.rows;
     p.units = tiles + b.sequences;
     int64_t longest = b.width << c.page_log2;
-    if (window > 0 && window + 2 * kStep < longest) longest = window + 2 * kStep;
-    const int64_t have = (tiles > b.sequences ? tiles : b.sequences) * c.heads, slots = 2 * (int64_t)num_sms;
+    if (window > 0 && window + p.rows + 2 * kStep < longest) longest = window + p.rows + 2 * kStep;
+    const int64_t have = (tiles > b.sequences ? tiles : b.sequences) * c.heads, slots = (p.rows == 256 ? 1 : 2) * (int64_t)num_sms;
     const int64_t most = (longest + kStep - 1) / kStep;
-    const bool cluster = most <= 8 * kMaxCluster || have * kMaxCluster >= slots;
-    int64_t splits = cluster ? (4 * slots + have - 1) / have : slots / have;
-    if (splits > most) splits = most;
-    if (cluster && splits > kMaxCluster) splits = kMaxCluster;
+    int64_t splits;
+    if (p.rows == 256) {
+        splits = slots / have;
+        if (splits > most / 4) splits = most / 4;
+        p.cluster = false;
+    } else {
+        p.cluster = most <= 8 * kMaxCluster || have * kMaxCluster >= slots;
+        splits = p.cluster ? (2 * slots + have - 1) / have : slots / have;
+        if (splits > most) splits = most;
+        if (p.cluster && splits > kMaxCluster) splits = kMaxCluster;
+    }
     p.splits = (int)(splits < 1 ? 1 : splits);
-    p.scratch_bytes = p.splits > kMaxCluster ? p.units * c.heads * p.splits * (p.rows * (c.dim + 2) * 4) : 0;
+    p.scratch_bytes = p.splits > 1 && !p.cluster ? p.units * c.heads * p.splits * (p.rows * (c.dim + 2) * 4) : 0;
     return p;
 }
 

@@ -1,0 +1,500 @@
+// kv_prompt.cu -- attention of many query rows (prompts) over the paged 8-bit
+// cache, on the 5th-generation tensor cores.
+//
+// One CTA takes 256 query rows of a sequence and cache head -- two tiles of
+// 128, so that what is done to the keys and values of a block of 128 tokens
+// serves both -- and walks the tokens.  Its warps have fixed roles:
+//   warps 0-3, 4-7  softmax of tile 0 and tile 1, one thread a row: scores
+//       from tensor memory, weights back as binary16 over the scores, and the
+//       sums so far rescaled in tensor memory when a maximum is passed;
+//   warps 8-11  the cache: codes of a block from global memory into
+//       registers, as binary16 integers into shared memory (exact), in the
+//       128-byte swizzle that the matrix unit reads; the keys with d, the
+//       values with the token as the reduced dimension, from the same layout;
+//   warp 12  one thread issues tcgen05.mma: S_i = Q_i K^T (both from shared
+//       memory), O_i += P_i V (P from tensor memory).
+// The two tiles are half a step apart: while one tile's softmax runs, the
+// matrix unit works for the other.  Tensor memory holds S_0, S_1 (128 columns
+// each, P over the first half of its S) and O_0, O_1: all of its 512 columns.
+//
+// Bound by three things of nearly the same size per block and tile of 128 x
+// 128 x 128: the matrix unit (1024 cycles), the shared memory behind it (Q,
+// K, V operands and half of the conversion: about 1150), and 16384
+// exponentials with the dozen instructions around each four of them.
+//
+// Every wait is bounded; a role that gives up raises the abort flag, all stop,
+// and the matrix unit is drained before tensor memory is freed.
+#include "kv_attention.cuh"
+
+namespace libgemm {
+namespace {
+
+constexpr int kTile = 128, kRows = 2 * kTile, kStep = 128;   // rows of a tile and a CTA, tokens of a block
+constexpr int kSub = 16, kSubs = kStep / kSub;               // tokens that share a page for certain
+constexpr int kSlots = 4;                                    // blocks whose page data are kept
+constexpr int kSoftWarps = 8, kCacheWarps = 4, kThreads = (kSoftWarps + kCacheWarps + 1) * 32;
+constexpr int kSlab = kTile * 128;                           // 128 rows of 64 binary16
+
+// What a softmax thread needs of 16 tokens: the key scale, log2 and inverse
+// of the value scale relative to the tile's largest times 2^15.
+struct PageData {
+    float ks, log_v, inv_v;
+    uint32_t plain;      // 1: there, and reads as numbers; 0: reads as NaN; 2: not there
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kOperand = D / 64 * kSlab;          // 128 x D binary16
+    static constexpr int kQ = 0, kK = 2 * kOperand, kV = kK + 2 * kOperand;
+    static constexpr int kInfo = kV + 2 * kOperand;
+    static constexpr int kBars = kInfo + kSlots * kSubs * (int)sizeof(PageData);
+    static constexpr int kBytes = kBars + 256 + 1024;        // and the alignment
+};
+// Barriers: keys and values full / empty (two buffers), per tile scores full,
+// weights full, output done; the drain.
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kODone = 12, kDrain = 14, kNumBars = 15 };
+
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+        "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+        "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Chunk c (eight binary16) of row r of a 64-wide slab: 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// A whole warp waits, and goes on or gives up together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, err, kWaitLimitNs));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a, bool o_vec) {
+    using L = Smem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem, s_ref;
+    __shared__ int s_abort;
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    PageData* info = reinterpret_cast<PageData*>(smem + L::kInfo);
+    const uint32_t bars = base + L::kBars;
+    volatile int* abort_flag = &s_abort;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int u = blockIdx.x / a.splits, split = blockIdx.x % a.splits, h = blockIdx.y;
+    Tile tile;
+    if (!tile.find(a, u, kRows, kStep, threadIdx.x == 0 && h == 0 && split == 0) || split >= tile.active) return;
+    const int begin = split * tile.per, blocks = min(tile.steps, begin + tile.per) - begin;
+    const int tok_begin = tile.tok0 + begin * kStep;
+    const int tiles = tile.r0 + kTile < tile.nrows ? 2 : 1;
+    const int32_t* table = a.b.table + tile.seq * a.b.width;
+    const int log2 = a.c.page_log2;
+
+    if (threadIdx.x == 0) {
+        s_ref = 0;
+        s_abort = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bars + 8 * (kKFull + i), kCacheWarps * 32);
+            mbar_init(bars + 8 * (kVFull + i), kCacheWarps * 32);
+            mbar_init(bars + 8 * (kKEmpty + i), 1);
+            mbar_init(bars + 8 * (kVEmpty + i), 1);
+            mbar_init(bars + 8 * (kSFull + i), 2);   // the matrix unit, and its issuer for the page data
+            mbar_init(bars + 8 * (kPFull + i), kTile);
+            mbar_init(bars + 8 * (kODone + i), 1);
+        }
+        mbar_init(bars + 8 * kDrain, 1);
+        mbar_fence_init();
+    }
+    if (warp == kSoftWarps + kCacheWarps) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
+        tmem_relinquish();
+    }
+    // The softmax threads bring their row of Q to shared memory (as binary16;
+    // bfloat16 rows brought to [1, 2) by a power of two, exact but for elements
+    // under 2^-14 of the row's largest); all look for the largest value scale.
+    float row_scale = 0.0f;
+    const int in_tile = threadIdx.x % kTile, which = threadIdx.x / kTile;   // for softmax threads
+    const int my_row = tile.r0 + threadIdx.x;
+    if (warp < kSoftWarps) {
+        const bool live = my_row < tile.nrows;
+        [[maybe_unused]] const int64_t q_bytes =
+            ((a.b.rows - 1) * a.Q.row + (a.q_heads - 1) * a.Q.head + D) * (int64_t)sizeof(T);
+        const unsigned r = live ? my_row : 0;
+        const T* p = static_cast<const T*>(a.Q.p) + (int64_t)(tile.row0 + r / a.share) * a.Q.row + (int64_t)(h * a.share + r % a.share) * a.Q.head;
+        float up = 1.0f, down = 1.0f;
+        if constexpr (!std::is_same<T, __half>::value) {
+            float top = 0.0f;
+            for (int c = 0; c < D / 8; ++c) {
+                Eight<T> x = {};
+                if (live && GEMM_DBG_OK(p + 8 * c, a.Q.p, q_bytes, 16)) x = load_eight(p + 8 * c, a.q_vec);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x.at(e)));
+            }
+            const int e = (int)(__float_as_uint(top) >> 23);   // biased exponent
+            if (top > 0.0f && top < INFINITY) {
+                const int k = max(1, min(253, e));
+                up = __uint_as_float((uint32_t)k << 23);             // 2^(k - 127)
+                down = __uint_as_float((uint32_t)(254 - k) << 23);   // 2^(127 - k)
+            }
+        }
+        row_scale = fabsf(a.scale_log2) * up;
+        if (a.scale_log2 < 0.0f) down = -down;
+        const uint32_t q0 = base + L::kQ + which * L::kOperand;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+            Eight<T> x = {};
+            if (live && GEMM_DBG_OK(p + 8 * c, a.Q.p, q_bytes, 16)) x = load_eight(p + 8 * c, a.q_vec);
+            st_shared_v4(q0 + c / 8 * kSlab + swizzled(in_tile, c % 8), pack2<__half>(x.at(0) * down, x.at(1) * down),
+                         pack2<__half>(x.at(2) * down, x.at(3) * down), pack2<__half>(x.at(4) * down, x.at(5) * down),
+                         pack2<__half>(x.at(6) * down, x.at(7) * down));
+        }
+        fence_proxy_async_shared();
+    }
+    __syncthreads();   // s_ref is 0
+    {
+        uint32_t top = 0;   // magnitudes compare as their bits; NaN scales do not count
+        const int first = tok_begin >> log2, last = blocks > 0 ? (min(tile.hi, tok_begin + blocks * kStep) - 1) >> log2 : first - 1;
+        for (int i = first + threadIdx.x; i <= last; i += kThreads) {
+            const int64_t page = __ldg(table + i);
+            if (page < 0 || page >= a.c.pages) continue;
+            const float* p = a.c.vs + page * a.c.heads + h;
+            if (!GEMM_DBG_OK(p, a.c.vs, a.c.pages * a.c.heads * 4, 4)) continue;
+            const float v = __ldg(p);
+            if (v > 0.0f) top = max(top, __float_as_uint(v));
+        }
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if (lane == 0 && top) atomicMax(&s_ref, top);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const float ref = __uint_as_float(s_ref);
+
+    if (warp >= kSoftWarps && warp < kSoftWarps + kCacheWarps) {
+        // ---------------- the cache ----------------
+        constexpr int kLanes = D / 16;                  // lanes of a token, 16 codes each
+        constexpr int kPassRows = kCacheWarps * 32 / kLanes, kPasses = kStep / kPassRows;
+        const int ct = threadIdx.x - kSoftWarps * 32;
+        // A quarter of a warp holds halves of two neighbouring rows: its 16-byte
+        // stores then meet all eight chunk positions of the swizzle.
+        const int piece = D == 128 ? ct % 4 + 4 * (ct / 8 % 2) : ct % 4;
+        const int sub_row = D == 128 ? ct / 16 * 2 + ct / 4 % 2 : ct / 4;
+        [[maybe_unused]] const int64_t code_bytes = a.c.pages * a.c.heads * ((int64_t)D << log2);
+        const float to_v = ref > 0.0f ? __fdividef(kPScale, ref) : 0.0f;
+
+        // Lane i < 8 looks after 16 tokens of a block: their page's place, and its scales.
+        struct Sub { int64_t from; float ks, vs; bool live; };
+        auto look = [&](int j) {
+            Sub s{0, 0.0f, 0.0f, false};
+            const int tok = tok_begin + j * kStep + (lane % kSubs) * kSub;
+            if (j < blocks && tok < tile.hi) {
+                const int64_t page = __ldg(table + (tok >> log2));
+                s.live = page >= 0 && page < a.c.pages;
+                if (!s.live) atomicOr(a.err, kErrIndex);
+                else {
+                    const int64_t ph = page * a.c.heads + h;
+                    s.from = ((ph << log2) + (tok & ((1 << log2) - 1))) * D;
+                    s.ks = __ldg(a.c.ks + ph);
+                    s.vs = __ldg(a.c.vs + ph);
+                }
+            }
+            return s;
+        };
+        auto fetch = [&](const Sub& s, const uint8_t* codes, uint4 (&w)[kPasses]) {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int row = i * kPassRows + sub_row, sub = row / kSub;
+                const int64_t from = __shfl_sync(0xFFFFFFFFu, s.from, sub);
+                const bool live = __shfl_sync(0xFFFFFFFFu, s.live, sub);
+                const uint8_t* p = codes + from + (row % kSub) * D + 16 * piece;
+                w[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+                if (live && GEMM_DBG_OK(p, codes, code_bytes, 16)) w[i] = __ldg(reinterpret_cast<const uint4*>(p));
+            }
+        };
+        auto put = [&](uint32_t to, const uint4 (&w)[kPasses]) {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int row = i * kPassRows + sub_row, c = 2 * piece % 8;
+                const uint32_t at = to + 2 * piece / 8 * kSlab;
+                st_shared_v4(at + swizzled(row, c), codes01(w[i].x), codes23(w[i].x), codes01(w[i].y), codes23(w[i].y));
+                st_shared_v4(at + swizzled(row, c + 1), codes01(w[i].z), codes23(w[i].z), codes01(w[i].w), codes23(w[i].w));
+            }
+            fence_proxy_async_shared();
+        };
+        Sub now = look(0);
+        uint4 kw[kPasses], vw[kPasses];
+        fetch(now, a.c.k, kw);
+        for (int j = 0; j < blocks; ++j) {
+            const int buf = j & 1;
+            const uint32_t parity = (uint32_t)(j >> 1) & 1u;
+            fetch(now, a.c.v, vw);
+            const Sub next = look(j + 1);
+            if (!warp_wait(bars + 8 * (kKEmpty + buf), parity ^ 1u, abort_flag, a.err)) break;
+            // the page data of a block are read until its weights are done: before its values' buffer is free again
+            if (warp == kSoftWarps && lane < kSubs) {
+                const bool plain = now.live && now.ks == now.ks && now.vs == now.vs;
+                // A page of zeros adds nothing with any weight; one of 2^-60 of the
+                // largest scale or less is taken for that much.
+                const float v = plain && now.vs > 0.0f ? fmaxf(now.vs * to_v, 2.8421709e-14f) : kPScale;
+                info[j % kSlots * kSubs + lane] = PageData{now.ks, __log2f(v), __fdividef(1.0f, v), plain ? 1u : now.live ? 0u : 2u};
+            }
+            put(base + L::kK + buf * L::kOperand, kw);
+            mbar_arrive(bars + 8 * (kKFull + buf));
+            fetch(next, a.c.k, kw);
+            if (!warp_wait(bars + 8 * (kVEmpty + buf), parity ^ 1u, abort_flag, a.err)) break;
+            put(base + L::kV + buf * L::kOperand, vw);
+            mbar_arrive(bars + 8 * (kVFull + buf));
+            now = next;
+        }
+    } else if (warp == kSoftWarps + kCacheWarps) {
+        // ---------------- the matrix unit ----------------
+        if (lane == 0) {
+            constexpr uint32_t kIdS = make_idesc(0, kTile, kStep, false, false), kIdO = make_idesc(0, kTile, D, false, true);
+            auto scores = [&](int i, int buf) {   // S_i = Q_i K^T
+                const uint32_t q = base + L::kQ + i * L::kOperand, k = base + L::kK + buf * L::kOperand;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma<TcKind::kF16>(tmem + i * kStep, smem_desc_sw128(q + kk / 4 * kSlab + kk % 4 * 32, 16, 1024),
+                                         smem_desc_sw128(k + kk / 4 * kSlab + kk % 4 * 32, 16, 1024), kIdS, kk != 0);
+                tc_commit(bars + 8 * (kSFull + i));
+                mbar_arrive(bars + 8 * (kSFull + i));
+            };
+            bool ok = blocks > 0 && mbar_wait(bars + 8 * kKFull, 0, abort_flag, a.err, kWaitLimitNs);
+            if (ok) {
+                tc_fence_after();
+                for (int i = 0; i < tiles; ++i) scores(i, 0);
+                tc_commit(bars + 8 * kKEmpty);
+            }
+            for (int j = 0; ok && j < blocks; ++j) {
+                const int buf = j & 1;
+                ok = mbar_wait(bars + 8 * (kVFull + buf), (uint32_t)(j >> 1) & 1u, abort_flag, a.err, kWaitLimitNs);
+                for (int i = 0; ok && i < tiles; ++i) {
+                    if (!(ok = mbar_wait(bars + 8 * (kPFull + i), (uint32_t)j & 1u, abort_flag, a.err, kWaitLimitNs))) break;
+                    tc_fence_after();
+                    const uint32_t v = base + L::kV + buf * L::kOperand;
+#pragma unroll
+                    for (int kk = 0; kk < kStep / 16; ++kk)   // O_i += P_i V
+                        tc_mma_ts(tmem + 2 * kStep + i * kStep, tmem + i * kStep + kk * 8,
+                                  smem_desc_sw128(v + kk * 16 * 128, kSlab, 1024), kIdO, (j | kk) != 0);
+                    tc_commit(bars + 8 * (kODone + i));
+                    if (i == tiles - 1) tc_commit(bars + 8 * (kVEmpty + buf));
+                    if (j + 1 < blocks) {
+                        if (i == 0 && !(ok = mbar_wait(bars + 8 * (kKFull + (buf ^ 1)), (uint32_t)((j + 1) >> 1) & 1u, abort_flag, a.err, kWaitLimitNs))) break;
+                        tc_fence_after();
+                        scores(i, buf ^ 1);
+                        if (i == tiles - 1) tc_commit(bars + 8 * (kKEmpty + (buf ^ 1)));
+                    }
+                }
+            }
+            // Everything issued is done before tensor memory is freed.
+            tc_commit(bars + 8 * kDrain);
+            const uint64_t t0 = global_ns();
+            while (!mbar_try_wait(bars + 8 * kDrain, 0))
+                if (global_ns() - t0 > kWaitLimitNs) {
+                    atomicOr(a.err, kErrTimeout);
+                    break;
+                }
+        }
+        __syncwarp();
+    } else if (which < tiles) {
+        // ---------------- softmax: one row a thread ----------------
+        const uint32_t quarter = (uint32_t)(warp % 4 * 32) << 16;
+        const uint32_t s_at = tmem + which * kStep + quarter, o_at = tmem + 2 * kStep + which * kStep + quarter;
+        const int first = tile.r0 + which * kTile, last = min(first + kTile, tile.nrows) - 1;
+        const int full_lo = tile.row_lo(a, last), full_hi = tile.row_hi(a, first);
+        const bool live = my_row < tile.nrows;
+        const int lo = live ? tile.row_lo(a, my_row) : 0, hi = live ? tile.row_hi(a, my_row) : tile.hi;
+        float m = kLowest, l = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < blocks; ++j) {
+            if (!(ok = warp_wait(bars + 8 * (kSFull + which), (uint32_t)j & 1u, abort_flag, a.err))) break;
+            tc_fence_after();
+            const PageData* page = info + j % kSlots * kSubs;
+            const int tok = tok_begin + j * kStep;
+            bool plain = tok >= full_lo && tok + kStep <= full_hi;
+            {
+                uint32_t all = 1;
+#pragma unroll
+                for (int b = 0; b < kSubs; ++b) all &= page[b].plain;
+                plain = plain && (all & 1u);
+            }
+            // The scores of 32 tokens; hidden ones -inf, those of a page that
+            // reads as NaN NaN (their scale is NaN, so hidden ones need it not).
+            auto load = [&](int c, float (&x)[32], float (&f)[2]) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(s_at + 32 * c, v);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    f[b] = row_scale * page[2 * c + b].ks;
+                    if (f[b] < 1.1754943508222875e-38f) f[b] = 1.1754943508222875e-38f;   // -inf times it stays -inf
+                }
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
+                if (!plain) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const uint32_t kind = page[2 * c + b].plain;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int t = tok + 32 * c + 16 * b + e;
+                            if (t < lo || t >= hi || kind == 2u) x[16 * b + e] = kNegInf;
+                            else if (kind == 0u) x[16 * b + e] = __uint_as_float(0x7FC00000u);
+                        }
+                        if (kind != 1u) f[b] = 1.0f;
+                    }
+                }
+            };
+            float top = kLowest;
+#pragma unroll
+            for (int c = 0; c < kStep / 32; ++c) {
+                float x[32], f[2];
+                load(c, x, f);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float t = x[16 * b];
+#pragma unroll
+                    for (int e = 1; e < 16; ++e) t = fmaxf(t, x[16 * b + e]);
+                    top = fmaxf(top, t * f[b]);
+                }
+            }
+            // The sums so far are brought to a new maximum only when it is passed.
+            if (__any_sync(0xFFFFFFFFu, top > m + kLag)) {
+                const float nm = fmaxf(m, top), keep = exp2_approx(m - nm);
+                m = nm;
+                l *= keep;
+                if (j > 0) {
+                    if (!(ok = warp_wait(bars + 8 * (kODone + which), (uint32_t)(j - 1) & 1u, abort_flag, a.err))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(o_at + 32 * c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            uint32_t y[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(v[16 * b + e]) * keep);
+                            tmem_st_x16(o_at + 32 * c + 16 * b, y);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < kStep / 32; ++c) {
+                float x[32], f[2];
+                load(c, x, f);
+                uint32_t p[16];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float shift = page[2 * c + b].log_v - m;
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float w0 = exp2_approx(fmaf(x[16 * b + e], f[b], shift)), w1 = exp2_approx(fmaf(x[16 * b + e + 1], f[b], shift));
+                        sum += w0 + w1;
+                        p[8 * b + e / 2] = pack2<__half>(w0, w1);
+                    }
+                    l = fmaf(sum, page[2 * c + b].inv_v, l);
+                }
+                tmem_st_x16(s_at + 16 * c, p);   // over scores that have been read
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(bars + 8 * (kPFull + which));
+        }
+        if (ok && blocks > 0) ok = warp_wait(bars + 8 * (kODone + which), (uint32_t)(blocks - 1) & 1u, abort_flag, a.err);
+        tc_fence_after();
+        if (ok) {
+            [[maybe_unused]] const int64_t o_bytes =
+                ((a.b.rows - 1) * a.O.row + (a.q_heads - 1) * a.O.head + D) * (int64_t)sizeof(T);
+            const bool whole = tile.active == 1;
+            const float unit = blocks == 0 || l == 0.0f ? 0.0f : whole ? ref / kPScale / l : ref / kPScale;
+            T* dst = live ? out_row<T>(a, tile, h, my_row) : nullptr;
+            float* part = whole ? nullptr : a.partial + (((int64_t)u * a.c.heads + h) * a.splits + split) * ((int64_t)kRows * (D + 2));
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32] = {};
+                if (blocks > 0) tmem_ld_32x32b_x32(o_at + 32 * c, v);
+                tmem_ld_wait();
+                float y[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = unit == 0.0f ? 0.0f : __uint_as_float(v[e]) * unit;
+                if (!live) {
+                } else if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(part + (int64_t)threadIdx.x * D + 32 * c + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                } else if (o_vec) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        if (GEMM_DBG_OK(dst + 32 * c + e, a.O.p, o_bytes, 16))
+                            *reinterpret_cast<uint4*>(dst + 32 * c + e) =
+                                make_uint4(pack2<T>(y[e], y[e + 1]), pack2<T>(y[e + 2], y[e + 3]), pack2<T>(y[e + 4], y[e + 5]), pack2<T>(y[e + 6], y[e + 7]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (GEMM_DBG_OK(dst + 32 * c + e, a.O.p, o_bytes, sizeof(T))) dst[32 * c + e] = from_float<T>(y[e]);
+                }
+                __syncwarp();
+            }
+            if (live && !whole) {
+                part[(int64_t)kRows * D + 2 * threadIdx.x] = m;
+                part[(int64_t)kRows * D + 2 * threadIdx.x + 1] = l;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kSoftWarps + kCacheWarps) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch(const AttnArgs& a, const KvPlan& plan, cudaStream_t stream) {
+    const bool o_vec = (reinterpret_cast<uintptr_t>(a.O.p) & 15u) == 0 && a.O.row % 8 == 0 && a.O.head % 8 == 0;
+    kv_prompt_kernel<T, D><<<dim3((unsigned)(plan.units * plan.splits), (unsigned)a.c.heads), kThreads, Smem<D>::kBytes, stream>>>(a, o_vec);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t allow_smem() {
+    return cudaFuncSetAttribute(kv_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+}
+
+}  // namespace
+
+LIBGEMM_DEBUG_READER(kv_prompt_debug_flags)
+
+cudaError_t kv_prompt_setup() {
+    cudaError_t e = allow_smem<__nv_bfloat16, 64>();
+    if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, 128>();
+    if (e == cudaSuccess) e = allow_smem<__half, 64>();
+    if (e == cudaSuccess) e = allow_smem<__half, 128>();
+    return e;
+}
+
+cudaError_t launch_kv_prompt(const AttnArgs& a, ElemType type, const KvPlan& plan, cudaStream_t stream) {
+    if (type == ElemType::kBF16)
+        return a.c.dim == 128 ? launch<__nv_bfloat16, 128>(a, plan, stream) : launch<__nv_bfloat16, 64>(a, plan, stream);
+    return a.c.dim == 128 ? launch<__half, 128>(a, plan, stream) : launch<__half, 64>(a, plan, stream);
+}
+
+}  // namespace libgemm
