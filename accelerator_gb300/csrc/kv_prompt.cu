@@ -11,7 +11,7 @@
 //       registers, as binary16 integers into shared memory (exact), in the
 //       128-byte swizzle that the matrix unit reads; the keys with d, the
 //       values with the token as the reduced dimension, from the same layout;
-//   warp 12  one thread issues tcgen05.mma: S_i = Q_i K^T (both from shared
+//   warps 12-15  one thread issues tcgen05.mma: S_i = Q_i K^T (both from shared
 //       memory), O_i += P_i V (P from tensor memory).
 // The two tiles are half a step apart: while one tile's softmax runs, the
 // matrix unit works for the other.  Tensor memory holds S_0, S_1 (128 columns
@@ -32,7 +32,11 @@ namespace {
 constexpr int kTile = 128, kRows = 2 * kTile, kStep = 128;   // rows of a tile and a CTA, tokens of a block
 constexpr int kSub = 16, kSubs = kStep / kSub;               // tokens that share a page for certain
 constexpr int kSlots = 4;                                    // blocks whose page data are kept
-constexpr int kSoftWarps = 8, kCacheWarps = 4, kThreads = (kSoftWarps + kCacheWarps + 1) * 32;
+constexpr int kSoftWarps = 8, kCacheWarps = 4, kThreads = (kSoftWarps + kCacheWarps + 4) * 32;
+// Registers of a thread: launched with 128, then shared out among the roles
+// (whole warpgroups), whose sum is that of the launch.
+constexpr int kLaunchRegs = 128, kSoftRegs = 184, kCacheRegs = 104, kIssueRegs = 40;
+static_assert(kSoftRegs * kSoftWarps + kCacheRegs * kCacheWarps + kIssueRegs * 4 <= kLaunchRegs * kThreads / 32, "");
 constexpr int kSlab = kTile * 128;                           // 128 rows of 64 binary16
 
 // What a softmax thread needs of 16 tokens: the key scale, log2 and inverse
@@ -72,6 +76,19 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t (&r)[1
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld_x16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // Chunk c (eight binary16) of row r of a 64-wide slab: 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
@@ -185,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
 
     if (warp >= kSoftWarps && warp < kSoftWarps + kCacheWarps) {
         // ---------------- the cache ----------------
+        fewer_registers<kCacheRegs>();
         constexpr int kLanes = D / 16;                  // lanes of a token, 16 codes each
         constexpr int kPassRows = kCacheWarps * 32 / kLanes, kPasses = kStep / kPassRows;
         const int ct = threadIdx.x - kSoftWarps * 32;
@@ -259,9 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             mbar_arrive(bars + 8 * (kVFull + buf));
             now = next;
         }
-    } else if (warp == kSoftWarps + kCacheWarps) {
+    } else if (warp >= kSoftWarps + kCacheWarps) {
         // ---------------- the matrix unit ----------------
-        if (lane == 0) {
+        fewer_registers<kIssueRegs>();
+        if (threadIdx.x == (kSoftWarps + kCacheWarps) * 32) {
             constexpr uint32_t kIdS = make_idesc(0, kTile, kStep, false, false), kIdO = make_idesc(0, kTile, D, false, true);
             auto scores = [&](int i, int buf) {   // S_i = Q_i K^T
                 const uint32_t q = base + L::kQ + i * L::kOperand, k = base + L::kK + buf * L::kOperand;
@@ -309,7 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                 }
         }
         __syncwarp();
-    } else if (which < tiles) {
+    } else {
+        more_registers<kSoftRegs>();
+        if (which < tiles) {
         // ---------------- softmax: one row a thread ----------------
         const uint32_t quarter = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t s_at = tmem + which * kStep + quarter, o_at = tmem + 2 * kStep + which * kStep + quarter;
@@ -324,52 +345,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             tc_fence_after();
             const PageData* page = info + j % kSlots * kSubs;
             const int tok = tok_begin + j * kStep;
-            bool plain = tok >= full_lo && tok + kStep <= full_hi;
-            {
-                uint32_t all = 1;
+            uint32_t v[4][32];   // the row's scores, all in registers
 #pragma unroll
-                for (int b = 0; b < kSubs; ++b) all &= page[b].plain;
-                plain = plain && (all & 1u);
+            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_at + 32 * c, v[c]);
+            uint32_t plain = 1;
+#pragma unroll
+            for (int b = 0; b < kSubs; ++b) plain &= page[b].plain;
+            tmem_ld_wait();
+            if (tok < full_lo || tok + kStep > full_hi) {   // hidden tokens: -inf
+                const int first_seen = lo - tok, end_seen = hi - tok;
+#pragma unroll
+                for (int e = 0; e < kStep; ++e)
+                    if (e < first_seen || e >= end_seen) v[e / 32][e % 32] = 0xFF800000u;
+                asm volatile("");
             }
-            // The scores of 32 tokens; hidden ones -inf, those of a page that
-            // reads as NaN NaN (their scale is NaN, so hidden ones need it not).
-            auto load = [&](int c, float (&x)[32], float (&f)[2]) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(s_at + 32 * c, v);
+            if (!(plain & 1u)) {   // pages that are not there: hidden; that read as NaN: NaN, where seen
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    f[b] = row_scale * page[2 * c + b].ks;
-                    if (f[b] < 1.1754943508222875e-38f) f[b] = 1.1754943508222875e-38f;   // -inf times it stays -inf
-                }
-                tmem_ld_wait();
+                for (int b = 0; b < kSubs; ++b) {
+                    const uint32_t kind = page[b].plain;
+                    if (kind == 1u) continue;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
-                if (!plain) {
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const uint32_t kind = page[2 * c + b].plain;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int t = tok + 32 * c + 16 * b + e;
-                            if (t < lo || t >= hi || kind == 2u) x[16 * b + e] = kNegInf;
-                            else if (kind == 0u) x[16 * b + e] = __uint_as_float(0x7FC00000u);
-                        }
-                        if (kind != 1u) f[b] = 1.0f;
+                    for (int e = 0; e < kSub; ++e) {
+                        uint32_t& x = v[b / 2][b % 2 * 16 + e];
+                        if (kind == 2u) x = 0xFF800000u;
+                        else if (x != 0xFF800000u) x = 0x7FC00000u;
                     }
                 }
+                asm volatile("");
+            }
+            // Factors stay above 0, so that -inf times one stays that; a NaN
+            // scale's tokens are NaN or -inf already.
+            auto factor = [&](int b) {
+                const float f = row_scale * page[b].ks;
+                return f >= 1.1754943508222875e-38f ? f : 1.1754943508222875e-38f;
             };
             float top = kLowest;
 #pragma unroll
-            for (int c = 0; c < kStep / 32; ++c) {
-                float x[32], f[2];
-                load(c, x, f);
+            for (int b = 0; b < kSubs; ++b) {
+                const uint32_t* x = &v[b / 2][b % 2 * 16];
+                float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    float t = x[16 * b];
-#pragma unroll
-                    for (int e = 1; e < 16; ++e) t = fmaxf(t, x[16 * b + e]);
-                    top = fmaxf(top, t * f[b]);
-                }
+                for (int e = 2; e < kSub; e += 2) t0 = fmaxf(t0, __uint_as_float(x[e])), t1 = fmaxf(t1, __uint_as_float(x[e + 1]));
+                top = fmaxf(top, fmaxf(t0, t1) * factor(b));
             }
             // The sums so far are brought to a new maximum only when it is passed.
             if (__any_sync(0xFFFFFFFFu, top > m + kLag)) {
@@ -380,39 +397,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                     if (!(ok = warp_wait(bars + 8 * (kODone + which), (uint32_t)(j - 1) & 1u, abort_flag, a.err))) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(o_at + 32 * c, v);
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t y[16];
+                        tmem_ld_x16(o_at + 16 * c, y);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            uint32_t y[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(v[16 * b + e]) * keep);
-                            tmem_st_x16(o_at + 32 * c + 16 * b, y);
-                        }
+                        for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * keep);
+                        tmem_st_x16(o_at + 16 * c, y);
                     }
                 }
             }
+            float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < kStep / 32; ++c) {
-                float x[32], f[2];
-                load(c, x, f);
+            for (int c = 0; c < 4; ++c) {
                 uint32_t p[16];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const float shift = page[2 * c + b].log_v - m;
-                    float sum = 0.0f;
+                    const PageData& pd = page[2 * c + b];
+                    const float f = factor(2 * c + b), shift = pd.log_v - m;
+                    const float2 f2 = make_float2(f, f), shift2 = make_float2(shift, shift);
+                    float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
-                        const float w0 = exp2_approx(fmaf(x[16 * b + e], f[b], shift)), w1 = exp2_approx(fmaf(x[16 * b + e + 1], f[b], shift));
-                        sum += w0 + w1;
-                        p[8 * b + e / 2] = pack2<__half>(w0, w1);
+                        const uint32_t* x = &v[c][16 * b + e];
+                        float2 w = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f2, shift2);
+                        w = make_float2(exp2_approx(w.x), exp2_approx(w.y));
+                        s2 = __fadd2_rn(s2, w);
+                        p[8 * b + e / 2] = pack2<__half>(w.x, w.y);
                     }
-                    l = fmaf(sum, page[2 * c + b].inv_v, l);
+                    sum[b] = fmaf(s2.x + s2.y, pd.inv_v, sum[b]);
                 }
-                tmem_st_x16(s_at + 16 * c, p);   // over scores that have been read
+                tmem_st_x16(s_at + 16 * c, p);   // over scores that are in registers
             }
+            l += sum[0] + sum[1];
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(bars + 8 * (kPFull + which));
@@ -457,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                 part[(int64_t)kRows * D + 2 * threadIdx.x + 1] = l;
             }
         }
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -476,6 +494,11 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t allow_smem() {
+    // The roles' shares of the registers would wait for ever if the launch had fewer.
+    cudaFuncAttributes f;
+    const cudaError_t e = cudaFuncGetAttributes(&f, kv_prompt_kernel<T, D>);
+    if (e != cudaSuccess) return e;
+    if (f.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
     return cudaFuncSetAttribute(kv_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
 }
 
