@@ -18,17 +18,6 @@ constexpr int kSubs = 2;         // a warp takes this many times 16 tokens at on
 constexpr int kStep = kWarps * kSubs * kSub;   // tokens of a stage
 constexpr int kRingBytes = 96 * 1024;  // two CTAs of an SM keep 192 KB in flight
 constexpr int kMaxCluster = 8;
-// Untiled bulk copy into this CTA's shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
@@ -130,9 +119,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                 mine.vs = live ? __ldg(a.c.vs + ph) : 0.0f;
                 from = ((ph << log2) + (tok & ((1 << log2) - 1))) * D;
             }
-            int ok = 1;
-            if (lane == 0) ok = mbar_wait(bars + 8 * (R::kStages + stage), phase ^ 1u, abort_flag, a.err, kWaitLimitNs);
-            if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+            if (!warp_wait(bars + 8 * (R::kStages + stage), phase ^ 1u, abort_flag, a.err)) break;
             const int sub = lane - s % 4 * 8;   // this lane's part of the stage, if it has one
             const bool here = sub >= 0 && sub < 8;
             // the first 16 tokens of a page's part fetch all of it
@@ -243,8 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         uint32_t phase = 0;
         int stage = 0;
         for (int s = 0; s < steps; ++s) {
-            // the warp goes on or gives up together
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars + 8 * stage, phase, abort_flag, a.err, kWaitLimitNs))) break;
+            if (!warp_wait(bars + 8 * stage, phase, abort_flag, a.err)) break;
             const SubInfo* in = info + (stage * kWarps + warp) * kSubs;
             const uint32_t kat = ring + stage * R::kStageBytes + warp * (kSubs * kSub * D), vat = kat + kStep * D;
             const int tok = tok_begin + s * kStep + warp * (kSubs * kSub);
@@ -395,8 +381,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars + 8 * (R::kStages + stage));
+            warp_arrive(bars + 8 * (R::kStages + stage));
             if (++stage == R::kStages) stage = 0, phase ^= 1u;
         }
         __syncthreads();   // the ring is free: every copy has landed and been used

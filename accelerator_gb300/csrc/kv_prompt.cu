@@ -7,12 +7,13 @@
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1, one thread a row: scores
 //       from tensor memory, weights back as binary16 over the scores, and the
 //       sums so far rescaled in tensor memory when a maximum is passed;
-//   warps 8-11  the cache: codes of a block from global memory into
-//       registers, as binary16 integers into shared memory (exact), in the
-//       128-byte swizzle that the matrix unit reads; the keys with d, the
-//       values with the token as the reduced dimension, from the same layout;
-//   warps 12-15  one thread issues tcgen05.mma: S_i = Q_i K^T (both from shared
-//       memory), O_i += P_i V (P from tensor memory).
+//   warps 8-11  the cache: codes of a block from where the copies put them, as
+//       binary16 integers (exact) in the 128-byte swizzle that the matrix unit
+//       reads; the keys with d, the values with the token as the reduced
+//       dimension, from the same layout;
+//   warp 12  one thread issues tcgen05.mma: S_i = Q_i K^T (both from shared
+//       memory), O_i += P_i V (P from tensor memory);
+//   warp 13  looks the pages up and copies their codes in bulk.
 // The two tiles are half a step apart: while one tile's softmax runs, the
 // matrix unit works for the other.  Tensor memory holds S_0, S_1 (128 columns
 // each, P over the first half of its S) and O_0, O_1: all of its 512 columns.
@@ -50,13 +51,13 @@ template <int D>
 struct Smem {
     static constexpr int kOperand = D / 64 * kSlab;          // 128 x D binary16
     static constexpr int kQ = 0, kK = 2 * kOperand, kV = kK + 2 * kOperand;
-    static constexpr int kInfo = kV + 2 * kOperand;
+    static constexpr int kCodes = kV + 2 * kOperand, kInfo = kCodes + 2 * kStep * D;   // codes: keys, values
     static constexpr int kBars = kInfo + kSlots * kSubs * (int)sizeof(PageData);
     static constexpr int kBytes = kBars + 256 + 1024;        // and the alignment
 };
 // Barriers: keys and values full / empty (two buffers), per tile scores full,
-// weights full, output done; the drain.
-enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kODone = 12, kDrain = 14, kNumBars = 15 };
+// weights full, output done; codes full / empty (keys, values); the drain.
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kODone = 12, kCFull = 14, kCEmpty = 16, kDrain = 18 };
 
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -90,13 +91,14 @@ __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.
 template <int N>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Chunk c (eight binary16) of row r of a 64-wide slab: 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-
-// A whole warp waits, and goes on or gives up together.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, err, kWaitLimitNs));
-}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a, bool o_vec) {
@@ -123,13 +125,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
         s_ref = 0;
         s_abort = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + 8 * (kKFull + i), kCacheWarps * 32);
-            mbar_init(bars + 8 * (kVFull + i), kCacheWarps * 32);
+            mbar_init(bars + 8 * (kKFull + i), kCacheWarps);
+            mbar_init(bars + 8 * (kVFull + i), kCacheWarps);
             mbar_init(bars + 8 * (kKEmpty + i), 1);
             mbar_init(bars + 8 * (kVEmpty + i), 1);
             mbar_init(bars + 8 * (kSFull + i), 2);   // the matrix unit, and its issuer for the page data
-            mbar_init(bars + 8 * (kPFull + i), kTile);
+            mbar_init(bars + 8 * (kPFull + i), kTile / 32);
             mbar_init(bars + 8 * (kODone + i), 1);
+            mbar_init(bars + 8 * (kCFull + i), 1);
+            mbar_init(bars + 8 * (kCEmpty + i), kCacheWarps);
         }
         mbar_init(bars + 8 * kDrain, 1);
         mbar_fence_init();
@@ -210,72 +214,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
         // stores then meet all eight chunk positions of the swizzle.
         const int piece = D == 128 ? ct % 4 + 4 * (ct / 8 % 2) : ct % 4;
         const int sub_row = D == 128 ? ct / 16 * 2 + ct / 4 % 2 : ct / 4;
-        [[maybe_unused]] const int64_t code_bytes = a.c.pages * a.c.heads * ((int64_t)D << log2);
-        const float to_v = ref > 0.0f ? __fdividef(kPScale, ref) : 0.0f;
-
-        // Lane i < 8 looks after 16 tokens of a block: their page's place, and its scales.
-        struct Sub { int64_t from; float ks, vs; bool live; };
-        auto look = [&](int j) {
-            Sub s{0, 0.0f, 0.0f, false};
-            const int tok = tok_begin + j * kStep + (lane % kSubs) * kSub;
-            if (j < blocks && tok < tile.hi) {
-                const int64_t page = __ldg(table + (tok >> log2));
-                s.live = page >= 0 && page < a.c.pages;
-                if (!s.live) atomicOr(a.err, kErrIndex);
-                else {
-                    const int64_t ph = page * a.c.heads + h;
-                    s.from = ((ph << log2) + (tok & ((1 << log2) - 1))) * D;
-                    s.ks = __ldg(a.c.ks + ph);
-                    s.vs = __ldg(a.c.vs + ph);
-                }
-            }
-            return s;
+        uint4 w[kPasses];
+        auto get = [&](int values, uint32_t parity) {
+            if (!warp_wait(bars + 8 * (kCFull + values), parity, abort_flag, a.err)) return false;
+            const uint32_t from = base + L::kCodes + values * (kStep * D) + sub_row * D + 16 * piece;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) w[i] = lds128(from + i * kPassRows * D);
+            return true;
         };
-        auto fetch = [&](const Sub& s, const uint8_t* codes, uint4 (&w)[kPasses]) {
+        auto put = [&](uint32_t to) {
+            const int c = 2 * piece % 8;
+            const uint32_t at = to + 2 * piece / 8 * kSlab + sub_row * 128, r = sub_row & 7;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
-                const int row = i * kPassRows + sub_row, sub = row / kSub;
-                const int64_t from = __shfl_sync(0xFFFFFFFFu, s.from, sub);
-                const bool live = __shfl_sync(0xFFFFFFFFu, s.live, sub);
-                const uint8_t* p = codes + from + (row % kSub) * D + 16 * piece;
-                w[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-                if (live && GEMM_DBG_OK(p, codes, code_bytes, 16)) w[i] = __ldg(reinterpret_cast<const uint4*>(p));
-            }
-        };
-        auto put = [&](uint32_t to, const uint4 (&w)[kPasses]) {
-#pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                const int row = i * kPassRows + sub_row, c = 2 * piece % 8;
-                const uint32_t at = to + 2 * piece / 8 * kSlab;
-                st_shared_v4(at + swizzled(row, c), codes01(w[i].x), codes23(w[i].x), codes01(w[i].y), codes23(w[i].y));
-                st_shared_v4(at + swizzled(row, c + 1), codes01(w[i].z), codes23(w[i].z), codes01(w[i].w), codes23(w[i].w));
+                const uint32_t row = at + i * kPassRows * 128;
+                st_shared_v4(row + ((c ^ r) << 4), codes01(w[i].x), codes23(w[i].x), codes01(w[i].y), codes23(w[i].y));
+                st_shared_v4(row + (((c + 1) ^ r) << 4), codes01(w[i].z), codes23(w[i].z), codes01(w[i].w), codes23(w[i].w));
             }
             fence_proxy_async_shared();
         };
-        Sub now = look(0);
-        uint4 kw[kPasses], vw[kPasses];
-        fetch(now, a.c.k, kw);
         for (int j = 0; j < blocks; ++j) {
             const int buf = j & 1;
             const uint32_t parity = (uint32_t)(j >> 1) & 1u;
-            fetch(now, a.c.v, vw);
-            const Sub next = look(j + 1);
+            if (!get(0, (uint32_t)j & 1u)) break;
+            warp_arrive(bars + 8 * kCEmpty);
             if (!warp_wait(bars + 8 * (kKEmpty + buf), parity ^ 1u, abort_flag, a.err)) break;
-            // the page data of a block are read until its weights are done: before its values' buffer is free again
-            if (warp == kSoftWarps && lane < kSubs) {
-                const bool plain = now.live && now.ks == now.ks && now.vs == now.vs;
-                // A page of zeros adds nothing with any weight; one of 2^-60 of the
-                // largest scale or less is taken for that much.
-                const float v = plain && now.vs > 0.0f ? fmaxf(now.vs * to_v, 2.8421709e-14f) : kPScale;
-                info[j % kSlots * kSubs + lane] = PageData{now.ks, __log2f(v), __fdividef(1.0f, v), plain ? 1u : now.live ? 0u : 2u};
-            }
-            put(base + L::kK + buf * L::kOperand, kw);
-            mbar_arrive(bars + 8 * (kKFull + buf));
-            fetch(next, a.c.k, kw);
+            put(base + L::kK + buf * L::kOperand);
+            warp_arrive(bars + 8 * (kKFull + buf));
+            if (!get(1, (uint32_t)j & 1u)) break;
+            warp_arrive(bars + 8 * (kCEmpty + 1));
             if (!warp_wait(bars + 8 * (kVEmpty + buf), parity ^ 1u, abort_flag, a.err)) break;
-            put(base + L::kV + buf * L::kOperand, vw);
-            mbar_arrive(bars + 8 * (kVFull + buf));
-            now = next;
+            put(base + L::kV + buf * L::kOperand);
+            warp_arrive(bars + 8 * (kVFull + buf));
         }
     } else if (warp >= kSoftWarps + kCacheWarps) {
         // ---------------- the matrix unit ----------------
@@ -326,6 +296,69 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                     atomicOr(a.err, kErrTimeout);
                     break;
                 }
+        }
+        if (warp == kSoftWarps + kCacheWarps + 1) {
+            // ---------------- the copies: lane i < 8 looks after 16 tokens of a block ----------------
+            [[maybe_unused]] const int64_t code_bytes = a.c.pages * a.c.heads * ((int64_t)D << log2);
+            const float to_v = ref > 0.0f ? __fdividef(kPScale, ref) : 0.0f;
+            const int chunk = min(kStep, 1 << log2);   // tokens of one copy
+            struct Sub { int64_t from; float ks, vs; bool live; };
+            auto look = [&](int j) {
+                Sub s{0, 0.0f, 0.0f, false};
+                const int tok = tok_begin + j * kStep + lane * kSub;
+                if (lane < kSubs && j < blocks && tok < tile.hi) {
+                    const int64_t page = __ldg(table + (tok >> log2));
+                    s.live = page >= 0 && page < a.c.pages;
+                    if (!s.live) atomicOr(a.err, kErrIndex);
+                    else {
+                        const int64_t ph = page * a.c.heads + h;
+                        s.from = ((ph << log2) + (tok & ((1 << log2) - 1))) * D;
+                        s.ks = __ldg(a.c.ks + ph);
+                        s.vs = __ldg(a.c.vs + ph);
+                    }
+                }
+                return s;
+            };
+            Sub now = look(0);
+            int issued[2] = {0, 0};
+            for (int j = 0; j < blocks; ++j) {
+                const Sub next = look(j + 1);
+                // the first 16 tokens of a page's part fetch all of it
+                bool copies = now.live && lane * kSub % chunk == 0;
+                if (copies) copies = GEMM_DBG_OK(a.c.k + now.from, a.c.k, code_bytes, chunk * D) && GEMM_DBG_OK(a.c.v + now.from, a.c.v, code_bytes, chunk * D);
+                const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xFFFFFFFFu, copies)) * chunk * D);
+                bool ok = true;
+#pragma unroll
+                for (int values = 0; values < 2; ++values) {
+                    // Page data of block j go where those of block j - 4 were: its keys' turn
+                    // comes when the keys of j - 1 are taken, so the values of j - 4 are used up.
+                    if (!(ok = warp_wait(bars + 8 * (kCEmpty + values), ((uint32_t)j & 1u) ^ 1u, abort_flag, a.err))) break;
+                    if (values == 0 && lane < kSubs) {
+                        // A page of zeros adds nothing with any weight; one of 2^-60 of the
+                        // largest scale or less is taken for that much.
+                        const bool plain = now.live && now.ks == now.ks && now.vs == now.vs;
+                        const float v = plain && now.vs > 0.0f ? fmaxf(now.vs * to_v, 2.8421709e-14f) : kPScale;
+                        info[j % kSlots * kSubs + lane] = PageData{now.ks, __log2f(v), __fdividef(1.0f, v), plain ? 1u : now.live ? 0u : 2u};
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * (kCFull + values), bytes);
+                    __syncwarp();
+                    if (copies)
+                        bulk_load(base + L::kCodes + values * (kStep * D) + lane * kSub * D, (values ? a.c.v : a.c.k) + now.from, chunk * D, bars + 8 * (kCFull + values));
+                    issued[values] = j + 1;
+                }
+                if (!ok) break;
+                now = next;
+            }
+            // Copies in flight land before the CTA may leave.
+            if (lane < 2 && issued[lane] > 0) {
+                const uint64_t t0 = global_ns();
+                while (!mbar_try_wait(bars + 8 * (kCFull + lane), (uint32_t)(issued[lane] - 1) & 1u))
+                    if (global_ns() - t0 > kWaitLimitNs) {
+                        atomicOr(a.err, kErrTimeout);
+                        break;
+                    }
+            }
         }
         __syncwarp();
     } else {
@@ -383,10 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
 #pragma unroll
             for (int b = 0; b < kSubs; ++b) {
                 const uint32_t* x = &v[b / 2][b % 2 * 16];
-                float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
-#pragma unroll
-                for (int e = 2; e < kSub; e += 2) t0 = fmaxf(t0, __uint_as_float(x[e])), t1 = fmaxf(t1, __uint_as_float(x[e + 1]));
-                top = fmaxf(top, fmaxf(t0, t1) * factor(b));
+                auto at = [&](int e) { return __uint_as_float(x[e]); };
+                const float t0 = max3(max3(at(0), at(1), at(2)), at(3), at(4)), t1 = max3(max3(at(5), at(6), at(7)), at(8), at(9));
+                const float t2 = max3(max3(at(10), at(11), at(12)), at(13), at(14));
+                top = fmaxf(top, max3(max3(t0, t1, t2), at(15), at(15)) * factor(b));
             }
             // The sums so far are brought to a new maximum only when it is passed.
             if (__any_sync(0xFFFFFFFFu, top > m + kLag)) {
@@ -432,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             l += sum[0] + sum[1];
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(bars + 8 * (kPFull + which));
+            warp_arrive(bars + 8 * (kPFull + which));
         }
         if (ok && blocks > 0) ok = warp_wait(bars + 8 * (kODone + which), (uint32_t)(blocks - 1) & 1u, abort_flag, a.err);
         tc_fence_after();
