@@ -86,6 +86,16 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t addr, uint32_t (&r)[16]) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(addr));
 }
+// Waits for the tensor memory loads; nothing that reads r moves before it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                      "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -384,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             uint32_t plain = 1;
 #pragma unroll
             for (int b = 0; b < kSubs; ++b) plain &= page[b].plain;
-            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_wait_for(v[c]);
             if (tok < full_lo || tok + kStep > full_hi) {   // hidden tokens: -inf
                 const int first_seen = lo - tok, end_seen = hi - tok;
 #pragma unroll
@@ -449,15 +460,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                     const PageData& pd = page[2 * c + b];
                     const float f = factor(2 * c + b), shift = pd.log_v - m;
                     const float2 f2 = make_float2(f, f), shift2 = make_float2(shift, shift);
-                    float2 s2 = make_float2(0.0f, 0.0f);
+                    float2 s2 = make_float2(0.0f, 0.0f), s3 = s2;
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
+                    for (int e = 0; e < 16; e += 4) {
                         const uint32_t* x = &v[c][16 * b + e];
                         float2 w = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), f2, shift2);
+                        float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), f2, shift2);
                         w = make_float2(exp2_approx(w.x), exp2_approx(w.y));
+                        y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
                         s2 = __fadd2_rn(s2, w);
+                        s3 = __fadd2_rn(s3, y);
                         p[8 * b + e / 2] = pack2<__half>(w.x, w.y);
+                        p[8 * b + e / 2 + 1] = pack2<__half>(y.x, y.y);
                     }
+                    s2 = __fadd2_rn(s2, s3);
                     sum[b] = fmaf(s2.x + s2.y, pd.inv_v, sum[b]);
                 }
                 tmem_st_x16(s_at + 16 * c, p);   // over scores that are in registers
