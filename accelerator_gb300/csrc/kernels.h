@@ -227,7 +227,7 @@ cudaError_t launch_kv_read(const KvView& c, void* K, void* V, ElemType type, con
 // Attention: `splits` CTAs share the tokens of a tile of rows, as a cluster
 // or, with scratch (plan.scratch_bytes), joined by a second launch.
 struct KvPlan {
-    int rows;             // query rows of a tile
+    int rows, gap;        // query rows of a tile; how many a sequence's last tile may lack
     int64_t units;        // upper bound of the row tiles of the batch
     int splits;
     bool cluster;         // the splits of a tile are a cluster

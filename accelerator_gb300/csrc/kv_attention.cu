@@ -567,6 +567,8 @@ cudaError_t kv_attention_setup() {
 // shared, and joined likewise, only if the tiles leave half the GPU idle.
 constexpr int64_t kPromptRows = 64;
 
+int64_t gcd(int64_t a, int64_t b) { return b ? gcd(b, a % b) : a; }
+
 KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, int num_sms) {
     KvPlan p;
     const int64_t share = q_heads / c.heads, all = b.rows * share;
@@ -574,9 +576,11 @@ KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, i
              : all <= kPromptRows * b.sequences ? 16
                                                 : 256;
     const int64_t tiles = all / p.rows;
-    p.units = tiles + b.sequences;
+    p.gap = p.rows - (int)gcd(p.rows, share);
+    p.units = (all + b.sequences * (int64_t)p.gap) / p.rows;   // at least the tiles that there are
     int64_t longest = b.width << c.page_log2;
     if (window > 0 && window + p.rows + 2 * kStep < longest) longest = window + p.rows + 2 * kStep;
+    if (p.units < 1) p.units = 1;
     const int64_t have = (tiles > b.sequences ? tiles : b.sequences) * c.heads, slots = (p.rows == 256 ? 1 : 2) * (int64_t)num_sms;
     const int64_t most = (longest + kStep - 1) / kStep;
     int64_t splits;
@@ -600,7 +604,7 @@ cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& 
                                 const KvBatch& b, const KvPlan& plan, void* scratch,
                                 unsigned* err, int* launches, cudaStream_t stream) {
     const bool q_vec = (reinterpret_cast<uintptr_t>(Q.p) & 15u) == 0 && Q.row % 8 == 0 && Q.head % 8 == 0;
-    const AttnArgs a{c, Q, O, b, q_heads, (unsigned)(q_heads / c.heads), scale * 1.44269504088896341f, causal,
+    const AttnArgs a{c, Q, O, b, q_heads, (unsigned)(q_heads / c.heads), plan.gap, scale * 1.44269504088896341f, causal,
                      (int)(window < INT32_MAX ? window : INT32_MAX), plan.splits, q_vec, static_cast<float*>(scratch), err};
     if (type == ElemType::kBF16)
         return c.dim == 128 ? launch<__nv_bfloat16, 128>(a, plan, launches, stream)

@@ -48,6 +48,7 @@ struct AttnArgs {
     KvBatch b;
     int q_heads;
     unsigned share;              // query heads that read one cache head; rows * share fits 31 bits
+    int gap;                     // a tile's rows less their greatest common divisor with share
     float scale_log2;            // scale * log2(e)
     int causal;
     int window;
@@ -80,8 +81,10 @@ struct Tile {
     }
     __device__ __forceinline__ bool find(const AttnArgs& a, int u, int rows, int step, bool report) {
         const Starts starts{a.b.starts, a.b.sequences, a.b.rows};
-        // Sequence q's tiles are units floor(starts[q] * share / rows) + q + j.
-        seq = last_not_above(a.b.sequences, u, [&](int i) { return (unsigned)starts.at(i) * a.share / rows + i; });
+        // Sequence q's tiles are units unit_of(q) + j: its rows are a multiple of
+        // share, so that they need at most (rows + gap) / tile tiles.
+        auto unit_of = [&](int64_t start, int i) { return (int)((start * a.share + (int64_t)i * a.gap) / rows); };
+        seq = last_not_above(a.b.sequences, u, [&](int i) { return unit_of(starts.at(i), i); });
         row0 = (int)starts.at(seq);
         const int count = (int)starts.at(seq + 1) - row0, length = __ldg(a.b.at + seq);
         if (!starts.whole(u == 0, seq)) {
@@ -89,7 +92,7 @@ struct Tile {
             return false;
         }
         nrows = count * (int)a.share;
-        r0 = (u - (int)((unsigned)row0 * a.share / rows) - seq) * rows;
+        r0 = (u - unit_of(row0, seq)) * rows;
         if (r0 < 0 || r0 >= nrows) return false;
         len = length;
         if (length < 0 || length > (a.b.width << a.c.page_log2)) {

@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
     const uint32_t bars = base + L::kBars;
     volatile int* abort_flag = &s_abort;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int u = blockIdx.x / a.splits, split = blockIdx.x % a.splits, h = blockIdx.y;
+    // Heads fastest: sequences come one after another, long ones seldom last.
+    const int h = blockIdx.x % a.c.heads, split = blockIdx.x / a.c.heads % a.splits, u = blockIdx.x / a.c.heads / a.splits;
     Tile tile;
     if (!tile.find(a, u, kRows, kStep, threadIdx.x == 0 && h == 0 && split == 0) || split >= tile.active) return;
     const int begin = split * tile.per, blocks = min(tile.steps, begin + tile.per) - begin;
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
 template <typename T, int D>
 cudaError_t launch(const AttnArgs& a, const KvPlan& plan, cudaStream_t stream) {
     const bool o_vec = (reinterpret_cast<uintptr_t>(a.O.p) & 15u) == 0 && a.O.row % 8 == 0 && a.O.head % 8 == 0;
-    kv_prompt_kernel<T, D><<<dim3((unsigned)(plan.units * plan.splits), (unsigned)a.c.heads), kThreads, Smem<D>::kBytes, stream>>>(a, o_vec);
+    kv_prompt_kernel<T, D><<<(unsigned)(plan.units * plan.splits * a.c.heads), kThreads, Smem<D>::kBytes, stream>>>(a, o_vec);
     return cudaGetLastError();
 }
 

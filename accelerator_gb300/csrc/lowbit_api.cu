@@ -232,7 +232,7 @@ int gemm_kv_attention(const gemm_kv_cache* cache, const void* Q, int64_t q_row_s
     const int64_t q_bytes = rows_span(tokens, q_heads, v.dim, q_row_stride, q_head_stride, 2);
     const int64_t o_bytes = rows_span(tokens, q_heads, v.dim, o_row_stride, o_head_stride, 2);
     if (overlap(Q, q_bytes, O, o_bytes) || overlaps_cache(v, O, o_bytes)) return GEMM_ERR_INVALID_ARG;
-    if (tokens * (q_heads / v.heads) > kIndexMax - 16 || tokens * (q_heads / v.heads) / 8 + sequences > kIndexMax / 8)
+    if (tokens * (q_heads / v.heads) > kIndexMax - 16 || tokens * (q_heads / v.heads) / 8 + sequences > kIndexMax / 8 / v.heads)
         return GEMM_ERR_INVALID_ARG;
     int sms = 0;
     unsigned* err = nullptr;
