@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
     Tile tile;
     // A cluster's CTAs have one tile: they leave here together or not at all.
     if (!tile.find(a, u, kRows, kStep, threadIdx.x == 0 && h == 0 && split == 0) || (!cluster && split >= tile.active)) return;
+    grid_launch_dependents();   // a joining launch may start its set-up
     const int step_begin = min(tile.steps, split * tile.per);
     const int steps = min(tile.steps, step_begin + tile.per) - step_begin;
     const int tok_begin = tile.tok0 + step_begin * kStep;
@@ -125,16 +126,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
             // the first 16 tokens of a page's part fetch all of it
             bool copies = here && mine.live && sub * kSub % chunk == 0;
             if (copies) copies = GEMM_DBG_OK(a.c.k + from, a.c.k, code_bytes, chunk * D) && GEMM_DBG_OK(a.c.v + from, a.c.v, code_bytes, chunk * D);
-            if (here) info[stage * 8 + sub] = mine;
             const int parts = __popc(__ballot_sync(0xFFFFFFFFu, copies));
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, (uint32_t)(parts * 2 * chunk * D));
-            __syncwarp();
+            // The copies go first, then the scales, which may still be on their
+            // way; the stage is not full before the arrival below.
             if (copies) {
                 const uint32_t to = ring + stage * R::kStageBytes + sub * kSub * D;
                 bulk_load(to, a.c.k + from, chunk * D, bars + 8 * stage);
                 bulk_load(to + kStep * D, a.c.v + from, chunk * D, bars + 8 * stage);
             }
+            if (here) info[stage * 8 + sub] = mine;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, (uint32_t)(parts * 2 * chunk * D));
             ++issued;
             if (++stage == R::kStages) stage = 0, phase ^= 1u;
         }
@@ -475,6 +477,7 @@ __global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a, int ro
     const int u = blockIdx.x, h = blockIdx.y, r = blockIdx.z, d = threadIdx.x % D, q = threadIdx.x / D;
     Tile tile;
     if (!tile.find(a, u, rows, step, false) || tile.active == 1 || tile.r0 + r >= tile.nrows) return;
+    grid_dependency_wait();   // launched while the partial results are still being made
     const int64_t slot = (int64_t)rows * (D + 2);
     const float* part = a.partial + ((int64_t)u * a.c.heads + h) * a.splits * slot;
     const float* ml = part + rows * D + 2 * r;
@@ -527,8 +530,16 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStr
     *launches = 1;
     if (e == cudaSuccess && a.partial) {
         static_assert(kStep == 128, "both kernels count tokens in the same steps");
-        kv_join_kernel<T, D><<<dim3((unsigned)plan.units, (unsigned)a.c.heads, (unsigned)plan.rows), 4 * D, 0, stream>>>(a, plan.rows, kStep);
-        e = cudaGetLastError();
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)plan.units, (unsigned)a.c.heads, (unsigned)plan.rows);
+        cfg.blockDim = dim3(4 * D);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = kUsePdl;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D>, a, plan.rows, kStep);
         *launches = 2;
     }
     return e;

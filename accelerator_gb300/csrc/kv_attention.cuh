@@ -84,7 +84,7 @@ struct Tile {
         // Sequence q's tiles are units unit_of(q) + j: its rows are a multiple of
         // share, so that they need at most (rows + gap) / tile tiles.
         auto unit_of = [&](int64_t start, int i) { return (int)((start * a.share + (int64_t)i * a.gap) / rows); };
-        seq = last_not_above(a.b.sequences, u, [&](int i) { return unit_of(starts.at(i), i); });
+        seq = last_not_above(a.b.sequences, u, u, [&](int i) { return unit_of(starts.at(i), i); });
         row0 = (int)starts.at(seq);
         const int count = (int)starts.at(seq + 1) - row0, length = __ldg(a.b.at + seq);
         if (!starts.whole(u == 0, seq)) {

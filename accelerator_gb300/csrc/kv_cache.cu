@@ -31,7 +31,7 @@ __device__ __forceinline__ bool find_part(const KvView& c, const KvBatch& b, int
     const bool report = threadIdx.x == 0 && blockIdx.y == 0;
     const Starts starts{b.starts, b.sequences, b.rows};
     const int log2 = c.page_log2, P = 1 << log2;
-    const int q = last_not_above(b.sequences, u, [&](int i) { return (starts.at(i) >> log2) + 2 * (int64_t)i; });
+    const int q = last_not_above(b.sequences, u, u / 2, [&](int i) { return (starts.at(i) >> log2) + 2 * (int64_t)i; });
     const int64_t row0 = starts.at(q), count = starts.at(q + 1) - row0, first = __ldg(b.at + q);
     if (!starts.whole(u == 0, q) || (count > 0 && (first < 0 || first + count > (b.width << log2)))) {
         if (report) atomicOr(err, kErrIndex);
