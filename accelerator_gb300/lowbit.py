@@ -15,17 +15,21 @@ library), ``TypeError`` (a tensor's type, device or layout) or ``ValueError``
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
 from . import binding
 from .binding import GemmError
 
-_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_F32, _BF16, _F16, _I32 = torch.float32, torch.bfloat16, torch.float16, torch.int32
+_TYPES = {_F32: 0, _BF16: 1, _F16: 2}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 PAGE_TOKENS = (16, 32, 64, 128)
 HEAD_DIMS = (64, 128)
 GROUPS = (32, 64, 128)
+
+# A small call's time is the host's: the checks below are written out in each
+# function, in the fewest steps, and what is wrong is told apart only then.
 
 
 class _CKvCache(ctypes.Structure):
@@ -33,14 +37,6 @@ class _CKvCache(ctypes.Structure):
                 ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
                 ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
                 ("page_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
-
-
-def _stream(stream, device):
-    """The address of `stream`, or of the current stream of `device` (asked for
-    by number: making a Stream object of it costs 3 us, a kernel's launch)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index) or None
-    return stream.cuda_stream or None
 
 
 def _empty(shape, dtype, device, stream):
@@ -51,6 +47,12 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _stream(stream, index):
+    """The address of `stream`, or of the current stream of device `index`
+    (asked for by number: making a Stream object of it costs 3 us)."""
+    return (_raw_stream(index) if stream is None else stream.cuda_stream) or None
+
+
 def _need(cond, name, what):
     if not cond:
         raise TypeError(f"{name} must be {what}")
@@ -58,8 +60,8 @@ def _need(cond, name, what):
 
 def _rows2(t, name):
     """A 2-D CUDA tensor whose rows are dense; returns its row stride."""
-    _need(t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1), name,
-          "a 2-D CUDA tensor with dense rows")
+    if not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise TypeError(f"{name} must be a 2-D CUDA tensor with dense rows")
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
@@ -69,19 +71,24 @@ class W4Matrix:
     """A K x N matrix in 4 bits: the packed codes (uint8), the scales
     (bfloat16), its sizes and the group length.  Layout: include/gemm.h."""
 
-    __slots__ = ("codes", "scales", "K", "N", "group", "_args")
+    __slots__ = ("codes", "scales", "K", "N", "group", "index", "_codes", "_scales")
 
     def __init__(self, codes, scales, K, N, group):
         code_bytes, scale_bytes = w4_sizes(K, N, group)
         _need(codes.is_cuda and codes.is_contiguous() and codes.element_size() * codes.numel() == code_bytes,
               "codes", f"a contiguous CUDA tensor of {code_bytes} bytes")
-        _need(scales.is_cuda and scales.is_contiguous() and scales.dtype == torch.bfloat16
+        _need(scales.is_cuda and scales.is_contiguous() and scales.dtype == _BF16
               and 2 * scales.numel() == scale_bytes, "scales",
               f"a contiguous CUDA bfloat16 tensor of {scale_bytes // 2} elements")
         if codes.device != scales.device:
             raise TypeError("codes and scales must be on one device")
+        self._set(codes, scales, K, N, group)
+
+    def _set(self, codes, scales, K, N, group):
         self.codes, self.scales, self.K, self.N, self.group = codes, scales, int(K), int(N), int(group)
-        self._args = (codes.data_ptr() or None, scales.data_ptr() or None)
+        self.index = codes.get_device()
+        self._codes, self._scales = codes.data_ptr() or None, scales.data_ptr() or None
+        return self
 
     @property
     def device(self):
@@ -101,15 +108,18 @@ def w4_quantize(B, group=128, stream=None) -> W4Matrix:
     """B (K x N; float32, bfloat16 or float16, dense rows) in 4 bits: for each
     column and `group` rows s = max|b| * (1 / 7) in bfloat16 and q = round(b / s)."""
     ldb = _rows2(B, "B")
-    _need(B.dtype in _TYPES, "B", "float32, bfloat16 or float16")
+    kind = _TYPES.get(B.dtype)
+    if kind is None:
+        raise TypeError("B must be float32, bfloat16 or float16")
     K, N = B.shape
     code_bytes, scale_bytes = w4_sizes(K, N, group)
-    codes = _empty(code_bytes, torch.uint8, B.device, stream)
-    scales = _empty(scale_bytes // 2, torch.bfloat16, B.device, stream)
-    W = W4Matrix(codes, scales, K, N, group)
-    rc = binding.lib().gemm_w4_quantize(B.data_ptr() or None, ldb, _TYPES[B.dtype], K, N, group, *W._args,
-                                        _stream(stream, B.device))
-    if rc != binding.OK:
+    device = B.device
+    codes = _empty(code_bytes, torch.uint8, device, stream)
+    scales = _empty(scale_bytes // 2, _BF16, device, stream)
+    W = W4Matrix.__new__(W4Matrix)._set(codes, scales, K, N, group)
+    rc = binding.lib().gemm_w4_quantize(B.data_ptr() or None, ldb, kind, K, N, group, W._codes, W._scales,
+                                        _stream(stream, W.index))
+    if rc:
         raise GemmError(rc, "gemm_w4_quantize")
     return W
 
@@ -117,23 +127,23 @@ def w4_quantize(B, group=128, stream=None) -> W4Matrix:
 def w4_dequantize(W: W4Matrix, out=None, dtype=torch.bfloat16, stream=None):
     """The K x N values that W stands for, each rounded once to `dtype` (or
     into `out`)."""
+    K, N = W.K, W.N
     if out is None:
-        out = _empty((W.K, W.N), dtype, W.device, stream)
-    ldb = _rows2(out, "out")
-    _need(out.dtype in _TYPES, "out", "float32, bfloat16 or float16")
-    _same_device("out", out, W.device)
-    if tuple(out.shape) != (W.K, W.N):
-        raise ValueError(f"out has shape {tuple(out.shape)}, not {(W.K, W.N)}")
-    rc = binding.lib().gemm_w4_dequantize(*W._args, W.K, W.N, W.group, out.data_ptr() or None, ldb,
-                                          _TYPES[out.dtype], _stream(stream, out.device))
-    if rc != binding.OK:
+        out = _empty((K, N), dtype, W.codes.device, stream)
+        ldb = N
+    else:
+        ldb, dtype = _rows2(out, "out"), out.dtype
+        _need(out.get_device() == W.index, "out", f"on {W.device}")
+        if tuple(out.shape) != (K, N):
+            raise ValueError(f"out has shape {tuple(out.shape)}, not {(K, N)}")
+    kind = _TYPES.get(dtype)
+    if kind is None:
+        raise TypeError("out must be float32, bfloat16 or float16")
+    rc = binding.lib().gemm_w4_dequantize(W._codes, W._scales, K, N, W.group, out.data_ptr() or None, ldb, kind,
+                                          _stream(stream, W.index))
+    if rc:
         raise GemmError(rc, "gemm_w4_dequantize")
     return out
-
-
-def _same_device(name, t, device):
-    if t.device != device:
-        raise TypeError(f"{name} is on {t.device}, not on {device}")
 
 
 def gemm_w4(X, W: W4Matrix, C=None, dtype=None, stream=None):
@@ -141,23 +151,28 @@ def gemm_w4(X, W: W4Matrix, C=None, dtype=None, stream=None):
     type or float32 (`dtype`, or `C` itself); X's type by default.  Returns C."""
     ldx = _rows2(X, "X")
     xt = X.dtype
-    _need(xt == torch.bfloat16 or xt == torch.float16, "X", "bfloat16 or float16")
+    if xt is not _BF16 and xt is not _F16:
+        raise TypeError("X must be bfloat16 or float16")
     M, K = X.shape
+    N, index = W.N, W.index
     if K != W.K:
         raise ValueError(f"X has {K} columns, W has {W.K} rows")
-    _same_device("X", X, W.codes.device)
+    if X.get_device() != index:
+        raise TypeError(f"X is on {X.device}, not on {W.device}")
     if C is None:
-        C = _empty((M, W.N), dtype or xt, X.device, stream)
-        ldc = W.N
+        ct = dtype or xt
+        C = _empty((M, N), ct, X.device, stream)
+        ldc = N
     else:
-        ldc = _rows2(C, "C")
-        _same_device("C", C, X.device)
-        if tuple(C.shape) != (M, W.N):
-            raise ValueError(f"C has shape {tuple(C.shape)}, not {(M, W.N)}")
-    _need(C.dtype == xt or C.dtype == torch.float32, "C", "of X's type or float32")
-    rc = binding.lib().gemm_w4(X.data_ptr() or None, ldx, _TYPES[xt], *W._args, C.data_ptr() or None, ldc,
-                               _TYPES[C.dtype], M, K, W.N, W.group, _stream(stream, X.device))
-    if rc != binding.OK:
+        ldc, ct = _rows2(C, "C"), C.dtype
+        _need(C.get_device() == index, "C", f"on {W.device}")
+        if tuple(C.shape) != (M, N):
+            raise ValueError(f"C has shape {tuple(C.shape)}, not {(M, N)}")
+    if ct is not xt and ct is not _F32:
+        raise TypeError("C must be of X's type or float32")
+    rc = binding.lib().gemm_w4(X.data_ptr() or None, ldx, _TYPES[xt], W._codes, W._scales, C.data_ptr() or None, ldc,
+                               _TYPES[ct], M, K, N, W.group, _stream(stream, index))
+    if rc:
         raise GemmError(rc, "gemm_w4")
     return C
 
@@ -168,7 +183,7 @@ class KvCache:
     """A paged cache of keys and values: codes uint8 [pages, heads,
     page_tokens, head_dim] and scales float32 [pages, heads] of each."""
 
-    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "heads", "head_dim", "page_tokens", "device",
+    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "heads", "head_dim", "page_tokens", "device", "index",
                  "_c", "_ref")
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
@@ -176,12 +191,11 @@ class KvCache:
         _need(len(shape) == 4 and shape[2] in PAGE_TOKENS and shape[3] in HEAD_DIMS, "k_codes",
               f"[pages, heads, page_tokens in {PAGE_TOKENS}, head_dim in {HEAD_DIMS}]")
         for name, t, want, dt in (("k_codes", k_codes, shape, torch.uint8), ("v_codes", v_codes, shape, torch.uint8),
-                                  ("k_scales", k_scales, shape[:2], torch.float32),
-                                  ("v_scales", v_scales, shape[:2], torch.float32)):
+                                  ("k_scales", k_scales, shape[:2], _F32), ("v_scales", v_scales, shape[:2], _F32)):
             _need(tuple(t.shape) == want and t.dtype == dt and t.is_cuda and t.is_contiguous()
                   and t.device == k_codes.device, name, f"a contiguous CUDA {dt} tensor of shape {want}")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
         pages, self.heads, self.page_tokens, self.head_dim = shape
         self._c = _CKvCache(k_codes.data_ptr() or None, v_codes.data_ptr() or None, k_scales.data_ptr() or None,
                             v_scales.data_ptr() or None, pages, self.heads, self.page_tokens, self.head_dim)
@@ -192,28 +206,32 @@ class KvCache:
         """A cache of `pages` pages; a page needs no initial contents."""
         shape = (pages, heads, page_tokens, head_dim)
         return cls(*(torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2)),
-                   *(torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
+                   *(torch.zeros(shape[:2], dtype=_F32, device=device) for _ in range(2)))
 
 
 def _batch(cache, page_table, starts, at, name):
     """Checks the index tensors of a call; returns (table width, sequences)."""
-    for n, t, dims in (("page_table", page_table, 2), ("starts", starts, 1), (name, at, 1)):
-        if t.dtype != torch.int32 or t.dim() != dims or t.device != cache.device or not t.is_contiguous():
-            raise TypeError(f"{n} must be a contiguous {dims}-D int32 tensor on {cache.device}")
+    index = cache.index
+    if not (page_table.dtype is starts.dtype is at.dtype is _I32 and page_table.get_device() == index
+            and starts.get_device() == index and at.get_device() == index and page_table.is_contiguous()
+            and starts.is_contiguous() and at.is_contiguous() and page_table.dim() == 2 and starts.dim() == at.dim() == 1):
+        raise TypeError(f"page_table (2-D), starts and {name} (1-D) must be contiguous int32 tensors on {cache.device}")
+    rows, width = page_table.shape
     sequences = at.shape[0]
-    if page_table.shape[0] != sequences or starts.shape[0] != sequences + 1:
-        raise ValueError(f"{sequences} entries of {name}, {page_table.shape[0]} page table rows and "
-                         f"{starts.shape[0]} starts do not fit together")
-    return page_table.shape[1], sequences
+    if rows != sequences or starts.shape[0] != sequences + 1:
+        raise ValueError(f"{sequences} entries of {name}, {rows} page table rows and {starts.shape[0]} starts do not "
+                         "fit together")
+    return width, sequences
 
 
-def _rows3(t, name, cache, heads=None):
-    """Rows of heads x head_dim elements with dense elements; returns (row stride, head stride)."""
-    if (t.dim() != 3 or t.device != cache.device or t.shape[2] != cache.head_dim or t.stride(2) != 1
-            or (heads is not None and t.shape[1] != heads)):
-        raise TypeError(f"{name} must be a tensor on {cache.device} of rows x {heads or 'heads'} x "
-                        f"{cache.head_dim} with dense elements")
-    return t.stride(0), t.stride(1)
+def _rows3(t, name, cache):
+    """Rows of heads x head_dim elements with dense elements; returns (rows, heads, row stride, head stride)."""
+    if t.dim() == 3 and t.get_device() == cache.index:
+        rows, heads, dim = t.shape
+        row, head, one = t.stride()
+        if dim == cache.head_dim and one == 1:
+            return rows, heads, row, head
+    raise TypeError(f"{name} must be a tensor on {cache.device} of rows x heads x {cache.head_dim} with dense elements")
 
 
 def kv_append(cache: KvCache, K, V, page_table, starts, first, stream=None):
@@ -222,15 +240,19 @@ def kv_append(cache: KvCache, K, V, page_table, starts, first, stream=None):
     becomes token first[b] + i of sequence b.  A page's scale grows to the
     largest magnitude / 127, and its older codes with it."""
     width, sequences = _batch(cache, page_table, starts, first, "first")
-    kr, kh = _rows3(K, "K", cache, cache.heads)
-    vr, vh = _rows3(V, "V", cache, cache.heads)
-    _need(K.dtype in _TYPES and V.dtype == K.dtype, "K and V", "of one type: float32, bfloat16 or float16")
-    if K.shape[0] != V.shape[0]:
-        raise ValueError(f"{K.shape[0]} keys and {V.shape[0]} values")
-    rc = binding.lib().gemm_kv_append(cache._ref, K.data_ptr() or None, kr, kh, V.data_ptr() or None, vr, vh,
-                                      _TYPES[K.dtype], page_table.data_ptr() or None, width, starts.data_ptr(),
-                                      first.data_ptr() or None, K.shape[0], sequences, _stream(stream, cache.device))
-    if rc != binding.OK:
+    rows, heads, kr, kh = _rows3(K, "K", cache)
+    v_rows, v_heads, vr, vh = _rows3(V, "V", cache)
+    kind = _TYPES.get(K.dtype)
+    if kind is None or V.dtype is not K.dtype:
+        raise TypeError("K and V must be of one type: float32, bfloat16 or float16")
+    if heads != cache.heads or v_heads != heads:
+        raise TypeError(f"K and V must have {cache.heads} heads")
+    if rows != v_rows:
+        raise ValueError(f"{rows} keys and {v_rows} values")
+    rc = binding.lib().gemm_kv_append(cache._ref, K.data_ptr() or None, kr, kh, V.data_ptr() or None, vr, vh, kind,
+                                      page_table.data_ptr() or None, width, starts.data_ptr(),
+                                      first.data_ptr() or None, rows, sequences, _stream(stream, cache.index))
+    if rc:
         raise GemmError(rc, "gemm_kv_append")
 
 
@@ -239,13 +261,16 @@ def kv_read(cache: KvCache, page_table, starts, first, tokens, dtype=torch.bfloa
     starts[b] + i is token first[b] + i of sequence b.  `tokens` is starts[-1],
     known on the host."""
     width, sequences = _batch(cache, page_table, starts, first, "first")
-    _need(dtype in _TYPES, "dtype", "float32, bfloat16 or float16")
-    K = _empty((tokens, cache.heads, cache.head_dim), dtype, cache.device, stream)
-    V = _empty((tokens, cache.heads, cache.head_dim), dtype, cache.device, stream)
-    rc = binding.lib().gemm_kv_read(cache._ref, K.data_ptr() or None, V.data_ptr() or None, _TYPES[dtype],
+    kind = _TYPES.get(dtype)
+    if kind is None:
+        raise TypeError("dtype must be float32, bfloat16 or float16")
+    shape = (tokens, cache.heads, cache.head_dim)
+    K = _empty(shape, dtype, cache.device, stream)
+    V = _empty(shape, dtype, cache.device, stream)
+    rc = binding.lib().gemm_kv_read(cache._ref, K.data_ptr() or None, V.data_ptr() or None, kind,
                                     page_table.data_ptr() or None, width, starts.data_ptr(),
-                                    first.data_ptr() or None, tokens, sequences, _stream(stream, cache.device))
-    if rc != binding.OK:
+                                    first.data_ptr() or None, tokens, sequences, _stream(stream, cache.index))
+    if rc:
         raise GemmError(rc, "gemm_kv_read")
     return K, V
 
@@ -259,19 +284,23 @@ def kv_attention(Q, cache: KvCache, page_table, starts, lengths, scale=None, cau
     them.  scale: 1 / sqrt(head_dim) by default.  A query that sees nothing
     gets 0.  Returns O, shaped and typed like Q."""
     width, sequences = _batch(cache, page_table, starts, lengths, "lengths")
-    qr, qh = _rows3(Q, "Q", cache)
-    _need(Q.dtype == torch.bfloat16 or Q.dtype == torch.float16, "Q", "bfloat16 or float16")
+    rows, heads, qr, qh = _rows3(Q, "Q", cache)
+    kind = Q.dtype
+    if kind is not _BF16 and kind is not _F16:
+        raise TypeError("Q must be bfloat16 or float16")
     if out is None:
-        out = _empty(Q.shape, Q.dtype, Q.device, stream)
+        dim = cache.head_dim
+        out = _empty((rows, heads, dim), kind, cache.device, stream)
+        orow, oh = heads * dim, dim
     else:
-        _need(out.dtype == Q.dtype and out.shape == Q.shape, "out", "of Q's type and shape")
-    orow, oh = _rows3(out, "out", cache)
+        o_rows, o_heads, orow, oh = _rows3(out, "out", cache)
+        _need(out.dtype is kind and o_rows == rows and o_heads == heads, "out", "of Q's type and shape")
     if scale is None:
-        scale = 1.0 / math.sqrt(cache.head_dim)
+        scale = cache.head_dim ** -0.5
     rc = binding.lib().gemm_kv_attention(cache._ref, Q.data_ptr() or None, qr, qh, out.data_ptr() or None, orow, oh,
-                                         _TYPES[Q.dtype], Q.shape[1], scale, causal, window,
-                                         page_table.data_ptr() or None, width, starts.data_ptr(),
-                                         lengths.data_ptr() or None, Q.shape[0], sequences, _stream(stream, cache.device))
-    if rc != binding.OK:
+                                         _TYPES[kind], heads, scale, causal, window, page_table.data_ptr() or None,
+                                         width, starts.data_ptr(), lengths.data_ptr() or None, rows, sequences,
+                                         _stream(stream, cache.index))
+    if rc:
         raise GemmError(rc, "gemm_kv_attention")
     return out
