@@ -50,16 +50,19 @@ __device__ __forceinline__ bool find_part(const KvView& c, const KvBatch& b, int
     return true;
 }
 
-__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
-    return (uint32_t)((int)a + 128) | (uint32_t)((int)b + 128) << 8 | (uint32_t)((int)c + 128) << 16 |
-           (uint32_t)((int)d + 128) << 24;
+// Codes of four values: rint(x * f) + 128 as bytes.  |x * f| stays under 127.5:
+// f is 1 / s and s at least max|x| * (1 / 127), but for three roundings.
+__device__ __forceinline__ uint32_t codes_of(float2 a, float2 b, float f) {
+    // single products: a packed one and the sum after it become one operation, without the rounding between them
+    const float2 to_byte = make_float2(12583040.0f, 12583040.0f);   // 1.5 * 2^23 + 128
+    return low_bytes(__fadd2_rn(make_float2(__fmul_rn(a.x, f), __fmul_rn(a.y, f)), to_byte),
+                     __fadd2_rn(make_float2(__fmul_rn(b.x, f), __fmul_rn(b.y, f)), to_byte));
 }
-__device__ __forceinline__ float code_of(float x, float inv) {
-    return fminf(fmaxf(rintf(__fmul_rn(x, inv)), -127.0f), 127.0f);
-}
-// Byte i of a word of codes as c, exactly: u in the low fraction bits of 2^23.
-__device__ __forceinline__ float value_of(uint32_t w, int i) {
-    return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | i)) - 8388736.0f;
+// Bytes i and i + 1 of a word of codes as c, exactly: u in the low fraction bits of 2^23.
+__device__ __forceinline__ float2 values_of(uint32_t w, int i) {
+    return __fadd2_rn(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | i)),
+                                  __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | (i + 1)))),
+                      make_float2(-8388736.0f, -8388736.0f));
 }
 
 // UNITS groups of 8 elements a thread: a page's elements / 8 / kThreads.
@@ -91,14 +94,13 @@ __global__ void __launch_bounds__(kThreads)
         const T* p = x + (int64_t)(e / per_row) * src.row + e % per_row * 8;
         if (e < n && GEMM_DBG_OK(p, src.p, x_bytes, 8 * sizeof(T))) held[i] = load_eight(p, vec);
     }
-    uint32_t m = 0;   // magnitudes compare as their bits; from 0x7F800000 on they are not finite
+    Tops<T> tops;
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
         if (i * kThreads >= n) break;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(held[i].at(j)) & 0x7FFFFFFFu);
+        tops.take(held[i]);
     }
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    uint32_t m = __reduce_max_sync(0xFFFFFFFFu, tops.all());
     if (tid % 32 == 0) s_top[tid / 32] = m;
     __syncthreads();   // also: every thread has read the old scale
 #pragma unroll
@@ -113,10 +115,11 @@ __global__ void __launch_bounds__(kThreads)
         const int e = tid + i * kThreads;
         uint8_t* o = out + part.begin * c.dim + e * 8;
         if (e >= n || !GEMM_DBG_OK(o, codes, code_bytes, 8)) break;
-        float q[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = bad ? 0.0f : code_of(held[i].at(j), inv);
-        *reinterpret_cast<uint2*>(o) = make_uint2(pack_codes(q[0], q[1], q[2], q[3]), pack_codes(q[4], q[5], q[6], q[7]));
+        const Eight<T>& x = held[i];
+        uint2 w = make_uint2(codes_of(make_float2(x.at(0), x.at(1)), make_float2(x.at(2), x.at(3)), inv),
+                             codes_of(make_float2(x.at(4), x.at(5)), make_float2(x.at(6), x.at(7)), inv));
+        if (bad) w = make_uint2(0x80808080u, 0x80808080u);
+        *reinterpret_cast<uint2*>(o) = w;
     }
     if (!bad && before < s) {   // the scale grew: the page's older codes follow
         const float r = __fmul_rn(before, inv);
@@ -124,10 +127,7 @@ __global__ void __launch_bounds__(kThreads)
             uint2* o = reinterpret_cast<uint2*>(out) + e;
             if (!GEMM_DBG_OK(o, codes, code_bytes, 8)) continue;
             const uint2 w = *o;
-            float q[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = rintf(__fmul_rn(value_of(j < 4 ? w.x : w.y, j & 3), r));
-            *o = make_uint2(pack_codes(q[0], q[1], q[2], q[3]), pack_codes(q[4], q[5], q[6], q[7]));
+            *o = make_uint2(codes_of(values_of(w.x, 0), values_of(w.x, 2), r), codes_of(values_of(w.y, 0), values_of(w.y, 2), r));
         }
     }
 }
@@ -161,15 +161,15 @@ __global__ void __launch_bounds__(kThreads)
         const int e = tid + i * kThreads;
         T* o = to + (int64_t)(e / per_row) * c.heads * c.dim + e % per_row * 8;
         if (e >= n || !GEMM_DBG_OK(o, out, out_bytes, 8 * sizeof(T))) break;
-        float v[8];
+        float2 v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(value_of(j < 4 ? held[i].x : held[i].y, j & 3), s);
+        for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(values_of(j < 2 ? held[i].x : held[i].y, 2 * j & 3), make_float2(s, s));
         if constexpr (sizeof(T) == 4) {
-            reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            reinterpret_cast<float4*>(o)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+            reinterpret_cast<float4*>(o)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
         } else {
-            *reinterpret_cast<uint4*>(o) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
-                                                      pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+            *reinterpret_cast<uint4*>(o) = make_uint4(pack2<T>(v[0].x, v[0].y), pack2<T>(v[1].x, v[1].y),
+                                                      pack2<T>(v[2].x, v[2].y), pack2<T>(v[3].x, v[3].y));
         }
     }
 }

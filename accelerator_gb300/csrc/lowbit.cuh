@@ -118,6 +118,63 @@ __device__ __forceinline__ Eight<T> load_eight(const T* p, bool vec) {
     return e;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t c;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+    return c;
+}
+
+// The largest magnitude of each of eight columns, as the bits of a float (from
+// 0x7F800000 on: not finite); 16-bit types are compared two at a time.
+template <typename T>
+struct Tops {
+    uint32_t m[sizeof(T) == 4 ? 8 : 4] = {};
+    __device__ __forceinline__ void take(const Eight<T>& x) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(x.v);
+#pragma unroll
+        for (int i = 0; i < (sizeof(T) == 4 ? 8 : 4); ++i) {
+            if constexpr (sizeof(T) == 4) m[i] = max(m[i], w[i] & 0x7FFFFFFFu);
+            else m[i] = max_u16x2(m[i], w[i] & 0x7FFF7FFFu);
+        }
+    }
+    __device__ __forceinline__ void across(int mask) {   // and of the lane that differs in `mask`
+#pragma unroll
+        for (int i = 0; i < (sizeof(T) == 4 ? 8 : 4); ++i) {
+            const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, m[i], mask);
+            if constexpr (sizeof(T) == 4) m[i] = max(m[i], o);
+            else m[i] = max_u16x2(m[i], o);
+        }
+    }
+    __device__ __forceinline__ uint32_t bits(int i) const {
+        if constexpr (sizeof(T) == 4) return m[i];
+        else if constexpr (std::is_same<T, __half>::value)
+            return __float_as_uint(__half2float(__ushort_as_half((unsigned short)(m[i / 2] >> (16 * (i & 1))))));
+        else return i & 1 ? m[i / 2] & 0xFFFF0000u : m[i / 2] << 16;
+    }
+    __device__ __forceinline__ uint32_t all() const {   // over the eight
+        uint32_t t = 0;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t = max(t, m[i]);
+            return t;
+        } else {
+            t = max_u16x2(max_u16x2(m[0], m[1]), max_u16x2(m[2], m[3]));
+            Tops<T> one;
+            one.m[0] = max(t & 0xFFFFu, t >> 16);
+            return one.bits(0);
+        }
+    }
+};
+
+// The low bytes of four words.  An integer of a byte that is added to 1.5 *
+// 2^23 is rounded there, ties to even, and left in the low byte.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
+    return low_bytes(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+}
+
 // The largest b in [0, n) with value(b) <= x, for a non-decreasing value();
 // 0 if there is none.  The lanes of a warp look at 32 places at once: a chain
 // of two loads for a thousand sequences where halving has ten.

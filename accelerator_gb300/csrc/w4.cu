@@ -24,8 +24,8 @@ struct W4 {
     __host__ __device__ int64_t nb() const { return (N + 15) / 16; }
 };
 
-// Both conversions take tiles of 128 rows x 64 columns, a whole number of
-// groups and blocks, with 256 threads of 32 elements each.
+// The quantiser takes tiles of 128 rows x 64 columns, a whole number of groups
+// and blocks, with 256 threads of 32 elements each.
 constexpr int kQRows = 128, kQCols = 64, kQThreads = 256;
 
 __device__ __forceinline__ void tile_at(const W4& w, int64_t& k0, int64_t& n0) {
@@ -35,6 +35,15 @@ __device__ __forceinline__ void tile_at(const W4& w, int64_t& k0, int64_t& n0) {
 }
 
 // ---- quantise ----------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float pick(const Eight<T>& x, int j) {   // at(j) for a j that is not known in advance
+    float v = x.at(0);
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+        if (k == j) v = x.at(k);
+    return v;
+}
+
 // A thread holds four neighbouring rows of eight columns, all loaded before
 // the first is used.  The largest magnitude of a column goes over four lanes
 // by shuffles and over two warps through shared memory (a group of 32 rows);
@@ -66,14 +75,14 @@ __global__ void __launch_bounds__(kQThreads)
             x[i] = load_eight(part, false);
         }
     }
+    Tops<T> tops;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {   // magnitudes compare as their bits; from 0x7F800000 on they are not finite
-        uint32_t m = 0;
+    for (int i = 0; i < 4; ++i) tops.take(x[i]);
+    tops.across(8);
+    tops.across(16);
+    if (tid % 32 < 8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(x[i].at(j)) & 0x7FFFFFFFu);
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-        if (tid % 32 < 8) top[tid / 32][8 * c8 + j] = m;
+        for (int j = 0; j < 8; ++j) top[tid / 32][8 * c8 + j] = tops.bits(j);
     }
     __syncthreads();
     {
@@ -102,21 +111,35 @@ __global__ void __launch_bounds__(kQThreads)
     // stays under 7.04, as s is at most 2^-8 below max|b| / 7.
     uint32_t mine[8];
     const int hi = c8 & 1, part = r / 8;
+    bool tiny = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float s = scale[part][8 * c8 + j], inv = inverse[part][8 * c8 + j];
-        uint32_t v = 0;
+        const float2 i2 = make_float2(inv, inv), n2 = make_float2(-s, -s), to_nibble = make_float2(12582920.0f, 12582920.0f);   // 1.5 * 2^23 + 8
+        float2 u[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float b = x[i].at(j);
-            const float t = __fmul_rn(b, inv);
-            float q = __fmaf_rn(__fmaf_rn(-t, s, b), inv, t);
-            if (s < 7.9e-31f && s > 0.0f) q = __fdiv_rn(b, s);
-            // 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low bits
-            const uint32_t u = __float_as_uint(__fadd_rn(q, 12582912.0f)) + 8u;
-            v |= (u & 15u) << (4 * (4 * (i & 1) + 2 * (i >> 1)));
+        for (int p = 0; p < 2; ++p) {
+            const float2 b = make_float2(x[2 * p].at(j), x[2 * p + 1].at(j));
+            const float2 t = __fmul2_rn(b, i2);
+            u[p] = __fadd2_rn(__ffma2_rn(__ffma2_rn(t, n2, b), i2, t), to_nibble);
         }
+        // rows 0, 2, 1, 3 in the nibbles 0, 2, 4, 6
+        const uint32_t v = low_bytes(__float_as_uint(u[0].x), __float_as_uint(u[1].x), __float_as_uint(u[0].y), __float_as_uint(u[1].y));
         mine[j] = (s == 0.0f ? 0x08080808u : v) << (4 * hi);
+        tiny |= s < 7.9e-31f && s > 0.0f;
+    }
+    if (tiny) {
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+            const float s = scale[part][8 * c8 + j];
+            if (!(s < 7.9e-31f && s > 0.0f)) continue;
+            uint32_t v = 0;
+            for (int i = 0; i < 4; ++i)
+                v |= (uint32_t)((int)rintf(__fdiv_rn(pick(x[i], j), s)) + 8) << (8 * (2 * (i & 1) + (i >> 1)));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k == j) mine[k] = v << (4 * hi);
+        }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {   // the even thread keeps columns 0-3 of 8, the odd one 4-7
@@ -136,58 +159,70 @@ __global__ void __launch_bounds__(kQThreads)
 }
 
 // ---- dequantise --------------------------------------------------------------
-// A warp takes a block, a thread its 16 bytes; the values pass through a
-// tile in shared memory whose pieces of eight columns are permuted by the row
-// (piece ^ row / 8), so that neither side meets itself in a bank.
+// A thread takes word 4t + j of each of a block's eight g -- four rows of all of
+// its 16 columns -- so that what it stores is a row's 16 neighbours, and eight
+// lanes' words are whole sectors.
+constexpr int kDRows = 256;     // of a CTA: a warp half a block of each of four, side by side
+
 template <typename T>
 __global__ void __launch_bounds__(kQThreads)
     w4_dequantize_kernel(W4 w, T* __restrict__ B, int64_t ldb, bool vec) {
-    __shared__ __align__(16) T tile[kQRows][kQCols];
-    int64_t k0, n0;
-    tile_at(w, k0, n0);
-    const int tid = threadIdx.x;
-    {
-        const int nbl = tid / 64, kbl = tid / 32 % 2, lane = tid % 32, g = lane / 4, t = lane % 4;
-        const int64_t nb = n0 / 16 + nbl, kb = k0 / 64 + kbl;
-        const uint4* p = reinterpret_cast<const uint4*>(w.codes + (nb * w.kb + kb) * 128) + lane;
-        if (nb < w.nb() && kb < w.kb && GEMM_DBG_OK(p, w.codes, w.nb() * w.kb * 512, 16)) {
-            const uint4 v = __ldg(p);
-            const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+    const int64_t across = (w.N + kQCols - 1) / kQCols;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, tj = warp % 2 * 8 + lane % 8;
+    const int64_t kb = blockIdx.x / across * (kDRows / 64) + warp / 2, nb = blockIdx.x % across * (kQCols / 16) + lane / 8;
+    if (nb >= w.nb() || kb >= w.kb) return;
+    const int64_t k = kb * 64 + 32 * (tj % 4 / 2) + 8 * (tj / 4) + 4 * (tj % 2), n = nb * 16;
+    if (k >= w.K) return;
+    const uint32_t* p = w.codes + (nb * w.kb + kb) * 128 + tj;
+    const uint16_t* sp = w.scales + (nb * w.groups + k / w.group) * 16;
+    if (!GEMM_DBG_OK(p, w.codes, w.nb() * w.kb * 512, 4) || !GEMM_DBG_OK(p + 112, w.codes, w.nb() * w.kb * 512, 4) ||
+        !GEMM_DBG_OK(sp, w.scales, w.nb() * w.groups * 32, 32))
+        return;
+    uint32_t words[8], scales[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t k = kb * 64 + 32 * (j >> 1);
-                const uint16_t* sp = w.scales + ((nb * w.groups + k / w.group) * 8 + g) * 2;
-                uint32_t s2 = 0;   // the scales of columns g and g + 8
-                if (k < w.K && GEMM_DBG_OK(sp, w.scales, w.nb() * w.groups * 32, 4))
-                    s2 = __ldg(reinterpret_cast<const uint32_t*>(sp));
-                const int row = kbl * 64 + 32 * (j >> 1) + 8 * t + 4 * (j & 1);
+    for (int g = 0; g < 8; ++g) words[g] = __ldg(p + 16 * g);
+    {   // of columns g and g + 8 together
+        uint2 s2[4];
 #pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    const int hi = b & 1, e = (b >> 2) + 2 * ((b >> 1) & 1);
-                    const float s = __uint_as_float(hi ? s2 & 0xFFFF0000u : s2 << 16);
-                    const float q = __uint_as_float(((ws[j] >> (4 * b)) & 15u) | 0x4B000000u) - 8388616.0f;
-                    tile[row + e][8 * ((2 * nbl + hi) ^ (row / 8 & 7)) + g] = from_float<T>(__fmul_rn(q, s));
-                }
-            }
-        }
+        for (int i = 0; i < 4; ++i) s2[i] = __ldg(reinterpret_cast<const uint2*>(sp) + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scales[2 * i] = s2[i].x, scales[2 * i + 1] = s2[i].y;
     }
-    __syncthreads();
     [[maybe_unused]] const int64_t b_bytes = ((w.K - 1) * ldb + w.N) * (int64_t)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = tid / 8 + 32 * i, c8 = tid % 8;
-        const int64_t k = k0 + row, n = n0 + 8 * c8;
-        if (k >= w.K) break;
-        const T* from = &tile[row][8 * (c8 ^ (row / 8 & 7))];
-        T* to = B + k * ldb + n;
-        if (vec && n + 8 <= w.N) {
-            if (!GEMM_DBG_OK(to, B, b_bytes, 8 * sizeof(T))) continue;
+    for (int e = 0; e < 4; ++e) {
+        if (k + e >= w.K) break;
+        float2 v[2][4];
 #pragma unroll
-            for (int j = 0; j < (int)sizeof(T) / 2; ++j) reinterpret_cast<uint4*>(to)[j] = reinterpret_cast<const uint4*>(from)[j];
+        for (int hi = 0; hi < 2; ++hi) {
+            const int shift = 4 * (4 * (e & 1) + 2 * (e >> 1) + hi);
+            auto one = [&](int g) { return __uint_as_float(((words[g] >> shift) & 15u) | 0x4B000000u); };
+            auto scale = [&](int g) { return __uint_as_float(hi ? scales[g] & 0xFFFF0000u : scales[g] << 16); };
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[hi][i] = __fmul2_rn(__fadd2_rn(make_float2(one(2 * i), one(2 * i + 1)), make_float2(-8388616.0f, -8388616.0f)),
+                                      make_float2(scale(2 * i), scale(2 * i + 1)));
+        }
+        T* to = B + (k + e) * ldb + n;
+        if (vec && n + 16 <= w.N) {
+            if (!GEMM_DBG_OK(to, B, b_bytes, 16 * sizeof(T))) continue;
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                const float2* y = v[hi];
+                if constexpr (sizeof(T) == 4) {
+                    reinterpret_cast<float4*>(to)[2 * hi] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+                    reinterpret_cast<float4*>(to)[2 * hi + 1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
+                } else {
+                    reinterpret_cast<uint4*>(to)[hi] = make_uint4(pack2<T>(y[0].x, y[0].y), pack2<T>(y[1].x, y[1].y),
+                                                                  pack2<T>(y[2].x, y[2].y), pack2<T>(y[3].x, y[3].y));
+                }
+            }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (n + j < w.N && GEMM_DBG_OK(to + j, B, b_bytes, sizeof(T))) to[j] = from[j];
+            for (int c = 0; c < 16; ++c) {
+                const float2 y = v[c / 8][c % 8 / 2];
+                if (n + c < w.N && GEMM_DBG_OK(to + c, B, b_bytes, sizeof(T))) to[c] = from_float<T>(c & 1 ? y.y : y.x);
+            }
         }
     }
 }
@@ -471,7 +506,7 @@ cudaError_t launch_w4_dequantize(const void* codes, const void* scales, int64_t 
                                  int group, void* B, int64_t ldb, ElemType type,
                                  cudaStream_t stream) {
     const W4 w = view(codes, scales, K, N, group);
-    const unsigned grid = (unsigned)(((K + kQRows - 1) / kQRows) * ((N + kQCols - 1) / kQCols));
+    const unsigned grid = (unsigned)(((K + kDRows - 1) / kDRows) * ((N + kQCols - 1) / kQCols));
     const int64_t es = type == ElemType::kF32 ? 4 : 2;
     const bool vec = (reinterpret_cast<uintptr_t>(B) & 15u) == 0 && ldb * es % 16 == 0;
     if (type == ElemType::kF32)
