@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads)
     float* scales = values ? c.vs : c.ks;
     Part part;
     if (!find_part(c, b, blockIdx.x, err, part)) return;
-    const int per_row = c.dim / 8, n = (part.end - part.begin) * per_row;
+    const int row_log2 = c.dim == 64 ? 3 : 4, n = (part.end - part.begin) << row_log2;   // groups of a row; in all
     const T* x = static_cast<const T*>(src.p) + part.row * src.row + h * src.head;
     [[maybe_unused]] const int64_t x_bytes =
         ((b.rows - 1) * src.row + (c.heads - 1) * src.head + c.dim) * (int64_t)sizeof(T);
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < UNITS; ++i) {
         const int e = tid + i * kThreads;
         if (i * kThreads >= n) break;
-        const T* p = x + (int64_t)(e / per_row) * src.row + e % per_row * 8;
+        const T* p = x + (int64_t)(e >> row_log2) * src.row + (e & ((1 << row_log2) - 1)) * 8;
         if (e < n && GEMM_DBG_OK(p, src.p, x_bytes, 8 * sizeof(T))) held[i] = load_eight(p, vec);
     }
     Tops<T> tops;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (!bad && before < s) {   // the scale grew: the page's older codes follow
         const float r = __fmul_rn(before, inv);
-        for (int e = tid; e < part.begin * per_row; e += kThreads) {
+        for (int e = tid; e < part.begin << row_log2; e += kThreads) {
             uint2* o = reinterpret_cast<uint2*>(out) + e;
             if (!GEMM_DBG_OK(o, codes, code_bytes, 8)) continue;
             const uint2 w = *o;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint8_t* codes = values ? c.v : c.k;
     const float* scales = values ? c.vs : c.ks;
     T* out = values ? V : K;
-    const int per_row = c.dim / 8, n = (part.end - part.begin) * per_row;
+    const int row_log2 = c.dim == 64 ? 3 : 4, n = (part.end - part.begin) << row_log2;   // groups of a row; in all
     const int64_t ph = part.page * c.heads + h;
     const uint8_t* from = codes + ((ph << c.page_log2) + part.begin) * c.dim;
     T* to = out + (part.row * c.heads + h) * c.dim;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
         const int e = tid + i * kThreads;
-        T* o = to + (int64_t)(e / per_row) * c.heads * c.dim + e % per_row * 8;
+        T* o = to + (int64_t)(e >> row_log2) * c.heads * c.dim + (e & ((1 << row_log2) - 1)) * 8;
         if (e >= n || !GEMM_DBG_OK(o, out, out_bytes, 8 * sizeof(T))) break;
         float2 v[4];
 #pragma unroll

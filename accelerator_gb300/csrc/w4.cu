@@ -21,6 +21,7 @@ struct W4 {
     uint16_t* scales;
     int64_t K, N;
     int group, kb, groups;   // blocks of 64 rows, groups of rows
+    int group_log2;
     __host__ __device__ int64_t nb() const { return (N + 15) / 16; }
 };
 
@@ -29,9 +30,9 @@ struct W4 {
 constexpr int kQRows = 128, kQCols = 64, kQThreads = 256;
 
 __device__ __forceinline__ void tile_at(const W4& w, int64_t& k0, int64_t& n0) {
-    const int64_t across = (w.N + kQCols - 1) / kQCols;
-    k0 = blockIdx.x / across * kQRows;
-    n0 = blockIdx.x % across * kQCols;
+    const unsigned across = (unsigned)((w.N + kQCols - 1) / kQCols);
+    k0 = (int64_t)(blockIdx.x / across) * kQRows;
+    n0 = (int64_t)(blockIdx.x % across) * kQCols;
 }
 
 // ---- quantise ----------------------------------------------------------------
@@ -51,10 +52,10 @@ __device__ __forceinline__ float pick(const Eight<T>& x, int j) {   // at(j) for
 // neighbour make half of it each and swap; the words leave in 16-byte pieces
 // by way of shared memory.
 template <typename T>
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kQThreads, 4)
     w4_quantize_kernel(const T* __restrict__ B, int64_t ldb, bool vec, W4 w) {
     __shared__ uint32_t top[kQThreads / 32][kQCols];
-    __shared__ float scale[4][kQCols], inverse[4][kQCols];
+    __shared__ __align__(16) float scale[4][kQCols], inverse[4][kQCols];
     __shared__ __align__(16) uint32_t words[4 * 296];   // [16 columns][64 rows][128 words], spread over the banks
     int64_t k0, n0;
     tile_at(w, k0, n0);
@@ -86,9 +87,9 @@ __global__ void __launch_bounds__(kQThreads)
     }
     __syncthreads();
     {
-        const int c = tid % kQCols, part = tid / kQCols, per = w.group / 32;
+        const int c = tid % kQCols, part = tid / kQCols, per = w.group / 32, first = part & ~(per - 1);
         uint32_t m = 0;
-        for (int i = 0; i < 2 * per; ++i) m = max(m, top[part / per * per * 2 + i][c]);
+        for (int i = 0; i < 2 * per; ++i) m = max(m, top[first * 2 + i][c]);
         const __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(__uint_as_float(m), 1.0f / 7.0f));
         float s = __bfloat162float(sb);
         uint16_t bits = __bfloat16_as_ushort(sb);
@@ -96,8 +97,8 @@ __global__ void __launch_bounds__(kQThreads)
         else if (s < kTiny) s = 0.0f, bits = 0;
         scale[part][c] = s;
         inverse[part][c] = s == 0.0f ? 0.0f : __fdiv_rn(1.0f, s);
-        const int64_t g = (k0 + part * 32) / w.group, n = n0 + c;
-        if (part % per == 0 && k0 + part * 32 < w.K && n < w.nb() * 16) {
+        const int64_t g = (k0 + part * 32) >> w.group_log2, n = n0 + c;
+        if (part == first && k0 + part * 32 < w.K && n < w.nb() * 16) {
             uint16_t* p = w.scales + ((n / 16 * w.groups + g) * 8 + n % 8) * 2 + n % 16 / 8;
             if (GEMM_DBG_OK(p, w.scales, w.nb() * w.groups * 32, 2)) *p = bits;
         }
@@ -112,9 +113,15 @@ __global__ void __launch_bounds__(kQThreads)
     uint32_t mine[8];
     const int hi = c8 & 1, part = r / 8;
     bool tiny = false;
+    float s8[8], inv8[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+        *reinterpret_cast<float4*>(s8 + j) = *reinterpret_cast<const float4*>(&scale[part][8 * c8 + j]);
+        *reinterpret_cast<float4*>(inv8 + j) = *reinterpret_cast<const float4*>(&inverse[part][8 * c8 + j]);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float s = scale[part][8 * c8 + j], inv = inverse[part][8 * c8 + j];
+        const float s = s8[j], inv = inv8[j];
         const float2 i2 = make_float2(inv, inv), n2 = make_float2(-s, -s), to_nibble = make_float2(12582920.0f, 12582920.0f);   // 1.5 * 2^23 + 8
         float2 u[2];
 #pragma unroll
@@ -159,69 +166,102 @@ __global__ void __launch_bounds__(kQThreads)
 }
 
 // ---- dequantise --------------------------------------------------------------
-// A thread takes word 4t + j of each of a block's eight g -- four rows of all of
-// its 16 columns -- so that what it stores is a row's 16 neighbours, and eight
-// lanes' words are whole sectors.
-constexpr int kDRows = 256;     // of a CTA: a warp half a block of each of four, side by side
+// A warp takes 64 rows of eight blocks side by side.  Their words come in
+// 16-byte pieces and pass through shared memory, so that a thread gets word 4t +
+// j of each of a block's eight g: four rows of all of its 16 columns, and what
+// it stores is a row's 16 neighbours, a warp's 128.
+constexpr int kDWarps = 4, kDCols = 128, kDPad = 136;   // kDPad: words of a block in shared memory
+
+// 32 bytes at once (32-byte aligned).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kDWarps * 32)
     w4_dequantize_kernel(W4 w, T* __restrict__ B, int64_t ldb, bool vec) {
-    const int64_t across = (w.N + kQCols - 1) / kQCols;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, tj = warp % 2 * 8 + lane % 8;
-    const int64_t kb = blockIdx.x / across * (kDRows / 64) + warp / 2, nb = blockIdx.x % across * (kQCols / 16) + lane / 8;
-    if (nb >= w.nb() || kb >= w.kb) return;
-    const int64_t k = kb * 64 + 32 * (tj % 4 / 2) + 8 * (tj / 4) + 4 * (tj % 2), n = nb * 16;
-    if (k >= w.K) return;
-    const uint32_t* p = w.codes + (nb * w.kb + kb) * 128 + tj;
-    const uint16_t* sp = w.scales + (nb * w.groups + k / w.group) * 16;
-    if (!GEMM_DBG_OK(p, w.codes, w.nb() * w.kb * 512, 4) || !GEMM_DBG_OK(p + 112, w.codes, w.nb() * w.kb * 512, 4) ||
-        !GEMM_DBG_OK(sp, w.scales, w.nb() * w.groups * 32, 32))
-        return;
-    uint32_t words[8], scales[8];
+    __shared__ __align__(16) uint32_t s_words[kDWarps][kDCols / 16][kDPad];
+    __shared__ __align__(16) T s_rows[kDWarps][4][kDCols + 16 / sizeof(T)];   // where rows are not aligned
+    const unsigned across = (unsigned)((w.N + kDCols - 1) / kDCols);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t kb = (int64_t)(blockIdx.x / across) * kDWarps + warp, nb0 = (int64_t)(blockIdx.x % across) * (kDCols / 16);
+    if (kb >= w.kb) return;
+    uint4 piece[8] = {};
 #pragma unroll
-    for (int g = 0; g < 8; ++g) words[g] = __ldg(p + 16 * g);
-    {   // of columns g and g + 8 together
-        uint2 s2[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s2[i] = __ldg(reinterpret_cast<const uint2*>(sp) + i);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) scales[2 * i] = s2[i].x, scales[2 * i + 1] = s2[i].y;
+    for (int i = 0; i < 8; ++i) {
+        const uint4* p = reinterpret_cast<const uint4*>(w.codes + ((nb0 + i) * w.kb + kb) * 128) + lane;
+        if (nb0 + i < w.nb() && GEMM_DBG_OK(p, w.codes, w.nb() * w.kb * 512, 16)) piece[i] = __ldg(p);
     }
+    const int64_t nb = nb0 + lane / 4, n = nb * 16, n0 = nb0 * 16;
+    const int t = lane % 4;
+    uint32_t scales[2][8] = {};   // of columns g and g + 8 together, for both halves of the rows
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t k = kb * 64 + 32 * h;
+        const uint16_t* sp = w.scales + (nb * w.groups + (k >> w.group_log2)) * 16;
+        if (nb >= w.nb() || k >= w.K || !GEMM_DBG_OK(sp, w.scales, w.nb() * w.groups * 32, 32)) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint2 s2 = __ldg(reinterpret_cast<const uint2*>(sp) + i);
+            scales[h][2 * i] = s2.x, scales[h][2 * i + 1] = s2.y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(&s_words[warp][i][4 * lane]) = piece[i];
+    __syncwarp();
     [[maybe_unused]] const int64_t b_bytes = ((w.K - 1) * ldb + w.N) * (int64_t)sizeof(T);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (k + e >= w.K) break;
-        float2 v[2][4];
+    for (int j = 0; j < 4; ++j) {
+        const int h = j / 2;
+        uint32_t words[8];
 #pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-            const int shift = 4 * (4 * (e & 1) + 2 * (e >> 1) + hi);
-            auto one = [&](int g) { return __uint_as_float(((words[g] >> shift) & 15u) | 0x4B000000u); };
-            auto scale = [&](int g) { return __uint_as_float(hi ? scales[g] & 0xFFFF0000u : scales[g] << 16); };
+        for (int g = 0; g < 8; ++g) words[g] = s_words[warp][lane / 4][16 * g + 4 * t + j];
+        const int64_t k = kb * 64 + 32 * h + 8 * t + 4 * (j % 2);
+        T* to = B + k * ldb + n;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[hi][i] = __fmul2_rn(__fadd2_rn(make_float2(one(2 * i), one(2 * i + 1)), make_float2(-8388616.0f, -8388616.0f)),
-                                      make_float2(scale(2 * i), scale(2 * i + 1)));
-        }
-        T* to = B + (k + e) * ldb + n;
-        if (vec && n + 16 <= w.N) {
-            if (!GEMM_DBG_OK(to, B, b_bytes, 16 * sizeof(T))) continue;
+        for (int e = 0; e < 4; ++e, to += ldb) {
+            float2 v[8];   // columns 2i, 2i + 1
 #pragma unroll
             for (int hi = 0; hi < 2; ++hi) {
-                const float2* y = v[hi];
-                if constexpr (sizeof(T) == 4) {
-                    reinterpret_cast<float4*>(to)[2 * hi] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
-                    reinterpret_cast<float4*>(to)[2 * hi + 1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
-                } else {
-                    reinterpret_cast<uint4*>(to)[hi] = make_uint4(pack2<T>(y[0].x, y[0].y), pack2<T>(y[1].x, y[1].y),
-                                                                  pack2<T>(y[2].x, y[2].y), pack2<T>(y[3].x, y[3].y));
-                }
-            }
-        } else {
+                const int shift = 4 * (4 * (e & 1) + 2 * (e >> 1) + hi);
+                auto one = [&](int g) { return __uint_as_float(((words[g] >> shift) & 15u) | 0x4B000000u); };
+                auto scale = [&](int g) { return __uint_as_float(hi ? scales[h][g] & 0xFFFF0000u : scales[h][g] << 16); };
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const float2 y = v[c / 8][c % 8 / 2];
-                if (n + c < w.N && GEMM_DBG_OK(to + c, B, b_bytes, sizeof(T))) to[c] = from_float<T>(c & 1 ? y.y : y.x);
+                for (int i = 0; i < 4; ++i)
+                    v[4 * hi + i] = __fmul2_rn(__fadd2_rn(make_float2(one(2 * i), one(2 * i + 1)), make_float2(-8388616.0f, -8388616.0f)),
+                                               make_float2(scale(2 * i), scale(2 * i + 1)));
+            }
+            // the whole width in aligned pieces, or by way of shared memory
+            if (vec && n0 + kDCols <= w.N) {
+                if (k + e >= w.K || !GEMM_DBG_OK(to, B, b_bytes, 16 * sizeof(T))) continue;
+                uint32_t r[sizeof(T) == 4 ? 2 : 1][8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (sizeof(T) == 4) {
+                        r[i / 4][2 * i % 8] = __float_as_uint(v[i].x);
+                        r[i / 4][2 * i % 8 + 1] = __float_as_uint(v[i].y);
+                    } else {
+                        r[0][i] = pack2<T>(v[i].x, v[i].y);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(T) / 2; ++i) store32(reinterpret_cast<uint8_t*>(to) + 32 * i, r[i]);
+            } else {
+                T* row = s_rows[warp][t] + 16 * (lane / 4);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) row[2 * i] = from_float<T>(v[i].x), row[2 * i + 1] = from_float<T>(v[i].y);
+                __syncwarp();
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t kr = k - 8 * t + 8 * r + e;   // the row of the lanes with t = r
+                    T* out = B + kr * ldb + n0;
+#pragma unroll
+                    for (int c = lane; c < kDCols; c += 32)
+                        if (kr < w.K && n0 + c < w.N && GEMM_DBG_OK(out + c, B, b_bytes, sizeof(T))) out[c] = s_rows[warp][r][c];
+                }
+                __syncwarp();
             }
         }
     }
@@ -434,7 +474,7 @@ __global__ void __launch_bounds__(kPWarps * 32, resident(MT))
 W4 view(const void* codes, const void* scales, int64_t K, int64_t N, int group) {
     return W4{const_cast<uint32_t*>(static_cast<const uint32_t*>(codes)),
               const_cast<uint16_t*>(static_cast<const uint16_t*>(scales)), K, N, group,
-              (int)((K + 63) / 64), (int)((K + group - 1) / group)};
+              (int)((K + 63) / 64), (int)((K + group - 1) / group), group == 32 ? 5 : group == 64 ? 6 : 7};
 }
 
 template <typename T, typename U, int MT, int WN, bool HALF, bool VEC>
@@ -506,15 +546,15 @@ cudaError_t launch_w4_dequantize(const void* codes, const void* scales, int64_t 
                                  int group, void* B, int64_t ldb, ElemType type,
                                  cudaStream_t stream) {
     const W4 w = view(codes, scales, K, N, group);
-    const unsigned grid = (unsigned)(((K + kDRows - 1) / kDRows) * ((N + kQCols - 1) / kQCols));
+    const unsigned grid = (unsigned)(((K + kDWarps * 64 - 1) / (kDWarps * 64)) * ((N + kDCols - 1) / kDCols));
     const int64_t es = type == ElemType::kF32 ? 4 : 2;
-    const bool vec = (reinterpret_cast<uintptr_t>(B) & 15u) == 0 && ldb * es % 16 == 0;
+    const bool vec = (reinterpret_cast<uintptr_t>(B) & 31u) == 0 && ldb * es % 32 == 0;
     if (type == ElemType::kF32)
-        w4_dequantize_kernel<float><<<grid, kQThreads, 0, stream>>>(w, static_cast<float*>(B), ldb, vec);
+        w4_dequantize_kernel<float><<<grid, kDWarps * 32, 0, stream>>>(w, static_cast<float*>(B), ldb, vec);
     else if (type == ElemType::kBF16)
-        w4_dequantize_kernel<__nv_bfloat16><<<grid, kQThreads, 0, stream>>>(w, static_cast<__nv_bfloat16*>(B), ldb, vec);
+        w4_dequantize_kernel<__nv_bfloat16><<<grid, kDWarps * 32, 0, stream>>>(w, static_cast<__nv_bfloat16*>(B), ldb, vec);
     else
-        w4_dequantize_kernel<__half><<<grid, kQThreads, 0, stream>>>(w, static_cast<__half*>(B), ldb, vec);
+        w4_dequantize_kernel<__half><<<grid, kDWarps * 32, 0, stream>>>(w, static_cast<__half*>(B), ldb, vec);
     return cudaGetLastError();
 }
 
