@@ -141,17 +141,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
             if (++stage == R::kStages) stage = 0, phase ^= 1u;
         }
         // Copies in flight land before the CTA may leave or reuse the ring.
-        for (int s = max(0, issued - R::kStages); s < issued; ++s) {
-            if (lane == 0) {
-                const uint32_t bar = bars + 8 * (s % R::kStages), parity = (uint32_t)(s / R::kStages) & 1u;
-                const uint64_t t0 = global_ns();
-                while (!mbar_try_wait(bar, parity))
-                    if (global_ns() - t0 > kWaitLimitNs) {
-                        atomicOr(a.err, kErrTimeout);
-                        break;
-                    }
-            }
-        }
+        if (lane == 0)
+            for (int s = max(0, issued - R::kStages); s < issued; ++s) drain(bars + 8 * (s % R::kStages), (uint32_t)(s / R::kStages) & 1u, a.err);
         __syncwarp();
         __syncthreads();   // the ring is free
         __syncthreads();   // the warps' results are in it

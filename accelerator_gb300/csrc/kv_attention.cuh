@@ -11,35 +11,11 @@ constexpr float kNegInf = -INFINITY, kLowest = -3.402823466e38f;
 // Weights enter the second product as binary16 times 2^15, under 2^16: the
 // maximum that they are relative to may lag behind by this much (in log2).
 constexpr float kPScale = 32768.0f, kLag = 0.9f;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// A whole warp waits, and goes on or gives up together.  One lane looks: an
-// arrival or a look by every lane is 32 operations on one word.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
-    return __any_sync(0xFFFFFFFFu, threadIdx.x % 32 == 0 && mbar_wait(bar, parity, abort_flag, err, kWaitLimitNs));
-}
-// Arrives once for a whole warp, after all its lanes' accesses.
-__device__ __forceinline__ void warp_arrive(uint32_t bar) {
-    __syncwarp();
-    if (threadIdx.x % 32 == 0) mbar_arrive(bar);
-}
-
-// Untiled bulk copy into this CTA's shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
 }
 
 struct AttnArgs {

@@ -56,8 +56,9 @@ struct Smem {
     static constexpr int kBytes = kBars + 256 + 1024;        // and the alignment
 };
 // Barriers: keys and values full / empty (two buffers), per tile scores full,
-// weights full, output done; codes full / empty (keys, values); the drain.
-enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kODone = 12, kCFull = 14, kCEmpty = 16, kDrain = 18 };
+// weights full (of the first and of the last 64 tokens), output done; codes
+// full / empty (keys, values); the drain.
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kODone = 14, kCFull = 16, kCEmpty = 18, kDrain = 20 };
 
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -142,7 +143,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             mbar_init(bars + 8 * (kKEmpty + i), 1);
             mbar_init(bars + 8 * (kVEmpty + i), 1);
             mbar_init(bars + 8 * (kSFull + i), 2);   // the matrix unit, and its issuer for the page data
-            mbar_init(bars + 8 * (kPFull + i), kTile / 32);
+            mbar_init(bars + 8 * (kPFull + 2 * i), kTile / 32);
+            mbar_init(bars + 8 * (kPFull + 2 * i + 1), kTile / 32);
             mbar_init(bars + 8 * (kODone + i), 1);
             mbar_init(bars + 8 * (kCFull + i), 1);
             mbar_init(bars + 8 * (kCEmpty + i), kCacheWarps);
@@ -283,13 +285,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                 const int buf = j & 1;
                 ok = mbar_wait(bars + 8 * (kVFull + buf), (uint32_t)(j >> 1) & 1u, abort_flag, a.err, kWaitLimitNs);
                 for (int i = 0; ok && i < tiles; ++i) {
-                    if (!(ok = mbar_wait(bars + 8 * (kPFull + i), (uint32_t)j & 1u, abort_flag, a.err, kWaitLimitNs))) break;
-                    tc_fence_after();
                     const uint32_t v = base + L::kV + buf * L::kOperand;
+                    // O_i += P_i V, each half as soon as its weights are there
+                    for (int half = 0; ok && half < 2; ++half) {
+                        if (!(ok = mbar_wait(bars + 8 * (kPFull + 2 * i + half), (uint32_t)j & 1u, abort_flag, a.err, kWaitLimitNs))) break;
+                        tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < kStep / 16; ++kk)   // O_i += P_i V
-                        tc_mma_ts(tmem + 2 * kStep + i * kStep, tmem + i * kStep + kk * 8,
-                                  smem_desc_sw128(v + kk * 16 * 128, kSlab, 1024), kIdO, (j | kk) != 0);
+                        for (int k = 0; k < kStep / 32; ++k) {
+                            const int kk = half * (kStep / 32) + k;
+                            tc_mma_ts(tmem + 2 * kStep + i * kStep, tmem + i * kStep + kk * 8,
+                                      smem_desc_sw128(v + kk * 16 * 128, kSlab, 1024), kIdO, (j | kk) != 0);
+                        }
+                    }
+                    if (!ok) break;
                     tc_commit(bars + 8 * (kODone + i));
                     if (i == tiles - 1) tc_commit(bars + 8 * (kVEmpty + buf));
                     if (j + 1 < blocks) {
@@ -302,12 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             }
             // Everything issued is done before tensor memory is freed.
             tc_commit(bars + 8 * kDrain);
-            const uint64_t t0 = global_ns();
-            while (!mbar_try_wait(bars + 8 * kDrain, 0))
-                if (global_ns() - t0 > kWaitLimitNs) {
-                    atomicOr(a.err, kErrTimeout);
-                    break;
-                }
+            drain(bars + 8 * kDrain, 0, a.err);
         }
         if (warp == kSoftWarps + kCacheWarps + 1) {
             // ---------------- the copies: lane i < 8 looks after 16 tokens of a block ----------------
@@ -364,12 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             }
             // Copies in flight land before the CTA may leave.
             if (lane < 2 && issued[lane] > 0) {
-                const uint64_t t0 = global_ns();
-                while (!mbar_try_wait(bars + 8 * (kCFull + lane), (uint32_t)(issued[lane] - 1) & 1u))
-                    if (global_ns() - t0 > kWaitLimitNs) {
-                        atomicOr(a.err, kErrTimeout);
-                        break;
-                    }
+                drain(bars + 8 * (kCFull + lane), (uint32_t)(issued[lane] - 1) & 1u, a.err);
             }
         }
         __syncwarp();
@@ -391,48 +389,56 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             const PageData* page = info + j % kSlots * kSubs;
             const int tok = tok_begin + j * kStep;
             uint32_t v[4][32];   // the row's scores, all in registers
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_at + 32 * c, v[c]);
+            tmem_ld_32x32b_x32(s_at, v[0]);
+            tmem_ld_32x32b_x32(s_at + 32, v[1]);
             uint32_t plain = 1;
 #pragma unroll
             for (int b = 0; b < kSubs; ++b) plain &= page[b].plain;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_wait_for(v[c]);
-            if (tok < full_lo || tok + kStep > full_hi) {   // hidden tokens: -inf
-                const int first_seen = lo - tok, end_seen = hi - tok;
-#pragma unroll
-                for (int e = 0; e < kStep; ++e)
-                    if (e < first_seen || e >= end_seen) v[e / 32][e % 32] = 0xFF800000u;
-                asm volatile("");
-            }
-            if (!(plain & 1u)) {   // pages that are not there: hidden; that read as NaN: NaN, where seen
-#pragma unroll
-                for (int b = 0; b < kSubs; ++b) {
-                    const uint32_t kind = page[b].plain;
-                    if (kind == 1u) continue;
-#pragma unroll
-                    for (int e = 0; e < kSub; ++e) {
-                        uint32_t& x = v[b / 2][b % 2 * 16 + e];
-                        if (kind == 2u) x = 0xFF800000u;
-                        else if (x != 0xFF800000u) x = 0x7FC00000u;
-                    }
-                }
-                asm volatile("");
-            }
             // Factors stay above 0, so that -inf times one stays that; a NaN
             // scale's tokens are NaN or -inf already.
             auto factor = [&](int b) {
                 const float f = row_scale * page[b].ks;
                 return f >= 1.1754943508222875e-38f ? f : 1.1754943508222875e-38f;
             };
+            const bool hidden = tok < full_lo || tok + kStep > full_hi;
+            const int first_seen = lo - tok, end_seen = hi - tok;
             float top = kLowest;
 #pragma unroll
-            for (int b = 0; b < kSubs; ++b) {
-                const uint32_t* x = &v[b / 2][b % 2 * 16];
-                auto at = [&](int e) { return __uint_as_float(x[e]); };
-                const float t0 = max3(max3(at(0), at(1), at(2)), at(3), at(4)), t1 = max3(max3(at(5), at(6), at(7)), at(8), at(9));
-                const float t2 = max3(max3(at(10), at(11), at(12)), at(13), at(14));
-                top = fmaxf(top, max3(max3(t0, t1, t2), at(15), at(15)) * factor(b));
+            for (int half = 0; half < 2; ++half) {   // the second half loads meanwhile
+                tmem_ld_wait_for(v[2 * half]);
+                tmem_ld_wait_for(v[2 * half + 1]);
+                if (half == 0) {
+                    tmem_ld_32x32b_x32(s_at + 64, v[2]);
+                    tmem_ld_32x32b_x32(s_at + 96, v[3]);
+                }
+                if (hidden) {   // hidden tokens: -inf
+#pragma unroll
+                    for (int e = 64 * half; e < 64 * half + 64; ++e)
+                        if (e < first_seen || e >= end_seen) v[e / 32][e % 32] = 0xFF800000u;
+                    asm volatile("");
+                }
+                if (!(plain & 1u)) {   // pages that are not there: hidden; that read as NaN: NaN, where seen
+#pragma unroll
+                    for (int b = 4 * half; b < 4 * half + 4; ++b) {
+                        const uint32_t kind = page[b].plain;
+                        if (kind == 1u) continue;
+#pragma unroll
+                        for (int e = 0; e < kSub; ++e) {
+                            uint32_t& x = v[b / 2][b % 2 * 16 + e];
+                            if (kind == 2u) x = 0xFF800000u;
+                            else if (x != 0xFF800000u) x = 0x7FC00000u;
+                        }
+                    }
+                    asm volatile("");
+                }
+#pragma unroll
+                for (int b = 4 * half; b < 4 * half + 4; ++b) {
+                    const uint32_t* x = &v[b / 2][b % 2 * 16];
+                    auto at = [&](int e) { return __uint_as_float(x[e]); };
+                    const float t0 = max3(max3(at(0), at(1), at(2)), at(3), at(4)), t1 = max3(max3(at(5), at(6), at(7)), at(8), at(9));
+                    const float t2 = max3(max3(at(10), at(11), at(12)), at(13), at(14));
+                    top = fmaxf(top, max3(max3(t0, t1, t2), at(15), at(15)) * factor(b));
+                }
             }
             // The sums so far are brought to a new maximum only when it is passed.
             if (__any_sync(0xFFFFFFFFu, top > m + kLag)) {
@@ -479,11 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                     sum[b] = fmaf(s2.x + s2.y, pd.inv_v, sum[b]);
                 }
                 tmem_st_x16(s_at + 16 * c, p);   // over scores that are in registers
+                if (c & 1) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    warp_arrive(bars + 8 * (kPFull + 2 * which + c / 2));
+                }
             }
             l += sum[0] + sum[1];
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(bars + 8 * (kPFull + which));
         }
         if (ok && blocks > 0) ok = warp_wait(bars + 8 * (kODone + which), (uint32_t)(blocks - 1) & 1u, abort_flag, a.err);
         tc_fence_after();

@@ -74,6 +74,46 @@ __device__ __forceinline__ void mma_16816<__nv_bfloat16>(float (&d)[4], uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+constexpr uint64_t kWaitLimitNs = 2000000000ull;   // of any single wait
+
+// A whole warp waits, and goes on or gives up together.  One lane looks: an
+// arrival or a look by every lane is 32 operations on one word.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+    return __any_sync(0xFFFFFFFFu, threadIdx.x % 32 == 0 && mbar_wait(bar, parity, abort_flag, err, kWaitLimitNs));
+}
+// Arrives once for a whole warp, after all its lanes' accesses.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(bar);
+}
+
+// Untiled bulk copy into this CTA's shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+// Waits for copies of this thread to land, whatever the other roles do.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, unsigned* err) {
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, kErrTimeout);
+            break;
+        }
+}
+
 // Two code bytes u = c + 128 beside a byte 0x64 each are the binary16 values
 // 1024 + u; less 1152 they are c, exactly.
 __device__ __forceinline__ uint32_t halves_from_biased(uint32_t x) {

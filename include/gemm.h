@@ -295,7 +295,7 @@ GEMM_API int gemm_w4_sizes(int64_t K, int64_t N, int group, int64_t* code_bytes,
  * product with the binary32 1 / 7), rounded to bfloat16, q = b / s rounded to the nearest integer (ties to even) and held to
  * [-7, 7].  A group whose s is under 2^-126 becomes zeros; one that holds a
  * NaN or an infinity gets s = NaN, so that every product with it is NaN.
- * codes: 16-byte aligned; scales: 4-byte aligned.
+ * codes: 16-byte aligned, scales 4-byte aligned, here and below.
  */
 GEMM_API int gemm_w4_quantize(const void* B, int64_t ldb, int type, int64_t K, int64_t N,
                               int group, void* codes, void* scales, struct CUstream_st* stream);
@@ -308,7 +308,7 @@ GEMM_API int gemm_w4_dequantize(const void* codes, const void* scales, int64_t K
 /*
  * C = X*W.  X: M x K, row stride ldx elements, bfloat16 or binary16
  * (x_type); C: M x N, row stride ldc, of x_type or float (c_type),
- * overwritten, not overlapping the inputs.  Made for few rows: up to 8 rows
+ * overwritten, not overlapping the inputs.  Made for few rows: up to 32 rows
  * read W once, and each further 32 read it again.  Products q * x are exact,
  * summed in binary32 over a group (or a part of one) and scaled there; C is
  * rounded once.  The order of the sums depends on the sizes alone.  K == 0
