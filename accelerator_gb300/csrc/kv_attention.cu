@@ -426,8 +426,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                 ml[0] = top, ml[1] = sum;
             }
         } else {
-            part[i] = acc;
-            if (d == 0) part[kRows * D + 2 * r] = top, part[kRows * D + 2 * r + 1] = sum;
+            if (GEMM_DBG_OK(part + i, a.partial, a.partial_bytes, 4)) part[i] = acc;
+            if (d == 0 && GEMM_DBG_OK(part + kRows * D + 2 * r, a.partial, a.partial_bytes, 8))
+                part[kRows * D + 2 * r] = top, part[kRows * D + 2 * r + 1] = sum;
         }
     }
     if (!cluster) return;
@@ -472,6 +473,7 @@ __global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a, int ro
     const int64_t slot = (int64_t)rows * (D + 2);
     const float* part = a.partial + ((int64_t)u * a.c.heads + h) * a.splits * slot;
     const float* ml = part + rows * D + 2 * r;
+    if (!GEMM_DBG_OK(ml + (tile.active - 1) * slot, a.partial, a.partial_bytes, 8)) return;
     float top = kLowest;
     for (int s = threadIdx.x % 32; s < tile.active; s += 32) top = fmaxf(top, ml[s * slot]);
 #pragma unroll
@@ -607,7 +609,7 @@ cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& 
                                 unsigned* err, int* launches, cudaStream_t stream) {
     const bool q_vec = (reinterpret_cast<uintptr_t>(Q.p) & 15u) == 0 && Q.row % 8 == 0 && Q.head % 8 == 0;
     const AttnArgs a{c, Q, O, b, q_heads, (unsigned)(q_heads / c.heads), plan.gap, scale * 1.44269504088896341f, causal,
-                     (int)(window < INT32_MAX ? window : INT32_MAX), plan.splits, q_vec, static_cast<float*>(scratch), err};
+                     (int)(window < INT32_MAX ? window : INT32_MAX), plan.splits, q_vec, plan.scratch_bytes, static_cast<float*>(scratch), err};
     if (type == ElemType::kBF16)
         return c.dim == 128 ? launch<__nv_bfloat16, 128>(a, plan, launches, stream)
                             : launch<__nv_bfloat16, 64>(a, plan, launches, stream);

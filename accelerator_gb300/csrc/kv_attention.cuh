@@ -30,6 +30,7 @@ struct AttnArgs {
     int window;
     int splits;                  // CTAs that share a tile's tokens: a cluster, or with `partial` any number
     bool q_vec;                  // Q in 16-byte loads
+    int64_t partial_bytes;
     float* partial;              // [unit][head][split] x (rows x dim sums, then rows x (max, sum))
     unsigned* err;
 };

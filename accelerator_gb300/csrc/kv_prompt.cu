@@ -514,7 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                 } else if (!whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4*>(part + (int64_t)threadIdx.x * D + 32 * c + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        if (GEMM_DBG_OK(part + (int64_t)threadIdx.x * D + 32 * c + e, a.partial, a.partial_bytes, 16))
+                            *reinterpret_cast<float4*>(part + (int64_t)threadIdx.x * D + 32 * c + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
                 } else if (o_vec) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                 }
                 __syncwarp();
             }
-            if (live && !whole) {
+            if (live && !whole && GEMM_DBG_OK(part + (int64_t)kRows * D + 2 * threadIdx.x, a.partial, a.partial_bytes, 8)) {
                 part[(int64_t)kRows * D + 2 * threadIdx.x] = m;
                 part[(int64_t)kRows * D + 2 * threadIdx.x + 1] = l;
             }
