@@ -301,6 +301,21 @@ __device__ __forceinline__ void unpack8<__nv_bfloat16>(uint32_t w, uint32_t (&a)
     }
 }
 
+// Eight neighbours of one row of X as four pairs, where rows are aligned to 8, 4 or 2 bytes.
+template <typename T>
+__device__ __forceinline__ uint4 load_x8(const T* p, int align) {
+    if (align == 8) {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(p)), b = __ldg(reinterpret_cast<const uint2*>(p) + 1);
+        return make_uint4(a.x, a.y, b.x, b.y);
+    }
+    if (align == 4) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+        return make_uint4(__ldg(q), __ldg(q + 1), __ldg(q + 2), __ldg(q + 3));
+    }
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+    auto two = [&](int e) { return (uint32_t)__ldg(q + e) | (uint32_t)__ldg(q + e + 1) << 16; };
+    return make_uint4(two(0), two(2), two(4), two(6));
+}
 // Eight neighbours x[k .. k + 7] of one row of X as four pairs; 0 past K.
 template <typename T>
 __device__ __noinline__ uint4 load_x8_edge(const T* row, int k, int K) {
@@ -328,10 +343,10 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 // WK-th block of 32 columns (two blocks of 16, so that a part of X that is
 // loaded serves both).  The sums are added up over the warps, then over the
 // cluster's CTAs through distributed shared memory, always in that order.
-template <typename T, typename U, int MT, int WN, bool HALF, bool VEC>
+template <typename T, typename U, int MT, int WN, bool HALF>
 __global__ void __launch_bounds__(kPWarps * 32, resident(MT))
     w4_gemm_kernel(const T* __restrict__ X, int64_t ldx, W4 w, U* __restrict__ C, int64_t ldc,
-                   int64_t M, int splits, int64_t tiles_n) {
+                   int64_t M, int splits, int64_t tiles_n, int align) {
     constexpr int WK = kPWarps / WN, kCols = 32 * WN, kRows = 8 * MT;
     __shared__ float part[WK][kRows][kCols + 4];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -377,13 +392,21 @@ __global__ void __launch_bounds__(kPWarps * 32, resident(MT))
     uint4 x[kX][2][MT];
     auto fetch_x = [&](int slot, int kb) {
         kb = min(kb, kb1 - 1);
-        if (VEC && kb * 64 + 64 <= K) {
+        if (align == 16 && kb * 64 + 64 <= K) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const T* p = rows[m] + kb * 64 + 32 * h;
                     if (GEMM_DBG_OK(p, X, x_bytes, 16)) x[slot][h][m] = __ldg(reinterpret_cast<const uint4*>(p));
+                }
+        } else if (kb * 64 + 64 <= K) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const T* p = rows[m] + kb * 64 + 32 * h;
+                    if (GEMM_DBG_OK(p, X, x_bytes, 16)) x[slot][h][m] = load_x8(p, align);
                 }
         } else {
 #pragma unroll
@@ -477,9 +500,9 @@ W4 view(const void* codes, const void* scales, int64_t K, int64_t N, int group) 
               (int)((K + 63) / 64), (int)((K + group - 1) / group), group == 32 ? 5 : group == 64 ? 6 : 7};
 }
 
-template <typename T, typename U, int MT, int WN, bool HALF, bool VEC>
+template <typename T, typename U, int MT, int WN, bool HALF>
 cudaError_t launch_product(const T* X, int64_t ldx, const W4& w, U* C, int64_t ldc, int64_t M,
-                           int num_sms, cudaStream_t stream) {
+                           int align, int num_sms, cudaStream_t stream) {
     constexpr int WK = kPWarps / WN;
     const int64_t tiles_n = (w.nb() + 2 * WN - 1) / (2 * WN), tiles = tiles_n * ((M + 8 * MT - 1) / (8 * MT));
     // The blocks of rows are shared over a cluster of the size for which the
@@ -503,18 +526,18 @@ cudaError_t launch_product(const T* X, int64_t ldx, const W4& w, U* C, int64_t l
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, w4_gemm_kernel<T, U, MT, WN, HALF, VEC>, X, ldx, w, C, ldc, M, splits, tiles_n);
+    return cudaLaunchKernelEx(&cfg, w4_gemm_kernel<T, U, MT, WN, HALF>, X, ldx, w, C, ldc, M, splits, tiles_n, align);
 }
 
 // More rows go with more columns to a CTA: X is read once for every tile of
 // columns, 2 * rows bytes beside each column's half byte of codes.
-template <typename T, typename U, bool VEC>
+template <typename T, typename U>
 cudaError_t launch_by_rows(const T* X, int64_t ldx, const W4& w, U* C, int64_t ldc, int64_t M,
-                           int num_sms, cudaStream_t stream) {
+                           int align, int num_sms, cudaStream_t stream) {
     auto go = [&](auto mt, auto wn) {
         constexpr int MT = decltype(mt)::value, WN = decltype(wn)::value;
-        return w.group == 32 ? launch_product<T, U, MT, WN, true, VEC>(X, ldx, w, C, ldc, M, num_sms, stream)
-                             : launch_product<T, U, MT, WN, false, VEC>(X, ldx, w, C, ldc, M, num_sms, stream);
+        return w.group == 32 ? launch_product<T, U, MT, WN, true>(X, ldx, w, C, ldc, M, align, num_sms, stream)
+                             : launch_product<T, U, MT, WN, false>(X, ldx, w, C, ldc, M, align, num_sms, stream);
     };
     using std::integral_constant;
     if (M <= 2) return go(integral_constant<int, 1>(), integral_constant<int, 1>());
@@ -562,12 +585,13 @@ cudaError_t launch_w4_gemm(const void* X, int64_t ldx, ElemType x_type, const vo
                            const void* scales, void* C, int64_t ldc, ElemType c_type, int64_t M,
                            int64_t K, int64_t N, int group, int num_sms, cudaStream_t stream) {
     const W4 w = view(codes, scales, K, N, group);
-    const bool vec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && (ldx % 8 == 0 || M == 1);
+    // the widest loads that every row of X allows, in bytes
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(X) | (M > 1 ? (uintptr_t)ldx * 2 : 0);
+    const int align = (bits & 15u) == 0 ? 16 : (bits & 7u) == 0 ? 8 : (bits & 3u) == 0 ? 4 : 2;
     auto go = [&](auto x, auto c) {
         using T = decltype(x);
         using U = decltype(c);
-        return vec ? launch_by_rows<T, U, true>(static_cast<const T*>(X), ldx, w, static_cast<U*>(C), ldc, M, num_sms, stream)
-                   : launch_by_rows<T, U, false>(static_cast<const T*>(X), ldx, w, static_cast<U*>(C), ldc, M, num_sms, stream);
+        return launch_by_rows<T, U>(static_cast<const T*>(X), ldx, w, static_cast<U*>(C), ldc, M, align, num_sms, stream);
     };
     if (x_type == ElemType::kBF16)
         return c_type == ElemType::kF32 ? go(__nv_bfloat16(), float()) : go(__nv_bfloat16(), __nv_bfloat16());

@@ -71,7 +71,7 @@ class W4Matrix:
     """A K x N matrix in 4 bits: the packed codes (uint8), the scales
     (bfloat16), its sizes and the group length.  Layout: include/gemm.h."""
 
-    __slots__ = ("codes", "scales", "K", "N", "group", "index", "_codes", "_scales")
+    __slots__ = ("_codes", "_scales", "K", "N", "group", "index", "device", "_code_ptr", "_scale_ptr")
 
     def __init__(self, codes, scales, K, N, group):
         code_bytes, scale_bytes = w4_sizes(K, N, group)
@@ -82,26 +82,35 @@ class W4Matrix:
               f"a contiguous CUDA bfloat16 tensor of {scale_bytes // 2} elements")
         if codes.device != scales.device:
             raise TypeError("codes and scales must be on one device")
-        self._set(codes, scales, K, N, group)
+        self._codes, self._scales, self.K, self.N, self.group = codes, scales, int(K), int(N), int(group)
+        self.index, self.device = codes.get_device(), codes.device
+        self._code_ptr, self._scale_ptr = codes.data_ptr() or None, scales.data_ptr() or None
 
-    def _set(self, codes, scales, K, N, group):
-        self.codes, self.scales, self.K, self.N, self.group = codes, scales, int(K), int(N), int(group)
-        self.index = codes.get_device()
-        self._codes, self._scales = codes.data_ptr() or None, scales.data_ptr() or None
-        return self
+    @classmethod
+    def _in(cls, both, code_bytes, K, N, group):
+        """Codes and scales one after the other in the bytes of `both`."""
+        W = cls.__new__(cls)
+        W._codes, W._scales, W.K, W.N, W.group = both, code_bytes, K, N, group
+        W.index, W.device = both.get_device(), both.device
+        at = both.data_ptr()
+        W._code_ptr, W._scale_ptr = at or None, at + code_bytes if at else None
+        return W
 
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self):
+        return self._codes[:self._scales] if isinstance(self._scales, int) else self._codes
+
+    @property
+    def scales(self):
+        return self._codes[self._scales:].view(_BF16) if isinstance(self._scales, int) else self._scales
 
 
 def w4_sizes(K: int, N: int, group: int):
     """(bytes of the codes, bytes of the scales) of a K x N matrix."""
-    a, b = ctypes.c_int64(), ctypes.c_int64()
-    rc = binding.lib().gemm_w4_sizes(K, N, group, ctypes.byref(a), ctypes.byref(b))
-    if rc != binding.OK:
-        raise GemmError(rc, "gemm_w4_sizes")
-    return a.value, b.value
+    if group not in GROUPS or K < 0 or N < 0:
+        raise GemmError(binding.ERR_INVALID_ARG, "gemm_w4_sizes")
+    blocks = -(-N // 16)
+    return blocks * -(-K // 64) * 512, blocks * -(-K // group) * 32
 
 
 def w4_quantize(B, group=128, stream=None) -> W4Matrix:
@@ -113,11 +122,8 @@ def w4_quantize(B, group=128, stream=None) -> W4Matrix:
         raise TypeError("B must be float32, bfloat16 or float16")
     K, N = B.shape
     code_bytes, scale_bytes = w4_sizes(K, N, group)
-    device = B.device
-    codes = _empty(code_bytes, torch.uint8, device, stream)
-    scales = _empty(scale_bytes // 2, _BF16, device, stream)
-    W = W4Matrix.__new__(W4Matrix)._set(codes, scales, K, N, group)
-    rc = binding.lib().gemm_w4_quantize(B.data_ptr() or None, ldb, kind, K, N, group, W._codes, W._scales,
+    W = W4Matrix._in(_empty(code_bytes + scale_bytes, torch.uint8, B.device, stream), code_bytes, K, N, group)
+    rc = binding.lib().gemm_w4_quantize(B.data_ptr() or None, ldb, kind, K, N, group, W._code_ptr, W._scale_ptr,
                                         _stream(stream, W.index))
     if rc:
         raise GemmError(rc, "gemm_w4_quantize")
@@ -129,7 +135,7 @@ def w4_dequantize(W: W4Matrix, out=None, dtype=torch.bfloat16, stream=None):
     into `out`)."""
     K, N = W.K, W.N
     if out is None:
-        out = _empty((K, N), dtype, W.codes.device, stream)
+        out = _empty((K, N), dtype, W.device, stream)
         ldb = N
     else:
         ldb, dtype = _rows2(out, "out"), out.dtype
@@ -139,7 +145,7 @@ def w4_dequantize(W: W4Matrix, out=None, dtype=torch.bfloat16, stream=None):
     kind = _TYPES.get(dtype)
     if kind is None:
         raise TypeError("out must be float32, bfloat16 or float16")
-    rc = binding.lib().gemm_w4_dequantize(W._codes, W._scales, K, N, W.group, out.data_ptr() or None, ldb, kind,
+    rc = binding.lib().gemm_w4_dequantize(W._code_ptr, W._scale_ptr, K, N, W.group, out.data_ptr() or None, ldb, kind,
                                           _stream(stream, W.index))
     if rc:
         raise GemmError(rc, "gemm_w4_dequantize")
@@ -170,7 +176,7 @@ def gemm_w4(X, W: W4Matrix, C=None, dtype=None, stream=None):
             raise ValueError(f"C has shape {tuple(C.shape)}, not {(M, N)}")
     if ct is not xt and ct is not _F32:
         raise TypeError("C must be of X's type or float32")
-    rc = binding.lib().gemm_w4(X.data_ptr() or None, ldx, _TYPES[xt], W._codes, W._scales, C.data_ptr() or None, ldc,
+    rc = binding.lib().gemm_w4(X.data_ptr() or None, ldx, _TYPES[xt], W._code_ptr, W._scale_ptr, C.data_ptr() or None, ldc,
                                _TYPES[ct], M, K, N, W.group, _stream(stream, index))
     if rc:
         raise GemmError(rc, "gemm_w4")

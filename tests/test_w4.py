@@ -242,6 +242,10 @@ def test_sizes(libgemm):
     assert f(65, 17, 64, ctypes.byref(a), ctypes.byref(b)) == libgemm.OK
     assert (a.value, b.value) == (2 * 2 * 512, 2 * 2 * 32)
     assert f(0, 17, 64, ctypes.byref(a), ctypes.byref(b)) == libgemm.OK and (a.value, b.value) == (0, 0)
+    from accelerator_gb300 import lowbit
+    for K, N, group in ((0, 5, 32), (5, 0, 64), (1, 1, 128), (64, 16, 32), (1000, 333, 64), (8192, 8191, 128), (129, 17, 128)):
+        assert f(K, N, group, ctypes.byref(a), ctypes.byref(b)) == libgemm.OK
+        assert lowbit.w4_sizes(K, N, group) == (a.value, b.value)
     for args in ((-1, 4, 32), (4, -1, 32), (4, 4, 16), (1 << 31, 4, 32), (1 << 30, 1 << 30, 32)):
         assert f(*args, ctypes.byref(a), ctypes.byref(b)) == libgemm.ERR_INVALID_ARG
     assert f(4, 4, 32, None, ctypes.byref(b)) == libgemm.ERR_INVALID_ARG
