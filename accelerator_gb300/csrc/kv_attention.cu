@@ -461,41 +461,65 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
     cluster_sync();   // no CTA leaves while another reads its results
 }
 
-// Joins the splits of one row of a tile, in order: four threads share an
-// output element's splits.
-template <typename T, int D>
+// Joins the splits of a tile's rows, in order.  A block of 4 * D threads takes
+// 4 * D / (LANES * GROUPS) rows; GROUPS teams of LANES threads share a row's
+// splits: one row and four teams where rows are few and splits many, a warp to
+// a row where it is the other way.
+template <typename T, int D, int LANES, int GROUPS>
 __global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a, int rows, int step) {
-    __shared__ float s_acc[4][D], s_sum[4];
-    const int u = blockIdx.x, h = blockIdx.y, r = blockIdx.z, d = threadIdx.x % D, q = threadIdx.x / D;
+    constexpr int kEach = D / LANES, kAtOnce = 4 * D / (LANES * GROUPS);   // elements of a thread, rows of a block
+    __shared__ float s_acc[GROUPS][kAtOnce][D], s_sum[GROUPS][kAtOnce];
+    const int u = blockIdx.x, h = blockIdx.y;
+    const int lane = threadIdx.x % LANES, q = threadIdx.x / LANES % GROUPS, mine = threadIdx.x / (LANES * GROUPS);
     Tile tile;
-    if (!tile.find(a, u, rows, step, false) || tile.active == 1 || tile.r0 + r >= tile.nrows) return;
+    const bool found = tile.find(a, u, rows, step, false);
     grid_dependency_wait();   // launched while the partial results are still being made
+    if (!found || tile.active == 1) return;
     const int64_t slot = (int64_t)rows * (D + 2);
     const float* part = a.partial + ((int64_t)u * a.c.heads + h) * a.splits * slot;
-    const float* ml = part + rows * D + 2 * r;
-    if (!GEMM_DBG_OK(ml + (tile.active - 1) * slot, a.partial, a.partial_bytes, 8)) return;
-    float top = kLowest;
-    for (int s = threadIdx.x % 32; s < tile.active; s += 32) top = fmaxf(top, ml[s * slot]);
+    const int share = (tile.active + GROUPS - 1) / GROUPS, end = min(tile.active, (q + 1) * share);
+    const int r = blockIdx.z * kAtOnce + mine;
+    const bool live = tile.r0 + r < tile.nrows;
+    float sum = 0.0f, acc[kEach] = {};
+    if (live) {
+        const float* ml = part + rows * D + 2 * r;
+        float top = kLowest;
+        for (int s = threadIdx.x % 32; s < tile.active; s += 32)
+            if (GEMM_DBG_OK(ml + s * slot, a.partial, a.partial_bytes, 8)) top = fmaxf(top, ml[s * slot]);
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-    const int share = (tile.active + 3) / 4, end = min(tile.active, (q + 1) * share);
-    float sum = 0.0f, acc = 0.0f;
+        for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));   // a warp has one row
 #pragma unroll 4
-    for (int s = q * share; s < end; ++s) {
-        const float f = exp2_approx(ml[s * slot] - top);
-        sum = fmaf(f, ml[s * slot + 1], sum);
-        acc = fmaf(f, part[s * slot + r * D + d], acc);
+        for (int s = q * share; s < end; ++s) {
+            const float f = exp2_approx(ml[s * slot] - top);
+            sum = fmaf(f, ml[s * slot + 1], sum);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) acc[e] = fmaf(f, part[s * slot + r * D + lane + e * LANES], acc[e]);
+        }
     }
-    s_acc[q][d] = acc;
-    if (d == 0) s_sum[q] = sum;
-    __syncthreads();
-    if (q != 0) return;
+    if constexpr (GROUPS > 1) {
+        if (live) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) s_acc[q][mine][lane + e * LANES] = acc[e];
+            if (lane == 0) s_sum[q][mine] = sum;
+        }
+        __syncthreads();
+        if (q != 0) return;
+        if (live) {
+#pragma unroll
+            for (int g = 1; g < GROUPS; ++g) {
+                sum += s_sum[g][mine];
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) acc[e] += s_acc[g][mine][lane + e * LANES];
+            }
+        }
+    }
+    if (!live) return;
     [[maybe_unused]] const int64_t o_bytes =
         ((a.b.rows - 1) * a.O.row + (a.q_heads - 1) * a.O.head + D) * (int64_t)sizeof(T);
-    acc = ((s_acc[0][d] + s_acc[1][d]) + s_acc[2][d]) + s_acc[3][d];
-    sum = ((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3];
-    T* dst = out_row<T>(a, tile, h, tile.r0 + r) + d;
-    if (GEMM_DBG_OK(dst, a.O.p, o_bytes, sizeof(T))) *dst = from_float<T>(sum == 0.0f ? 0.0f : acc / sum);
+    T* dst = out_row<T>(a, tile, h, tile.r0 + r) + lane;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+        if (GEMM_DBG_OK(dst + e * LANES, a.O.p, o_bytes, sizeof(T))) dst[e * LANES] = from_float<T>(sum == 0.0f ? 0.0f : acc[e] / sum);
 }
 
 template <typename T, int D, int NQ>
@@ -524,7 +548,8 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStr
     if (e == cudaSuccess && a.partial) {
         static_assert(kStep == 128, "both kernels count tokens in the same steps");
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)plan.units, (unsigned)a.c.heads, (unsigned)plan.rows);
+        const bool many = plan.rows == 256;
+        cfg.gridDim = dim3((unsigned)plan.units, (unsigned)a.c.heads, (unsigned)(many ? plan.rows / (4 * D / 32) : plan.rows));
         cfg.blockDim = dim3(4 * D);
         cfg.stream = stream;
         cudaLaunchAttribute attr;
@@ -532,7 +557,8 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStr
         attr.val.programmaticStreamSerializationAllowed = kUsePdl;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D>, a, plan.rows, kStep);
+        e = many ? cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, 32, 1>, a, plan.rows, kStep)
+                 : cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, D, 4>, a, plan.rows, kStep);
         *launches = 2;
     }
     return e;
