@@ -461,13 +461,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
     cluster_sync();   // no CTA leaves while another reads its results
 }
 
-// Joins the splits of a tile's rows, in order.  A block of 4 * D threads takes
-// 4 * D / (LANES * GROUPS) rows; GROUPS teams of LANES threads share a row's
-// splits: one row and four teams where rows are few and splits many, a warp to
-// a row where it is the other way.
-template <typename T, int D, int LANES, int GROUPS>
-__global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a, int rows, int step) {
-    constexpr int kEach = D / LANES, kAtOnce = 4 * D / (LANES * GROUPS);   // elements of a thread, rows of a block
+// Joins the splits of a tile's rows, in order.  GROUPS teams of LANES threads
+// share a row's splits: a block of 1024 to a row where rows are few and splits
+// many, so that all loads are in flight at once, a warp to a row where it is
+// the other way.
+template <typename T, int D, int LANES, int GROUPS, int THREADS>
+__global__ void __launch_bounds__(THREADS) kv_join_kernel(const AttnArgs a, int rows, int step) {
+    constexpr int kEach = D / LANES, kAtOnce = THREADS / (LANES * GROUPS);   // elements of a thread, rows of a block
     __shared__ float s_acc[GROUPS][kAtOnce][D], s_sum[GROUPS][kAtOnce];
     const int u = blockIdx.x, h = blockIdx.y;
     const int lane = threadIdx.x % LANES, q = threadIdx.x / LANES % GROUPS, mine = threadIdx.x / (LANES * GROUPS);
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(4 * D) kv_join_kernel(const AttnArgs a, int ro
             if (GEMM_DBG_OK(ml + s * slot, a.partial, a.partial_bytes, 8)) top = fmaxf(top, ml[s * slot]);
 #pragma unroll
         for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));   // a warp has one row
-#pragma unroll 4
+#pragma unroll 8
         for (int s = q * share; s < end; ++s) {
             const float f = exp2_approx(ml[s * slot] - top);
             sum = fmaf(f, ml[s * slot + 1], sum);
@@ -549,16 +549,16 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStr
         static_assert(kStep == 128, "both kernels count tokens in the same steps");
         cudaLaunchConfig_t cfg = {};
         const bool many = plan.rows == 256;
-        cfg.gridDim = dim3((unsigned)plan.units, (unsigned)a.c.heads, (unsigned)(many ? plan.rows / (4 * D / 32) : plan.rows));
-        cfg.blockDim = dim3(4 * D);
+        cfg.gridDim = dim3((unsigned)plan.units, (unsigned)a.c.heads, (unsigned)(many ? plan.rows / 8 : plan.rows));
+        cfg.blockDim = dim3(many ? 256 : 1024);
         cfg.stream = stream;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr.val.programmaticStreamSerializationAllowed = kUsePdl;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = many ? cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, 32, 1>, a, plan.rows, kStep)
-                 : cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, D, 4>, a, plan.rows, kStep);
+        e = many ? cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, 32, 1, 256>, a, plan.rows, kStep)
+                 : cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, D, 1024 / D, 1024>, a, plan.rows, kStep);
         *launches = 2;
     }
     return e;
@@ -586,8 +586,11 @@ cudaError_t kv_attention_setup() {
 }
 
 // How many rows a tile has follows from the rows of a sequence and cache head,
-// on average: up to 8 and 16 the kernel for few rows, beyond kPromptRows the one
-// on the tensor memory (whose 128-row products are then more than half full).
+// on average: up to 8 and up to kPromptRows the kernel for few rows, in tiles of
+// 8 and 16, beyond that the one on the tensor memory, although its 128-row
+// products are then three quarters empty: a tile of 16 reads all of the cache
+// again (4 sequences of 31 queries x 2 heads over 3934 tokens: 53 us in tiles of
+// 16, 41 us in one of 256; 15 of 5 x 2 over 254: 12 us in one tile of 16).
 //
 // Few rows: tiles that fill an eighth of the GPU's CTA slots or more, or whose
 // tokens are few, have their tokens shared over a cluster (joined through
@@ -595,7 +598,7 @@ cudaError_t kv_attention_setup() {
 // sequences differ in length.  Fewer tiles over long sequences are shared over
 // one round of CTAs and joined by a second kernel.  Many rows: the tokens are
 // shared, and joined likewise, only if the tiles leave half the GPU idle.
-constexpr int64_t kPromptRows = 64;
+constexpr int64_t kPromptRows = 32;
 
 int64_t gcd(int64_t a, int64_t b) { return b ? gcd(b, a % b) : a; }
 

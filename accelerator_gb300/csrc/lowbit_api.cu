@@ -77,6 +77,7 @@ int kv_view(const gemm_kv_cache* c, const int32_t* table, int64_t width, const i
         if (c->page_tokens == 1 << i) log2 = i;
     if (log2 < 0 || c->heads < 1 || c->heads > 32767 || c->pages < 0 || c->pages > kIndexMax)
         return GEMM_ERR_INVALID_ARG;
+    if (width > (kIndexMax - 1023) >> log2) return GEMM_ERR_INVALID_ARG;   // positions and the steps past them fit 32 bits
     if (tokens == 0) return GEMM_OK;
     if (sequences == 0) return GEMM_ERR_INVALID_ARG;
     if (!starts || !at || (width > 0 && !table)) return GEMM_ERR_INVALID_ARG;

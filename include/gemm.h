@@ -342,6 +342,7 @@ typedef struct gemm_kv_cache {
  * new tokens (or queries) one after another.
  *   page_table  int32[sequences][table_width]: the page that holds a
  *               sequence's tokens page_tokens * i ... in column i
+ *               (table_width * page_tokens <= 2^31 - 1024)
  *   starts      int32[sequences + 1]: sequence b's rows are starts[b] ..
  *               starts[b + 1] - 1 (ascending; starts[0] = 0, the last one
  *               = tokens); a sequence may have none

@@ -453,7 +453,7 @@ def _call(libgemm, what, **change):
 @pytest.mark.parametrize("what", ["append", "read", "attention"])
 @pytest.mark.parametrize("change,want", [
     ({"null": 1}, 1), ({"dim": 96}, 1), ({"page": 24}, 1), ({"page": 8}, 1), ({"heads": 0}, 1), ({"pages": -1}, 1),
-    ({"tokens": -1}, 1), ({"tokens": 1 << 31}, 1), ({"sequences": 0}, 1), ({"width": -1}, 1), ({"kind": 3}, 1),
+    ({"tokens": -1}, 1), ({"tokens": 1 << 31}, 1), ({"sequences": 0}, 1), ({"width": -1}, 1), ({"width": 1 << 27}, 1), ({"kind": 3}, 1),
     ({"k": 0}, 1), ({"vs": 0}, 1), ({"table": 0}, 1), ({"starts": 0}, 1), ({"at": 0}, 1), ({"X": 0}, 1), ({"Y": 0}, 1),
     ({"k": FAKE + 8}, 2), ({"ks": FAKE + 2 * G + 2}, 2), ({"table": FAKE + 6 * G + 1}, 2), ({"X": FAKE + 4 * G + 1}, 2),
     ({"Y": FAKE + G}, 1), ({"tokens": 0, "sequences": 0, "X": 0, "Y": 0}, 0)])
