@@ -47,7 +47,7 @@ int w4_convert(const void* B, int64_t ldb, int type, int64_t K, int64_t N, int g
     if (K == 0 || N == 0) return GEMM_OK;
     if (ldb > kElemMax / K || !B || !codes || !scales) return GEMM_ERR_INVALID_ARG;
     const int64_t es = type_size(type);
-    if (!aligned(B, es) || !aligned(codes, 16) || !aligned(scales, 4)) return GEMM_ERR_MISALIGNED;
+    if (!aligned(B, es) || !aligned(codes, 16) || !aligned(scales, 16)) return GEMM_ERR_MISALIGNED;
     const int64_t bytes = span(K, N, ldb, es);
     if (overlap(B, bytes, codes, cb) || overlap(B, bytes, scales, sb) || overlap(codes, cb, scales, sb))
         return GEMM_ERR_INVALID_ARG;
@@ -139,7 +139,7 @@ int gemm_w4(const void* X, int64_t ldx, int x_type, const void* codes, const voi
         return GEMM_ERR_INVALID_ARG;
     if (!C || (K > 0 && (!X || !codes || !scales))) return GEMM_ERR_INVALID_ARG;
     const int64_t ces = type_size(c_type);
-    if (!aligned(X, 2) || !aligned(C, ces) || !aligned(codes, 16) || !aligned(scales, 4)) return GEMM_ERR_MISALIGNED;
+    if (!aligned(X, 2) || !aligned(C, ces) || !aligned(codes, 16) || !aligned(scales, 16)) return GEMM_ERR_MISALIGNED;
     const int64_t c_bytes = span(M, N, ldc, ces);
     if (overlap(C, c_bytes, X, span(M, K, ldx, 2)) || overlap(C, c_bytes, codes, cb) || overlap(C, c_bytes, scales, sb))
         return GEMM_ERR_INVALID_ARG;

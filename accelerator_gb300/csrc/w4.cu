@@ -535,7 +535,7 @@ cudaError_t launch_product(const T* X, int64_t ldx, const W4& w, U* C, int64_t l
     attr.val.clusterDim.x = (unsigned)splits;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, w4_gemm_kernel<T, U, MT, WN, HALF>, X, ldx, w, C, ldc, M, splits, tiles_n, align);
 }
 

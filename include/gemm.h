@@ -295,7 +295,7 @@ GEMM_API int gemm_w4_sizes(int64_t K, int64_t N, int group, int64_t* code_bytes,
  * product with the binary32 1 / 7), rounded to bfloat16, q = b / s rounded to the nearest integer (ties to even) and held to
  * [-7, 7].  A group whose s is under 2^-126 becomes zeros; one that holds a
  * NaN or an infinity gets s = NaN, so that every product with it is NaN.
- * codes: 16-byte aligned, scales 4-byte aligned, here and below.
+ * codes and scales: 16-byte aligned, here and below.
  */
 GEMM_API int gemm_w4_quantize(const void* B, int64_t ldb, int type, int64_t K, int64_t N,
                               int group, void* codes, void* scales, struct CUstream_st* stream);

@@ -353,11 +353,13 @@ def test_bad_indices_are_reported(libgemm):
 
 
 @gpu
-def test_capture_and_other_stream(libgemm):
+@pytest.mark.parametrize("width", [40, 200])     # the long one takes scratch and a second launch
+def test_capture_and_other_stream(libgemm, width):
     import torch
     from accelerator_gb300 import lowbit
-    pool = Pool(2, 40, 2, 128, 64, seed=17)
-    table, starts, first, lengths = ints(pool.table), ints([0, 1, 2]), ints([2000, 55]), ints([2001, 56])
+    pool = Pool(2, width, 2, 128, 64, seed=17)
+    n = 50 * width
+    table, starts, first, lengths = ints(pool.table), ints([0, 1, 2]), ints([n, 55]), ints([n + 1, 56])
     K, V, Q = pool.rows(2, 2, "bf16"), pool.rows(2, 2, "bf16"), pool.rows(2, 8, "bf16")
 
     def step(stream=None):

@@ -260,7 +260,7 @@ G = 1 << 20
     ((FAKE, 32, 3, 64, 32, 32, FAKE + G, FAKE + 2 * G), 1), ((FAKE, 32, 0, -1, 32, 32, FAKE + G, FAKE + 2 * G), 1),
     ((0, 32, 0, 64, 32, 32, FAKE + G, FAKE + 2 * G), 1), ((FAKE, 32, 0, 64, 32, 32, 0, FAKE + 2 * G), 1),
     ((FAKE, 32, 0, 64, 32, 32, FAKE + G, 0), 1), ((FAKE + 2, 32, 0, 64, 32, 32, FAKE + G, FAKE + 2 * G), 2),
-    ((FAKE, 32, 0, 64, 32, 32, FAKE + G + 8, FAKE + 2 * G), 2), ((FAKE, 32, 0, 64, 32, 32, FAKE + G, FAKE + 2 * G + 2), 2),
+    ((FAKE, 32, 0, 64, 32, 32, FAKE + G + 8, FAKE + 2 * G), 2), ((FAKE, 32, 0, 64, 32, 32, FAKE + G, FAKE + 2 * G + 4), 2), ((FAKE, 32, 0, 64, 32, 32, FAKE + G, FAKE + 2 * G + 2), 2),
     ((FAKE, 32, 0, 64, 32, 32, FAKE + 16, FAKE + 2 * G), 1), ((FAKE, 32, 0, 64, 32, 32, FAKE + G, FAKE + G + 16), 1),
     ((0, 32, 0, 0, 32, 32, 0, 0), 0)])
 def test_quantize_checks(libgemm, call, want):
