@@ -191,7 +191,7 @@ unsigned kv_cache_debug_flags();
 unsigned kv_attention_debug_flags();
 unsigned kv_prompt_debug_flags();
 // Work units of a launch are counted in the grid's x; the callers keep
-// (K / 128) * (N / 64) and 8 * (N / 32) * (M / 8) within it.
+// (K / 128) * (N / 32) and 8 * (N / 32) * (M / 8) within it.
 cudaError_t launch_w4_quantize(const void* B, int64_t ldb, ElemType type, int64_t K, int64_t N,
                                int group, void* codes, void* scales, cudaStream_t stream);
 cudaError_t launch_w4_dequantize(const void* codes, const void* scales, int64_t K, int64_t N,

@@ -135,6 +135,12 @@ struct Eight {
             return __half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (16 * (i & 1)))));
         else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
     }
+    __device__ __forceinline__ void put(int i, float y) {   // y one of the type's values, not of binary16
+        uint32_t* w = reinterpret_cast<uint32_t*>(v);
+        const uint32_t bits = __float_as_uint(y);
+        if constexpr (sizeof(T) == 4) w[i] = bits;
+        else w[i / 2] = i & 1 ? (w[i / 2] & 0xFFFFu) | (bits & 0xFFFF0000u) : (w[i / 2] & 0xFFFF0000u) | bits >> 16;
+    }
 };
 template <typename T>
 __device__ __forceinline__ Eight<T> load_eight(const T* p, bool vec) {

@@ -30,7 +30,7 @@ int w4_shape(int64_t K, int64_t N, int group, int64_t* codes, int64_t* scales) {
     if (K < 0 || N < 0 || K > kIndexMax - 255 || N > kIndexMax - 255) return GEMM_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return GEMM_ERR_INVALID_ARG;
     const int64_t nb = (N + 15) / 16, kb = (K + 63) / 64, groups = (K + group - 1) / group;
-    if (((K + 127) / 128) * ((N + 63) / 64) > kIndexMax) return GEMM_ERR_INVALID_ARG;
+    if (((K + 127) / 128) * ((N + 31) / 32) > kIndexMax) return GEMM_ERR_INVALID_ARG;
     *codes = nb * kb * 512;
     *scales = nb * groups * 32;
     return GEMM_OK;

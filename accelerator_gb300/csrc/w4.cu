@@ -25,9 +25,9 @@ struct W4 {
     __host__ __device__ int64_t nb() const { return (N + 15) / 16; }
 };
 
-// The quantiser takes tiles of 128 rows x 64 columns, a whole number of groups
-// and blocks, with 256 threads of 32 elements each.
-constexpr int kQRows = 128, kQCols = 64, kQThreads = 256;
+// The quantiser takes tiles of 128 rows x 32 columns, a whole number of groups
+// and blocks, with 128 threads of 32 elements each.
+constexpr int kQRows = 128, kQCols = 32, kQThreads = 128;
 
 __device__ __forceinline__ void tile_at(const W4& w, int64_t& k0, int64_t& n0) {
     const unsigned across = (unsigned)((w.N + kQCols - 1) / kQCols);
@@ -36,32 +36,24 @@ __device__ __forceinline__ void tile_at(const W4& w, int64_t& k0, int64_t& n0) {
 }
 
 // ---- quantise ----------------------------------------------------------------
-template <typename T>
-__device__ __forceinline__ float pick(const Eight<T>& x, int j) {   // at(j) for a j that is not known in advance
-    float v = x.at(0);
-#pragma unroll
-    for (int k = 1; k < 8; ++k)
-        if (k == j) v = x.at(k);
-    return v;
-}
-
 // A thread holds four neighbouring rows of eight columns, all loaded before
-// the first is used.  The largest magnitude of a column goes over four lanes
-// by shuffles and over two warps through shared memory (a group of 32 rows);
+// the first is used, and a warp 32 rows, over which shuffles find the largest
+// magnitude of a column (over warps, for longer groups, shared memory does);
 // a word of codes is four rows of two columns eight apart, so a thread and its
 // neighbour make half of it each and swap; the words leave in 16-byte pieces
-// by way of shared memory.  Bound by instructions (20 an element, 2.4 a cycle)
-// and the loads between two barriers: 8192 x 8192 bfloat16 in 59 us, 2.8 TB/s
-// read and written (67 us with one element at a time and conversions to int).
+// by way of shared memory.  Bound by instructions (19 an element, 2.8 a cycle)
+// and the loads between two barriers, which eight small CTAs an SM overlap: 8192
+// x 8192 bfloat16 in 49 us, 3.4 TB/s read and written (59 us as four CTAs of 256
+// threads, 67 us with one element at a time and conversions to int).
 template <typename T>
-__global__ void __launch_bounds__(kQThreads, 4)
+__global__ void __launch_bounds__(kQThreads, 8)
     w4_quantize_kernel(const T* __restrict__ B, int64_t ldb, bool vec, W4 w) {
-    __shared__ uint32_t top[kQThreads / 32][kQCols];
+    __shared__ uint32_t top[4][kQCols];
     __shared__ __align__(16) float scale[4][kQCols], inverse[4][kQCols];
-    __shared__ __align__(16) uint32_t words[4 * 296];   // [16 columns][64 rows][128 words], spread over the banks
+    __shared__ __align__(16) uint32_t words[2 * 296];   // [16 columns][64 rows][128 words], spread over the banks
     int64_t k0, n0;
     tile_at(w, k0, n0);
-    const int tid = threadIdx.x, c8 = tid % 8, r = tid / 8;
+    const int tid = threadIdx.x, c8 = tid % 4, r = tid / 4;   // a warp has 32 rows
     [[maybe_unused]] const int64_t b_bytes = ((w.K - 1) * ldb + w.N) * (int64_t)sizeof(T);
     Eight<T> x[4] = {};
 #pragma unroll
@@ -81,9 +73,10 @@ __global__ void __launch_bounds__(kQThreads, 4)
     Tops<T> tops;
 #pragma unroll
     for (int i = 0; i < 4; ++i) tops.take(x[i]);
+    tops.across(4);
     tops.across(8);
     tops.across(16);
-    if (tid % 32 < 8) {
+    if (tid % 32 < 4) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) top[tid / 32][8 * c8 + j] = tops.bits(j);
     }
@@ -91,7 +84,7 @@ __global__ void __launch_bounds__(kQThreads, 4)
     {
         const int c = tid % kQCols, part = tid / kQCols, per = w.group / 32, first = part & ~(per - 1);
         uint32_t m = 0;
-        for (int i = 0; i < 2 * per; ++i) m = max(m, top[first * 2 + i][c]);
+        for (int i = 0; i < per; ++i) m = max(m, top[first + i][c]);
         const __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(__uint_as_float(m), 1.0f / 7.0f));
         float s = __bfloat162float(sb);
         uint16_t bits = __bfloat16_as_ushort(sb);
@@ -110,16 +103,30 @@ __global__ void __launch_bounds__(kQThreads, 4)
     // correctly rounded one, for b / s is often halfway between two integers.
     // From t = b * (1 / s) the residual b - t * s (exact in one fused
     // multiply-add) gives it (Markstein 1990) as long as nothing underflows,
-    // which needs s above about 2^-100; below, the division itself.  |b / s|
-    // stays under 7.04, as s is at most 2^-8 below max|b| / 7.
+    // which needs s above about 2^-100: below, b and s are taken times 2^64.
+    // |b / s| stays under 7.04, as s is at most 2^-8 below max|b| / 7.
     uint32_t mine[8];
     const int hi = c8 & 1, part = r / 8;
-    bool tiny = false;
     float s8[8], inv8[8];
 #pragma unroll
     for (int j = 0; j < 8; j += 4) {
         *reinterpret_cast<float4*>(s8 + j) = *reinterpret_cast<const float4*>(&scale[part][8 * c8 + j]);
         *reinterpret_cast<float4*>(inv8 + j) = *reinterpret_cast<const float4*>(&inverse[part][8 * c8 + j]);
+    }
+    if constexpr (!std::is_same<T, __half>::value) {   // binary16's least s is above that
+        bool tiny = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tiny |= s8[j] < 7.9e-31f && s8[j] > 0.0f;
+        if (tiny) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool up = s8[j] < 7.9e-31f && s8[j] > 0.0f;
+                if (up) s8[j] *= 18446744073709551616.0f, inv8[j] *= 5.421010862427522e-20f;   // 2^64, 2^-64
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (up) x[i].put(j, x[i].at(j) * 18446744073709551616.0f);
+            }
+        }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -135,20 +142,6 @@ __global__ void __launch_bounds__(kQThreads, 4)
         // rows 0, 2, 1, 3 in the nibbles 0, 2, 4, 6
         const uint32_t v = low_bytes(__float_as_uint(u[0].x), __float_as_uint(u[1].x), __float_as_uint(u[0].y), __float_as_uint(u[1].y));
         mine[j] = (s == 0.0f ? 0x08080808u : v) << (4 * hi);
-        tiny |= s < 7.9e-31f && s > 0.0f;
-    }
-    if (tiny) {
-#pragma unroll 1
-        for (int j = 0; j < 8; ++j) {
-            const float s = scale[part][8 * c8 + j];
-            if (!(s < 7.9e-31f && s > 0.0f)) continue;
-            uint32_t v = 0;
-            for (int i = 0; i < 4; ++i)
-                v |= (uint32_t)((int)rintf(__fdiv_rn(pick(x[i], j), s)) + 8) << (8 * (2 * (i & 1) + (i >> 1)));
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k == j) mine[k] = v << (4 * hi);
-        }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {   // the even thread keeps columns 0-3 of 8, the odd one 4-7

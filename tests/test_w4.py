@@ -109,6 +109,25 @@ def test_magnitudes_at_the_ends_of_the_range(libgemm):
     assert (got[:, 1] == 0).all() and (got[:, 2] != 0).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_small_magnitudes_round_alike(libgemm, kind):
+    """Steps down to 2^-126, where a quotient's remainder would underflow: ties
+    and values beside them as at any other magnitude."""
+    from accelerator_gb300 import lowbit
+    steps = np.array([-126, -125, -118, -110, -101, -100, -99, -60, 0, 40])
+    B = np.empty((128, len(steps)), np.float32)
+    for c, e in enumerate(steps):
+        B[:, c] = np.ldexp(np.float32(1), e) * (np.arange(128) % 29 - 14) / 2        # multiples of half a step
+        B[::3, c] *= np.float32(1 + 2.0 ** -7)
+        B[0, c] = np.ldexp(np.float32(7), e)
+    B = as_numpy(on_gpu(B, kind)) if kind != "fp32" else B
+    W = lowbit.w4_quantize(on_gpu(B, kind), 64)
+    q, s = ref.w4_quantize(B, 64)
+    assert (s != 0).all()
+    np.testing.assert_array_equal(W.codes.cpu().numpy().view(np.uint32), ref.w4_pack(q, s, 64)[0])
+
+
 def product_limit(X, V, Y, out_kind):
     """Sums of K exact products in binary32, at most K / 8 + 64 roundings of
     2^-23 of S deep, and the result's own rounding."""
