@@ -25,7 +25,9 @@
 // back 430, output 740 -- with two tiles in turn the matrix unit is busy for
 // 60 % of it.  4 x 1000 rows of 32 heads over up to 8192 tokens of 8: 412 us,
 // 625 TFLOP/s.  Measured and left: scores loaded and weighed 32 at a time (593
-// us), weights against the previous maximum in one pass (524 us).
+// us), weights against the previous maximum in one pass (524 us), scores of 64
+// tokens in two buffers a tile, so that the next are ready early (511 us: a
+// product 64 wide takes the matrix unit as long as one 128 wide, 515 cycles).
 //
 // Every wait is bounded; a role that gives up raises the abort flag, all stop,
 // and the matrix unit is drained before tensor memory is freed.
