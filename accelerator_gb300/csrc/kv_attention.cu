@@ -219,13 +219,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         const int full_hi = tile.row_hi(a, tile.r0);
 
         constexpr int MT = D / 16;      // row tiles of O^T: row g of tile i is d = g * D / 8 + 2i, row g + 8 the next
-        float o[NQ][MT][4], m[NQ][2], l[NQ][2], ref = 0.0f;
+        // A row's sums: l of the weights exp2(s_j - m) in binary32, o of those times
+        // their page's value scale v_j times up = 2^15 / r as binary16, where m and r
+        // are the row's own largest s_j and exp2(s_j - m) * v_j so far, of tokens that
+        // it sees (r at least kLeast, so that up stays finite).
+        float o[NQ][MT][4], m[NQ][2], l[NQ][2], up[NQ][2];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
             m[n][0] = m[n][1] = kLowest;
             l[n][0] = l[n][1] = 0.0f;
+            up[n][0] = up[n][1] = kPScale / kLeast;
         }
 
         uint32_t phase = 0;
@@ -288,50 +293,56 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                     }
                 }
                 const float vs[2] = {in[0].vs, in[1].vs};
+                // A page's value scale for a row: finite, so that a weight of 0 stays 0;
+                // where it is held to 2^127 the weights are under 2^-111.
+                auto factor = [&](int b, int n, int i) { return fminf(vs[b] * up[n][i], 1.7014118e38f); };
                 float w[kSubs][NQ][4];
-                bool above = fmaxf(vs[0], vs[1]) > ref;
+                auto weigh = [&] {   // returns the largest weight of either product
+                    float most = 0.0f;
 #pragma unroll
-                for (int b = 0; b < kSubs; ++b)
+                    for (int b = 0; b < kSubs; ++b)
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n)
+                        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            w[b][n][e] = fmaf(sc[b][n][e], f[b][n][e & 1], -m[n][e & 1]);
-                            above |= w[b][n][e] > kLag;
-                        }
-                // The sums so far are brought to a new maximum, or a new largest
-                // value scale, only when one is passed.
-                if (__any_sync(0xFFFFFFFFu, above)) {
-                    const float nref = fmaxf(ref, fmaxf(vs[0], vs[1]));
-                    const float grow = ref == nref ? 1.0f : __fdividef(ref, nref);   // ref = 0 at first: o is still 0
-                    ref = nref;
+                            for (int e = 0; e < 4; ++e) {
+                                w[b][n][e] = exp2_approx(fmaf(sc[b][n][e], f[b][n][e & 1], -m[n][e & 1]));
+                                most = max3(most, w[b][n][e], w[b][n][e] * factor(b, n, e & 1));
+                            }
+                    return most;
+                };
+                // The sums so far are brought to new maxima only when one is passed
+                // by so much that a weight might not fit binary16.
+                if (__any_sync(0xFFFFFFFFu, weigh() > kMostP)) {
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        float keep[2];
+                        float grow[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float top = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]) * f[0][n][i],
-                                              fmaxf(sc[1][n][i], sc[1][n][2 + i]) * f[1][n][i]);
+                            const float t0 = fmaxf(sc[0][n][i], sc[0][n][2 + i]) * f[0][n][i];
+                            const float t1 = fmaxf(sc[1][n][i], sc[1][n][2 + i]) * f[1][n][i];
+                            float top = fmaxf(t0, t1);
                             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
                             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
                             top = fmaxf(fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16)), m[n][i]);
-                            keep[i] = exp2_approx(m[n][i] - top);
+                            const float keep = exp2_approx(m[n][i] - top), held = keep * __fdividef(kPScale, up[n][i]);
                             m[n][i] = top;
-                            l[n][i] *= keep[i];
-                            keep[i] *= grow;
+                            l[n][i] *= keep;
+                            float rel = fmaxf(exp2_approx(t0 - top) * vs[0], exp2_approx(t1 - top) * vs[1]);
+                            rel = fmaxf(rel, __shfl_xor_sync(0xFFFFFFFFu, rel, 4));
+                            rel = fmaxf(rel, __shfl_xor_sync(0xFFFFFFFFu, rel, 8));
+                            rel = fmaxf(rel, __shfl_xor_sync(0xFFFFFFFFu, rel, 16));
+                            rel = max3(rel, held, kLeast);
+                            up[n][i] = __fdividef(kPScale, rel);
+                            grow[i] = __fdividef(held, rel);   // 1 at most
                         }
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
-                            o[n][i][0] *= keep[0], o[n][i][1] *= keep[1];
-                            o[n][i][2] *= keep[0], o[n][i][3] *= keep[1];
+                            o[n][i][0] *= grow[0], o[n][i][1] *= grow[1];
+                            o[n][i][2] *= grow[0], o[n][i][3] *= grow[1];
                         }
-#pragma unroll
-                        for (int b = 0; b < kSubs; ++b)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) w[b][n][e] = fmaf(sc[b][n][e], f[b][n][e & 1], -m[n][e & 1]);
                     }
+                    weigh();
                 }
-                const float inv_ref = ref == 0.0f ? 0.0f : __fdividef(kPScale, ref);
 #pragma unroll
                 for (int b = 0; b < kSubs; ++b) {
                     uint32_t vw[4][D / 32];
@@ -346,27 +357,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                             vw[i][0] = x.x, vw[i][1] = x.y;
                         }
                     }
-                    // A page's value scale relative to the largest so far, times 2^15:
-                    // the weight is a binary16 under 2^16, normal down to 2^-29 of the
-                    // largest possible.
-                    const float fv = vs[b] * inv_ref;
-                    uint32_t pf[NQ][2];
+                    // Binary16 under 2^16, normal down to 2^-29 of the row's largest.
+                    uint32_t pt[NQ][2];
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
                         float p[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            w[b][n][e] = exp2_approx(w[b][n][e]);
-                            p[e] = w[b][n][e] * fv;
-                        }
-                        if (fv != fv) {   // a page that reads as NaN, likewise
+                        for (int e = 0; e < 4; ++e) p[e] = w[b][n][e] * factor(b, n, e & 1);
+                        if (vs[b] != vs[b]) {   // a page that reads as NaN, likewise
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) p[e] = sc[b][n][e] == kNegInf ? 0.0f : fv;
+                            for (int e = 0; e < 4; ++e) p[e] = sc[b][n][e] == kNegInf ? 0.0f : vs[b];
                         }
                         l[n][0] += w[b][n][0] + w[b][n][2];
                         l[n][1] += w[b][n][1] + w[b][n][3];
-                        pf[n][0] = transpose8(pack2<__half>(p[0], p[1]));
-                        pf[n][1] = transpose8(pack2<__half>(p[2], p[3]));
+                        pt[n][0] = transpose8(pack2<__half>(p[0], p[1]));
+                        pt[n][1] = transpose8(pack2<__half>(p[2], p[3]));
                     }
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e) {
@@ -376,8 +381,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
                         const uint32_t f1[4] = {codes01(a23), codes23(a23), codes01(b23), codes23(b23)};
 #pragma unroll
                         for (int n = 0; n < NQ; ++n) {
-                            mma_16816<__half>(o[n][2 * e], f0[0], f0[1], f0[2], f0[3], pf[n][0], pf[n][1]);
-                            mma_16816<__half>(o[n][2 * e + 1], f1[0], f1[1], f1[2], f1[3], pf[n][0], pf[n][1]);
+                            mma_16816<__half>(o[n][2 * e], f0[0], f0[1], f0[2], f0[3], pt[n][0], pt[n][1]);
+                            mma_16816<__half>(o[n][2 * e + 1], f1[0], f1[1], f1[2], f1[3], pt[n][0], pt[n][1]);
                         }
                     }
                 }
@@ -388,17 +393,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         __syncthreads();   // the ring is free: every copy has landed and been used
 
         // Join the warps: each has a maximum, a sum and unnormalised outputs.
-        const float unit = ref / kPScale;
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = 8 * n + 2 * t + i;
+                const int at = warp * kRows + 8 * n + 2 * t + i;
+                const float unit = 1.0f / up[n][i];
                 l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 4);
                 l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 8);
                 l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 16);
-                if (g == 0) s_m[warp * kRows + r] = m[n][i], s_l[warp * kRows + r] = l[n][i];
-                float4* row = reinterpret_cast<float4*>(s_o + (warp * kRows + r) * kLd + g * (D / 8));
+                if (g == 0) s_m[at] = m[n][i], s_l[at] = l[n][i];
+                float4* row = reinterpret_cast<float4*>(s_o + at * kLd + g * (D / 8));
 #pragma unroll
                 for (int e = 0; e < MT / 2; ++e)
                     row[e] = make_float4(o[n][2 * e][i] * unit, o[n][2 * e][2 + i] * unit, o[n][2 * e + 1][i] * unit,

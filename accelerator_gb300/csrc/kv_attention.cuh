@@ -8,14 +8,22 @@
 namespace libgemm {
 
 constexpr float kNegInf = -INFINITY, kLowest = -3.402823466e38f;
-// Weights enter the second product as binary16 times 2^15, under 2^16: the
-// maximum that they are relative to may lag behind by this much (in log2).
-constexpr float kPScale = 32768.0f, kLag = 0.9f;
+// Weights (with their page's value scale) enter the second product as binary16
+// times 2^15 relative to the row's largest, under 2^16: the maximum that they are
+// relative to may lag behind by this much (in log2).  A largest of less than
+// 2^-110 counts as that.
+constexpr float kPScale = 32768.0f, kLag = 0.9f, kMostP = 61147.0f /* 2^(15 + kLag) */, kLeast = 7.7037198e-34f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 struct AttnArgs {
