@@ -46,10 +46,10 @@ constexpr int kLaunchRegs = 128, kSoftRegs = 184, kCacheRegs = 104, kIssueRegs =
 static_assert(kSoftRegs * kSoftWarps + kCacheRegs * kCacheWarps + kIssueRegs * 4 <= kLaunchRegs * kThreads / 32, "");
 constexpr int kSlab = kTile * 128;                           // 128 rows of 64 binary16
 
-// What a softmax thread needs of 16 tokens: the key scale, log2 and inverse
-// of the value scale relative to the tile's largest times 2^15.
-struct PageData {
-    float ks, log_v, inv_v;
+// What a softmax thread needs of 16 tokens: the key scale, log2 of the
+// value scale (-inf for one of 0).
+struct alignas(16) PageData {
+    float ks, log_v;
     uint32_t plain;      // 1: there, and reads as numbers; 0: reads as NaN; 2: not there
 };
 
@@ -115,7 +115,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a, bool o_vec) {
     using L = Smem<D>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint32_t s_tmem, s_ref;
+    __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
@@ -135,7 +135,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
     const int log2 = a.c.page_log2;
 
     if (threadIdx.x == 0) {
-        s_ref = 0;
         s_abort = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars + 8 * (kKFull + i), kCacheWarps);
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
     }
     // The softmax threads bring their row of Q to shared memory (as binary16;
     // bfloat16 rows brought to [1, 2) by a power of two, exact but for elements
-    // under 2^-14 of the row's largest); all look for the largest value scale.
+    // under 2^-14 of the row's largest).
     float row_scale = 0.0f;
     const int in_tile = threadIdx.x % kTile, which = threadIdx.x / kTile;   // for softmax threads
     const int my_row = tile.r0 + threadIdx.x;
@@ -197,26 +196,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
         }
         fence_proxy_async_shared();
     }
-    __syncthreads();   // s_ref is 0
-    {
-        uint32_t top = 0;   // magnitudes compare as their bits; NaN scales do not count
-        const int first = tok_begin >> log2, last = blocks > 0 ? (min(tile.hi, tok_begin + blocks * kStep) - 1) >> log2 : first - 1;
-        for (int i = first + threadIdx.x; i <= last; i += kThreads) {
-            const int64_t page = __ldg(table + i);
-            if (page < 0 || page >= a.c.pages) continue;
-            const float* p = a.c.vs + page * a.c.heads + h;
-            if (!GEMM_DBG_OK(p, a.c.vs, a.c.pages * a.c.heads * 4, 4)) continue;
-            const float v = __ldg(p);
-            if (v > 0.0f) top = max(top, __float_as_uint(v));
-        }
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if (lane == 0 && top) atomicMax(&s_ref, top);
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const float ref = __uint_as_float(s_ref);
 
     if (warp >= kSoftWarps && warp < kSoftWarps + kCacheWarps) {
         // ---------------- the cache ----------------
@@ -315,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
         if (warp == kSoftWarps + kCacheWarps + 1) {
             // ---------------- the copies: lane i < 8 looks after 16 tokens of a block ----------------
             [[maybe_unused]] const int64_t code_bytes = a.c.pages * a.c.heads * ((int64_t)D << log2);
-            const float to_v = ref > 0.0f ? __fdividef(kPScale, ref) : 0.0f;
             const int chunk = min(kStep, 1 << log2);   // tokens of one copy
             struct Sub { int64_t from; float ks, vs; bool live; };
             auto look = [&](int j) {
@@ -349,11 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                     // comes when the keys of j - 1 are taken, so the values of j - 4 are used up.
                     if (!(ok = warp_wait(bars + 8 * (kCEmpty + values), ((uint32_t)j & 1u) ^ 1u, abort_flag, a.err))) break;
                     if (values == 0 && lane < kSubs) {
-                        // A page of zeros adds nothing with any weight; one of 2^-60 of the
-                        // largest scale or less is taken for that much.
                         const bool plain = now.live && now.ks == now.ks && now.vs == now.vs;
-                        const float v = plain && now.vs > 0.0f ? fmaxf(now.vs * to_v, 2.8421709e-14f) : kPScale;
-                        info[j % kSlots * kSubs + lane] = PageData{now.ks, __log2f(v), __fdividef(1.0f, v), plain ? 1u : now.live ? 0u : 2u};
+                        info[j % kSlots * kSubs + lane] = PageData{now.ks, plain ? log2f(now.vs) : 0.0f, plain ? 1u : now.live ? 0u : 2u};
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(bars + 8 * (kCFull + values), bytes);
@@ -381,7 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
         const int full_lo = tile.row_lo(a, last), full_hi = tile.row_hi(a, first);
         const bool live = my_row < tile.nrows;
         const int lo = live ? tile.row_lo(a, my_row) : 0, hi = live ? tile.row_hi(a, my_row) : tile.hi;
-        float m = kLowest, l = 0.0f;
+        // The row's own largest score s_j and s_j + log2 of its page's value scale
+        // v_j so far, of tokens that it sees: l sums exp2(s_j - m) in binary32, the
+        // second product takes 2^15 exp2(s_j + log2 v_j - mv) as binary16.
+        float m = kLowest, mv = kLowest, l = 0.0f;
         bool ok = true;
         for (int j = 0; j < blocks; ++j) {
             if (!(ok = warp_wait(bars + 8 * (kSFull + which), (uint32_t)j & 1u, abort_flag, a.err))) break;
@@ -402,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             };
             const bool hidden = tok < full_lo || tok + kStep > full_hi;
             const int first_seen = lo - tok, end_seen = hi - tok;
-            float top = kLowest;
+            float top = kLowest, top_v = kLowest;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {   // the second half loads meanwhile
                 tmem_ld_wait_for(v[2 * half]);
@@ -437,14 +419,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                     auto at = [&](int e) { return __uint_as_float(x[e]); };
                     const float t0 = max3(max3(at(0), at(1), at(2)), at(3), at(4)), t1 = max3(max3(at(5), at(6), at(7)), at(8), at(9));
                     const float t2 = max3(max3(at(10), at(11), at(12)), at(13), at(14));
-                    top = fmaxf(top, max3(max3(t0, t1, t2), at(15), at(15)) * factor(b));
+                    const float t = max3(max3(t0, t1, t2), at(15), at(15)) * factor(b);
+                    top = fmaxf(top, t);
+                    top_v = fmaxf(top_v, t + page[b].log_v);
                 }
             }
-            // The sums so far are brought to a new maximum only when it is passed.
-            if (__any_sync(0xFFFFFFFFu, top > m + kLag)) {
-                const float nm = fmaxf(m, top), keep = exp2_approx(m - nm);
+            // The sums so far are brought to new maxima only when one is passed (that of
+            // the scores, which the binary32 sum is relative to, by more).
+            if (__any_sync(0xFFFFFFFFu, top > m + 16.0f || top_v > mv + kLag)) {
+                const float nm = fmaxf(m, top), nmv = fmaxf(mv, top_v), keep = exp2_approx(mv - nmv);
+                l *= exp2_approx(m - nm);
                 m = nm;
-                l *= keep;
+                mv = nmv;
                 if (j > 0) {
                     if (!(ok = warp_wait(bars + 8 * (kODone + which), (uint32_t)(j - 1) & 1u, abort_flag, a.err))) break;
                     tc_fence_after();
@@ -459,6 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                     }
                 }
             }
+            // A page's value scale is taken for one at which a weight of 1 is 2^-60 of the
+            // row's largest if it is less (0 too): none of its weights is a binary16
+            // above 0, and their sum can be had from the same exponentials.
+            const float shift_v = 15.0f - mv, least = 15.0f - 60.0f - m;
             float sum[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -466,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const PageData& pd = page[2 * c + b];
-                    const float f = factor(2 * c + b), shift = pd.log_v - m;
+                    const float f = factor(2 * c + b), shift = fmaxf(pd.log_v + shift_v, least);
                     const float2 f2 = make_float2(f, f), shift2 = make_float2(shift, shift);
                     float2 s2 = make_float2(0.0f, 0.0f), s3 = s2;
 #pragma unroll
@@ -482,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                         p[8 * b + e / 2 + 1] = pack2<__half>(y.x, y.y);
                     }
                     s2 = __fadd2_rn(s2, s3);
-                    sum[b] = fmaf(s2.x + s2.y, pd.inv_v, sum[b]);
+                    sum[b] = fmaf(s2.x + s2.y, exp2_approx(-shift - m), sum[b]);
                 }
                 tmem_st_x16(s_at + 16 * c, p);   // over scores that are in registers
                 if (c & 1) {
@@ -499,7 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             [[maybe_unused]] const int64_t o_bytes =
                 ((a.b.rows - 1) * a.O.row + (a.q_heads - 1) * a.O.head + D) * (int64_t)sizeof(T);
             const bool whole = tile.active == 1;
-            const float unit = blocks == 0 || l == 0.0f ? 0.0f : whole ? ref / kPScale / l : ref / kPScale;
+            // O is in units of 2^(mv - 15), results and partial sums in those of 2^m, by
+            // two factors that are both in range.
+            const bool none = blocks == 0 || l == 0.0f;
+            const float half_unit = exp2_approx(0.5f * (mv - m)), unit = half_unit * (whole ? 1.0f / kPScale / l : 1.0f / kPScale);
             T* dst = live ? out_row<T>(a, tile, h, my_row) : nullptr;
             float* part = whole ? nullptr : a.partial + (((int64_t)u * a.c.heads + h) * a.splits + split) * ((int64_t)kRows * (D + 2));
 #pragma unroll 1
@@ -509,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                 tmem_ld_wait();
                 float y[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = unit == 0.0f ? 0.0f : __uint_as_float(v[e]) * unit;
+                for (int e = 0; e < 32; ++e) y[e] = none ? 0.0f : __uint_as_float(v[e]) * half_unit * unit;
                 if (!live) {
                 } else if (!whole) {
 #pragma unroll

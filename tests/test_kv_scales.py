@@ -1,6 +1,6 @@
-"""Attention over pages whose value scales are tiny, zero or orders apart: each
-row against 64 bits, within a limit that follows from the tokens which that row
-sees."""
+"""Attention over pages whose value scales are tiny, zero or orders apart, for
+both kernels (few query rows and many): each row against 64 bits, within a
+limit that follows from the tokens which that row sees."""
 import pytest
 import torch
 
@@ -8,8 +8,8 @@ import kv_ref as ref
 
 pytestmark = pytest.mark.gpu
 
-# rows of a sequence x heads to a key head: tiles of 8 and 16 rows
-FORMS = [(1, 4), (5, 3)]
+# rows of a sequence x heads to a key head: tiles of 8 and 16 rows, the kernel for many rows
+FORMS = [(1, 4), (5, 3), (60, 2)]
 
 
 @pytest.fixture(params=FORMS, ids=lambda f: f"{f[0]}x{f[1]}")
