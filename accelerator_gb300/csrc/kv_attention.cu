@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
         for (int s = 0; s < steps; ++s) {
             if (s % 4 == 0) {
                 const int tok = tok_begin + s * kStep + lane * kSub;
-                bool live = tok < tile.hi;
+                bool live = tile.page_seen(tok, log2);
                 const int64_t page = live ? __ldg(table + (tok >> log2)) : 0;
                 if (live && (page < 0 || page >= a.c.pages)) {
                     atomicOr(a.err, kErrIndex);

@@ -51,7 +51,7 @@ struct Tile {
     int r0, nrows;               // first row (query, head pair) of the tile; rows of the sequence
     int len, p0;                 // cached tokens; position of query 0
     int tok0;                    // first token, a multiple of the step
-    int hi;                      // end of the tokens any row sees
+    int lo, hi;                  // the tokens that any row sees: lo .. hi - 1
     int steps, per, active;      // steps in all, per split, splits that have any
 
     // Row r sees the tokens row_lo(r) .. row_hi(r) - 1; both grow with r.
@@ -63,6 +63,12 @@ struct Tile {
     __device__ __forceinline__ int row_lo(const AttnArgs& a, int r) const {
         const int p = p0 + (int)((unsigned)r / a.share);
         return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+    }
+    // Whether the page of token `tok` holds a token that any row sees: of a step
+    // that begins before the window or ends past the last token, not all do, and
+    // the table need not name those that do not.
+    __device__ __forceinline__ bool page_seen(int tok, int page_log2) const {
+        return tok < hi && tok >> page_log2 >= lo >> page_log2;
     }
     __device__ __forceinline__ bool find(const AttnArgs& a, int u, int rows, int step, bool report) {
         const Starts starts{a.b.starts, a.b.sequences, a.b.rows};
@@ -86,7 +92,8 @@ struct Tile {
         }
         p0 = len - count;
         hi = row_hi(a, min(r0 + rows, nrows) - 1);
-        tok0 = row_lo(a, r0) / step * step;
+        lo = row_lo(a, r0);
+        tok0 = lo / step * step;
         steps = hi > tok0 ? (hi - tok0 + step - 1) / step : 0;
         per = max(1, (steps + a.splits - 1) / a.splits);
         active = max(1, (steps + per - 1) / per);

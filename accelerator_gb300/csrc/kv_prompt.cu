@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             auto look = [&](int j) {
                 Sub s{0, 0.0f, 0.0f, false};
                 const int tok = tok_begin + j * kStep + lane * kSub;
-                if (lane < kSubs && j < blocks && tok < tile.hi) {
+                if (lane < kSubs && j < blocks && tile.page_seen(tok, log2)) {
                     const int64_t page = __ldg(table + (tok >> log2));
                     s.live = page >= 0 && page < a.c.pages;
                     if (!s.live) atomicOr(a.err, kErrIndex);
