@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const AttnArg
     const bool cluster = a.splits > 1 && !a.partial;
     Tile tile;
     // A cluster's CTAs have one tile: they leave here together or not at all.
-    if (!tile.find(a, u, kRows, kStep, threadIdx.x == 0 && h == 0 && split == 0) || (!cluster && split >= tile.active)) return;
+    if (!tile.find(a, u, kRows, kStep, h == 0 && split == 0) || (!cluster && split >= tile.active)) return;
     grid_launch_dependents();   // a joining launch may start its set-up
     const int step_begin = min(tile.steps, split * tile.per);
     const int steps = min(tile.steps, step_begin + tile.per) - step_begin;

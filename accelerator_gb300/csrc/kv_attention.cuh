@@ -70,16 +70,18 @@ struct Tile {
     __device__ __forceinline__ bool page_seen(int tok, int page_log2) const {
         return tok < hi && tok >> page_log2 >= lo >> page_log2;
     }
-    __device__ __forceinline__ bool find(const AttnArgs& a, int u, int rows, int step, bool report) {
+    // `check` for one CTA of a unit: it reports what is out of range.
+    __device__ __forceinline__ bool find(const AttnArgs& a, int u, int rows, int step, bool check) {
         const Starts starts{a.b.starts, a.b.sequences, a.b.rows};
+        if (u == 0 && check) starts.check(a.err);
         // Sequence q's tiles are units unit_of(q) + j: its rows are a multiple of
         // share, so that they need at most (rows + gap) / tile tiles.
         auto unit_of = [&](int64_t start, int i) { return (int)((start * a.share + (int64_t)i * a.gap) / rows); };
         seq = last_not_above(a.b.sequences, u, u, [&](int i) { return unit_of(starts.at(i), i); });
         row0 = (int)starts.at(seq);
         const int count = (int)starts.at(seq + 1) - row0, length = __ldg(a.b.at + seq);
-        if (!starts.whole(u == 0, seq)) {
-            if (report) atomicOr(a.err, kErrIndex);
+        if (!starts.good(seq)) {
+            if (check && threadIdx.x == 0) atomicOr(a.err, kErrIndex);
             return false;
         }
         nrows = count * (int)a.share;
@@ -87,7 +89,7 @@ struct Tile {
         if (r0 < 0 || r0 >= nrows) return false;
         len = length;
         if (length < 0 || length > (a.b.width << a.c.page_log2)) {
-            if (report) atomicOr(a.err, kErrIndex);
+            if (check && threadIdx.x == 0) atomicOr(a.err, kErrIndex);
             len = 0;
         }
         p0 = len - count;

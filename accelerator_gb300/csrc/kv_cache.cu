@@ -34,14 +34,16 @@ __device__ __forceinline__ bool find_part(const KvView& c, const KvBatch& b, int
     const bool report = threadIdx.x == 0 && blockIdx.y == 0;
     const Starts starts{b.starts, b.sequences, b.rows};
     const int log2 = c.page_log2, P = 1 << log2;
+    if (u == 0 && blockIdx.y == 0) starts.check(err);
     const int q = last_not_above(b.sequences, u, u / 2, [&](int i) { return (starts.at(i) >> log2) + 2 * (int64_t)i; });
     const int64_t row0 = starts.at(q), count = starts.at(q + 1) - row0, first = __ldg(b.at + q);
-    if (!starts.whole(u == 0, q) || (count > 0 && (first < 0 || first + count > (b.width << log2)))) {
+    if (!starts.good(q) || (count > 0 && (first < 0 || first + count > (b.width << log2)))) {
         if (report) atomicOr(err, kErrIndex);
         return false;
     }
     const int64_t blk = (first >> log2) + u - (row0 >> log2) - 2 * (int64_t)q, lo = blk << log2;
-    if (count == 0 || lo >= first + count) return false;
+    // (a unit before the sequence's: where offsets descend the search may end there)
+    if (count == 0 || blk < first >> log2 || lo >= first + count) return false;
     part.begin = (int)(first > lo ? first - lo : 0);
     part.end = (int)(first + count - lo < P ? first + count - lo : P);
     part.row = row0 + lo + part.begin - first;

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
     // Heads fastest: sequences come one after another, long ones seldom last.
     const int h = blockIdx.x % a.c.heads, split = blockIdx.x / a.c.heads % a.splits, u = blockIdx.x / a.c.heads / a.splits;
     Tile tile;
-    if (!tile.find(a, u, kRows, kStep, threadIdx.x == 0 && h == 0 && split == 0) || split >= tile.active) return;
+    if (!tile.find(a, u, kRows, kStep, h == 0 && split == 0) || split >= tile.active) return;
     grid_launch_dependents();   // a joining launch may start its set-up
     const int begin = split * tile.per, blocks = min(tile.steps, begin + tile.per) - begin;
     const int tok_begin = tile.tok0 + begin * kStep;

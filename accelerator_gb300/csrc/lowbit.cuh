@@ -263,9 +263,13 @@ struct Starts {
         const int64_t s = __ldg(p + b), e = __ldg(p + b + 1);
         return s >= 0 && s <= e && e <= rows;
     }
-    // good(b), and with `ends` (one unit of a launch) the offsets begin at 0 and end at `rows`.
-    __device__ __forceinline__ bool whole(bool ends, int b) const {
-        return good(b) && (!ends || (__ldg(p) == 0 && __ldg(p + n) == rows));
+    // Called by one CTA of a launch: reports offsets that do not ascend from 0 to `rows`.
+    // A unit of the launch reports its own sequence's, but where offsets descend
+    // a sequence may have no unit.
+    __device__ __forceinline__ void check(unsigned* err) const {
+        bool bad = false;
+        for (int b = threadIdx.x; b < n; b += blockDim.x) bad |= !good(b);
+        if (bad || (threadIdx.x == 0 && (__ldg(p) != 0 || __ldg(p + n) != rows))) atomicOr(err, kErrIndex);
     }
 };
 
