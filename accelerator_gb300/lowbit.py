@@ -65,13 +65,35 @@ def _rows2(t, name):
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
+class _Handle:
+    """What holds addresses and sizes of its tensors: fixed once it is made
+    (the tensors' contents are the caller's); a copy is made of tensors anew."""
+
+    __slots__ = ()
+
+    def _hold(self, **fields):
+        for name, value in fields.items():
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{type(self).__name__} cannot be changed: make another")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{type(self).__name__} cannot be changed: make another")
+
+
 # ---- 4-bit weights ----------------------------------------------------------
 
-class W4Matrix:
+class _W4Fields:
+    """A W4Matrix in the making: an object of this class can be assigned to."""
+    __slots__ = ("_codes", "_scales", "K", "N", "group", "index", "device", "_code_ptr", "_scale_ptr")
+
+
+class W4Matrix(_Handle, _W4Fields):
     """A K x N matrix in 4 bits: the packed codes (uint8), the scales
     (bfloat16), its sizes and the group length.  Layout: include/gemm.h."""
 
-    __slots__ = ("_codes", "_scales", "K", "N", "group", "index", "device", "_code_ptr", "_scale_ptr")
+    __slots__ = ()
 
     def __init__(self, codes, scales, K, N, group):
         code_bytes, scale_bytes = w4_sizes(K, N, group)
@@ -82,19 +104,22 @@ class W4Matrix:
               f"a contiguous CUDA bfloat16 tensor of {scale_bytes // 2} elements")
         if codes.device != scales.device:
             raise TypeError("codes and scales must be on one device")
-        self._codes, self._scales, self.K, self.N, self.group = codes, scales, int(K), int(N), int(group)
-        self.index, self.device = codes.get_device(), codes.device
-        self._code_ptr, self._scale_ptr = codes.data_ptr() or None, scales.data_ptr() or None
+        self._hold(_codes=codes, _scales=scales, K=int(K), N=int(N), group=int(group), index=codes.get_device(),
+                   device=codes.device, _code_ptr=codes.data_ptr() or None, _scale_ptr=scales.data_ptr() or None)
 
-    @classmethod
-    def _in(cls, both, code_bytes, K, N, group):
+    @staticmethod
+    def _in(both, code_bytes, K, N, group):
         """Codes and scales one after the other in the bytes of `both`."""
-        W = cls.__new__(cls)
+        W = _W4Fields()
         W._codes, W._scales, W.K, W.N, W.group = both, code_bytes, K, N, group
         W.index, W.device = both.get_device(), both.device
         at = both.data_ptr()
         W._code_ptr, W._scale_ptr = at or None, at + code_bytes if at else None
+        W.__class__ = W4Matrix      # fixed from here on, at a fifth of what _hold takes
         return W
+
+    def __reduce__(self):
+        return type(self), (self.codes, self.scales, self.K, self.N, self.group)
 
     @property
     def codes(self):
@@ -185,7 +210,7 @@ def gemm_w4(X, W: W4Matrix, C=None, dtype=None, stream=None):
 
 # ---- the 8-bit cache -----------------------------------------------------------
 
-class KvCache:
+class KvCache(_Handle):
     """A paged cache of keys and values: codes uint8 [pages, heads,
     page_tokens, head_dim] and scales float32 [pages, heads] of each."""
 
@@ -200,12 +225,15 @@ class KvCache:
                                   ("k_scales", k_scales, shape[:2], _F32), ("v_scales", v_scales, shape[:2], _F32)):
             _need(tuple(t.shape) == want and t.dtype == dt and t.is_cuda and t.is_contiguous()
                   and t.device == k_codes.device, name, f"a contiguous CUDA {dt} tensor of shape {want}")
-        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
-        self.device, self.index = k_codes.device, k_codes.get_device()
-        pages, self.heads, self.page_tokens, self.head_dim = shape
-        self._c = _CKvCache(k_codes.data_ptr() or None, v_codes.data_ptr() or None, k_scales.data_ptr() or None,
-                            v_scales.data_ptr() or None, pages, self.heads, self.page_tokens, self.head_dim)
-        self._ref = ctypes.byref(self._c)
+        pages, heads, page_tokens, head_dim = shape
+        c = _CKvCache(k_codes.data_ptr() or None, v_codes.data_ptr() or None, k_scales.data_ptr() or None,
+                      v_scales.data_ptr() or None, pages, heads, page_tokens, head_dim)
+        self._hold(k_codes=k_codes, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales, device=k_codes.device,
+                   index=k_codes.get_device(), heads=heads, page_tokens=page_tokens, head_dim=head_dim, _c=c,
+                   _ref=ctypes.byref(c))
+
+    def __reduce__(self):
+        return type(self), (self.k_codes, self.v_codes, self.k_scales, self.v_scales)
 
     @classmethod
     def empty(cls, pages, heads, head_dim, page_tokens=64, device="cuda"):
