@@ -99,6 +99,19 @@ int64_t rows_span(int64_t rows, int64_t heads, int64_t dim, int64_t row, int64_t
     return rows > 0 ? ((rows - 1) * row + (heads - 1) * head + dim) * es : 0;
 }
 
+// Whether two elements of rows x heads x dim with these strides are one: a
+// result that many threads write has to have a place for each.
+bool overlap_within(int64_t rows, int64_t heads, int64_t dim, int64_t row, int64_t head) {
+    if ((rows > 1 && row < dim) || (heads > 1 && head < dim)) return true;
+    if (rows <= 1 || heads <= 1 || row >= (heads - 1) * head + dim || head >= (rows - 1) * row + dim) return false;
+    for (int64_t h = 1; h < heads; ++h) {   // neither lies inside the other: h heads on as far as r rows on, or nearly?
+        const int64_t below = h * head / row;
+        for (int64_t r = below > 0 ? below : 1; r <= below + 1 && r < rows; ++r)
+            if (r * row - h * head < dim && h * head - r * row < dim) return true;
+    }
+    return false;
+}
+
 bool overlaps_cache(const KvView& v, const void* p, int64_t bytes) {
     const int64_t codes = v.pages * v.heads * ((int64_t)v.dim << v.page_log2), scales = v.pages * v.heads * 4;
     return overlap(p, bytes, v.k, codes) || overlap(p, bytes, v.v, codes) || overlap(p, bytes, v.ks, scales) ||
@@ -232,7 +245,9 @@ int gemm_kv_attention(const gemm_kv_cache* cache, const void* Q, int64_t q_row_s
     if (!aligned(Q, 2) || !aligned(O, 2)) return GEMM_ERR_MISALIGNED;
     const int64_t q_bytes = rows_span(tokens, q_heads, v.dim, q_row_stride, q_head_stride, 2);
     const int64_t o_bytes = rows_span(tokens, q_heads, v.dim, o_row_stride, o_head_stride, 2);
-    if (overlap(Q, q_bytes, O, o_bytes) || overlaps_cache(v, O, o_bytes)) return GEMM_ERR_INVALID_ARG;
+    if (overlap(Q, q_bytes, O, o_bytes) || overlaps_cache(v, O, o_bytes) ||
+        overlap_within(tokens, q_heads, v.dim, o_row_stride, o_head_stride))
+        return GEMM_ERR_INVALID_ARG;
     if (tokens * (q_heads / v.heads) > kIndexMax - 16 || tokens * (q_heads / v.heads) / 8 + sequences > kIndexMax / 8 / v.heads)
         return GEMM_ERR_INVALID_ARG;
     int sms = 0;

@@ -392,10 +392,11 @@ GEMM_API int gemm_kv_read(const gemm_kv_cache* cache, void* K, void* V, int type
  * window > 0 (causal only) only j > p - window.  A query that sees no token
  * (p < 0, or an empty cache) gets 0.  Q and O: rows of q_heads x head_dim
  * elements of `type` (bfloat16 or binary16), strides as above; O must not
- * overlap the inputs.  Softmax statistics and sums are binary32; a weight
- * times its page's value scale enters the second product as binary16 relative
- * to the largest that the row sees, O is rounded once.  The order of the sums
- * depends on the sizes, the lengths and the page table's width alone.
+ * overlap the inputs, nor its rows and heads one another.  Softmax statistics
+ * and sums are binary32; a weight times its page's value scale enters the
+ * second product as binary16 relative to the largest that the row sees, O is
+ * rounded once.  The order of the sums depends on the sizes, the lengths and
+ * the page table's width alone.
  */
 GEMM_API int gemm_kv_attention(const gemm_kv_cache* cache, const void* Q, int64_t q_row_stride,
                                int64_t q_head_stride, void* O, int64_t o_row_stride,
