@@ -7,10 +7,11 @@ a W of 4-bit integers with a bfloat16 scale for each column and group of rows.
 8-bit keys and values with one scale per page and head, and the attention of
 ragged queries over it.
 
-As in ``binding``: argument marshalling only, on torch's current stream unless
-one is given, asynchronous, errors as ``binding.GemmError`` (a status of the
-library), ``TypeError`` (a tensor's type, device or layout) or ``ValueError``
-(sizes that do not fit together).
+As in ``binding``: argument marshalling only, on the current CUDA device, whose
+tensors the operands have to be, and on torch's current stream unless one is
+given, asynchronous, errors as ``binding.GemmError`` (a status of the library),
+``TypeError`` (a tensor's type, device or layout) or ``ValueError`` (sizes that
+do not fit together).
 """
 from __future__ import annotations
 
@@ -23,7 +24,7 @@ from .binding import GemmError
 
 _F32, _BF16, _F16, _I32 = torch.float32, torch.bfloat16, torch.float16, torch.int32
 _TYPES = {_F32: 0, _BF16: 1, _F16: 2}
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 PAGE_TOKENS = (16, 32, 64, 128)
 HEAD_DIMS = (64, 128)
 GROUPS = (32, 64, 128)
@@ -49,7 +50,10 @@ def _empty(shape, dtype, device, stream):
 
 def _stream(stream, index):
     """The address of `stream`, or of the current stream of device `index`
-    (asked for by number: making a Stream object of it costs 3 us)."""
+    (asked for by number: making a Stream object of it costs 3 us).  The
+    library works on the current device, so that has to be the tensors'."""
+    if _current_device() != index:
+        raise TypeError(f"the tensors are on cuda:{index}, the current device is cuda:{_current_device()}")
     return (_raw_stream(index) if stream is None else stream.cuda_stream) or None
 
 
