@@ -32,6 +32,10 @@ struct DeviceState {
     // reserved (release threshold: never), so repeated calls reuse memory
     // instead of mapping it afresh after every synchronisation.
     cudaMemPool_t pool = nullptr;
+    // The attention kernels' attributes: at the first attention call, not in
+    // every product's first call, and a failure there is theirs alone.
+    std::atomic<bool> attention_done{false};
+    int attention_status = GEMM_OK;
 };
 
 std::mutex g_mu;
@@ -77,8 +81,7 @@ int device_state(DeviceState** out) {
         } else if (major != 10 || minor != 3) {
             st.status = GEMM_ERR_UNSUPPORTED_DEVICE;
         } else if (cudaGetSymbolAddress(reinterpret_cast<void**>(&st.err), g_error_word) != cudaSuccess ||
-                   ffma_setup() != cudaSuccess || tc_setup() != cudaSuccess ||
-                   kv_attention_setup() != cudaSuccess) {
+                   ffma_setup() != cudaSuccess || tc_setup() != cudaSuccess) {
             st.status = GEMM_ERR_CUDA;
         } else if (!make_pool(dev, &st.pool)) {
             st.status = GEMM_ERR_CUDA;
@@ -447,6 +450,21 @@ int tc_product(const TcPlan& plan, const void* A, const void* B, float* C, int64
 }
 
 void count_launch() { g_launches++; }
+
+int attention_setup() {
+    DeviceState* st = nullptr;
+    const int rc = device_state(&st);
+    if (rc != GEMM_OK || st->attention_done.load(std::memory_order_acquire)) return rc != GEMM_OK ? rc : st->attention_status;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!st->attention_done.load(std::memory_order_relaxed)) {
+        if (kv_attention_setup() != cudaSuccess) {
+            st->attention_status = GEMM_ERR_CUDA;
+            cudaGetLastError();
+        }
+        st->attention_done.store(true, std::memory_order_release);
+    }
+    return st->attention_status;
+}
 
 void* scratch_alloc(int64_t bytes, cudaStream_t stream) {
     DeviceState* st = nullptr;

@@ -241,6 +241,8 @@ cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& 
                                 unsigned* err, int* launches, cudaStream_t stream);
 
 // ---- host-side hooks of the C ABI (api.cu) ----
+// Set-up of the attention kernels on the current device, once; a gemm_status code.
+int attention_setup();
 // Stream-ordered scratch from the current device's pool; nullptr if none is
 // to be had.  Freed with cudaFreeAsync on the same stream.
 void* scratch_alloc(int64_t bytes, cudaStream_t stream);

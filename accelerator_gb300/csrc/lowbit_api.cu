@@ -254,6 +254,7 @@ int gemm_kv_attention(const gemm_kv_cache* cache, const void* Q, int64_t q_row_s
     unsigned* err = nullptr;
     rc = device_setup(&sms, &err);
     if (rc != GEMM_OK) return rc;
+    if ((rc = attention_setup()) != GEMM_OK) return rc;
     const KvPlan plan = kv_plan(v, b, q_heads, window, sms);
     void* scratch = nullptr;
     if (plan.scratch_bytes > 0 && !(scratch = scratch_alloc(plan.scratch_bytes, stream))) return GEMM_ERR_NO_MEMORY;
