@@ -76,10 +76,13 @@ __device__ __forceinline__ void mma_16816<__nv_bfloat16>(float (&d)[4], uint32_t
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // of any single wait
 
-// A whole warp waits, and goes on or gives up together.  One lane looks: an
-// arrival or a look by every lane is 32 operations on one word.
+// A whole warp waits, and goes on or gives up together.  One lane looks (an
+// arrival or a look by every lane is 32 operations on one word); a vote does not
+// order memory, so what that lane saw reaches the others by the __syncwarp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
-    return __any_sync(0xFFFFFFFFu, threadIdx.x % 32 == 0 && mbar_wait(bar, parity, abort_flag, err, kWaitLimitNs));
+    const bool seen = __any_sync(0xFFFFFFFFu, threadIdx.x % 32 == 0 && mbar_wait(bar, parity, abort_flag, err, kWaitLimitNs));
+    __syncwarp();
+    return seen;
 }
 // Arrives once for a whole warp, after all its lanes' accesses.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
