@@ -625,7 +625,7 @@ KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, i
     p.gap = p.rows - (int)gcd(p.rows, share);
     p.units = (all + b.sequences * (int64_t)p.gap) / p.rows;   // at least the tiles that there are
     int64_t longest = b.width << c.page_log2;
-    if (window > 0 && window + p.rows + 2 * kStep < longest) longest = window + p.rows + 2 * kStep;
+    if (window > 0 && window < longest - p.rows - 2 * kStep) longest = window + p.rows + 2 * kStep;
     if (p.units < 1) p.units = 1;
     const int64_t have = (tiles > b.sequences ? tiles : b.sequences) * c.heads, slots = (p.rows == 256 ? 1 : 2) * (int64_t)num_sms;
     const int64_t most = (longest + kStep - 1) / kStep;

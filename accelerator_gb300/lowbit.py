@@ -335,6 +335,8 @@ def kv_attention(Q, cache: KvCache, page_table, starts, lengths, scale=None, cau
         _need(out.dtype is kind and o_rows == rows and o_heads == heads, "out", "of Q's type and shape")
     if scale is None:
         scale = cache.head_dim ** -0.5
+    if window >= 1 << 63:       # as good as none, but ctypes would take its low 64 bits
+        window = (1 << 63) - 1
     rc = binding.lib().gemm_kv_attention(cache._ref, Q.data_ptr() or None, qr, qh, out.data_ptr() or None, orow, oh,
                                          _TYPES[kind], heads, scale, causal, window, page_table.data_ptr() or None,
                                          width, starts.data_ptr(), lengths.data_ptr() or None, rows, sequences,

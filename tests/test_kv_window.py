@@ -36,3 +36,14 @@ def test_a_missing_page_in_the_window_is_reported(libgemm, T):
     p.table[0, (600 - T - 30 + 1) // 16] = -1                # the page that holds the first row's first token
     p.attend(Q, [T], [600], window=30)
     assert libgemm.debug_status() == libgemm.ERR_INDEX
+
+
+@pytest.mark.parametrize("T,length", [(1, 20000), (60, 3000)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1, 2 ** 63, 2 ** 64, 2 ** 64 + 5])
+def test_a_window_past_every_token_is_none(libgemm, T, length, window):
+    """The same result, to the bit: the same split of the tokens, too."""
+    p = ref.Paged(1, -(-length // 64), 1, 64, 64)
+    Q = p.queries(T, 4, torch.float16)
+    want = ref.check(libgemm, p, Q, [T], [length])
+    assert torch.equal(p.attend(Q, [T], [length], window=window), want)
+    assert libgemm.debug_status() == libgemm.OK
