@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // as it then was).
 //
 // Bound by reading the codes while a CTA is under way: 64 sequences of up to
-// 8192 tokens, 64 heads over 8 of 128, 613 MB in 124 us, 5.0 TB/s or 73 % of the
+// 8192 tokens, 64 heads over 8 of 128, 613 MB in 125 us, 4.9 TB/s or 72 % of the
 // measured copy rate, and 6 TB/s between a CTA's first stage and its last.  The
 // rest is its beginning (3 us until its copies are under way) and its end (4 us
 // to join), which the SM's other CTA covers in part; more, smaller shares of a
@@ -602,8 +602,11 @@ cudaError_t kv_attention_setup() {
 // on average: up to 8 and up to kPromptRows the kernel for few rows, in tiles of
 // 8 and 16, beyond that the one on the tensor memory, although its 128-row
 // products are then three quarters empty: a tile of 16 reads all of the cache
-// again (4 sequences of 31 queries x 2 heads over 3934 tokens: 53 us in tiles of
-// 16, 41 us in one of 256; 15 of 5 x 2 over 254: 12 us in one tile of 16).
+// again.  4 sequences over 4000 tokens of 8 heads of 128, two query heads to each:
+// of 31 queries 77 us in tiles of 16 and 49 in one of 256, of 17 queries 63 and
+// 47, of 16 queries 46 in two tiles of 16.  (With 2 cache heads, too few tiles to
+// fill the GPU, 17 and 31 queries take 28 us in tiles of 16 and 38 in one of 256,
+// and batches that mix prompts and single tokens take one kernel for both.)
 //
 // Few rows: tiles that fill an eighth of the GPU's CTA slots or more, or whose
 // tokens are few, have their tokens shared over a cluster (joined through

@@ -9,7 +9,7 @@
 // the first, and the new elements stay in registers between the search for
 // their largest and the rounding.  11000 ragged tokens of 8 heads of 128: 18 us
 // to write (3.7 TB/s; at 2.9 instructions a cycle, so bound by them as much as
-// by memory) and 13 us to read back; one token for each of 64 sequences 7 and 9
+// by memory) and 13 us to read back; one token for each of 64 sequences 8 and 10
 // us, which are the chains of loads from offset to page to scale to code.
 #include "kernels.h"
 #include "lowbit.cuh"

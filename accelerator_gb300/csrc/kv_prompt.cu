@@ -22,12 +22,14 @@
 // and 2500 of shared memory (operands, and the codes' way into them); it took
 // about 5400 when traced, the length of one tile's chain: scores 880, their way to the
 // softmax 480, load and maximum 600, exponentials and weights 1250, their way
-// back 430, output 740 -- with two tiles in turn the matrix unit is busy for
-// 60 % of it.  4 x 1000 rows of 32 heads over up to 8192 tokens of 8: 412 us,
-// 625 TFLOP/s.  Measured and left: scores loaded and weighed 32 at a time (593
-// us), weights against the previous maximum in one pass (524 us), scores of 64
-// tokens in two buffers a tile, so that the next are ready early (511 us: a
-// product 64 wide takes the matrix unit as long as one 128 wide, 515 cycles).
+// back 430, output 740.  The tensor pipe's counter is active for 30 % of the
+// cycles.  4 x 1000 rows of 32 heads over up to 8192 tokens of 8: 418 us, 617
+// TFLOP/s; a second maximum a row (see `mv`) and what orders a warp behind its
+// waits are 6 us of it.  Measured and left, when it took 412 us: scores loaded and
+// weighed 32 at a time (593 us), weights against the previous maximum in one pass
+// (524 us), scores of 64 tokens in two buffers a tile, so that the next are ready
+// early (511 us: a product 64 wide takes the matrix unit as long as one 128 wide,
+// 515 cycles).
 //
 // Every wait is bounded; a role that gives up raises the abort flag, all stop,
 // and the matrix unit is drained before tensor memory is freed.

@@ -319,8 +319,9 @@ def kv_attention(Q, cache: KvCache, page_table, starts, lengths, scale=None, cau
     the cache.  Sequence b has lengths[b] tokens and the queries starts[b] ..
     starts[b + 1] - 1, which stand at its last positions; with `causal` a query
     sees the tokens up to its own, with `window` > 0 the last `window` of
-    them.  scale: 1 / sqrt(head_dim) by default.  A query that sees nothing
-    gets 0.  Returns O, shaped and typed like Q."""
+    them (pages wholly before every window need not be in the table).  scale:
+    1 / sqrt(head_dim) by default.  A query that sees nothing gets 0.  Returns
+    O, shaped and typed like Q."""
     width, sequences = _batch(cache, page_table, starts, lengths, "lengths")
     rows, heads, qr, qh = _rows3(Q, "Q", cache)
     kind = Q.dtype

@@ -390,13 +390,14 @@ GEMM_API int gemm_kv_read(const gemm_kv_cache* cache, void* K, void* V, int type
  *     O = sum over j of softmax_j(scale * Q . K_j) V_j
  * over the tokens 0 <= j < lengths[b], with causal != 0 only j <= p, and with
  * window > 0 (causal only) only j > p - window.  A query that sees no token
- * (p < 0, or an empty cache) gets 0.  Q and O: rows of q_heads x head_dim
- * elements of `type` (bfloat16 or binary16), strides as above; O must not
- * overlap the inputs, nor its rows and heads one another.  Softmax statistics
- * and sums are binary32; a weight times its page's value scale enters the
- * second product as binary16 relative to the largest that the row sees, O is
- * rounded once.  The order of the sums depends on the sizes, the lengths and
- * the page table's width alone.
+ * (p < 0, or an empty cache) gets 0.  Pages wholly before every query's window
+ * are not looked up: their entries of the table may be anything.  Q and O:
+ * rows of q_heads x head_dim elements of `type` (bfloat16 or binary16), strides
+ * as above; O must not overlap the inputs, nor its rows and heads one another.
+ * Softmax statistics and sums are binary32; a weight times its page's value
+ * scale enters the second product as binary16 relative to the largest that the
+ * row sees, O is rounded once.  The order of the sums depends on the sizes, the
+ * lengths and the page table's width alone.
  */
 GEMM_API int gemm_kv_attention(const gemm_kv_cache* cache, const void* Q, int64_t q_row_stride,
                                int64_t q_head_stride, void* O, int64_t o_row_stride,
