@@ -394,10 +394,11 @@ GEMM_API int gemm_kv_read(const gemm_kv_cache* cache, void* K, void* V, int type
  * are not looked up: their entries of the table may be anything.  Q and O:
  * rows of q_heads x head_dim elements of `type` (bfloat16 or binary16), strides
  * as above; O must not overlap the inputs, nor its rows and heads one another.
- * Softmax statistics and sums are binary32; a weight times its page's value
- * scale enters the second product as binary16 relative to the largest that the
- * row sees, O is rounded once.  The order of the sums depends on the sizes, the
- * lengths and the page table's width alone.
+ * Softmax statistics and sums are binary32 (a weight under 2^-126 of the row's
+ * largest counts as 0); a weight times its page's value scale enters the second
+ * product as binary16 relative to the largest that the row sees, O is rounded
+ * once.  The order of the sums depends on the sizes, the lengths and the page
+ * table's width alone.
  */
 GEMM_API int gemm_kv_attention(const gemm_kv_cache* cache, const void* Q, int64_t q_row_stride,
                                int64_t q_head_stride, void* O, int64_t o_row_stride,
