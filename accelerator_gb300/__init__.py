@@ -10,7 +10,7 @@ is an error, never a fallback.
 FP32, TF32, BF16, FP16, FP32_VIA_BF16 = 0, 1, 2, 3, 4
 
 __all__ = ["gemm", "gemm_ex", "GemmError", "FP32", "TF32", "BF16", "FP16", "FP32_VIA_BF16",
-           "W4Matrix", "w4_quantize", "w4_dequantize", "gemm_w4", "KvCache", "kv_append", "kv_read",
+           "W4Matrix", "w4_quantize", "w4_dequantize", "gemm_w4", "KvCache", "Kv4Cache", "kv_append", "kv_read",
            "kv_attention"]
 
 _LOWBIT = __all__[8:]

@@ -51,6 +51,8 @@ SIGNATURES = {
     "gemm_kv_attention": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _int, ctypes.c_int32,
                                  ctypes.c_float, _int, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
 }
+for _name in ("append", "read", "attention"):
+    SIGNATURES["gemm_kv4_" + _name] = SIGNATURES["gemm_kv_" + _name]
 
 _lock = threading.Lock()
 _lib = None

@@ -190,6 +190,8 @@ unsigned w4_debug_flags();
 unsigned kv_cache_debug_flags();
 unsigned kv_attention_debug_flags();
 unsigned kv_prompt_debug_flags();
+unsigned kv4_cache_debug_flags();
+unsigned kv4_attention_debug_flags();
 // Work units of a launch are counted in the grid's x; the callers keep
 // (K / 128) * (N / 32) and 8 * (N / 32) * (M / 8) within it.
 cudaError_t launch_w4_quantize(const void* B, int64_t ldb, ElemType type, int64_t K, int64_t N,
@@ -201,12 +203,16 @@ cudaError_t launch_w4_gemm(const void* X, int64_t ldx, ElemType x_type, const vo
                            const void* scales, void* C, int64_t ldc, ElemType c_type, int64_t M,
                            int64_t K, int64_t N, int group, int num_sms, cudaStream_t stream);
 
-// The paged cache as the kernels see it (layout in gemm.h).
+// The paged cache as the kernels see it (layouts in gemm.h): codes and scales
+// in 8 bits, or the records of pages and heads in 4.
 struct KvView {
     uint8_t *k, *v;
     float *ks, *vs;
     int64_t pages;
     int heads, page_log2, dim;
+    int bits;
+    uint8_t* data;   // 4 bits
+    __host__ __device__ int64_t record() const { return (int64_t)(dim + 4) << page_log2; }
 };
 // A batch: page table, row offsets and each sequence's first position (append,
 // read) or length (attention).
@@ -224,6 +230,10 @@ cudaError_t launch_kv_append(const KvView& c, const KvRows& K, const KvRows& V, 
                              const KvBatch& b, unsigned* err, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvView& c, void* K, void* V, ElemType type, const KvBatch& b,
                            unsigned* err, cudaStream_t stream);
+cudaError_t launch_kv4_append(const KvView& c, const KvRows& K, const KvRows& V, ElemType type,
+                              const KvBatch& b, unsigned* err, cudaStream_t stream);
+cudaError_t launch_kv4_read(const KvView& c, void* K, void* V, ElemType type, const KvBatch& b,
+                            unsigned* err, cudaStream_t stream);
 // Attention: `splits` CTAs share the tokens of a tile of rows, as a cluster
 // or, with scratch (plan.scratch_bytes), joined by a second launch.
 struct KvPlan {

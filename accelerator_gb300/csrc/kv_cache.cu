@@ -12,6 +12,7 @@
 // by memory) and 13 us to read back; one token for each of 64 sequences 8 and 10
 // us, which are the chains of loads from offset to page to scale to code.
 #include "kernels.h"
+#include "kv_part.cuh"
 #include "lowbit.cuh"
 
 namespace libgemm {
@@ -19,41 +20,6 @@ namespace {
 
 constexpr float kTiny = 1.1754943508222875e-38f;   // 2^-126
 constexpr int kThreads = 256;
-
-// The part of a page that a unit of a launch is about.
-struct Part {
-    int64_t row0;      // the batch row of the sequence's first token
-    int64_t row;       // the batch row of the first token of the part
-    int64_t page;
-    int begin, end;    // its tokens in the page
-};
-
-// Sequence q's pages are units floor(starts[q] / P) + 2q + j: T rows touch at
-// most floor(T / P) + 2 pages, which is how far apart these are.
-__device__ __forceinline__ bool find_part(const KvView& c, const KvBatch& b, int64_t u, unsigned* err, Part& part) {
-    const bool report = threadIdx.x == 0 && blockIdx.y == 0;
-    const Starts starts{b.starts, b.sequences, b.rows};
-    const int log2 = c.page_log2, P = 1 << log2;
-    if (u == 0 && blockIdx.y == 0) starts.check(err);
-    const int q = last_not_above(b.sequences, u, u / 2, [&](int i) { return (starts.at(i) >> log2) + 2 * (int64_t)i; });
-    const int64_t row0 = starts.at(q), count = starts.at(q + 1) - row0, first = __ldg(b.at + q);
-    if (!starts.good(q) || (count > 0 && (first < 0 || first + count > (b.width << log2)))) {
-        if (report) atomicOr(err, kErrIndex);
-        return false;
-    }
-    const int64_t blk = (first >> log2) + u - (row0 >> log2) - 2 * (int64_t)q, lo = blk << log2;
-    // (a unit before the sequence's: where offsets descend the search may end there)
-    if (count == 0 || blk < first >> log2 || lo >= first + count) return false;
-    part.begin = (int)(first > lo ? first - lo : 0);
-    part.end = (int)(first + count - lo < P ? first + count - lo : P);
-    part.row = row0 + lo + part.begin - first;
-    part.page = __ldg(b.table + q * b.width + blk);
-    if (part.page < 0 || part.page >= c.pages) {
-        if (report) atomicOr(err, kErrIndex);
-        return false;
-    }
-    return true;
-}
 
 // Codes of four values: rint(x * f) + 128 as bytes.  |x * f| stays under 127.5:
 // f is 1 / s and s at least max|x| * (1 / 127), but for three roundings.
@@ -81,7 +47,7 @@ __global__ void __launch_bounds__(kThreads)
     uint8_t* codes = values ? c.v : c.k;
     float* scales = values ? c.vs : c.ks;
     Part part;
-    if (!find_part(c, b, blockIdx.x, err, part)) return;
+    if (!find_part(c, b, c.page_log2, blockIdx.x, err, part)) return;
     const int row_log2 = c.dim == 64 ? 3 : 4, n = (part.end - part.begin) << row_log2;   // groups of a row; in all
     const T* x = static_cast<const T*>(src.p) + part.row * src.row + h * src.head;
     [[maybe_unused]] const int64_t x_bytes =
@@ -143,7 +109,7 @@ __global__ void __launch_bounds__(kThreads)
     const int tid = threadIdx.x, h = blockIdx.y >> 1;
     const bool values = blockIdx.y & 1;
     Part part;
-    if (!find_part(c, b, blockIdx.x, err, part)) return;
+    if (!find_part(c, b, c.page_log2, blockIdx.x, err, part)) return;
     const uint8_t* codes = values ? c.v : c.k;
     const float* scales = values ? c.vs : c.ks;
     T* out = values ? V : K;

@@ -65,8 +65,23 @@ int w4_convert(const void* B, int64_t ldb, int type, int64_t K, int64_t N, int g
     return GEMM_OK;
 }
 
-// Checks what the calls on a cache share.
-int kv_view(const gemm_kv_cache* c, const int32_t* table, int64_t width, const int32_t* starts,
+bool cache_pointers(const gemm_kv_cache* c) { return c->k_codes && c->v_codes && c->k_scales && c->v_scales; }
+bool cache_pointers(const gemm_kv4_cache* c) { return c->data; }
+bool cache_aligned(const gemm_kv_cache* c) {
+    return aligned(c->k_codes, 16) && aligned(c->v_codes, 16) && aligned(c->k_scales, 4) && aligned(c->v_scales, 4);
+}
+bool cache_aligned(const gemm_kv4_cache* c) { return aligned(c->data, 16); }
+KvView view_of(const gemm_kv_cache* c, int log2) {
+    return KvView{static_cast<uint8_t*>(c->k_codes), static_cast<uint8_t*>(c->v_codes), c->k_scales, c->v_scales,
+                  c->pages, c->heads, log2, c->head_dim, 8, nullptr};
+}
+KvView view_of(const gemm_kv4_cache* c, int log2) {
+    return KvView{nullptr, nullptr, nullptr, nullptr, c->pages, c->heads, log2, c->head_dim, 4, static_cast<uint8_t*>(c->data)};
+}
+
+// Checks what the calls on a cache (of 8 or 4 bits) share.
+template <typename Cache>
+int kv_view(const Cache* c, const int32_t* table, int64_t width, const int32_t* starts,
             const int32_t* at, int64_t tokens, int64_t sequences, KvView* view, KvBatch* batch) {
     if (!c || tokens < 0 || sequences < 0 || width < 0 || tokens > kIndexMax || sequences > kIndexMax ||
         width > kIndexMax)
@@ -81,12 +96,9 @@ int kv_view(const gemm_kv_cache* c, const int32_t* table, int64_t width, const i
     if (tokens == 0) return GEMM_OK;
     if (sequences == 0) return GEMM_ERR_INVALID_ARG;
     if (!starts || !at || (width > 0 && !table)) return GEMM_ERR_INVALID_ARG;
-    if (c->pages > 0 && (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)) return GEMM_ERR_INVALID_ARG;
-    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 4) ||
-        !aligned(c->v_scales, 4) || !aligned(table, 4) || !aligned(starts, 4) || !aligned(at, 4))
-        return GEMM_ERR_MISALIGNED;
-    *view = KvView{static_cast<uint8_t*>(c->k_codes), static_cast<uint8_t*>(c->v_codes), c->k_scales,
-                   c->v_scales, c->pages, c->heads, log2, c->head_dim};
+    if (c->pages > 0 && !cache_pointers(c)) return GEMM_ERR_INVALID_ARG;
+    if (!cache_aligned(c) || !aligned(table, 4) || !aligned(starts, 4) || !aligned(at, 4)) return GEMM_ERR_MISALIGNED;
+    *view = view_of(c, log2);
     *batch = KvBatch{table, starts, at, width, tokens, (int)sequences};
     return GEMM_OK;
 }
@@ -113,9 +125,112 @@ bool overlap_within(int64_t rows, int64_t heads, int64_t dim, int64_t row, int64
 }
 
 bool overlaps_cache(const KvView& v, const void* p, int64_t bytes) {
+    if (v.bits == 4) return overlap(p, bytes, v.data, v.pages * v.heads * v.record());
     const int64_t codes = v.pages * v.heads * ((int64_t)v.dim << v.page_log2), scales = v.pages * v.heads * 4;
     return overlap(p, bytes, v.k, codes) || overlap(p, bytes, v.v, codes) || overlap(p, bytes, v.ks, scales) ||
            overlap(p, bytes, v.vs, scales);
+}
+
+template <typename Cache>
+int kv_append(const Cache* cache, const void* K, int64_t k_row_stride, int64_t k_head_stride, const void* V,
+              int64_t v_row_stride, int64_t v_head_stride, int type, const int32_t* page_table, int64_t table_width,
+              const int32_t* starts, const int32_t* first, int64_t tokens, int64_t sequences,
+              struct CUstream_st* stream) {
+    KvView v{};
+    KvBatch b{};
+    int rc = kv_view(cache, page_table, table_width, starts, first, tokens, sequences, &v, &b);
+    if (rc != GEMM_OK) return rc;
+    if (!type_ok(type)) return GEMM_ERR_INVALID_ARG;
+    if (tokens == 0) return GEMM_OK;
+    if (!K || !V || !strides_ok(tokens, v.heads, k_row_stride, k_head_stride) ||
+        !strides_ok(tokens, v.heads, v_row_stride, v_head_stride))
+        return GEMM_ERR_INVALID_ARG;
+    const int64_t es = type_size(type);
+    if (!aligned(K, es) || !aligned(V, es)) return GEMM_ERR_MISALIGNED;
+    if (overlaps_cache(v, K, rows_span(tokens, v.heads, v.dim, k_row_stride, k_head_stride, es)) ||
+        overlaps_cache(v, V, rows_span(tokens, v.heads, v.dim, v_row_stride, v_head_stride, es)))
+        return GEMM_ERR_INVALID_ARG;
+    if ((tokens >> (v.bits == 4 ? 4 : v.page_log2)) + 2 * sequences > kIndexMax) return GEMM_ERR_INVALID_ARG;
+    int sms = 0;
+    unsigned* err = nullptr;
+    rc = device_setup(&sms, &err);
+    if (rc != GEMM_OK) return rc;
+    if ((v.bits == 4 ? launch_kv4_append : launch_kv_append)(
+            v, KvRows{const_cast<void*>(K), k_row_stride, k_head_stride}, KvRows{const_cast<void*>(V), v_row_stride, v_head_stride},
+            static_cast<ElemType>(type), b, err, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    count_launch();
+    return GEMM_OK;
+}
+
+template <typename Cache>
+int kv_read(const Cache* cache, void* K, void* V, int type, const int32_t* page_table, int64_t table_width,
+            const int32_t* starts, const int32_t* first, int64_t tokens, int64_t sequences,
+            struct CUstream_st* stream) {
+    KvView v{};
+    KvBatch b{};
+    int rc = kv_view(cache, page_table, table_width, starts, first, tokens, sequences, &v, &b);
+    if (rc != GEMM_OK) return rc;
+    if (!type_ok(type)) return GEMM_ERR_INVALID_ARG;
+    if (tokens == 0) return GEMM_OK;
+    if (!K || !V) return GEMM_ERR_INVALID_ARG;
+    if (!aligned(K, 16) || !aligned(V, 16)) return GEMM_ERR_MISALIGNED;
+    const int64_t bytes = tokens * v.heads * v.dim * type_size(type);
+    if (overlaps_cache(v, K, bytes) || overlaps_cache(v, V, bytes) || overlap(K, bytes, V, bytes))
+        return GEMM_ERR_INVALID_ARG;
+    if ((tokens >> (v.bits == 4 ? 4 : v.page_log2)) + 2 * sequences > kIndexMax) return GEMM_ERR_INVALID_ARG;
+    int sms = 0;
+    unsigned* err = nullptr;
+    rc = device_setup(&sms, &err);
+    if (rc != GEMM_OK) return rc;
+    if ((v.bits == 4 ? launch_kv4_read : launch_kv_read)(v, K, V, static_cast<ElemType>(type), b, err,
+                                                    reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    count_launch();
+    return GEMM_OK;
+}
+
+template <typename Cache>
+int kv_attention(const Cache* cache, const void* Q, int64_t q_row_stride, int64_t q_head_stride, void* O,
+                 int64_t o_row_stride, int64_t o_head_stride, int type, int32_t q_heads, float scale, int causal,
+                 int64_t window, const int32_t* page_table, int64_t table_width, const int32_t* starts,
+                 const int32_t* lengths, int64_t tokens, int64_t sequences, struct CUstream_st* stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    KvView v{};
+    KvBatch b{};
+    int rc = kv_view(cache, page_table, table_width, starts, lengths, tokens, sequences, &v, &b);
+    if (rc != GEMM_OK) return rc;
+    if ((type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) || q_heads < 1 || q_heads % cache->heads != 0 ||
+        window < 0 || (window > 0 && !causal) || !(scale == scale))
+        return GEMM_ERR_INVALID_ARG;
+    if (tokens == 0) return GEMM_OK;
+    if (!Q || !O || !strides_ok(tokens, q_heads, q_row_stride, q_head_stride) ||
+        !strides_ok(tokens, q_heads, o_row_stride, o_head_stride))
+        return GEMM_ERR_INVALID_ARG;
+    if (!aligned(Q, 2) || !aligned(O, 2)) return GEMM_ERR_MISALIGNED;
+    const int64_t q_bytes = rows_span(tokens, q_heads, v.dim, q_row_stride, q_head_stride, 2);
+    const int64_t o_bytes = rows_span(tokens, q_heads, v.dim, o_row_stride, o_head_stride, 2);
+    if (overlap(Q, q_bytes, O, o_bytes) || overlaps_cache(v, O, o_bytes) ||
+        overlap_within(tokens, q_heads, v.dim, o_row_stride, o_head_stride))
+        return GEMM_ERR_INVALID_ARG;
+    if (tokens * (q_heads / v.heads) > kIndexMax - 16 || tokens * (q_heads / v.heads) / 8 + sequences > kIndexMax / 8 / v.heads)
+        return GEMM_ERR_INVALID_ARG;
+    int sms = 0;
+    unsigned* err = nullptr;
+    rc = device_setup(&sms, &err);
+    if (rc != GEMM_OK) return rc;
+    if ((rc = attention_setup()) != GEMM_OK) return rc;
+    const KvPlan plan = kv_plan(v, b, q_heads, window, sms);
+    void* scratch = nullptr;
+    if (plan.scratch_bytes > 0 && !(scratch = scratch_alloc(plan.scratch_bytes, stream))) return GEMM_ERR_NO_MEMORY;
+    int launches = 0;
+    if (launch_kv_attention(v, KvRows{const_cast<void*>(Q), q_row_stride, q_head_stride},
+                            KvRows{O, o_row_stride, o_head_stride}, static_cast<ElemType>(type), q_heads,
+                            scale, causal != 0, window, b, plan, scratch, err, &launches, stream) != cudaSuccess)
+        rc = GEMM_ERR_CUDA;
+    for (int i = 0; i < launches; ++i) count_launch();
+    if (scratch && cudaFreeAsync(scratch, stream) != cudaSuccess && rc == GEMM_OK) rc = GEMM_ERR_CUDA;
+    return rc;
 }
 
 }  // namespace
@@ -172,56 +287,14 @@ int gemm_kv_append(const gemm_kv_cache* cache, const void* K, int64_t k_row_stri
                    int64_t v_head_stride, int type, const int32_t* page_table, int64_t table_width,
                    const int32_t* starts, const int32_t* first, int64_t tokens, int64_t sequences,
                    struct CUstream_st* stream) {
-    KvView v{};
-    KvBatch b{};
-    int rc = kv_view(cache, page_table, table_width, starts, first, tokens, sequences, &v, &b);
-    if (rc != GEMM_OK) return rc;
-    if (!type_ok(type)) return GEMM_ERR_INVALID_ARG;
-    if (tokens == 0) return GEMM_OK;
-    if (!K || !V || !strides_ok(tokens, v.heads, k_row_stride, k_head_stride) ||
-        !strides_ok(tokens, v.heads, v_row_stride, v_head_stride))
-        return GEMM_ERR_INVALID_ARG;
-    const int64_t es = type_size(type);
-    if (!aligned(K, es) || !aligned(V, es)) return GEMM_ERR_MISALIGNED;
-    if (overlaps_cache(v, K, rows_span(tokens, v.heads, v.dim, k_row_stride, k_head_stride, es)) ||
-        overlaps_cache(v, V, rows_span(tokens, v.heads, v.dim, v_row_stride, v_head_stride, es)))
-        return GEMM_ERR_INVALID_ARG;
-    if ((tokens >> v.page_log2) + 2 * sequences > kIndexMax) return GEMM_ERR_INVALID_ARG;
-    int sms = 0;
-    unsigned* err = nullptr;
-    rc = device_setup(&sms, &err);
-    if (rc != GEMM_OK) return rc;
-    if (launch_kv_append(v, KvRows{const_cast<void*>(K), k_row_stride, k_head_stride},
-                         KvRows{const_cast<void*>(V), v_row_stride, v_head_stride},
-                         static_cast<ElemType>(type), b, err, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-    count_launch();
-    return GEMM_OK;
+    return kv_append(cache, K, k_row_stride, k_head_stride, V, v_row_stride, v_head_stride, type, page_table, table_width,
+                     starts, first, tokens, sequences, stream);
 }
 
 int gemm_kv_read(const gemm_kv_cache* cache, void* K, void* V, int type, const int32_t* page_table,
                  int64_t table_width, const int32_t* starts, const int32_t* first, int64_t tokens,
                  int64_t sequences, struct CUstream_st* stream) {
-    KvView v{};
-    KvBatch b{};
-    int rc = kv_view(cache, page_table, table_width, starts, first, tokens, sequences, &v, &b);
-    if (rc != GEMM_OK) return rc;
-    if (!type_ok(type)) return GEMM_ERR_INVALID_ARG;
-    if (tokens == 0) return GEMM_OK;
-    if (!K || !V) return GEMM_ERR_INVALID_ARG;
-    if (!aligned(K, 16) || !aligned(V, 16)) return GEMM_ERR_MISALIGNED;
-    const int64_t bytes = tokens * v.heads * v.dim * type_size(type);
-    if (overlaps_cache(v, K, bytes) || overlaps_cache(v, V, bytes) || overlap(K, bytes, V, bytes))
-        return GEMM_ERR_INVALID_ARG;
-    if ((tokens >> v.page_log2) + 2 * sequences > kIndexMax) return GEMM_ERR_INVALID_ARG;
-    int sms = 0;
-    unsigned* err = nullptr;
-    rc = device_setup(&sms, &err);
-    if (rc != GEMM_OK) return rc;
-    if (launch_kv_read(v, K, V, static_cast<ElemType>(type), b, err, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-    count_launch();
-    return GEMM_OK;
+    return kv_read(cache, K, V, type, page_table, table_width, starts, first, tokens, sequences, stream);
 }
 
 int gemm_kv_attention(const gemm_kv_cache* cache, const void* Q, int64_t q_row_stride,
@@ -229,43 +302,34 @@ int gemm_kv_attention(const gemm_kv_cache* cache, const void* Q, int64_t q_row_s
                       int type, int32_t q_heads, float scale, int causal, int64_t window,
                       const int32_t* page_table, int64_t table_width, const int32_t* starts,
                       const int32_t* lengths, int64_t tokens, int64_t sequences,
-                      struct CUstream_st* stream_) {
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    KvView v{};
-    KvBatch b{};
-    int rc = kv_view(cache, page_table, table_width, starts, lengths, tokens, sequences, &v, &b);
-    if (rc != GEMM_OK) return rc;
-    if ((type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) || q_heads < 1 || q_heads % cache->heads != 0 ||
-        window < 0 || (window > 0 && !causal) || !(scale == scale))
-        return GEMM_ERR_INVALID_ARG;
-    if (tokens == 0) return GEMM_OK;
-    if (!Q || !O || !strides_ok(tokens, q_heads, q_row_stride, q_head_stride) ||
-        !strides_ok(tokens, q_heads, o_row_stride, o_head_stride))
-        return GEMM_ERR_INVALID_ARG;
-    if (!aligned(Q, 2) || !aligned(O, 2)) return GEMM_ERR_MISALIGNED;
-    const int64_t q_bytes = rows_span(tokens, q_heads, v.dim, q_row_stride, q_head_stride, 2);
-    const int64_t o_bytes = rows_span(tokens, q_heads, v.dim, o_row_stride, o_head_stride, 2);
-    if (overlap(Q, q_bytes, O, o_bytes) || overlaps_cache(v, O, o_bytes) ||
-        overlap_within(tokens, q_heads, v.dim, o_row_stride, o_head_stride))
-        return GEMM_ERR_INVALID_ARG;
-    if (tokens * (q_heads / v.heads) > kIndexMax - 16 || tokens * (q_heads / v.heads) / 8 + sequences > kIndexMax / 8 / v.heads)
-        return GEMM_ERR_INVALID_ARG;
-    int sms = 0;
-    unsigned* err = nullptr;
-    rc = device_setup(&sms, &err);
-    if (rc != GEMM_OK) return rc;
-    if ((rc = attention_setup()) != GEMM_OK) return rc;
-    const KvPlan plan = kv_plan(v, b, q_heads, window, sms);
-    void* scratch = nullptr;
-    if (plan.scratch_bytes > 0 && !(scratch = scratch_alloc(plan.scratch_bytes, stream))) return GEMM_ERR_NO_MEMORY;
-    int launches = 0;
-    if (launch_kv_attention(v, KvRows{const_cast<void*>(Q), q_row_stride, q_head_stride},
-                            KvRows{O, o_row_stride, o_head_stride}, static_cast<ElemType>(type), q_heads,
-                            scale, causal != 0, window, b, plan, scratch, err, &launches, stream) != cudaSuccess)
-        rc = GEMM_ERR_CUDA;
-    for (int i = 0; i < launches; ++i) count_launch();
-    if (scratch && cudaFreeAsync(scratch, stream) != cudaSuccess && rc == GEMM_OK) rc = GEMM_ERR_CUDA;
-    return rc;
+                      struct CUstream_st* stream) {
+    return kv_attention(cache, Q, q_row_stride, q_head_stride, O, o_row_stride, o_head_stride, type, q_heads, scale, causal,
+                        window, page_table, table_width, starts, lengths, tokens, sequences, stream);
+}
+
+int gemm_kv4_append(const gemm_kv4_cache* cache, const void* K, int64_t k_row_stride,
+                    int64_t k_head_stride, const void* V, int64_t v_row_stride,
+                   int64_t v_head_stride, int type, const int32_t* page_table, int64_t table_width,
+                   const int32_t* starts, const int32_t* first, int64_t tokens, int64_t sequences,
+                   struct CUstream_st* stream) {
+    return kv_append(cache, K, k_row_stride, k_head_stride, V, v_row_stride, v_head_stride, type, page_table, table_width,
+                     starts, first, tokens, sequences, stream);
+}
+
+int gemm_kv4_read(const gemm_kv4_cache* cache, void* K, void* V, int type, const int32_t* page_table,
+                 int64_t table_width, const int32_t* starts, const int32_t* first, int64_t tokens,
+                 int64_t sequences, struct CUstream_st* stream) {
+    return kv_read(cache, K, V, type, page_table, table_width, starts, first, tokens, sequences, stream);
+}
+
+int gemm_kv4_attention(const gemm_kv4_cache* cache, const void* Q, int64_t q_row_stride,
+                      int64_t q_head_stride, void* O, int64_t o_row_stride, int64_t o_head_stride,
+                      int type, int32_t q_heads, float scale, int causal, int64_t window,
+                      const int32_t* page_table, int64_t table_width, const int32_t* starts,
+                      const int32_t* lengths, int64_t tokens, int64_t sequences,
+                      struct CUstream_st* stream) {
+    return kv_attention(cache, Q, q_row_stride, q_head_stride, O, o_row_stride, o_head_stride, type, q_heads, scale, causal,
+                        window, page_table, table_width, starts, lengths, tokens, sequences, stream);
 }
 
 }  // extern "C"

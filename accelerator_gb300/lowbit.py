@@ -5,7 +5,8 @@ a W of 4-bit integers with a bfloat16 scale for each column and group of rows.
 
 ``KvCache`` with ``kv_append`` / ``kv_read`` / ``kv_attention``: a paged cache of
 8-bit keys and values with one scale per page and head, and the attention of
-ragged queries over it.
+ragged queries over it; ``Kv4Cache`` with the same calls: one of 4 bits with a
+scale per token and head.
 
 As in ``binding``: argument marshalling only, on the current CUDA device, whose
 tensors the operands have to be, and on torch's current stream unless one is
@@ -31,6 +32,11 @@ GROUPS = (32, 64, 128)
 
 # A small call's time is the host's: the checks below are written out in each
 # function, in the fewest steps, and what is wrong is told apart only then.
+
+
+class _CKv4Cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 class _CKvCache(ctypes.Structure):
@@ -212,14 +218,15 @@ def gemm_w4(X, W: W4Matrix, C=None, dtype=None, stream=None):
     return C
 
 
-# ---- the 8-bit cache -----------------------------------------------------------
+# ---- the caches ------------------------------------------------------------------
 
 class KvCache(_Handle):
-    """A paged cache of keys and values: codes uint8 [pages, heads,
+    """A paged cache of keys and values in 8 bits: codes uint8 [pages, heads,
     page_tokens, head_dim] and scales float32 [pages, heads] of each."""
 
     __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "heads", "head_dim", "page_tokens", "device", "index",
                  "_c", "_ref")
+    _append, _read, _attention = "gemm_kv_append", "gemm_kv_read", "gemm_kv_attention"
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
         shape = tuple(k_codes.shape)
@@ -247,6 +254,36 @@ class KvCache(_Handle):
                    *(torch.zeros(shape[:2], dtype=_F32, device=device) for _ in range(2)))
 
 
+class Kv4Cache(_Handle):
+    """A paged cache of keys and values in 4 bits, with a scale for each token
+    and head of either: uint8 [pages, heads, page_tokens * (head_dim + 4)], which
+    holds for a page and head the codes of keys and of values and their bfloat16
+    scales.  Layout: include/gemm.h."""
+
+    __slots__ = ("data", "heads", "head_dim", "page_tokens", "device", "index", "_c", "_ref")
+    _append, _read, _attention = "gemm_kv4_append", "gemm_kv4_read", "gemm_kv4_attention"
+
+    def __init__(self, data, page_tokens, head_dim):
+        _need(page_tokens in PAGE_TOKENS, "page_tokens", f"one of {PAGE_TOKENS}")
+        _need(head_dim in HEAD_DIMS, "head_dim", f"one of {HEAD_DIMS}")
+        record = page_tokens * (head_dim + 4)
+        _need(data.dim() == 3 and data.shape[2] == record and data.dtype == torch.uint8 and data.is_cuda
+              and data.is_contiguous(), "data", f"a contiguous CUDA uint8 tensor [pages, heads, {record}]")
+        pages, heads, _ = data.shape
+        c = _CKv4Cache(data.data_ptr() or None, pages, heads, page_tokens, head_dim)
+        self._hold(data=data, device=data.device, index=data.get_device(), heads=heads, page_tokens=int(page_tokens),
+                   head_dim=int(head_dim), _c=c, _ref=ctypes.byref(c))
+
+    def __reduce__(self):
+        return type(self), (self.data, self.page_tokens, self.head_dim)
+
+    @classmethod
+    def empty(cls, pages, heads, head_dim, page_tokens=64, device="cuda"):
+        """A cache of `pages` pages; a page needs no initial contents."""
+        return cls(torch.empty((pages, heads, page_tokens * (head_dim + 4)), dtype=torch.uint8, device=device),
+                   page_tokens, head_dim)
+
+
 def _batch(cache, page_table, starts, at, name):
     """Checks the index tensors of a call; returns (table width, sequences)."""
     index = cache.index
@@ -272,11 +309,12 @@ def _rows3(t, name, cache):
     raise TypeError(f"{name} must be a tensor on {cache.device} of rows x heads x {cache.head_dim} with dense elements")
 
 
-def kv_append(cache: KvCache, K, V, page_table, starts, first, stream=None):
+def kv_append(cache, K, V, page_table, starts, first, stream=None):
     """Writes new keys and values (tokens x heads x head_dim; float32, bfloat16
-    or float16; any row and head strides) into the cache: row starts[b] + i
-    becomes token first[b] + i of sequence b.  A page's scale grows to the
-    largest magnitude / 127, and its older codes with it."""
+    or float16; any row and head strides) into a KvCache or Kv4Cache: row
+    starts[b] + i becomes token first[b] + i of sequence b.  In 8 bits a page's
+    scale grows to the largest magnitude / 127, and its older codes with it; in 4
+    bits each token and head gets a scale of its own, the largest magnitude / 7."""
     width, sequences = _batch(cache, page_table, starts, first, "first")
     rows, heads, kr, kh = _rows3(K, "K", cache)
     v_rows, v_heads, vr, vh = _rows3(V, "V", cache)
@@ -287,15 +325,15 @@ def kv_append(cache: KvCache, K, V, page_table, starts, first, stream=None):
         raise TypeError(f"K and V must have {cache.heads} heads")
     if rows != v_rows:
         raise ValueError(f"{rows} keys and {v_rows} values")
-    rc = binding.lib().gemm_kv_append(cache._ref, K.data_ptr() or None, kr, kh, V.data_ptr() or None, vr, vh, kind,
+    rc = getattr(binding.lib(), cache._append)(cache._ref, K.data_ptr() or None, kr, kh, V.data_ptr() or None, vr, vh, kind,
                                       page_table.data_ptr() or None, width, starts.data_ptr(),
                                       first.data_ptr() or None, rows, sequences, _stream(stream, cache.index))
     if rc:
-        raise GemmError(rc, "gemm_kv_append")
+        raise GemmError(rc, cache._append)
 
 
-def kv_read(cache: KvCache, page_table, starts, first, tokens, dtype=torch.bfloat16, stream=None):
-    """(K, V) read back, each tokens x heads x head_dim of `dtype`: row
+def kv_read(cache, page_table, starts, first, tokens, dtype=torch.bfloat16, stream=None):
+    """(K, V) of a KvCache or Kv4Cache read back, each tokens x heads x head_dim of `dtype`: row
     starts[b] + i is token first[b] + i of sequence b.  `tokens` is starts[-1],
     known on the host."""
     width, sequences = _batch(cache, page_table, starts, first, "first")
@@ -305,18 +343,18 @@ def kv_read(cache: KvCache, page_table, starts, first, tokens, dtype=torch.bfloa
     shape = (tokens, cache.heads, cache.head_dim)
     K = _empty(shape, dtype, cache.device, stream)
     V = _empty(shape, dtype, cache.device, stream)
-    rc = binding.lib().gemm_kv_read(cache._ref, K.data_ptr() or None, V.data_ptr() or None, kind,
+    rc = getattr(binding.lib(), cache._read)(cache._ref, K.data_ptr() or None, V.data_ptr() or None, kind,
                                     page_table.data_ptr() or None, width, starts.data_ptr(),
                                     first.data_ptr() or None, tokens, sequences, _stream(stream, cache.index))
     if rc:
-        raise GemmError(rc, "gemm_kv_read")
+        raise GemmError(rc, cache._read)
     return K, V
 
 
-def kv_attention(Q, cache: KvCache, page_table, starts, lengths, scale=None, causal=True, window=0, out=None,
+def kv_attention(Q, cache, page_table, starts, lengths, scale=None, causal=True, window=0, out=None,
                  stream=None):
     """Attention of Q (tokens x q_heads x head_dim; bfloat16 or float16) over
-    the cache.  Sequence b has lengths[b] tokens and the queries starts[b] ..
+    a KvCache or Kv4Cache.  Sequence b has lengths[b] tokens and the queries starts[b] ..
     starts[b + 1] - 1, which stand at its last positions; with `causal` a query
     sees the tokens up to its own, with `window` > 0 the last `window` of
     them (pages wholly before every window need not be in the table).  scale:
@@ -338,10 +376,10 @@ def kv_attention(Q, cache: KvCache, page_table, starts, lengths, scale=None, cau
         scale = cache.head_dim ** -0.5
     if window >= 1 << 63:       # as good as none, but ctypes would take its low 64 bits
         window = (1 << 63) - 1
-    rc = binding.lib().gemm_kv_attention(cache._ref, Q.data_ptr() or None, qr, qh, out.data_ptr() or None, orow, oh,
+    rc = getattr(binding.lib(), cache._attention)(cache._ref, Q.data_ptr() or None, qr, qh, out.data_ptr() or None, orow, oh,
                                          _TYPES[kind], heads, scale, causal, window, page_table.data_ptr() or None,
                                          width, starts.data_ptr(), lengths.data_ptr() or None, rows, sequences,
                                          _stream(stream, cache.index))
     if rc:
-        raise GemmError(rc, "gemm_kv_attention")
+        raise GemmError(rc, cache._attention)
     return out

@@ -408,6 +408,61 @@ GEMM_API int gemm_kv_attention(const gemm_kv_cache* cache, const void* Q, int64_
                                const int32_t* lengths, int64_t tokens, int64_t sequences,
                                struct CUstream_st* stream);
 
+/*
+ * A paged cache of keys and values in 4 bits.  Pages are as above (page_tokens
+ * tokens of one sequence for every head); what differs is that every token and
+ * head has scales of its own, one for its keys and one for its values, so that a
+ * token is written without a change to any other.  Keys and values of a page and
+ * head are one record of page_tokens * (head_dim + 4) bytes, number p * heads + h:
+ *     key codes     page_tokens * head_dim / 2 bytes
+ *     value codes   the same
+ *     key scales, value scales   bfloat16[page_tokens] each, >= 0 or NaN
+ * A code is a nibble u = c + 8, c in [-7, 7], and stands for c * its scale.  Key
+ * codes: element d of token t is nibble d % 2 (0: the low one) of byte t *
+ * head_dim / 2 + d % 32 / 8 * (head_dim / 8) + d / 32 * 4 + d % 8 / 2.  Value
+ * codes, in blocks of 16 tokens: nibble d % 2 of byte t / 16 * (8 * head_dim) +
+ * t % 16 / 8 * (4 * head_dim) + (4 * (d % 64 / 8) + t % 8 / 2) * (head_dim / 8)
+ * + d / 64 * 8 + d % 8 / 4 * 4 + t % 2 * 2 + d % 4 / 2.  What one lane of a warp
+ * needs of 16 tokens for its matrix instructions is one 16-byte load of each 8
+ * tokens (8-byte with head_dim 64).  `data` is 16-byte aligned; a page needs no initial
+ * contents.  page_tokens and head_dim as above.
+ */
+typedef struct gemm_kv4_cache {
+    void* data;
+    int64_t pages;
+    int32_t heads, page_tokens, head_dim;
+} gemm_kv4_cache;
+
+/*
+ * As gemm_kv_append, into a cache of 4 bits.  Each row's head_dim elements x of a
+ * head get s = max|x| * (1 / 7) (one binary32 product with the binary32 1 / 7),
+ * rounded to bfloat16, and c = x / s rounded to the nearest integer (ties to even)
+ * and held to [-7, 7].  With s under 2^-126 they are zeros (c = 0, s = 0); a
+ * NaN or an infinity makes s NaN, so that this token reads as NaN for that head.
+ * Nothing else of the cache is written: a page may belong to two sequences, as
+ * long as no token of it is written twice in one call.
+ */
+GEMM_API int gemm_kv4_append(const gemm_kv4_cache* cache, const void* K, int64_t k_row_stride,
+                             int64_t k_head_stride, const void* V, int64_t v_row_stride,
+                             int64_t v_head_stride, int type, const int32_t* page_table,
+                             int64_t table_width, const int32_t* starts, const int32_t* first,
+                             int64_t tokens, int64_t sequences, struct CUstream_st* stream);
+
+/* As gemm_kv_read, from a cache of 4 bits. */
+GEMM_API int gemm_kv4_read(const gemm_kv4_cache* cache, void* K, void* V, int type,
+                           const int32_t* page_table, int64_t table_width, const int32_t* starts,
+                           const int32_t* first, int64_t tokens, int64_t sequences,
+                           struct CUstream_st* stream);
+
+/* As gemm_kv_attention, over a cache of 4 bits. */
+GEMM_API int gemm_kv4_attention(const gemm_kv4_cache* cache, const void* Q, int64_t q_row_stride,
+                                int64_t q_head_stride, void* O, int64_t o_row_stride,
+                                int64_t o_head_stride, int type, int32_t q_heads, float scale,
+                                int causal, int64_t window, const int32_t* page_table,
+                                int64_t table_width, const int32_t* starts,
+                                const int32_t* lengths, int64_t tokens, int64_t sequences,
+                                struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif
