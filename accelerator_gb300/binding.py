@@ -51,6 +51,9 @@ SIGNATURES = {
     "gemm_kv_attention": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _int, ctypes.c_int32,
                                  ctypes.c_float, _int, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
 }
+SIGNATURES["gemm_kv_plan"] = (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, ctypes.c_int32, _i64, _i64, *[_vp] * 8])
+SIGNATURES["gemm_rotary"] = (_int, [*[_vp, _i64, _i64, _vp, _i64, _i64, ctypes.c_int32] * 2, _int, _i64, ctypes.c_int32,
+                                    ctypes.c_int32, _int, _vp, _vp, ctypes.c_float, _int, _vp])
 for _name in ("append", "read", "attention"):
     SIGNATURES["gemm_kv4_" + _name] = SIGNATURES["gemm_kv_" + _name]
 

@@ -250,6 +250,33 @@ cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& 
                                 const KvBatch& b, const KvPlan& plan, void* scratch,
                                 unsigned* err, int* launches, cudaStream_t stream);
 
+// ---- what a batch of sequences needs around a cache (sequences.cu) ----
+unsigned sequences_debug_flags();
+// Arrays as in gemm.h.
+struct StepPlan {
+    int32_t* table;
+    const int32_t *lengths, *counts, *free, *available;
+    int32_t *starts, *first, *after, *heights, *left, *positions;
+    int64_t* slots;
+    int64_t width, capacity, tokens, sequences;
+    int page_log2;
+};
+cudaError_t launch_step_plan(const StepPlan& p, unsigned* err, int* launches, cudaStream_t stream);
+// One operand of a rotation; in place if `out` is `in`.
+struct RotaryRows {
+    KvRows in, out;
+    int heads;
+};
+struct RotaryArgs {
+    RotaryRows x[2];
+    int64_t rows;
+    int dim, part;
+    const int32_t* positions;
+    const uint64_t* turns;
+    float magnitude;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, ElemType type, bool interleaved, bool inverse, int num_sms, cudaStream_t stream);
+
 // ---- host-side hooks of the C ABI (api.cu) ----
 // Set-up of the attention kernels on the current device, once; a gemm_status code.
 int attention_setup();

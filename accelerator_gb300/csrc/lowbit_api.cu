@@ -2,29 +2,13 @@
 // (include/gemm.h): argument checks and dispatch.  Host code only.
 #include <cstdint>
 
+#include "api_checks.h"
 #include "gemm.h"
 #include "kernels.h"
 
 namespace {
 
 using namespace libgemm;
-
-constexpr int64_t kIndexMax = 0x7FFFFFFF;          // sizes held in 32 bits, grids
-constexpr int64_t kElemMax = INT64_MAX / 64;
-
-bool type_ok(int type) { return type == GEMM_TYPE_F32 || type == GEMM_TYPE_BF16 || type == GEMM_TYPE_F16; }
-int64_t type_size(int type) { return type == GEMM_TYPE_F32 ? 4 : 2; }
-bool aligned(const void* p, int64_t to) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(to - 1)) == 0; }
-
-bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return abytes > 0 && bbytes > 0 && x < y + (uint64_t)bbytes && y < x + (uint64_t)abytes;
-}
-
-// Bytes spanned by rows x cols elements of row stride ld.
-int64_t span(int64_t rows, int64_t cols, int64_t ld, int64_t es) {
-    return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * es : 0;
-}
 
 int w4_shape(int64_t K, int64_t N, int group, int64_t* codes, int64_t* scales) {
     if (K < 0 || N < 0 || K > kIndexMax - 255 || N > kIndexMax - 255) return GEMM_ERR_INVALID_ARG;
@@ -101,27 +85,6 @@ int kv_view(const Cache* c, const int32_t* table, int64_t width, const int32_t* 
     *view = view_of(c, log2);
     *batch = KvBatch{table, starts, at, width, tokens, (int)sequences};
     return GEMM_OK;
-}
-
-bool strides_ok(int64_t rows, int64_t heads, int64_t row, int64_t head) {
-    return row >= 0 && head >= 0 && row <= kElemMax / 4 / (rows > 0 ? rows : 1) && head <= kElemMax / 4 / heads;
-}
-
-int64_t rows_span(int64_t rows, int64_t heads, int64_t dim, int64_t row, int64_t head, int64_t es) {
-    return rows > 0 ? ((rows - 1) * row + (heads - 1) * head + dim) * es : 0;
-}
-
-// Whether two elements of rows x heads x dim with these strides are one: a
-// result that many threads write has to have a place for each.
-bool overlap_within(int64_t rows, int64_t heads, int64_t dim, int64_t row, int64_t head) {
-    if ((rows > 1 && row < dim) || (heads > 1 && head < dim)) return true;
-    if (rows <= 1 || heads <= 1 || row >= (heads - 1) * head + dim || head >= (rows - 1) * row + dim) return false;
-    for (int64_t h = 1; h < heads; ++h) {   // neither lies inside the other: h heads on as far as r rows on, or nearly?
-        const int64_t below = h * head / row;
-        for (int64_t r = below > 0 ? below : 1; r <= below + 1 && r < rows; ++r)
-            if (r * row - h * head < dim && h * head - r * row < dim) return true;
-    }
-    return false;
 }
 
 bool overlaps_cache(const KvView& v, const void* p, int64_t bytes) {

@@ -463,6 +463,78 @@ GEMM_API int gemm_kv4_attention(const gemm_kv4_cache* cache, const void* Q, int6
                                 const int32_t* lengths, int64_t tokens, int64_t sequences,
                                 struct CUstream_st* stream);
 
+/*
+ * ---- what a batch of sequences needs around a cache ----------------------
+ */
+
+/*
+ * The plan of a step, made on the device from what is there: row offsets,
+ * positions and slots of the new tokens, and the pages that they need.
+ *   lengths         int32[sequences]: tokens that each sequence has in the cache
+ *   counts          int32[sequences]: how many it gets (0: it rests)
+ *   free_pages      int32[free_capacity]: a stack of free pages, of which the
+ *                   first available[0] are on it
+ *   page_table      as above; its columns up to a sequence's present length
+ *                   name its pages, the others are written here
+ * and it writes
+ *   starts          int32[sequences + 1]: exclusive sums of the counts
+ *   first           int32[sequences]: the lengths as they were
+ *   new_lengths     int32[sequences]: lengths + counts; may be `lengths`
+ *   page_table      the pages that the new tokens begin: taken off the stack's
+ *                   top in the order of sequences and tokens
+ *   heights         int32[sequences + 1]: the stack's height before each sequence
+ *                   takes its pages, and after the last one (under 0: so many
+ *                   were missing)
+ *   left            int32[1]: what is left on the stack; may be `available`
+ *   positions       int32[tokens]: first[b] + i in row starts[b] + i
+ *   slots           int64[tokens]: page * page_tokens + position % page_tokens of
+ *                   that token's page, -1 where it has none
+ * `tokens` is the room that positions and slots have; rows past starts[sequences]
+ * get -1 in both.  page_tokens is a power of 2 up to 2^20.  Reported as
+ * GEMM_ERR_INDEX: a negative length or count (taken for 0), counts whose sum
+ * is over `tokens` (starts ends there and rows past it are not written), a sequence
+ * longer than the table is wide or a stack that runs out (the tokens without a page
+ * have -1 in slots, and, inside the table, in page_table), a height over free_capacity.
+ * The arrays do not overlap but where said.
+ */
+GEMM_API int gemm_kv_plan(int32_t* page_table, int64_t table_width, const int32_t* lengths,
+                          const int32_t* counts, const int32_t* free_pages,
+                          int64_t free_capacity, const int32_t* available, int32_t page_tokens,
+                          int64_t tokens, int64_t sequences, int32_t* starts, int32_t* first,
+                          int32_t* new_lengths, int32_t* heights, int32_t* left,
+                          int32_t* positions, int64_t* slots, struct CUstream_st* stream);
+
+/* How the elements of a head pair up: i with i + rotary_dim / 2, or 2i with 2i + 1. */
+enum gemm_rotary_layout { GEMM_ROTARY_HALF = 0, GEMM_ROTARY_INTERLEAVED = 1 };
+
+/*
+ * Rotary positions.  Pair i (i < rotary_dim / 2) of every head in row r, the
+ * elements (a, b), becomes
+ *     magnitude * (a cos x - b sin x),  magnitude * (b cos x + a sin x)
+ * with x = positions[r] * frequency i; with inverse != 0 by -x, which is the
+ * transposed map: the gradient's way back.  Elements from rotary_dim on are
+ * copied.  A row with a negative position is left as it is (its results are not
+ * written).
+ *   Q, K      rows of q_heads and k_heads heads of head_dim elements of `type`
+ *             (strides in elements, >= 0); K may be NULL with k_heads 0
+ *   Q_out, K_out  the results, likewise; each may be its input (same address and
+ *             strides) and must not overlap anything else.  Slices of one array do not
+ *             overlap where rows or heads of one lie between those of the other.
+ *   head_dim  up to 1024; rotary_dim: even, 2 .. head_dim
+ *   positions int32[rows], on the device
+ *   turns     uint64[rotary_dim / 2], on the device: frequency i in turns
+ *             (radians / 2 pi) a position, times 2^64, rounded.  The angle is the
+ *             product's fraction of a turn, exact for every position.
+ * Sines and cosines, products and sums are binary32; a result is rounded once.
+ */
+GEMM_API int gemm_rotary(const void* Q, int64_t q_row_stride, int64_t q_head_stride, void* Q_out,
+                         int64_t q_out_row_stride, int64_t q_out_head_stride, int32_t q_heads,
+                         const void* K, int64_t k_row_stride, int64_t k_head_stride, void* K_out,
+                         int64_t k_out_row_stride, int64_t k_out_head_stride, int32_t k_heads,
+                         int type, int64_t rows, int32_t head_dim, int32_t rotary_dim, int layout,
+                         const int32_t* positions, const uint64_t* turns, float magnitude,
+                         int inverse, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif
