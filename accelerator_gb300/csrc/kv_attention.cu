@@ -554,9 +554,10 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, cudaStream_t stream) {
 template <typename T, int D>
 cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStream_t stream) {
     const ElemType type = std::is_same<T, __half>::value ? ElemType::kF16 : ElemType::kBF16;
-    cudaError_t e = plan.rows == 8    ? launch<T, D, 1>(a, plan, stream)
-                    : plan.rows == 16 ? launch<T, D, 2>(a, plan, stream)
-                                      : launch_kv_prompt(a, type, plan, stream);
+    cudaError_t e = plan.rows == 256  ? launch_kv_prompt(a, type, plan, stream)
+                    : a.c.bits == 4   ? launch_kv4_few(a, type, plan, stream)
+                    : plan.rows == 8  ? launch<T, D, 1>(a, plan, stream)
+                                      : launch<T, D, 2>(a, plan, stream);
     *launches = 1;
     if (e == cudaSuccess && a.partial) {
         static_assert(kStep == 128, "both kernels count tokens in the same steps");
@@ -595,6 +596,7 @@ cudaError_t kv_attention_setup() {
     if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, 128>();
     if (e == cudaSuccess) e = allow_smem<__half, 64>();
     if (e == cudaSuccess) e = allow_smem<__half, 128>();
+    if (e == cudaSuccess) e = kv4_attention_setup();
     return e == cudaSuccess ? kv_prompt_setup() : e;
 }
 
@@ -622,7 +624,7 @@ KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, i
     KvPlan p;
     const int64_t share = q_heads / c.heads, all = b.rows * share;
     p.rows = all <= 8 * (int64_t)b.sequences    ? 8
-             : all <= kPromptRows * b.sequences ? 16
+             : all <= kPromptRows * b.sequences || c.bits == 4 ? 16
                                                 : 256;
     const int64_t tiles = all / p.rows;
     p.gap = p.rows - (int)gcd(p.rows, share);
@@ -655,10 +657,6 @@ cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& 
     const bool q_vec = (reinterpret_cast<uintptr_t>(Q.p) & 15u) == 0 && Q.row % 8 == 0 && Q.head % 8 == 0;
     const AttnArgs a{c, Q, O, b, q_heads, (unsigned)(q_heads / c.heads), plan.gap, scale * 1.44269504088896341f, causal,
                      (int)(window < INT32_MAX ? window : INT32_MAX), plan.splits, q_vec, plan.scratch_bytes, static_cast<float*>(scratch), err};
-    if (c.bits == 4) {
-        *launches = 1;
-        return launch_kv4_few(a, type, plan, stream);
-    }
     if (type == ElemType::kBF16)
         return c.dim == 128 ? launch<__nv_bfloat16, 128>(a, plan, launches, stream)
                             : launch<__nv_bfloat16, 64>(a, plan, launches, stream);

@@ -111,7 +111,8 @@ __device__ __forceinline__ T* out_row(const AttnArgs& a, const Tile& tile, int h
 
 // Many query rows (kv_prompt.cu): tiles of plan.rows = 256, tokens in steps of 128.
 cudaError_t kv_prompt_setup();
-// A cache in 4 bits (kv4_attention.cu).
+// Few query rows over a cache in 4 bits (kv4_attention.cu): tiles of 8 or 16.
+cudaError_t kv4_attention_setup();
 cudaError_t launch_kv4_few(const AttnArgs& a, ElemType type, const KvPlan& plan, cudaStream_t stream);
 cudaError_t launch_kv_prompt(const AttnArgs& a, ElemType type, const KvPlan& plan, cudaStream_t stream);
 

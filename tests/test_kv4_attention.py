@@ -136,7 +136,7 @@ def test_what_no_row_sees_is_not_used(libgemm, dim, kind, page, rows):
     Q = p.queries(rows, 8, kind)
     want, inside = (ref.check(libgemm, p, Q, [rows], [length], window=w) for w in (0, 40))
     used = [p.page_of(0, i) for i in range(-(-length // page))]
-    for poison in (float("nan"), float("inf"), 3e38):
+    for poison in (float("nan"), float("inf"), -float("inf"), 3e38, -3e38):
         for s in p.scales:
             for other in set(range(s.shape[0])) - set(used):
                 s[other] = poison
