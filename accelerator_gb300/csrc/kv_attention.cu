@@ -624,7 +624,7 @@ KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, i
     KvPlan p;
     const int64_t share = q_heads / c.heads, all = b.rows * share;
     p.rows = all <= 8 * (int64_t)b.sequences    ? 8
-             : all <= kPromptRows * b.sequences || c.bits == 4 ? 16
+             : all <= kPromptRows * b.sequences ? 16
                                                 : 256;
     const int64_t tiles = all / p.rows;
     p.gap = p.rows - (int)gcd(p.rows, share);

@@ -1,5 +1,5 @@
-// kv_prompt.cu -- attention of many query rows (prompts) over the paged 8-bit
-// cache, on the 5th-generation tensor cores.
+// kv_prompt.cu -- attention of many query rows (prompts) over a paged cache of 8
+// or 4 bits, on the 5th-generation tensor cores.
 //
 // One CTA takes 256 query rows of a sequence and cache head -- two tiles of
 // 128, so that what is done to the keys and values of a block of 128 tokens
@@ -31,6 +31,14 @@
 // early (511 us: a product 64 wide takes the matrix unit as long as one 128 wide,
 // 515 cycles).
 //
+// 4 bits.  A token's keys and values have scales of their own, and a code times its
+// scale, c in [-7, 7] times 8 bits, is exact in binary16's 11.  So the copying warp
+// brings the scales of 16 tokens down by one power of two, the largest into [2^11,
+// 2^12), as binary16 (exact for those over 2^-28 of the largest), the cache's
+// warps multiply codes by them, and what stands outside of the products is that
+// power of two alone, where the 8-bit cache has its page's scale.  Scales of tokens
+// that no row of the tile sees are taken for 0.
+//
 // Every wait is bounded; a role that gives up raises the abort flag, all stop,
 // and the matrix unit is drained before tensor memory is freed.
 #include "kv_attention.cuh"
@@ -43,9 +51,13 @@ constexpr int kSub = 16, kSubs = kStep / kSub;               // tokens that shar
 constexpr int kSlots = 4;                                    // blocks whose page data are kept
 constexpr int kSoftWarps = 8, kCacheWarps = 4, kThreads = (kSoftWarps + kCacheWarps + 4) * 32;
 // Registers of a thread: launched with 128, then shared out among the roles
-// (whole warpgroups), whose sum is that of the launch.
-constexpr int kLaunchRegs = 128, kSoftRegs = 184, kCacheRegs = 104, kIssueRegs = 40;
-static_assert(kSoftRegs * kSoftWarps + kCacheRegs * kCacheWarps + kIssueRegs * 4 <= kLaunchRegs * kThreads / 32, "");
+// (whole warpgroups), whose sum is that of the launch.  Of 4 bits the copying warp
+// also looks after scales.
+constexpr int kLaunchRegs = 128, kSoftRegs = 184;
+constexpr int cache_regs(int bits) { return bits == 8 ? 104 : 88; }
+constexpr int issue_regs(int bits) { return bits == 8 ? 40 : 56; }
+static_assert(kSoftRegs * kSoftWarps + cache_regs(8) * kCacheWarps + issue_regs(8) * 4 <= kLaunchRegs * kThreads / 32, "");
+static_assert(kSoftRegs * kSoftWarps + cache_regs(4) * kCacheWarps + issue_regs(4) * 4 <= kLaunchRegs * kThreads / 32, "");
 constexpr int kSlab = kTile * 128;                           // 128 rows of 64 binary16
 
 // What a softmax thread needs of 16 tokens: the key scale, log2 of the
@@ -53,13 +65,16 @@ constexpr int kSlab = kTile * 128;                           // 128 rows of 64 b
 struct alignas(16) PageData {
     float ks, log_v;
     uint32_t plain;      // 1: there, and reads as numbers; 0: reads as NaN; 2: not there
+    uint32_t nan;        // the tokens that do, of 0 in `plain`
 };
 
-template <int D>
+template <int D, int BITS>
 struct Smem {
     static constexpr int kOperand = D / 64 * kSlab;          // 128 x D binary16
     static constexpr int kQ = 0, kK = 2 * kOperand, kV = kK + 2 * kOperand;
-    static constexpr int kCodes = kV + 2 * kOperand, kInfo = kCodes + 2 * kStep * D;   // codes: keys, values
+    static constexpr int kCodeBytes = kStep * D * BITS / 8;  // keys' and values' each
+    static constexpr int kCodes = kV + 2 * kOperand, kScales = kCodes + 2 * kCodeBytes;
+    static constexpr int kInfo = kScales + (BITS == 4 ? 2 * kStep * 2 : 0);   // binary16 scales, keys' and values'
     static constexpr int kBars = kInfo + kSlots * kSubs * (int)sizeof(PageData);
     static constexpr int kBytes = kBars + 256 + 1024;        // and the alignment
 };
@@ -113,9 +128,15 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 // Chunk c (eight binary16) of row r of a 64-wide slab: 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-template <typename T, int D>
+// Nibbles of a word, c = u - 8 as pairs of binary16: bits 0-3 with 16-19, and 4-7 with 20-23.
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t bits_of(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+__device__ __forceinline__ __half2 nibbles_low(uint32_t w) { return __hsub2(as_half2((w & 0x000F000Fu) | 0x64006400u), as_half2(0x64086408u)); }    // 1024 + u
+__device__ __forceinline__ __half2 nibbles_high(uint32_t w) { return __hsub2(as_half2((w & 0x00F000F0u) | 0x54005400u), as_half2(0x54805480u)); }   // 64 + u
+
+template <typename T, int D, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a, bool o_vec) {
-    using L = Smem<D>;
+    using L = Smem<D, BITS>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -192,9 +213,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
         for (int c = 0; c < D / 8; ++c) {
             Eight<T> x = {};
             if (live && GEMM_DBG_OK(p + 8 * c, a.Q.p, q_bytes, 16)) x = load_eight(p + 8 * c, a.q_vec);
-            st_shared_v4(q0 + c / 8 * kSlab + swizzled(in_tile, c % 8), pack2<__half>(x.at(0) * down, x.at(1) * down),
-                         pack2<__half>(x.at(2) * down, x.at(3) * down), pack2<__half>(x.at(4) * down, x.at(5) * down),
-                         pack2<__half>(x.at(6) * down, x.at(7) * down));
+            // in the order in which a chunk has the keys' elements: of 4 bits e beside e + 4
+            constexpr int kMate = BITS == 4 ? 4 : 1, kNext = BITS == 4 ? 1 : 2;
+            auto two = [&](int i) { return pack2<__half>(x.at(kNext * i) * down, x.at(kNext * i + kMate) * down); };
+            st_shared_v4(q0 + c / 8 * kSlab + swizzled(in_tile, c % 8), two(0), two(1), two(2), two(3));
         }
         fence_proxy_async_shared();
     }
@@ -205,30 +227,93 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
 
     if (warp >= kSoftWarps && warp < kSoftWarps + kCacheWarps) {
         // ---------------- the cache ----------------
-        fewer_registers<kCacheRegs>();
-        constexpr int kLanes = D / 16;                  // lanes of a token, 16 codes each
+        fewer_registers<cache_regs(BITS)>();
+        // 8 bits: lanes of a token, 16 codes each; 4 bits: pieces of D / 8 bytes, of a
+        // token's keys and of two tokens' values.
+        constexpr int kLanes = BITS == 8 ? D / 16 : 4, kWords = D / 32;
         constexpr int kPassRows = kCacheWarps * 32 / kLanes, kPasses = kStep / kPassRows;
         const int ct = threadIdx.x - kSoftWarps * 32;
-        // A quarter of a warp holds halves of two neighbouring rows: its 16-byte
-        // stores then meet all eight chunk positions of the swizzle.
-        const int piece = D == 128 ? ct % 4 + 4 * (ct / 8 % 2) : ct % 4;
-        const int sub_row = D == 128 ? ct / 16 * 2 + ct / 4 % 2 : ct / 4;
-        uint4 w[kPasses];
+        // A quarter of a warp holds halves of two rows, neighbours or (4 bits) four
+        // apart: its 16-byte stores then meet all eight chunk positions of the swizzle.
+        const int piece = D == 128 && BITS == 8 ? ct % 4 + 4 * (ct / 8 % 2) : ct % 4;
+        const int sub_row = BITS == 4 ? ct / 32 * 8 + ct / 8 % 4 + 4 * (ct / 4 % 2) : D == 128 ? ct / 16 * 2 + ct / 4 % 2 : ct / 4;
+        uint4 w[BITS == 8 ? kPasses : 1];
+        uint32_t words[BITS == 4 ? kPasses : 1][kWords], scales[BITS == 4 ? kPasses : 1];
         auto get = [&](int values, uint32_t parity) {
             if (!warp_wait(bars + 8 * (kCFull + values), parity, abort_flag, a.err)) return false;
-            const uint32_t from = base + L::kCodes + values * (kStep * D) + sub_row * D + 16 * piece;
+            const uint32_t codes = base + L::kCodes + values * L::kCodeBytes;
+            if constexpr (BITS == 8) {
+                const uint32_t from = codes + sub_row * D + 16 * piece;
 #pragma unroll
-            for (int i = 0; i < kPasses; ++i) w[i] = lds128(from + i * kPassRows * D);
+                for (int i = 0; i < kPasses; ++i) w[i] = lds128(from + i * kPassRows * D);
+            } else {
+                const uint32_t at = base + L::kScales + values * (2 * kStep);
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    // values: warp by warp the eights of tokens, of which a lane has a pair
+                    const int row = sub_row + i * kPassRows, eight = i * kCacheWarps + ct / 32;
+                    const uint32_t from = codes + (values ? eight * (4 * D) + ct % 32 * (D / 8) : row * (D / 2) + piece * (D / 8));
+                    if constexpr (D == 128) {
+                        const uint4 v = lds128(from);
+                        words[i][0] = v.x, words[i][1] = v.y, words[i][2] = v.z, words[i][3] = v.w;
+                    } else {
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(words[i][0]), "=r"(words[i][1]) : "r"(from));
+                    }
+                    if (values) {
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(scales[i]) : "r"(at + 2 * (8 * eight + 2 * (ct % 4))));
+                    } else {
+                        uint16_t one;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(one) : "r"(at + 2 * row));
+                        scales[i] = (uint32_t)one * 0x10001u;
+                    }
+                }
+            }
             return true;
         };
-        auto put = [&](uint32_t to) {
-            const int c = 2 * piece % 8;
-            const uint32_t at = to + 2 * piece / 8 * kSlab + sub_row * 128, r = sub_row & 7;
+        auto put = [&](int values, uint32_t to) {
+            if constexpr (BITS == 8) {
+                const int c = 2 * piece % 8;
+                const uint32_t at = to + 2 * piece / 8 * kSlab + sub_row * 128, r = sub_row & 7;
 #pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                const uint32_t row = at + i * kPassRows * 128;
-                st_shared_v4(row + ((c ^ r) << 4), codes01(w[i].x), codes23(w[i].x), codes01(w[i].y), codes23(w[i].y));
-                st_shared_v4(row + (((c + 1) ^ r) << 4), codes01(w[i].z), codes23(w[i].z), codes01(w[i].w), codes23(w[i].w));
+                for (int i = 0; i < kPasses; ++i) {
+                    const uint32_t row = at + i * kPassRows * 128;
+                    st_shared_v4(row + ((c ^ r) << 4), codes01(w[i].x), codes23(w[i].x), codes01(w[i].y), codes23(w[i].y));
+                    st_shared_v4(row + (((c + 1) ^ r) << 4), codes01(w[i].z), codes23(w[i].z), codes01(w[i].w), codes23(w[i].w));
+                }
+            } else if (!values) {   // word e is the chunk of elements 32 e + 8 piece on
+                const uint32_t at = to + sub_row * 128, r = sub_row & 7;
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const __half2 s = as_half2(scales[i]);
+#pragma unroll
+                    for (int e = 0; e < kWords; ++e) {
+                        const uint32_t x = words[i][e], y = x >> 8;
+                        st_shared_v4(at + e / 2 * kSlab + i * kPassRows * 128 + (((4 * (e % 2) + piece) ^ r) << 4),
+                                     bits_of(__hmul2(nibbles_low(x), s)), bits_of(__hmul2(nibbles_high(x), s)),
+                                     bits_of(__hmul2(nibbles_low(y), s)), bits_of(__hmul2(nibbles_high(y), s)));
+                    }
+                }
+            } else {                // words 2e, 2e + 1 are four elements each of two tokens, chunk g of slab e
+                const int g = ct % 32 / 4, t = ct % 4;
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const uint32_t at = to + (8 * (i * kCacheWarps + ct / 32) + 2 * t) * 128;
+                    const __half2 s = as_half2(scales[i]);
+#pragma unroll
+                    for (int e = 0; e < D / 64; ++e) {
+                        uint32_t even[4], odd[4];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t x = words[i][2 * e + q], y = x >> 8;
+                            const uint32_t d0 = bits_of(__hmul2(nibbles_low(x), s)), d1 = bits_of(__hmul2(nibbles_high(x), s));
+                            const uint32_t d2 = bits_of(__hmul2(nibbles_low(y), s)), d3 = bits_of(__hmul2(nibbles_high(y), s));
+                            even[2 * q] = __byte_perm(d0, d1, 0x5410), even[2 * q + 1] = __byte_perm(d2, d3, 0x5410);
+                            odd[2 * q] = __byte_perm(d0, d1, 0x7632), odd[2 * q + 1] = __byte_perm(d2, d3, 0x7632);
+                        }
+                        st_shared_v4(at + e * kSlab + ((g ^ (2 * t)) << 4), even[0], even[1], even[2], even[3]);
+                        st_shared_v4(at + e * kSlab + 128 + ((g ^ (2 * t + 1)) << 4), odd[0], odd[1], odd[2], odd[3]);
+                    }
+                }
             }
             fence_proxy_async_shared();
         };
@@ -238,17 +323,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             if (!get(0, (uint32_t)j & 1u)) break;
             warp_arrive(bars + 8 * kCEmpty);
             if (!warp_wait(bars + 8 * (kKEmpty + buf), parity ^ 1u, abort_flag, a.err)) break;
-            put(base + L::kK + buf * L::kOperand);
+            put(0, base + L::kK + buf * L::kOperand);
             warp_arrive(bars + 8 * (kKFull + buf));
             if (!get(1, (uint32_t)j & 1u)) break;
             warp_arrive(bars + 8 * (kCEmpty + 1));
             if (!warp_wait(bars + 8 * (kVEmpty + buf), parity ^ 1u, abort_flag, a.err)) break;
-            put(base + L::kV + buf * L::kOperand);
+            put(1, base + L::kV + buf * L::kOperand);
             warp_arrive(bars + 8 * (kVFull + buf));
         }
     } else if (warp >= kSoftWarps + kCacheWarps) {
         // ---------------- the matrix unit ----------------
-        fewer_registers<kIssueRegs>();
+        fewer_registers<issue_regs(BITS)>();
         if (threadIdx.x == (kSoftWarps + kCacheWarps) * 32) {
             constexpr uint32_t kIdS = make_idesc(0, kTile, kStep, false, false), kIdO = make_idesc(0, kTile, D, false, true);
             auto scores = [&](int i, int buf) {   // S_i = Q_i K^T
@@ -298,18 +383,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             drain(bars + 8 * kDrain, 0, a.err);
         }
         if (warp == kSoftWarps + kCacheWarps + 1) {
-            // ---------------- the copies: lane i < 8 looks after 16 tokens of a block ----------------
+            // ---------------- the copies: lane i < 8 looks after 16 tokens of a block,
+            // of 4 bits lane i after 4, whose scales it brings down ----------------
+            constexpr int kTokens = BITS == 8 ? kSub : 4;
             [[maybe_unused]] const int64_t code_bytes = a.c.pages * a.c.heads * ((int64_t)D << log2);
+            [[maybe_unused]] const int64_t extent = a.c.pages * a.c.heads * a.c.record();
             const int chunk = min(kStep, 1 << log2);   // tokens of one copy
-            struct Sub { int64_t from; float ks, vs; bool live; };
+            struct Sub { int64_t from; float ks, vs; bool live; uint2 scales[BITS == 4 ? 2 : 1]; };
             auto look = [&](int j) {
-                Sub s{0, 0.0f, 0.0f, false};
-                const int tok = tok_begin + j * kStep + lane * kSub;
-                if (lane < kSubs && j < blocks && tile.page_seen(tok, log2)) {
+                Sub s{0, 0.0f, 0.0f, false, {}};
+                const int tok = tok_begin + j * kStep + lane * kTokens;
+                if (lane * kTokens < kStep && j < blocks && tile.page_seen(tok, log2)) {
                     const int64_t page = __ldg(table + (tok >> log2));
                     s.live = page >= 0 && page < a.c.pages;
                     if (!s.live) atomicOr(a.err, kErrIndex);
-                    else {
+                    else if constexpr (BITS == 4) {
+                        s.from = (page * a.c.heads + h) * a.c.record();   // of the page
+                        const uint8_t* at = a.c.data + s.from + (D << log2) + 2 * (tok & ((1 << log2) - 1));
+                        if (GEMM_DBG_OK(at, a.c.data, extent, 8)) s.scales[0] = __ldg(reinterpret_cast<const uint2*>(at));
+                        at += 2 << log2;
+                        if (GEMM_DBG_OK(at, a.c.data, extent, 8)) s.scales[1] = __ldg(reinterpret_cast<const uint2*>(at));
+                    } else {
                         const int64_t ph = page * a.c.heads + h;
                         s.from = ((ph << log2) + (tok & ((1 << log2) - 1))) * D;
                         s.ks = __ldg(a.c.ks + ph);
@@ -322,25 +416,66 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             int issued[2] = {0, 0};
             for (int j = 0; j < blocks; ++j) {
                 const Sub next = look(j + 1);
-                // the first 16 tokens of a page's part fetch all of it
-                bool copies = now.live && lane * kSub % chunk == 0;
-                if (copies) copies = GEMM_DBG_OK(a.c.k + now.from, a.c.k, code_bytes, chunk * D) && GEMM_DBG_OK(a.c.v + now.from, a.c.v, code_bytes, chunk * D);
-                const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xFFFFFFFFu, copies)) * chunk * D);
+                // the first tokens of a page's part fetch all of it
+                bool copies = now.live && lane * kTokens % chunk == 0;
+                if constexpr (BITS == 8) {
+                    if (copies) copies = GEMM_DBG_OK(a.c.k + now.from, a.c.k, code_bytes, chunk * D) && GEMM_DBG_OK(a.c.v + now.from, a.c.v, code_bytes, chunk * D);
+                } else {
+                    if (copies) copies = GEMM_DBG_OK(a.c.data + now.from, a.c.data, extent, chunk * D);
+                }
+                const uint32_t part = (uint32_t)(chunk * D * BITS / 8), bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, copies)) * part;
+                // 4 bits: of both operands, this lane's scales as binary16 times 2^(138 - e),
+                // e the largest's biased exponent of 16 tokens; bit i of `nan`: token i of these
+                uint32_t held[2][2] = {}, unit[2] = {}, nan = 0;
+                bool zero[2] = {};
+                if constexpr (BITS == 4) {
+                    const int tok = tok_begin + j * kStep + lane * kTokens;
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        uint32_t bits[4] = {now.scales[v].x & 0x7FFFu, now.scales[v].x >> 16 & 0x7FFFu, now.scales[v].y & 0x7FFFu, now.scales[v].y >> 16 & 0x7FFFu};
+                        uint32_t most = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (!now.live || tok + i < tile.lo || tok + i >= tile.hi) bits[i] = 0;
+                            if (bits[i] >= 0x7F80u) nan |= 1u << (lane % 4 * 4 + i), bits[i] = 0;
+                            most = max(most, bits[i]);
+                        }
+                        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+                        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+                        const uint32_t e = max(most >> 7, 12u);   // so that the power of two and its inverse are normal
+                        const float by = __uint_as_float((265u - e) << 23);
+                        held[v][0] = pack2<__half>(__uint_as_float(bits[0] << 16) * by, __uint_as_float(bits[1] << 16) * by);
+                        held[v][1] = pack2<__half>(__uint_as_float(bits[2] << 16) * by, __uint_as_float(bits[3] << 16) * by);
+                        unit[v] = e;
+                        zero[v] = most == 0;
+                    }
+                    nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, 1);
+                    nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, 2);
+                }
                 bool ok = true;
 #pragma unroll
                 for (int values = 0; values < 2; ++values) {
                     // Page data of block j go where those of block j - 4 were: its keys' turn
                     // comes when the keys of j - 1 are taken, so the values of j - 4 are used up.
                     if (!(ok = warp_wait(bars + 8 * (kCEmpty + values), ((uint32_t)j & 1u) ^ 1u, abort_flag, a.err))) break;
-                    if (values == 0 && lane < kSubs) {
+                    if constexpr (BITS == 4) {
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(base + L::kScales + values * (2 * kStep) + 8 * lane),
+                                     "r"(values ? held[1][0] : held[0][0]), "r"(values ? held[1][1] : held[0][1])
+                                     : "memory");
+                        if (values == 0 && lane % 4 == 0)
+                            info[j % kSlots * kSubs + lane / 4] =
+                                PageData{__uint_as_float((unit[0] - 11u) << 23), zero[1] ? kNegInf : (float)((int)unit[1] - 138), !now.live ? 2u : nan ? 0u : 1u, nan};
+                    } else if (values == 0 && lane < kSubs) {
                         const bool plain = now.live && now.ks == now.ks && now.vs == now.vs;
-                        info[j % kSlots * kSubs + lane] = PageData{now.ks, plain ? log2f(now.vs) : 0.0f, plain ? 1u : now.live ? 0u : 2u};
+                        info[j % kSlots * kSubs + lane] = PageData{now.ks, plain ? log2f(now.vs) : 0.0f, plain ? 1u : now.live ? 0u : 2u, 0xFFFFu};
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(bars + 8 * (kCFull + values), bytes);
                     __syncwarp();
-                    if (copies)
-                        bulk_load(base + L::kCodes + values * (kStep * D) + lane * kSub * D, (values ? a.c.v : a.c.k) + now.from, chunk * D, bars + 8 * (kCFull + values));
+                    if (copies) {
+                        const uint8_t* from = BITS == 4 ? a.c.data + now.from + values * part : (values ? a.c.v : a.c.k) + now.from;
+                        bulk_load(base + L::kCodes + values * L::kCodeBytes + lane * kTokens * (D * BITS / 8), from, part, bars + 8 * (kCFull + values));
+                    }
                     issued[values] = j + 1;
                 }
                 if (!ok) break;
@@ -410,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                         for (int e = 0; e < kSub; ++e) {
                             uint32_t& x = v[b / 2][b % 2 * 16 + e];
                             if (kind == 2u) x = 0xFF800000u;
-                            else if (x != 0xFF800000u) x = 0x7FC00000u;
+                            else if (x != 0xFF800000u && (BITS == 8 || page[b].nan >> e & 1u)) x = 0x7FC00000u;
                         }
                     }
                     asm volatile("");
@@ -427,9 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                 }
             }
             // The sums so far are brought to new maxima only when one is passed (that of
-            // the scores, which the binary32 sum is relative to, by more).
-            if (__any_sync(0xFFFFFFFFu, top > m + 16.0f || top_v > mv + kLag)) {
-                const float nm = fmaxf(m, top), nmv = fmaxf(mv, top_v), keep = exp2_approx(mv - nmv);
+            // the scores, which the binary32 sum is relative to, by more); of 4 bits in
+            // the rows alone that passed one, whatever their neighbours do.
+            const bool passed = top > m + 16.0f || top_v > mv + kLag;
+            if (__any_sync(0xFFFFFFFFu, passed)) {
+                const bool mine = BITS == 8 || passed;
+                const float nm = mine ? fmaxf(m, top) : m, nmv = mine ? fmaxf(mv, top_v) : mv, keep = exp2_approx(mv - nmv);
                 l *= exp2_approx(m - nm);
                 m = nm;
                 mv = nmv;
@@ -540,21 +678,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, int BITS>
 cudaError_t launch(const AttnArgs& a, const KvPlan& plan, cudaStream_t stream) {
     const bool o_vec = (reinterpret_cast<uintptr_t>(a.O.p) & 15u) == 0 && a.O.row % 8 == 0 && a.O.head % 8 == 0;
-    kv_prompt_kernel<T, D><<<(unsigned)(plan.units * plan.splits * a.c.heads), kThreads, Smem<D>::kBytes, stream>>>(a, o_vec);
+    kv_prompt_kernel<T, D, BITS><<<(unsigned)(plan.units * plan.splits * a.c.heads), kThreads, Smem<D, BITS>::kBytes, stream>>>(a, o_vec);
     return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <typename T, int D, int BITS>
 cudaError_t allow_smem() {
     // The roles' shares of the registers would wait for ever if the launch had fewer.
     cudaFuncAttributes f;
-    const cudaError_t e = cudaFuncGetAttributes(&f, kv_prompt_kernel<T, D>);
+    const cudaError_t e = cudaFuncGetAttributes(&f, kv_prompt_kernel<T, D, BITS>);
     if (e != cudaSuccess) return e;
     if (f.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-    return cudaFuncSetAttribute(kv_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+    return cudaFuncSetAttribute(kv_prompt_kernel<T, D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, BITS>::kBytes);
+}
+
+// Calls f with a kernel's type, head size and bits.
+template <typename F>
+cudaError_t with_kernel(ElemType type, int dim, int bits, F f) {
+    using std::integral_constant;
+    auto by_bits = [&](auto t, auto d) { return bits == 4 ? f(t, d, integral_constant<int, 4>()) : f(t, d, integral_constant<int, 8>()); };
+    auto by_dim = [&](auto t) { return dim == 64 ? by_bits(t, integral_constant<int, 64>()) : by_bits(t, integral_constant<int, 128>()); };
+    return type == ElemType::kBF16 ? by_dim(__nv_bfloat16()) : by_dim(__half());
 }
 
 }  // namespace
@@ -562,17 +709,21 @@ cudaError_t allow_smem() {
 LIBGEMM_DEBUG_READER(kv_prompt_debug_flags)
 
 cudaError_t kv_prompt_setup() {
-    cudaError_t e = allow_smem<__nv_bfloat16, 64>();
-    if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, 128>();
-    if (e == cudaSuccess) e = allow_smem<__half, 64>();
-    if (e == cudaSuccess) e = allow_smem<__half, 128>();
-    return e;
+    for (ElemType type : {ElemType::kBF16, ElemType::kF16})
+        for (int dim : {64, 128})
+            for (int bits : {4, 8}) {
+                const cudaError_t e = with_kernel(type, dim, bits, [](auto t, auto d, auto b) {
+                    return allow_smem<decltype(t), decltype(d)::value, decltype(b)::value>();
+                });
+                if (e != cudaSuccess) return e;
+            }
+    return cudaSuccess;
 }
 
 cudaError_t launch_kv_prompt(const AttnArgs& a, ElemType type, const KvPlan& plan, cudaStream_t stream) {
-    if (type == ElemType::kBF16)
-        return a.c.dim == 128 ? launch<__nv_bfloat16, 128>(a, plan, stream) : launch<__nv_bfloat16, 64>(a, plan, stream);
-    return a.c.dim == 128 ? launch<__half, 128>(a, plan, stream) : launch<__half, 64>(a, plan, stream);
+    return with_kernel(type, a.c.dim, a.c.bits, [&](auto t, auto d, auto b) {
+        return launch<decltype(t), decltype(d)::value, decltype(b)::value>(a, plan, stream);
+    });
 }
 
 }  // namespace libgemm

@@ -92,8 +92,10 @@ def attention(p, Q, counts, lengths, scale=None, causal=True, window=0):
                  sum of magnitudes, |q| (16 + |c|) s at most; a bfloat16 query's
                  elements under 2^-14 of the row's largest lose 2^-25 of that
                  largest each; a score's error moves its weight, and their sum
-      weights    w_j s_j is rounded to binary16: by 2^-11 of itself, or by 2^-25
-                 where it is 2^15 for the row's largest of them, times |c| <= 8
+      weights    w_j s_j is rounded to binary16 (of many rows w_j times the largest
+                 s of its 16 tokens): by 2^-11 of itself, or by 2^-25 where 2^15 is
+                 the largest product of a weight and a scale of the same 16 tokens,
+                 times |c| <= 8
       sums       p u and 8 p apart, in binary32: a chain of n / 64 products of 16 tokens
                  or fewer (four warps share them, or one step takes 128), and 64 steps to
                  join; each loses at most 2^-22 of the sum of magnitudes, 24 s_j w_j
@@ -127,7 +129,9 @@ def attention(p, Q, counts, lengths, scale=None, causal=True, window=0):
         reach = torch.einsum("thgd,hnd->hgtn", q.abs(), (16 + kc.abs()) * ks[..., None]) * abs(scale)
         reach = reach.masked_fill(~seen, 0).amax(-1)
         score = reach * ((p.dim + 8) * 2.0 ** -23 + 2.0 ** -18 * (Q.dtype is torch.bfloat16))
-        lost = 2.0 ** -40 * 8 * seen.sum(1) * (w * vs[:, None, None]).amax(-1)
+        pad = -n % 16
+        w16, s16 = (torch.nn.functional.pad(x, (0, pad)).unflatten(-1, (-1, 16)).amax(-1) for x in (w, vs))
+        lost = 2.0 ** -40 * 8 * seen.sum(1) * (w16 * s16[:, None, None]).amax(-1)
         chain = (n / 64 + 64) * 2.0 ** -22 * 24 * (w * vs[:, None, None]).sum(-1)
         y = torch.einsum("hgtn,hnd->hgtd", w, v)
         spread = torch.einsum("hgtn,hnd->hgtd", w, v.abs())
