@@ -27,7 +27,15 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kSub = 16;         // tokens of one product, all of one page
 constexpr int kSubs = 2;         // a warp takes this many times 16 tokens at once
 constexpr int kStep = kWarps * kSubs * kSub;   // tokens of a stage
-constexpr int kRingBytes = 102 * 1024;
+constexpr int resident(int nq) { return nq == 1 ? 3 : 2; }   // CTAs of an SM
+constexpr int ring_bytes(int nq) { return nq == 1 ? 70 * 1024 : 102 * 1024; }
+// Weights enter the second product relative to 2^12 for the row's largest: 2^3.9
+// over it still fit binary16, so that a row's sums are seldom brought to a new
+// maximum, and 2^-26 under it is still a normal number.
+constexpr float kTopP = 4096.0f;
+// A row's largest weight times value scale counts as this if it is less: the
+// factor up to kTopP stays finite when a weight of up to kMostP multiplies it.
+constexpr float kLeastP = 3.1554436e-30f;   // 2^-98
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
@@ -59,10 +67,10 @@ __device__ __forceinline__ void load_words(uint32_t addr, uint32_t (&w)[D / 32])
 }
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;   // u * 2^-24, u * 2^-20
 
-template <int D>
+template <int D, int NQ>
 struct Ring {
     static constexpr int kStageBytes = kStep * (D + 4);
-    static constexpr int kStages = kRingBytes / kStageBytes;   // 6 for 128, 12 for 64
+    static constexpr int kStages = ring_bytes(NQ) / kStageBytes;   // 4 or 6 for 128, 8 or 12 for 64
     // [stages][pages' records], then a word a stage, then the barriers
     static constexpr int kLiveAt = kStages * kStageBytes;
     static constexpr int kBarsAt = kLiveAt + (4 * kStages + 15) / 16 * 16;
@@ -83,8 +91,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // is the 16-row operand of both products and the queries its eight columns: S^T =
 // K Q^T, then O^T = V^T P^T, for which the weights are turned over in registers.
 template <typename T, int D, int NQ>
-__global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnArgs a) {
-    using R = Ring<D>;
+__global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_attention_kernel(const AttnArgs a) {
+    using R = Ring<D, NQ>;
     constexpr int kRows = 8 * NQ, kLd = D + 4, kWords = D / 32;
     static_assert(kWarps * kRows * (kLd + 2) * 4 + 8 * kRows <= R::kLiveAt, "the joining reuses the ring");
     extern __shared__ __align__(128) uint8_t smem[];
@@ -163,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
         // times that is binary16 (exact, but for elements under 2^-25 of the row's
         // largest, whose error stays under 2^-36 of it).
         uint32_t qf[NQ][2 * kWords][2];
-        float factor[NQ][2], begin[NQ][2];      // of the rows 8n + 2t, + 1, whose scores a lane gets
+        float factor[NQ][2], begin[NQ][4];      // of the rows 8n + 2t, + 1, whose scores a lane gets
         int row_lo[NQ][2], row_hi[NQ][2];
         [[maybe_unused]] const int64_t q_bytes =
             ((a.b.rows - 1) * a.Q.row + (a.q_heads - 1) * a.Q.head + D) * (int64_t)sizeof(T);
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                begin[n][i] = -8.0f * 9.5367431640625e-7f * __shfl_sync(0xFFFFFFFFu, sum, 4 * (2 * t + i));   // 2^-20
+                begin[n][i] = begin[n][2 + i] = -8.0f * 9.5367431640625e-7f * __shfl_sync(0xFFFFFFFFu, sum, 4 * (2 * t + i));   // 2^-20
                 // above 0, so that a hidden token's -inf stays that
                 factor[n][i] = fmaxf(fabsf(a.scale_log2) * __shfl_sync(0xFFFFFFFFu, up, 4 * (2 * t + i)), 1.1754943508222875e-38f);
                 // rows past the last one see all: they are not stored
@@ -218,9 +226,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
 
         constexpr int MT = D / 16;      // row tiles of O^T: row g of tile 2i + x is d = 64 (i / 2) + 8g + 4 (i % 2) + 2x, row g + 8 the next
         // A row's sums: l of the weights exp2(s_j - m) in binary32, o of those times
-        // their token's value scale v_j times up = 2^15 / r as binary16, and ones of these
+        // their token's value scale v_j times up = 2^12 / r as binary16, and ones of these
         // alone, where m and r are the row's own largest s_j and exp2(s_j - m) * v_j so
-        // far, of tokens that it sees (r at least kLeast, so that up stays finite).
+        // far, of tokens that it sees (r at least kLeastP).
         float o[NQ][MT][4], ones[NQ][4], m[NQ][2], l[NQ][2], up[NQ][2];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
@@ -229,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
             ones[n][0] = ones[n][1] = ones[n][2] = ones[n][3] = 0.0f;
             m[n][0] = m[n][1] = kLowest;
             l[n][0] = l[n][1] = 0.0f;
-            up[n][0] = up[n][1] = kPScale / kLeast;
+            up[n][0] = up[n][1] = kTopP / kLeastP;
         }
 
         uint32_t phase = 0;
@@ -248,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
                     in[b] = at & (page_tokens - 1);
                 }
                 // scores of tokens 16b + g and 16b + g + 8 for the rows 2t, 2t + 1
-                float sc[kSubs][NQ][4], vs[kSubs][2];
+                float sc[kSubs][NQ][4], vs[kSubs][2], held[kSubs][2], nan_sum = 0.0f;
 #pragma unroll
                 for (int b = 0; b < kSubs; ++b) {
                     const uint32_t kat = base[b] + in[b] * (D / 2) + g * (D / 2) + t * (D / 8);
@@ -258,11 +266,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
                     load_words<D>(kat + 8 * (D / 2), w1);
                     const float ks[2] = {lds_bf16(sat) * 16.0f, lds_bf16(sat + 16) * 16.0f};
                     vs[b][0] = lds_bf16(sat + 2 * page_tokens), vs[b][1] = lds_bf16(sat + 2 * page_tokens + 16);
+                    nan_sum += fabsf(vs[b][0]) + fabsf(vs[b][1]);
+                    // finite, whatever a token has that no row sees, so that a weight of 0 stays 0
+                    held[b][0] = fminf(fabsf(vs[b][0]), 3.3895314e38f), held[b][1] = fminf(fabsf(vs[b][1]), 3.3895314e38f);
                     float part[NQ][2][4];
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) part[n][0][e] = begin[n][e & 1], part[n][1][e] = 0.0f;
+                    constexpr float kZero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int i = 0; i < kWords; ++i)
 #pragma unroll
@@ -270,28 +278,28 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
                             const uint32_t lo = w0[i] >> (8 * x), hi = w1[i] >> (8 * x);
 #pragma unroll
                             for (int n = 0; n < NQ; ++n)
-                                mma_16816<__half>(part[n][x], lo & kLow, hi & kLow, lo & kHigh, hi & kHigh, qf[n][2 * i + x][0], qf[n][2 * i + x][1]);
+                                mma_16816_from(part[n][x], i > 0 ? part[n][x] : x ? kZero : begin[n], lo & kLow, hi & kLow, lo & kHigh, hi & kHigh,
+                                               qf[n][2 * i + x][0], qf[n][2 * i + x][1]);
                         }
 #pragma unroll
                     for (int n = 0; n < NQ; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) sc[b][n][e] = (part[n][0][e] + part[n][1][e]) * ks[e >> 1];
-                    // Tokens that some row does not see, pages that do not exist.
-                    const bool live = subs >> b & 1u;
-                    if (tok + 16 * b < full_lo || tok + 16 * b + kSub > full_hi || !live) {
+                }
+                // Tokens that some row does not see, pages that do not exist.
+                if (tok < full_lo || tok + kSubs * kSub > full_hi || (subs & 3u) != 3u) {
+#pragma unroll
+                    for (int b = 0; b < kSubs; ++b)
 #pragma unroll
                         for (int n = 0; n < NQ; ++n)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const int j = tok + 16 * b + g + 8 * (e >> 1);
-                                if (j < row_lo[n][e & 1] || j >= row_hi[n][e & 1] || !live) sc[b][n][e] = kNegInf;
+                                if (j < row_lo[n][e & 1] || j >= row_hi[n][e & 1] || !(subs >> b & 1u)) sc[b][n][e] = kNegInf;
                             }
-                        asm volatile("");   // a branch: few tokens come here
-                    }
+                    asm volatile("");   // a branch: few tokens come here
                 }
-                // A weight with its token's value scale, relative to the row's largest of
-                // them: the factor is finite whatever a token that no row sees has for a
-                // scale, so that a weight of 0 stays 0; where it is held to 2^127 the weights are under 2^-111.
+                // A weight, and it with its token's value scale, relative to the row's largest.
                 float w[kSubs][NQ][4], p[kSubs][NQ][4];
                 auto weigh = [&] {   // returns the largest weight of either product
                     float most = 0.0f;
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 w[b][n][e] = exp2_approx(fmaf(sc[b][n][e], factor[n][e & 1], -m[n][e & 1]));
-                                p[b][n][e] = w[b][n][e] * fminf(fabsf(vs[b][e >> 1]) * up[n][e & 1], 1.7014118e38f);
+                                p[b][n][e] = w[b][n][e] * up[n][e & 1] * held[b][e >> 1];   // (0 of a weight of 0)
                                 most = max3(most, w[b][n][e], p[b][n][e]);
                             }
                     return most;
@@ -310,7 +318,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
                 // A row's sums so far are brought to a new maximum only when it is passed
                 // by so much that a weight might not fit binary16, whatever the other
                 // rows do: a row's result does not depend on its neighbours.
-                if (__any_sync(0xFFFFFFFFu, weigh() > kMostP)) {
+                const bool nan = nan_sum != nan_sum;
+                if (__any_sync(0xFFFFFFFFu, weigh() > kMostP || nan)) {
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
                         float grow[2];
@@ -328,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
                             // (every lane takes part in every exchange, also those whose row stays)
                             const float highest = across(fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i])) * factor[n][i]);
                             const float top = passed ? fmaxf(highest, m[n][i]) : m[n][i];
-                            const float keep = exp2_approx(m[n][i] - top), held = keep * __fdividef(kPScale, up[n][i]);
+                            const float keep = exp2_approx(m[n][i] - top), sums = keep * __fdividef(kTopP, up[n][i]);
                             m[n][i] = top;
                             l[n][i] *= keep;
                             float rel = 0.0f;
@@ -336,11 +345,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
                             for (int b = 0; b < kSubs; ++b)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
-                                    if (sc[b][n][2 * e + i] != kNegInf) rel = fmaxf(rel, exp2_approx(fmaf(sc[b][n][2 * e + i], factor[n][i], -top)) * vs[b][e]);
+                                    if (sc[b][n][2 * e + i] != kNegInf) rel = fmaxf(rel, exp2_approx(fmaf(sc[b][n][2 * e + i], factor[n][i], -top)) * held[b][e]);
                             rel = across(rel);
-                            rel = max3(rel, held, kLeast);
-                            if (passed) up[n][i] = __fdividef(kPScale, rel);
-                            grow[i] = passed ? __fdividef(held, rel) : 1.0f;   // 1 at most
+                            rel = max3(rel, sums, kLeastP);
+                            if (passed) up[n][i] = __fdividef(kTopP, rel);
+                            grow[i] = passed ? __fdividef(sums, rel) : 1.0f;   // 1 at most
                         }
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
@@ -350,11 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
                         ones[n][0] *= grow[0], ones[n][1] *= grow[1];
                     }
                     weigh();
-                }
-                bool nan = false;
-#pragma unroll
-                for (int b = 0; b < kSubs; ++b) nan |= vs[b][0] != vs[b][0] || vs[b][1] != vs[b][1];
-                if (__any_sync(0xFFFFFFFFu, nan)) {   // values that read as NaN: for the rows that see them alone
+                    // values that read as NaN: for the rows that see them alone
 #pragma unroll
                     for (int b = 0; b < kSubs; ++b)
 #pragma unroll
@@ -362,7 +367,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (vs[b][e >> 1] != vs[b][e >> 1]) p[b][n][e] = sc[b][n][e] == kNegInf ? 0.0f : vs[b][e >> 1];
-                    asm volatile("");
                 }
 #pragma unroll
                 for (int b = 0; b < kSubs; ++b) {
@@ -370,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const AttnAr
                     uint32_t w0[kWords], w1[kWords];   // tokens 2t, 2t + 1; those 8 on
                     load_words<D>(vat, w0);
                     load_words<D>(vat + 4 * D, w1);
-                    // Binary16 under 2^16, normal down to 2^-29 of the row's largest.
+                    // Binary16 under 2^16, normal down to 2^-26 of the row's largest.
                     uint32_t pt[NQ][2];
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
@@ -486,7 +490,7 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(plan.units * plan.splits), (unsigned)a.c.heads);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Ring<D>::kBytes;
+    cfg.dynamicSmemBytes = Ring<D, NQ>::kBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -518,9 +522,9 @@ cudaError_t kv4_attention_setup() {
         for (int dim : {64, 128})
             for (int rows : {8, 16}) {
                 const cudaError_t e = with_kernel(type, dim, rows, [](auto t, auto d, auto nq) {
-                    constexpr int D = decltype(d)::value;
-                    return cudaFuncSetAttribute(kv4_attention_kernel<decltype(t), D, decltype(nq)::value>,
-                                                cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes);
+                    constexpr int D = decltype(d)::value, NQ = decltype(nq)::value;
+                    return cudaFuncSetAttribute(kv4_attention_kernel<decltype(t), D, NQ>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D, NQ>::kBytes);
                 });
                 if (e != cudaSuccess) return e;
             }

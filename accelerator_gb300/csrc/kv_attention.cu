@@ -632,7 +632,7 @@ KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, i
     int64_t longest = b.width << c.page_log2;
     if (window > 0 && window < longest - p.rows - 2 * kStep) longest = window + p.rows + 2 * kStep;
     if (p.units < 1) p.units = 1;
-    const int64_t have = (tiles > b.sequences ? tiles : b.sequences) * c.heads, slots = (p.rows == 256 ? 1 : 2) * (int64_t)num_sms;
+    const int64_t have = (tiles > b.sequences ? tiles : b.sequences) * c.heads, slots = (p.rows == 256 ? 1 : c.bits == 4 && p.rows == 8 ? 3 : 2) * (int64_t)num_sms;
     const int64_t most = (longest + kStep - 1) / kStep;
     int64_t splits;
     if (p.rows == 256) {

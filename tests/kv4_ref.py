@@ -93,7 +93,7 @@ def attention(p, Q, counts, lengths, scale=None, causal=True, window=0):
                  elements under 2^-14 of the row's largest lose 2^-25 of that
                  largest each; a score's error moves its weight, and their sum
       weights    w_j s_j is rounded to binary16 (of many rows w_j times the largest
-                 s of its 16 tokens): by 2^-11 of itself, or by 2^-25 where 2^15 is
+                 s of its 16 tokens): by 2^-11 of itself, or by 2^-25 where 2^12 is
                  the largest product of a weight and a scale of the same 16 tokens,
                  times |c| <= 8
       sums       p u and 8 p apart, in binary32: a chain of n / 64 products of 16 tokens
@@ -131,7 +131,7 @@ def attention(p, Q, counts, lengths, scale=None, causal=True, window=0):
         score = reach * ((p.dim + 8) * 2.0 ** -23 + 2.0 ** -18 * (Q.dtype is torch.bfloat16))
         pad = -n % 16
         w16, s16 = (torch.nn.functional.pad(x, (0, pad)).unflatten(-1, (-1, 16)).amax(-1) for x in (w, vs))
-        lost = 2.0 ** -40 * 8 * seen.sum(1) * (w16 * s16[:, None, None]).amax(-1)
+        lost = 2.0 ** -37 * 8 * seen.sum(1) * (w16 * s16[:, None, None]).amax(-1)
         chain = (n / 64 + 64) * 2.0 ** -22 * 24 * (w * vs[:, None, None]).sum(-1)
         y = torch.einsum("hgtn,hnd->hgtd", w, v)
         spread = torch.einsum("hgtn,hnd->hgtd", w, v.abs())
