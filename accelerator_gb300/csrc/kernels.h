@@ -241,6 +241,7 @@ struct KvPlan {
     int64_t units;        // upper bound of the row tiles of the batch
     int splits;
     bool cluster;         // the splits of a tile are a cluster
+    int ctas;             // few rows over 4 bits: CTAs that share all tiles' tokens evenly, instead of splits
     int64_t scratch_bytes;
 };
 cudaError_t kv_attention_setup();

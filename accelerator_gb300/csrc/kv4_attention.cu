@@ -86,31 +86,19 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// A tile of 8 * NQ rows over a share of its tokens.  One warp copies pages into a
-// ring of stages of 128 tokens, four take 32 tokens of each stage; the tokens' side
-// is the 16-row operand of both products and the queries its eight columns: S^T =
-// K Q^T, then O^T = V^T P^T, for which the weights are turned over in registers.
-template <typename T, int D, int NQ>
-__global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_attention_kernel(const AttnArgs a) {
+// The ring's place in shared memory, and where a warp is in its rounds.
+template <int D, int NQ>
+struct Stages {
     using R = Ring<D, NQ>;
-    constexpr int kRows = 8 * NQ, kLd = D + 4, kWords = D / 32;
-    static_assert(kWarps * kRows * (kLd + 2) * 4 + 8 * kRows <= R::kLiveAt, "the joining reuses the ring");
-    extern __shared__ __align__(128) uint8_t smem[];
-    const uint32_t ring = smem_u32(smem), bars = ring + R::kBarsAt;   // full[stages], empty[stages]
-    uint32_t* live_subs = reinterpret_cast<uint32_t*>(smem + R::kLiveAt);   // which 16s of a stage are there
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + R::kAbortAt);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const int u = blockIdx.x / a.splits, split = blockIdx.x % a.splits, h = blockIdx.y;
-    const bool cluster = a.splits > 1 && !a.partial;
-    Tile tile;
-    // A cluster's CTAs have one tile: they leave here together or not at all.
-    if (!tile.find(a, u, kRows, kStep, h == 0 && split == 0) || (!cluster && split >= tile.active)) return;
-    grid_launch_dependents();   // a joining launch may start its set-up
-    const int step_begin = min(tile.steps, split * tile.per);
-    const int steps = min(tile.steps, step_begin + tile.per) - step_begin;
-    const int tok_begin = tile.tok0 + step_begin * kStep;
-    const int log2 = a.c.page_log2, page_tokens = 1 << log2, record = (D + 4) << log2;
-    if (threadIdx.x == 0) {
+    uint32_t ring, bars;            // full[stages], empty[stages]
+    uint32_t* live_subs;            // which 16s of a stage are there
+    volatile int* abort_flag;
+    uint32_t phase = 0;
+    int stage = 0;
+    __device__ __forceinline__ explicit Stages(uint8_t* smem)
+        : ring(smem_u32(smem)), bars(ring + R::kBarsAt), live_subs(reinterpret_cast<uint32_t*>(smem + R::kLiveAt)),
+          abort_flag(reinterpret_cast<volatile int*>(smem + R::kAbortAt)) {}
+    __device__ __forceinline__ void init() const {   // one thread
         for (int s = 0; s < R::kStages; ++s) {
             mbar_init(bars + 8 * s, 1);
             mbar_init(bars + 8 * (R::kStages + s), kWarps);
@@ -118,84 +106,116 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_attention_kernel(c
         *abort_flag = 0;
         mbar_fence_init();
     }
-    __syncthreads();
+    __device__ __forceinline__ uint32_t at() const { return ring + stage * R::kStageBytes; }
+    __device__ __forceinline__ bool wait_full(unsigned* err) const { return warp_wait(bars + 8 * stage, phase, abort_flag, err); }
+    __device__ __forceinline__ bool wait_empty(unsigned* err) const { return warp_wait(bars + 8 * (R::kStages + stage), phase ^ 1u, abort_flag, err); }
+    __device__ __forceinline__ void release() { warp_arrive(bars + 8 * (R::kStages + stage)); }
+    __device__ __forceinline__ void next() {
+        if (++stage == R::kStages) stage = 0, phase ^= 1u;
+    }
+};
 
-    float* s_o = reinterpret_cast<float*>(smem);                     // [warps][rows][kLd]
-    float* s_m = s_o + kWarps * kRows * kLd;                      // [warps][rows]
-    float* s_l = s_m + kWarps * kRows;
-    if (warp == kWarps) {
-        // ---- copies: lane i looks up 16 tokens, those of four stages at a time ----
-        static_assert(kWarps * kSubs == 8, "");
-        const int32_t* table = a.b.table + tile.seq * a.b.width;
-        [[maybe_unused]] const int64_t extent = a.c.pages * a.c.heads * a.c.record();
-        bool live = false;
-        const uint8_t* from = nullptr;
-        uint32_t phase = 0;
-        int stage = 0, issued = 0;
-        for (int s = 0; s < steps; ++s) {
-            if (s % 4 == 0) {
-                const int tok = tok_begin + s * kStep + lane * kSub;
-                live = tile.page_seen(tok, log2);
-                const int64_t page = live ? __ldg(table + (tok >> log2)) : 0;
-                if (live && (page < 0 || page >= a.c.pages)) {
-                    atomicOr(a.err, kErrIndex);
-                    live = false;
-                }
-                from = a.c.data + (page * a.c.heads + h) * record;
+// The copying warp: `steps` stages of a tile's tokens from tok_begin on.  Lane i
+// looks up 16 tokens, those of four stages at a time.  False if a wait gave up.
+template <int D, int NQ>
+__device__ __forceinline__ bool copy_steps(const AttnArgs& a, const Tile& tile, int h, int tok_begin, int steps, Stages<D, NQ>& st, int& issued) {
+    static_assert(kWarps * kSubs == 8, "");
+    const int lane = threadIdx.x % 32, log2 = a.c.page_log2, record = (D + 4) << log2;
+    const int32_t* table = a.b.table + tile.seq * a.b.width;
+    [[maybe_unused]] const int64_t extent = a.c.pages * a.c.heads * a.c.record();
+    bool live = false;
+    const uint8_t* from = nullptr;
+    for (int s = 0; s < steps; ++s) {
+        if (s % 4 == 0) {
+            const int tok = tok_begin + s * kStep + lane * kSub;
+            live = tile.page_seen(tok, log2);
+            const int64_t page = live ? __ldg(table + (tok >> log2)) : 0;
+            if (live && (page < 0 || page >= a.c.pages)) {
+                atomicOr(a.err, kErrIndex);
+                live = false;
             }
-            if (!warp_wait(bars + 8 * (R::kStages + stage), phase ^ 1u, abort_flag, a.err)) break;
-            const int sub = lane - s % 4 * 8;   // this lane's part of the stage, if it has one
-            const bool here = sub >= 0 && sub < 8 && live;
-            bool copies = here && sub * kSub % page_tokens == 0;   // a page's first 16 tokens fetch all of it
-            if (copies) copies = GEMM_DBG_OK(from, a.c.data, extent, record);
-            const unsigned there = __ballot_sync(0xFFFFFFFFu, here), parts = __popc(__ballot_sync(0xFFFFFFFFu, copies));
-            if (copies) bulk_load(ring + stage * R::kStageBytes + (sub * kSub >> log2) * record, from, record, bars + 8 * stage);
-            __syncwarp();
-            if (lane == 0) {
-                live_subs[stage] = there >> (s % 4 * 8);
-                mbar_arrive_expect_tx(bars + 8 * stage, parts * record);
-            }
-            ++issued;
-            if (++stage == R::kStages) stage = 0, phase ^= 1u;
+            from = a.c.data + (page * a.c.heads + h) * record;
         }
-        // Copies in flight land before the CTA may leave or reuse the ring.
-        if (lane == 0)
-            for (int s = max(0, issued - R::kStages); s < issued; ++s) drain(bars + 8 * (s % R::kStages), (uint32_t)(s / R::kStages) & 1u, a.err);
+        if (!st.wait_empty(a.err)) return false;
+        const int sub = lane - s % 4 * 8;   // this lane's part of the stage, if it has one
+        const bool here = sub >= 0 && sub < 8 && live;
+        bool copies = here && (sub * kSub & ((1 << log2) - 1)) == 0;   // a page's first 16 tokens fetch all of it
+        if (copies) copies = GEMM_DBG_OK(from, a.c.data, extent, record);
+        const unsigned there = __ballot_sync(0xFFFFFFFFu, here), parts = __popc(__ballot_sync(0xFFFFFFFFu, copies));
+        if (copies) bulk_load(st.at() + (sub * kSub >> log2) * record, from, record, st.bars + 8 * st.stage);
         __syncwarp();
-        __syncthreads();   // the ring is free
-        __syncthreads();   // the warps' results are in it
-    } else {
-        // Query row 8n + g as the column g of B.  A lane's part of a row is 8
-        // neighbours of each 32: elements e and e + 4 a word's two halves hold
-        // together.  Rows are brought to [2^11, 2^12) by a power of two, so that 16
-        // times that is binary16 (exact, but for elements under 2^-25 of the row's
-        // largest, whose error stays under 2^-36 of it).
-        uint32_t qf[NQ][2 * kWords][2];
-        float factor[NQ][2], begin[NQ][4];      // of the rows 8n + 2t, + 1, whose scores a lane gets
-        int row_lo[NQ][2], row_hi[NQ][2];
-        [[maybe_unused]] const int64_t q_bytes =
-            ((a.b.rows - 1) * a.Q.row + (a.q_heads - 1) * a.Q.head + D) * (int64_t)sizeof(T);
+        if (lane == 0) {
+            st.live_subs[st.stage] = there >> (s % 4 * 8);
+            mbar_arrive_expect_tx(st.bars + 8 * st.stage, parts * record);
+        }
+        ++issued;
+        st.next();
+    }
+    return true;
+}
+// Copies in flight land before the CTA may leave or reuse the ring.
+template <int D, int NQ>
+__device__ __forceinline__ void drain_all(const Stages<D, NQ>& st, int issued, unsigned* err) {
+    constexpr int kStages = Ring<D, NQ>::kStages;
+    if (threadIdx.x % 32 == 0)
+        for (int s = max(0, issued - kStages); s < issued; ++s) drain(st.bars + 8 * (s % kStages), (uint32_t)(s / kStages) & 1u, err);
+    __syncwarp();
+}
+
+// Elements d .. d + 7 of a tile's row r, 0 past the last row.
+template <typename T, int D>
+__device__ __forceinline__ Eight<T> query(const AttnArgs& a, const Tile& tile, int h, int r, int d) {
+    [[maybe_unused]] const int64_t q_bytes = ((a.b.rows - 1) * a.Q.row + (a.q_heads - 1) * a.Q.head + D) * (int64_t)sizeof(T);
+    const unsigned row = tile.r0 + r;
+    Eight<T> x = {};
+    if (row >= (unsigned)tile.nrows) return x;
+    const T* p = static_cast<const T*>(a.Q.p) + (int64_t)(tile.row0 + row / a.share) * a.Q.row + (int64_t)(h * a.share + row % a.share) * a.Q.head + d;
+    if (GEMM_DBG_OK(p, a.Q.p, q_bytes, 16)) x = load_eight(p, a.q_vec);
+    return x;
+}
+
+// One warp's part of a tile of 8 * NQ rows: the tokens' side is the 16-row operand
+// of both products and the queries its eight columns: S^T = K Q^T, then O^T = V^T
+// P^T, for which the weights are turned over in registers.
+template <typename T, int D, int NQ>
+struct Attend {
+    static constexpr int kRows = 8 * NQ, kLd = D + 4, kWords = D / 32;
+    static constexpr int MT = D / 16;   // row tiles of O^T: row g of tile 2i + x is d = 64 (i / 2) + 8g + 4 (i % 2) + 2x, row g + 8 the next
+    // Query row 8n + g as the column g of B.  A lane's part of a row is 8
+    // neighbours of each 32: elements e and e + 4 a word's two halves hold
+    // together.  Rows are brought to [2^11, 2^12) by a power of two, so that 16
+    // times that is binary16 (exact, but for elements under 2^-25 of the row's
+    // largest, whose error stays under 2^-36 of it).
+    uint32_t qf[NQ][2 * kWords][2];
+    float factor[NQ][2], begin[NQ][4];      // of the rows 8n + 2t, + 1, whose scores a lane gets
+    int row_lo[NQ][2], row_hi[NQ][2];
+    int full_lo, full_hi;                   // tokens that every row of the tile sees
+    // A row's sums: l of the weights exp2(s_j - m) in binary32, o of those times
+    // their token's value scale v_j times up = 2^12 / r as binary16, and ones of these
+    // alone, where m and r are the row's own largest s_j and exp2(s_j - m) * v_j so
+    // far, of tokens that it sees (r at least kLeastP).
+    float o[NQ][MT][4], ones[NQ][4], m[NQ][2], l[NQ][2], up[NQ][2];
+
+    // get(r, d): elements d .. d + 7 of the tile's row r, 0 past its last.
+    template <typename F>
+    __device__ __forceinline__ void start(const AttnArgs& a, const Tile& tile, F get) {
+        const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            const unsigned r = tile.r0 + 8 * n + g;
-            const bool live = r < (unsigned)tile.nrows;
-            const T* p = static_cast<const T*>(a.Q.p) + (int64_t)(tile.row0 + (live ? r / a.share : 0)) * a.Q.row +
-                         (int64_t)(h * a.share + (live ? r % a.share : 0)) * a.Q.head;
-            Eight<T> x[kWords] = {};
+            Eight<T> x[kWords];
             float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
-                const T* pe = p + 32 * i + 8 * t;
-                if (live && GEMM_DBG_OK(pe, a.Q.p, q_bytes, 16)) x[i] = load_eight(pe, a.q_vec);
+            for (int i = 0; i < kWords; ++i) x[i] = get(8 * n + g, 32 * i + 8 * t);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i].at(e)));
-            }
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             // its biased exponent, in the range in which both powers below are normal
             const int k = top < INFINITY ? max(12, min(249, (int)(__float_as_uint(top) >> 23))) : 127;
             const float down = __uint_as_float((uint32_t)(265 - k) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);   // 2^(11 + 127 - k)
-            const float up = __uint_as_float((uint32_t)(k + 5) << 23);   // 2^(k - 127 - 11 + 20 - 4): the codes' 2^-20, 2^4 of it with the key's scale
+            const float back = __uint_as_float((uint32_t)(k + 5) << 23);   // 2^(k - 127 - 11 + 20 - 4): the codes' 2^-20, 2^4 of it with the key's scale
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kWords; ++i)
@@ -213,25 +233,12 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_attention_kernel(c
             for (int i = 0; i < 2; ++i) {
                 begin[n][i] = begin[n][2 + i] = -8.0f * 9.5367431640625e-7f * __shfl_sync(0xFFFFFFFFu, sum, 4 * (2 * t + i));   // 2^-20
                 // above 0, so that a hidden token's -inf stays that
-                factor[n][i] = fmaxf(fabsf(a.scale_log2) * __shfl_sync(0xFFFFFFFFu, up, 4 * (2 * t + i)), 1.1754943508222875e-38f);
+                factor[n][i] = fmaxf(fabsf(a.scale_log2) * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + i)), 1.1754943508222875e-38f);
                 // rows past the last one see all: they are not stored
                 const int rr = tile.r0 + 8 * n + 2 * t + i;
                 row_lo[n][i] = rr < tile.nrows ? tile.row_lo(a, rr) : 0;
                 row_hi[n][i] = rr < tile.nrows ? tile.row_hi(a, rr) : tile.hi;
             }
-        }
-        // tokens that every row of the tile sees
-        const int full_lo = tile.row_lo(a, min(tile.r0 + kRows, tile.nrows) - 1);
-        const int full_hi = tile.row_hi(a, tile.r0);
-
-        constexpr int MT = D / 16;      // row tiles of O^T: row g of tile 2i + x is d = 64 (i / 2) + 8g + 4 (i % 2) + 2x, row g + 8 the next
-        // A row's sums: l of the weights exp2(s_j - m) in binary32, o of those times
-        // their token's value scale v_j times up = 2^12 / r as binary16, and ones of these
-        // alone, where m and r are the row's own largest s_j and exp2(s_j - m) * v_j so
-        // far, of tokens that it sees (r at least kLeastP).
-        float o[NQ][MT][4], ones[NQ][4], m[NQ][2], l[NQ][2], up[NQ][2];
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
             ones[n][0] = ones[n][1] = ones[n][2] = ones[n][3] = 0.0f;
@@ -239,229 +246,297 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_attention_kernel(c
             l[n][0] = l[n][1] = 0.0f;
             up[n][0] = up[n][1] = kTopP / kLeastP;
         }
+        full_lo = tile.row_lo(a, min(tile.r0 + kRows, tile.nrows) - 1);
+        full_hi = tile.row_hi(a, tile.r0);
+    }
 
-        uint32_t phase = 0;
-        int stage = 0;
-        for (int s = 0; s < steps; ++s) {
-            if (!warp_wait(bars + 8 * stage, phase, abort_flag, a.err)) break;
-            const int tok = tok_begin + s * kStep + warp * (kSubs * kSub);
-            if (tok < tile.hi) {
-                const uint32_t subs = live_subs[stage] >> (warp * kSubs);
-                uint32_t base[kSubs];   // of each 16's page, and what of it comes before them
-                int in[kSubs];
+    // Where this warp's tokens lie in every stage: the keys' codes of token g of its
+    // first 16 and the values' piece of this lane, the key scale of that token, what
+    // the second 16 are further on, and what value scales are behind key scales.
+    uint32_t key_at, value_at, scale_at, next_codes, next_scales, to_values;
+    __device__ __forceinline__ void locate(int log2) {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+        const int page_tokens = 1 << log2, record = (D + 4) << log2, at = warp * (kSubs * kSub);
+        const uint32_t page = (at >> log2) * record, in = at & (page_tokens - 1);
+        key_at = page + in * (D / 2) + g * (D / 2) + t * (D / 8);
+        value_at = page + (page_tokens + in) * (D / 2) + lane * (D / 8);
+        scale_at = page + page_tokens * D + 2 * (in + g);
+        next_codes = log2 == 4 ? record : kSub * (D / 2);
+        next_scales = log2 == 4 ? record : 2 * kSub;
+        to_values = 2 * page_tokens;
+    }
+
+    // This warp's 32 tokens of a stage, from token `tok` on; `subs`: which 16s are there.
+    __device__ __forceinline__ void step(uint32_t stage_at, int tok, uint32_t subs) {
+        const int lane = threadIdx.x % 32, g = lane / 4;
+        // scores of tokens 16b + g and 16b + g + 8 (y) for the rows 2t (.x) and 2t + 1 (.y)
+        float2 sc[kSubs][NQ][2];
+        float vs[kSubs][2];
 #pragma unroll
-                for (int b = 0; b < kSubs; ++b) {
-                    const int at = warp * (kSubs * kSub) + b * kSub;
-                    base[b] = ring + stage * R::kStageBytes + (at >> log2) * record;
-                    in[b] = at & (page_tokens - 1);
-                }
-                // scores of tokens 16b + g and 16b + g + 8 for the rows 2t, 2t + 1
-                float sc[kSubs][NQ][4], vs[kSubs][2], held[kSubs][2], nan_sum = 0.0f;
+        for (int b = 0; b < kSubs; ++b) {
+            const uint32_t kat = stage_at + key_at + b * next_codes, sat = stage_at + scale_at + b * next_scales;
+            uint32_t w0[kWords], w1[kWords];
+            load_words<D>(kat, w0);
+            load_words<D>(kat + 8 * (D / 2), w1);
+            const float ks[2] = {lds_bf16(sat) * 16.0f, lds_bf16(sat + 16) * 16.0f};
+            vs[b][0] = lds_bf16(sat + to_values), vs[b][1] = lds_bf16(sat + to_values + 16);
+            float part[NQ][2][4];
+            constexpr float kZero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int b = 0; b < kSubs; ++b) {
-                    const uint32_t kat = base[b] + in[b] * (D / 2) + g * (D / 2) + t * (D / 8);
-                    const uint32_t sat = base[b] + page_tokens * D + 2 * (in[b] + g);
-                    uint32_t w0[kWords], w1[kWords];
-                    load_words<D>(kat, w0);
-                    load_words<D>(kat + 8 * (D / 2), w1);
-                    const float ks[2] = {lds_bf16(sat) * 16.0f, lds_bf16(sat + 16) * 16.0f};
-                    vs[b][0] = lds_bf16(sat + 2 * page_tokens), vs[b][1] = lds_bf16(sat + 2 * page_tokens + 16);
-                    nan_sum += fabsf(vs[b][0]) + fabsf(vs[b][1]);
-                    // finite, whatever a token has that no row sees, so that a weight of 0 stays 0
-                    held[b][0] = fminf(fabsf(vs[b][0]), 3.3895314e38f), held[b][1] = fminf(fabsf(vs[b][1]), 3.3895314e38f);
-                    float part[NQ][2][4];
-                    constexpr float kZero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < kWords; ++i)
 #pragma unroll
-                    for (int i = 0; i < kWords; ++i)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t lo = w0[i] >> (8 * x), hi = w1[i] >> (8 * x);
-#pragma unroll
-                            for (int n = 0; n < NQ; ++n)
-                                mma_16816_from(part[n][x], i > 0 ? part[n][x] : x ? kZero : begin[n], lo & kLow, hi & kLow, lo & kHigh, hi & kHigh,
-                                               qf[n][2 * i + x][0], qf[n][2 * i + x][1]);
-                        }
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t lo = w0[i] >> (8 * x), hi = w1[i] >> (8 * x);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[b][n][e] = (part[n][0][e] + part[n][1][e]) * ks[e >> 1];
+                        mma_16816_from(part[n][x], i > 0 ? part[n][x] : x ? kZero : begin[n], lo & kLow, hi & kLow, lo & kHigh, hi & kHigh,
+                                       qf[n][2 * i + x][0], qf[n][2 * i + x][1]);
                 }
-                // Tokens that some row does not see, pages that do not exist.
-                if (tok < full_lo || tok + kSubs * kSub > full_hi || (subs & 3u) != 3u) {
 #pragma unroll
-                    for (int b = 0; b < kSubs; ++b)
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                        for (int n = 0; n < NQ; ++n)
+                for (int y = 0; y < 2; ++y)
+                    sc[b][n][y] = __fmul2_rn(__fadd2_rn(make_float2(part[n][0][2 * y], part[n][0][2 * y + 1]), make_float2(part[n][1][2 * y], part[n][1][2 * y + 1])),
+                                             make_float2(ks[y], ks[y]));
+        }
+        // Tokens that some row does not see, pages that do not exist.  There a weight
+        // of 0 has to stay 0 whatever the token has for a scale, and a scale of NaN
+        // makes NaN of the rows alone that see it; elsewhere all rows see all tokens.
+        const bool masked = tok < full_lo || tok + kSubs * kSub > full_hi || (subs & 3u) != 3u;
+        uint32_t nan = 0;
+        if (masked) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int j = tok + 16 * b + g + 8 * (e >> 1);
-                                if (j < row_lo[n][e & 1] || j >= row_hi[n][e & 1] || !(subs >> b & 1u)) sc[b][n][e] = kNegInf;
-                            }
-                    asm volatile("");   // a branch: few tokens come here
-                }
-                // A weight, and it with its token's value scale, relative to the row's largest.
-                float w[kSubs][NQ][4], p[kSubs][NQ][4];
-                auto weigh = [&] {   // returns the largest weight of either product
-                    float most = 0.0f;
+            for (int b = 0; b < kSubs; ++b)
 #pragma unroll
-                    for (int b = 0; b < kSubs; ++b)
-#pragma unroll
-                        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                w[b][n][e] = exp2_approx(fmaf(sc[b][n][e], factor[n][e & 1], -m[n][e & 1]));
-                                p[b][n][e] = w[b][n][e] * up[n][e & 1] * held[b][e >> 1];   // (0 of a weight of 0)
-                                most = max3(most, w[b][n][e], p[b][n][e]);
-                            }
-                    return most;
-                };
-                // A row's sums so far are brought to a new maximum only when it is passed
-                // by so much that a weight might not fit binary16, whatever the other
-                // rows do: a row's result does not depend on its neighbours.
-                const bool nan = nan_sum != nan_sum;
-                if (__any_sync(0xFFFFFFFFu, weigh() > kMostP || nan)) {
+                for (int y = 0; y < 2; ++y) {
+                    const int j = tok + 16 * b + g + 8 * y;
+                    const bool live = subs >> b & 1u;
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        float grow[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            auto across = [](float x) {   // the largest of the lanes that have this row
-                                x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-                                x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-                                return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                            };
-                            float most = 0.0f;
-#pragma unroll
-                            for (int b = 0; b < kSubs; ++b) most = max3(max3(most, w[b][n][i], p[b][n][i]), w[b][n][2 + i], p[b][n][2 + i]);
-                            const bool passed = across(most) > kMostP;
-                            // (every lane takes part in every exchange, also those whose row stays)
-                            const float highest = across(fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i])) * factor[n][i]);
-                            const float top = passed ? fmaxf(highest, m[n][i]) : m[n][i];
-                            const float keep = exp2_approx(m[n][i] - top), sums = keep * __fdividef(kTopP, up[n][i]);
-                            m[n][i] = top;
-                            l[n][i] *= keep;
-                            float rel = 0.0f;
-#pragma unroll
-                            for (int b = 0; b < kSubs; ++b)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    if (sc[b][n][2 * e + i] != kNegInf) rel = fmaxf(rel, exp2_approx(fmaf(sc[b][n][2 * e + i], factor[n][i], -top)) * held[b][e]);
-                            rel = across(rel);
-                            rel = max3(rel, sums, kLeastP);
-                            if (passed) up[n][i] = __fdividef(kTopP, rel);
-                            grow[i] = passed ? __fdividef(sums, rel) : 1.0f;   // 1 at most
-                        }
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            o[n][i][0] *= grow[0], o[n][i][1] *= grow[1];
-                            o[n][i][2] *= grow[0], o[n][i][3] *= grow[1];
-                        }
-                        ones[n][0] *= grow[0], ones[n][1] *= grow[1];
+                        if (j < row_lo[n][0] || j >= row_hi[n][0] || !live) sc[b][n][y].x = kNegInf;
+                        if (j < row_lo[n][1] || j >= row_hi[n][1] || !live) sc[b][n][y].y = kNegInf;
                     }
-                    weigh();
-                    // values that read as NaN: for the rows that see them alone
-#pragma unroll
-                    for (int b = 0; b < kSubs; ++b)
-#pragma unroll
-                        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (vs[b][e >> 1] != vs[b][e >> 1]) p[b][n][e] = sc[b][n][e] == kNegInf ? 0.0f : vs[b][e >> 1];
+                    if (vs[b][y] != vs[b][y]) nan |= 1u << (2 * b + y);
+                    vs[b][y] = fminf(fabsf(vs[b][y]), 3.3895314e38f);
                 }
+            asm volatile("");   // a branch: few tokens come here
+        }
+        // A weight, and it with its token's value scale, relative to the row's largest.
+        float2 w[kSubs][NQ][2], p[kSubs][NQ][2];
+        auto weigh = [&] {   // returns the largest weight of either product
+            float most = 0.0f;
 #pragma unroll
-                for (int b = 0; b < kSubs; ++b) {
-                    const uint32_t vat = base[b] + (page_tokens + in[b]) * (D / 2) + lane * (D / 8);
-                    uint32_t w0[kWords], w1[kWords];   // tokens 2t, 2t + 1; those 8 on
-                    load_words<D>(vat, w0);
-                    load_words<D>(vat + 4 * D, w1);
-                    // Binary16 under 2^16, normal down to 2^-26 of the row's largest.
-                    uint32_t pt[NQ][2];
+            for (int n = 0; n < NQ; ++n) {
+                const float2 f = make_float2(factor[n][0], factor[n][1]), less = make_float2(-m[n][0], -m[n][1]), u = make_float2(up[n][0], up[n][1]);
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        l[n][0] += w[b][n][0] + w[b][n][2];
-                        l[n][1] += w[b][n][1] + w[b][n][3];
-                        pt[n][0] = transpose8(pack2<__half>(p[b][n][0], p[b][n][1]));
-                        pt[n][1] = transpose8(pack2<__half>(p[b][n][2], p[b][n][3]));
-                        constexpr uint32_t kOne = 0x3C003C00u;
-                        mma_16816<__half>(ones[n], kOne, kOne, kOne, kOne, pt[n][0], pt[n][1]);
+                for (int b = 0; b < kSubs; ++b)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float2 x = __ffma2_rn(sc[b][n][y], f, less);
+                        const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                        const float2 v = __fmul2_rn(__fmul2_rn(e, u), make_float2(vs[b][y], vs[b][y]));   // (0 of a weight of 0)
+                        w[b][n][y] = e, p[b][n][y] = v;
+                        most = max3(max3(most, e.x, v.x), e.y, v.y);
                     }
-#pragma unroll
-                    for (int i = 0; i < kWords; ++i)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t lo = w0[i] >> (8 * x), hi = w1[i] >> (8 * x);
-#pragma unroll
-                            for (int n = 0; n < NQ; ++n)
-                                mma_16816<__half>(o[n][2 * i + x], lo & kLow, lo & kHigh, hi & kLow, hi & kHigh, pt[n][0], pt[n][1]);
-                        }
-                }
             }
-            warp_arrive(bars + 8 * (R::kStages + stage));
-            if (++stage == R::kStages) stage = 0, phase ^= 1u;
+            return most;
+        };
+        // A row's sums so far are brought to a new maximum only when it is passed
+        // by so much that a weight might not fit binary16, whatever the other
+        // rows do: a row's result does not depend on its neighbours.
+        if (__any_sync(0xFFFFFFFFu, weigh() > kMostP)) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                float grow[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    auto of = [&](const float2& x) { return i ? x.y : x.x; };
+                    auto across = [](float x) {   // the largest of the lanes that have this row
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                        return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                    };
+                    float most = 0.0f, highest = kNegInf;
+#pragma unroll
+                    for (int b = 0; b < kSubs; ++b)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            most = max3(most, of(w[b][n][y]), of(p[b][n][y]));
+                            highest = fmaxf(highest, of(sc[b][n][y]));
+                        }
+                    // (every lane takes part in every exchange, also those whose row stays)
+                    const bool passed = across(most) > kMostP;
+                    highest = across(highest * factor[n][i]);
+                    const float top = passed ? fmaxf(highest, m[n][i]) : m[n][i];
+                    const float keep = exp2_approx(m[n][i] - top), sums = keep * __fdividef(kTopP, up[n][i]);
+                    m[n][i] = top;
+                    l[n][i] *= keep;
+                    float rel = 0.0f;
+#pragma unroll
+                    for (int b = 0; b < kSubs; ++b)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) rel = fmaxf(rel, exp2_approx(fmaf(of(sc[b][n][y]), factor[n][i], -top)) * vs[b][y]);
+                    rel = across(rel);
+                    rel = max3(rel, sums, kLeastP);
+                    if (passed) up[n][i] = __fdividef(kTopP, rel);
+                    grow[i] = passed ? __fdividef(sums, rel) : 1.0f;   // 1 at most
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    o[n][i][0] *= grow[0], o[n][i][1] *= grow[1];
+                    o[n][i][2] *= grow[0], o[n][i][3] *= grow[1];
+                }
+                ones[n][0] *= grow[0], ones[n][1] *= grow[1];
+            }
+            weigh();
+        }
+        if (masked && __any_sync(0xFFFFFFFFu, nan != 0)) {
+            const float bad = __uint_as_float(0x7FC00000u);
+#pragma unroll
+            for (int b = 0; b < kSubs; ++b)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        if (nan >> (2 * b + y) & 1u)
+                            p[b][n][y] = make_float2(sc[b][n][y].x == kNegInf ? 0.0f : bad, sc[b][n][y].y == kNegInf ? 0.0f : bad);
+        }
+#pragma unroll
+        for (int b = 0; b < kSubs; ++b) {
+            const uint32_t vat = stage_at + value_at + b * next_codes;
+            uint32_t w0[kWords], w1[kWords];   // tokens 2t, 2t + 1; those 8 on
+            load_words<D>(vat, w0);
+            load_words<D>(vat + 4 * D, w1);
+            // Binary16 under 2^16, normal down to 2^-26 of the row's largest.
+            uint32_t pt[NQ][2];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                const float2 sum = __fadd2_rn(__fadd2_rn(w[b][n][0], w[b][n][1]), make_float2(l[n][0], l[n][1]));
+                l[n][0] = sum.x, l[n][1] = sum.y;
+                pt[n][0] = transpose8(pack2<__half>(p[b][n][0].x, p[b][n][0].y));
+                pt[n][1] = transpose8(pack2<__half>(p[b][n][1].x, p[b][n][1].y));
+                constexpr uint32_t kOne = 0x3C003C00u;
+                mma_16816<__half>(ones[n], kOne, kOne, kOne, kOne, pt[n][0], pt[n][1]);
+            }
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t lo = w0[i] >> (8 * x), hi = w1[i] >> (8 * x);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+                        mma_16816<__half>(o[n][2 * i + x], lo & kLow, lo & kHigh, hi & kLow, hi & kHigh, pt[n][0], pt[n][1]);
+                }
+        }
+    }
+
+    // The sums of rows 8n .. 8n + 7 into s_o[warp][8][kLd], s_m and s_l[warp][8].
+    __device__ __forceinline__ void put(int n, float* s_o, float* s_m, float* s_l) {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = warp * 8 + 2 * t + i;
+            const float unit = 1.0f / up[n][i], eight = 8.0f * ones[n][i];
+            l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 4);
+            l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 8);
+            l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 16);
+            if (g == 0) s_m[at] = m[n][i], s_l[at] = l[n][i];
+#pragma unroll
+            for (int e = 0; e < kWords; ++e) {
+                // 2^24 and 2^20, less the codes' 8
+                auto value = [&](int x, int row) { return fmaf(o[n][2 * e + x][2 * row + i], row ? 1048576.0f : 16777216.0f, -eight) * unit; };
+                *reinterpret_cast<float4*>(s_o + at * kLd + 64 * (e / 2) + 8 * g + 4 * (e % 2)) =
+                    make_float4(value(0, 0), value(0, 1), value(1, 0), value(1, 1));
+            }
+        }
+    }
+    // Element d of row r (0 .. 7) of what the warps have put: maximum, sum of weights, result so far.
+    static __device__ __forceinline__ void joined(const float* s_o, const float* s_m, const float* s_l, int r, int d, float& top, float& sum, float& acc) {
+        top = s_m[r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w * 8 + r]);
+        sum = acc = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = exp2_approx(s_m[w * 8 + r] - top);
+            sum = fmaf(f, s_l[w * 8 + r], sum);
+            acc = fmaf(f, s_o[(w * 8 + r) * kLd + d], acc);
+        }
+    }
+};
+
+// Few tiles: one of 8 * NQ rows over a share of its tokens for each CTA, and a
+// tile's CTAs a cluster, which joins through distributed shared memory.  One warp
+// copies pages into a ring of stages of 128 tokens, four take 32 tokens of each.
+template <typename T, int D, int NQ>
+__global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_cluster_kernel(const AttnArgs a) {
+    using R = Ring<D, NQ>;
+    using A = Attend<T, D, NQ>;
+    constexpr int kRows = 8 * NQ, kGroup = kWarps * 8 * A::kLd;   // floats of eight rows
+    static_assert(NQ * kGroup * 4 + (2 * kWarps + 2) * kRows * 4 <= R::kLiveAt, "the joining reuses the ring");
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x / 32;
+    const int u = blockIdx.x / a.splits, split = blockIdx.x % a.splits, h = blockIdx.y;
+    Tile tile;
+    // A cluster's CTAs have one tile: they leave here together or not at all.
+    if (!tile.find(a, u, kRows, kStep, h == 0 && split == 0)) return;
+    const int step_begin = min(tile.steps, split * tile.per);
+    const int steps = min(tile.steps, step_begin + tile.per) - step_begin;
+    const int tok_begin = tile.tok0 + step_begin * kStep;
+    Stages<D, NQ> st(smem);
+    if (threadIdx.x == 0) st.init();
+    __syncthreads();
+
+    float* s_o = reinterpret_cast<float*>(smem);     // [NQ][warps][8][kLd]
+    float* s_m = s_o + NQ * kGroup;                  // [NQ][warps][8]
+    float* s_l = s_m + kWarps * kRows;
+    float* s_joined = s_l + kWarps * kRows;          // (maximum, sum) of each row
+    if (warp == kWarps) {
+        int issued = 0;
+        copy_steps(a, tile, h, tok_begin, steps, st, issued);
+        drain_all(st, issued, a.err);
+        __syncthreads();   // the ring is free
+        __syncthreads();   // the warps' results are in it
+    } else {
+        A rows;
+        rows.locate(a.c.page_log2);
+        rows.start(a, tile, [&](int r, int d) { return query<T, D>(a, tile, h, r, d); });
+        for (int s = 0; s < steps; ++s) {
+            if (!st.wait_full(a.err)) break;
+            const int tok = tok_begin + s * kStep + warp * (kSubs * kSub);
+            if (tok < tile.hi) rows.step(st.at(), tok, st.live_subs[st.stage] >> (warp * kSubs));
+            st.release();
+            st.next();
         }
         __syncthreads();   // the ring is free: every copy has landed and been used
-
-        // Join the warps: each has a maximum, a sum and unnormalised outputs.
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int at = warp * kRows + 8 * n + 2 * t + i;
-                const float unit = 1.0f / up[n][i], eight = 8.0f * ones[n][i];
-                l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 4);
-                l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 8);
-                l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 16);
-                if (g == 0) s_m[at] = m[n][i], s_l[at] = l[n][i];
-#pragma unroll
-                for (int e = 0; e < kWords; ++e) {
-                    // 2^24 and 2^20, less the codes' 8
-                    auto value = [&](int x, int row) { return fmaf(o[n][2 * e + x][2 * row + i], row ? 1048576.0f : 16777216.0f, -eight) * unit; };
-                    *reinterpret_cast<float4*>(s_o + at * kLd + 64 * (e / 2) + 8 * g + 4 * (e % 2)) =
-                        make_float4(value(0, 0), value(0, 1), value(1, 0), value(1, 1));
-                }
-            }
+        for (int n = 0; n < NQ; ++n) rows.put(n, s_o + n * kGroup, s_m + n * kWarps * 8, s_l + n * kWarps * 8);
         __syncthreads();
     }
 
     [[maybe_unused]] const int64_t o_bytes =
         ((a.b.rows - 1) * a.O.row + (a.q_heads - 1) * a.O.head + D) * (int64_t)sizeof(T);
     const int rows = min(tile.nrows - tile.r0, kRows);
-    const bool whole = a.splits == 1 || (!cluster && tile.active == 1);
-    float* part = a.partial ? a.partial + (((int64_t)u * a.c.heads + h) * a.splits + split) * (kRows * (D + 2)) : nullptr;
+    auto place = [&](int r, int d) { return s_o + r / 8 * kGroup + r % 8 * A::kLd + d; };   // warp 0's
     for (int i = threadIdx.x; i < rows * D; i += kThreads) {
         const int r = i / D, d = i % D;
-        float top = s_m[r];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w * kRows + r]);
-        float sum = 0.0f, acc = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2_approx(s_m[w * kRows + r] - top);
-            sum = fmaf(f, s_l[w * kRows + r], sum);
-            acc = fmaf(f, s_o[(w * kRows + r) * kLd + d], acc);
-        }
-        if (whole) {
+        float top, sum, acc;
+        A::joined(s_o + r / 8 * kGroup, s_m + r / 8 * kWarps * 8, s_l + r / 8 * kWarps * 8, r % 8, d, top, sum, acc);
+        if (a.splits == 1) {
             T* dst = out_row<T>(a, tile, h, tile.r0 + r) + d;
             if (GEMM_DBG_OK(dst, a.O.p, o_bytes, sizeof(T))) *dst = from_float<T>(sum == 0.0f ? 0.0f : acc / sum);
-        } else if (cluster) {
-            s_o[r * kLd + d] = acc;   // warp 0's place: read by this thread alone so far
-            if (d == 0) {
-                float* ml = s_l + kWarps * kRows + 2 * r;
-                ml[0] = top, ml[1] = sum;
-            }
         } else {
-            if (GEMM_DBG_OK(part + i, a.partial, a.partial_bytes, 4)) part[i] = acc;
-            if (d == 0 && GEMM_DBG_OK(part + kRows * D + 2 * r, a.partial, a.partial_bytes, 8))
-                part[kRows * D + 2 * r] = top, part[kRows * D + 2 * r + 1] = sum;
+            *place(r, d) = acc;   // read by this thread alone so far
+            if (d == 0) s_joined[2 * r] = top, s_joined[2 * r + 1] = sum;
         }
     }
-    if (!cluster) return;
+    if (a.splits == 1) return;
     // The cluster's CTAs each join a share of the results, in split order.
     cluster_sync();
     const int share = (rows * D + a.splits - 1) / a.splits;
     for (int i = split * share + threadIdx.x; i < min(rows * D, (split + 1) * share); i += kThreads) {
         const int r = i / D, d = i % D;
-        const uint32_t ml = smem_u32(s_l + kWarps * kRows + 2 * r), at = smem_u32(s_o + r * kLd + d);
+        const uint32_t ml = smem_u32(s_joined + 2 * r), at = smem_u32(place(r, d));
         float tops[kMaxCluster], sums[kMaxCluster], accs[kMaxCluster], top = kLowest;
 #pragma unroll
         for (int s = 0; s < kMaxCluster; ++s) {
@@ -485,20 +560,326 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_attention_kernel(c
     cluster_sync();   // no CTA leaves while another reads its results
 }
 
+// ---- many tiles ------------------------------------------------------------------
+// All steps of all tiles and heads stand in one line, sequences first, then tiles,
+// heads and steps, and each CTA of one round takes an equal piece of it: its first
+// and its last tile may be others' too, and a second launch joins those.  (A
+// sequence's tiles count as many steps each as its longest can have: a walk needs
+// lengths and row counts alone.)
+struct Walk {
+    int seq;
+    int64_t at, left;                  // place among the sequence's steps; steps still to go
+    int row0, count, len, tiles;
+    int64_t weight;                    // steps of each of its tiles and heads
+
+    // Sequence q's numbers; `report`: one thread of the launch says what is out of range.
+    __device__ __forceinline__ void look(const AttnArgs& a, int q, int rows, bool report) {
+        const Starts starts{a.b.starts, a.b.sequences, a.b.rows};
+        seq = q;
+        row0 = (int)starts.at(q);
+        const bool good = starts.good(q);
+        count = good ? (int)starts.at(q + 1) - row0 : 0;
+        len = __ldg(a.b.at + q);
+        if (count > 0 && (len < 0 || len > (a.b.width << a.c.page_log2))) {
+            if (report) atomicOr(a.err, kErrIndex);
+            len = 0;
+        }
+        if (!good && report) atomicOr(a.err, kErrIndex);
+        tiles = (int)(((int64_t)count * a.share + rows - 1) / rows);
+        weight = ((int64_t)len + kStep - 1) / kStep;
+        if (a.window > 0) {   // the window, the tile's positions, and a step's beginning
+            const int64_t seen = ((int64_t)a.window + rows / a.share + 1 + 2 * (kStep - 1)) / kStep;
+            weight = weight < seen ? weight : seen;
+        }
+        if (weight < 1) weight = 1;
+    }
+    __device__ __forceinline__ int64_t steps(const AttnArgs& a) const { return (int64_t)tiles * a.c.heads * weight; }
+};
+
+// A CTA's next part of one tile and head, as the copying warp tells it the others
+// at the head of a stage, the queries behind it.
+struct alignas(16) Piece {
+    Tile tile;
+    int unit, h, begin, steps, pieces;   // pieces: CTAs that share the tile, known where it begins
+    bool first, whole, end;              // end: there is none
+};
+
+// False at the end.
+__device__ __forceinline__ bool next_piece(const AttnArgs& a, Walk& w, int rows, int64_t per, Piece& piece) {
+    Tile& tile = piece.tile;
+    if (w.left <= 0) return false;
+    while (w.at >= w.steps(a)) {
+        w.at -= w.steps(a);
+        if (w.seq + 1 >= a.b.sequences) return false;
+        w.look(a, w.seq + 1, rows, false);
+    }
+    const int64_t which = w.at / w.weight, k = w.at - which * w.weight;
+    const int j = (int)(which / a.c.heads);
+    const int64_t n = w.weight - k < w.left ? w.weight - k : w.left;
+    piece.h = (int)(which - (int64_t)j * a.c.heads);
+    tile.place(a, w.seq, w.row0, w.count, w.len, j * rows, rows, kStep);
+    piece.unit = (int)(((int64_t)w.row0 * a.share + (int64_t)w.seq * a.gap) / rows) + j;
+    piece.begin = (int)(k < tile.steps ? k : tile.steps);
+    piece.steps = (int)(k + n < tile.steps ? k + n : tile.steps) - piece.begin;
+    piece.first = k == 0;
+    piece.whole = k == 0 && n == w.weight;
+    piece.pieces = 1 + (int)((w.weight - n + per - 1) / per);
+    w.at += n;
+    w.left -= n;
+    return true;
+}
+
+// A barrier of the four warps that compute, and whether all of them are `well`.
+__device__ __forceinline__ bool warps_agree(bool well) {
+    uint32_t all;
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        "setp.ne.u32 q, %1, 0;\n"
+        "bar.red.and.pred p, 1, %2, q;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(all)
+        : "r"((uint32_t)well), "n"(kWarps * 32)
+        : "memory");
+    return all != 0;
+}
+
 template <typename T, int D, int NQ>
-cudaError_t launch(const AttnArgs& a, const KvPlan& plan, cudaStream_t stream) {
+__global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_line_kernel(const AttnArgs a) {
+    using R = Ring<D, NQ>;
+    using A = Attend<T, D, NQ>;
+    constexpr int kRows = 8 * NQ;
+    static_assert(kWarps * 8 * A::kLd * 4 <= R::kStageBytes && sizeof(Piece) + kRows * D * 2 <= R::kStageBytes && R::kStageBytes % 16 == 0 && NQ <= R::kStages,
+                  "eight rows of four warps fit a stage, and a piece with its queries");
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_sum[kThreads / 32];
+    __shared__ Walk s_walk;
+    __shared__ float s_ml[2][2][NQ][kWarps * 8];     // of a piece and of the next: maxima, sums
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    grid_launch_dependents();   // the joining launch may start its set-up
+    Stages<D, NQ> st(smem);
+    if (threadIdx.x == 0) st.init();
+    if (blockIdx.x == 0) Starts{a.b.starts, a.b.sequences, a.b.rows}.check(a.err);
+
+    // Where this CTA's piece of the line begins: sums over sequences, a thread
+    // some neighbours, then the thread that has the beginning looks for it.
+    const int each = (a.b.sequences + kThreads - 1) / kThreads, q0 = min(a.b.sequences, (int)threadIdx.x * each), q1 = min(a.b.sequences, q0 + each);
+    Walk walk;
+    int64_t mine = 0;
+    for (int q = q0; q < q1; ++q) {
+        walk.look(a, q, kRows, blockIdx.x == 0);
+        mine += walk.steps(a);
+    }
+    int64_t before = mine;
+    for (int i = 1; i < 32; i *= 2) {
+        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, before, i);
+        if (lane >= i) before += x;
+    }
+    if (lane == 31) s_sum[warp] = before;
+    if (threadIdx.x == 0) s_walk.seq = -1;
+    __syncthreads();
+    int64_t all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) before += all;
+        all += s_sum[w];
+    }
+    before -= mine;
+    const int64_t per = (all + gridDim.x - 1) / gridDim.x, lo = per * blockIdx.x;
+    if (mine > 0 && before <= lo && lo < before + mine) {
+        int64_t at = lo - before;
+        for (int q = q0; q < q1; ++q) {
+            walk.look(a, q, kRows, false);
+            if (at < walk.steps(a)) break;
+            at -= walk.steps(a);
+        }
+        walk.at = at;
+        walk.left = per < all - lo ? per : all - lo;
+        s_walk = walk;
+    }
+    __syncthreads();
+    if (s_walk.seq < 0) return;   // past the end of the line
+    walk = s_walk;
+
+    if (warp == kWarps) {
+        int issued = 0;
+        Piece piece;
+        for (bool ok = true; ok;) {
+            piece.end = !next_piece(a, walk, kRows, per, piece);
+            if (!(ok = st.wait_empty(a.err))) break;
+            uint8_t* at = smem + st.stage * R::kStageBytes;
+            if (lane == 0) *reinterpret_cast<Piece*>(at) = piece;
+            if (!piece.end) {
+                Eight<T> x[kRows * D / 256];
+#pragma unroll
+                for (int i = 0; i < kRows * D / 256; ++i) x[i] = query<T, D>(a, piece.tile, piece.h, (i * 32 + lane) / (D / 8), (i * 32 + lane) % (D / 8) * 8);
+#pragma unroll
+                for (int i = 0; i < kRows * D / 256; ++i) *reinterpret_cast<uint4*>(at + sizeof(Piece) + 16 * (i * 32 + lane)) = x[i].v[0];
+            }
+            auto pass = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(st.bars + 8 * st.stage);
+                ++issued;
+                st.next();
+            };
+            pass();
+            if (piece.end) break;
+            ok = copy_steps(a, piece.tile, piece.h, piece.tile.tok0 + piece.begin * kStep, piece.steps, st, issued);
+            for (int n = 0; ok && n < NQ; ++n) {   // stages for the warps to join in
+                if ((ok = st.wait_empty(a.err))) pass();
+            }
+        }
+        drain_all(st, issued, a.err);
+        return;
+    }
+    [[maybe_unused]] const int64_t o_bytes =
+        ((a.b.rows - 1) * a.O.row + (a.q_heads - 1) * a.O.head + D) * (int64_t)sizeof(T);
+    A rows;
+    rows.locate(a.c.page_log2);
+    bool ok = true;   // of all four warps alike, from one joining to the next
+    for (int turn = 0; ok; turn ^= 1) {
+        if (!(ok = warps_agree(st.wait_full(a.err)))) break;
+        const uint8_t* at = smem + st.stage * R::kStageBytes;
+        const Piece piece = *reinterpret_cast<const Piece*>(at);
+        if (piece.end) break;
+        const Tile& tile = piece.tile;
+        rows.start(a, tile, [&](int r, int d) {
+            Eight<T> x;
+            x.v[0] = *reinterpret_cast<const uint4*>(at + sizeof(Piece) + (r * D + d) * 2);
+            return x;
+        });
+        fence_proxy_async_shared();   // copies into this stage come after
+        st.release();
+        st.next();
+        const int tok_begin = tile.tok0 + piece.begin * kStep;
+        for (int s = 0; ok && s < piece.steps; ++s) {
+            if (!(ok = st.wait_full(a.err))) break;
+            const int tok = tok_begin + s * kStep + warp * (kSubs * kSub);
+            if (tok < tile.hi) rows.step(st.at(), tok, st.live_subs[st.stage] >> (warp * kSubs));
+            st.release();
+            st.next();
+        }
+        if (ok && threadIdx.x == 0 && piece.first) {
+            int2* to = a.where + (int64_t)piece.unit * a.c.heads + piece.h;
+            if (GEMM_DBG_OK(to, a.where, a.where_bytes, 8)) *to = make_int2(blockIdx.x, piece.whole ? 1 : piece.pieces);
+        }
+        // A slot for the tile that others began, one for that which others go on with.
+        float* slot = a.partial + ((int64_t)blockIdx.x * 2 + (piece.first ? 1 : 0)) * (kRows * (D + 2));
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            ok = ok && st.wait_full(a.err);
+            float* s_o = reinterpret_cast<float*>(smem + st.stage * R::kStageBytes);
+            float *s_m = s_ml[turn][0][n], *s_l = s_ml[turn][1][n];
+            if (ok) rows.put(n, s_o, s_m, s_l);
+            if (!(ok = warps_agree(ok))) break;
+            const int live = min(tile.nrows - tile.r0 - 8 * n, 8);
+            for (int i = threadIdx.x; i < live * D; i += kWarps * 32) {
+                const int r = i / D, d = i % D;
+                float top, sum, acc;
+                A::joined(s_o, s_m, s_l, r, d, top, sum, acc);
+                if (piece.whole) {
+                    T* dst = out_row<T>(a, tile, piece.h, tile.r0 + 8 * n + r) + d;
+                    if (GEMM_DBG_OK(dst, a.O.p, o_bytes, sizeof(T))) *dst = from_float<T>(sum == 0.0f ? 0.0f : acc / sum);
+                } else {
+                    float *to = slot + (8 * n + r) * D + d, *ml = slot + kRows * D + 2 * (8 * n + r);
+                    if (GEMM_DBG_OK(to, a.partial, a.partial_bytes, 4)) *to = acc;
+                    if (d == 0 && GEMM_DBG_OK(ml, a.partial, a.partial_bytes, 8)) ml[0] = top, ml[1] = sum;
+                }
+            }
+            fence_proxy_async_shared();   // copies into this stage come after
+            st.release();
+            st.next();
+        }
+    }
+}
+
+// Joins the tiles that were shared, in the order of their tokens: a warp a row
+// (TEAM = 1), or eight warps one where few tiles are shared by many CTAs each, so that
+// all parts' loads are under way at once.
+template <typename T, int D, int NQ, int TEAM>
+__global__ void __launch_bounds__(256) kv4_line_join_kernel(const AttnArgs a) {
+    constexpr int kRows = 8 * NQ, kEach = D / 32;
+    __shared__ float s_acc[TEAM][D], s_sum[TEAM];
+    const int u = blockIdx.x, h = blockIdx.y, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    Tile tile;
+    const bool found = tile.find(a, u, kRows, kStep, false);
+    grid_dependency_wait();   // launched while the parts are still being made
+    if (!found) return;
+    const int2* at = a.where + (int64_t)u * a.c.heads + h;
+    if (!GEMM_DBG_OK(at, a.where, a.where_bytes, 8)) return;
+    const int first = at->x, pieces = at->y, ctas = (int)(a.partial_bytes / (2 * kRows * (D + 2) * 4));
+    if (pieces <= 1 || first < 0 || pieces > ctas - first) return;   // (also if the wait of a part gave up)
+    [[maybe_unused]] const int64_t o_bytes =
+        ((a.b.rows - 1) * a.O.row + (a.q_heads - 1) * a.O.head + D) * (int64_t)sizeof(T);
+    const int member = warp % TEAM, r = blockIdx.z * (8 / TEAM) + warp / TEAM;
+    if (TEAM == 1 ? tile.r0 + r >= tile.nrows : tile.r0 + (int)blockIdx.z >= tile.nrows) return;   // of a team all or none
+    auto part = [&](int i) { return a.partial + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * (kRows * (D + 2)); };
+    float top = kLowest, sum = 0.0f, acc[kEach] = {};
+    for (int i = lane; i < pieces; i += 32) {
+        const float* ml = part(i) + kRows * D + 2 * r;
+        if (GEMM_DBG_OK(ml, a.partial, a.partial_bytes, 8)) top = fmaxf(top, ml[0]);
+    }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
+    const int share = (pieces + TEAM - 1) / TEAM;
+#pragma unroll 8
+    for (int i = member * share; i < min(pieces, (member + 1) * share); ++i) {
+        const float *from = part(i), *ml = from + kRows * D + 2 * r;
+        if (!GEMM_DBG_OK(ml, a.partial, a.partial_bytes, 8)) continue;
+        const float f = exp2_approx(ml[0] - top);
+        sum = fmaf(f, ml[1], sum);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) acc[e] = fmaf(f, from[r * D + lane + 32 * e], acc[e]);
+    }
+    if constexpr (TEAM > 1) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) s_acc[member][lane + 32 * e] = acc[e];
+        if (lane == 0) s_sum[member] = sum;
+        __syncthreads();
+        if (member > 0) return;
+#pragma unroll
+        for (int w = 1; w < TEAM; ++w) {
+            sum += s_sum[w];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) acc[e] += s_acc[w][lane + 32 * e];
+        }
+    }
+    T* dst = out_row<T>(a, tile, h, tile.r0 + r) + lane;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+        if (GEMM_DBG_OK(dst + 32 * e, a.O.p, o_bytes, sizeof(T))) dst[32 * e] = from_float<T>(sum == 0.0f ? 0.0f : acc[e] / sum);
+}
+
+template <typename T, int D, int NQ>
+cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(plan.units * plan.splits), (unsigned)a.c.heads);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Ring<D, NQ>::kBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = a.partial ? 1 : (unsigned)plan.splits;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_attention_kernel<T, D, NQ>, a);
+    *launches = 1;
+    if (plan.ctas == 0) {
+        cfg.gridDim = dim3((unsigned)(plan.units * plan.splits), (unsigned)a.c.heads);
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)plan.splits;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        return cudaLaunchKernelEx(&cfg, kv4_cluster_kernel<T, D, NQ>, a);
+    }
+    cfg.gridDim = dim3((unsigned)plan.ctas);
+    cfg.numAttrs = 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_line_kernel<T, D, NQ>, a);
+    if (e != cudaSuccess) return e;
+    *launches = 2;
+    const bool team = plan.ctas > 8 * plan.units * a.c.heads;
+    cfg.gridDim = dim3((unsigned)plan.units, (unsigned)a.c.heads, team ? plan.rows : NQ);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = kUsePdl;
+    cfg.numAttrs = 1;
+    return team ? cudaLaunchKernelEx(&cfg, kv4_line_join_kernel<T, D, NQ, 8>, a) : cudaLaunchKernelEx(&cfg, kv4_line_join_kernel<T, D, NQ, 1>, a);
 }
 
 // Calls f with a kernel's type, head size and eights of rows.
@@ -522,19 +903,36 @@ cudaError_t kv4_attention_setup() {
         for (int dim : {64, 128})
             for (int rows : {8, 16}) {
                 const cudaError_t e = with_kernel(type, dim, rows, [](auto t, auto d, auto nq) {
+                    using T = decltype(t);
                     constexpr int D = decltype(d)::value, NQ = decltype(nq)::value;
-                    return cudaFuncSetAttribute(kv4_attention_kernel<decltype(t), D, NQ>,
-                                                cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D, NQ>::kBytes);
+                    const auto most = cudaFuncAttributeMaxDynamicSharedMemorySize;
+                    const cudaError_t c = cudaFuncSetAttribute(kv4_cluster_kernel<T, D, NQ>, most, Ring<D, NQ>::kBytes);
+                    return c != cudaSuccess ? c : cudaFuncSetAttribute(kv4_line_kernel<T, D, NQ>, most, Ring<D, NQ>::kBytes);
                 });
                 if (e != cudaSuccess) return e;
             }
     return cudaSuccess;
 }
 
-cudaError_t launch_kv4_few(const AttnArgs& a, ElemType type, const KvPlan& plan, cudaStream_t stream) {
+cudaError_t launch_kv4_few(const AttnArgs& a, ElemType type, const KvPlan& plan, int* launches, cudaStream_t stream) {
     return with_kernel(type, a.c.dim, plan.rows, [&](auto t, auto d, auto nq) {
-        return launch<decltype(t), decltype(d)::value, decltype(nq)::value>(a, plan, stream);
+        return launch<decltype(t), decltype(d)::value, decltype(nq)::value>(a, plan, launches, stream);
     });
+}
+
+// The host's part of launch_kv4_few: how few rows' tokens are shared.
+void kv4_few_plan(KvPlan& p, const KvView& c, int64_t have, int64_t most, int num_sms) {
+    const int64_t slots = (int64_t)resident(p.rows / 8) * num_sms;
+    p.ctas = 0;
+    p.cluster = true;
+    p.scratch_bytes = 0;
+    if (most <= 8 * kMaxCluster && have * (most < kMaxCluster ? most : kMaxCluster) <= slots) {
+        p.splits = (int)(most < 1 ? 1 : most < kMaxCluster ? most : kMaxCluster);
+        return;
+    }
+    p.splits = 1;
+    p.ctas = (int)(have * most < slots ? have * most : slots);
+    p.scratch_bytes = 8 * p.units * c.heads + (int64_t)p.ctas * 2 * (p.rows * (c.dim + 2) * 4);
 }
 
 }  // namespace libgemm

@@ -554,8 +554,8 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, cudaStream_t stream) {
 template <typename T, int D>
 cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStream_t stream) {
     const ElemType type = std::is_same<T, __half>::value ? ElemType::kF16 : ElemType::kBF16;
+    if (a.c.bits == 4 && plan.rows != 256) return launch_kv4_few(a, type, plan, launches, stream);
     cudaError_t e = plan.rows == 256  ? launch_kv_prompt(a, type, plan, stream)
-                    : a.c.bits == 4   ? launch_kv4_few(a, type, plan, stream)
                     : plan.rows == 8  ? launch<T, D, 1>(a, plan, stream)
                                       : launch<T, D, 2>(a, plan, stream);
     *launches = 1;
@@ -621,7 +621,7 @@ constexpr int64_t kPromptRows = 32;
 int64_t gcd(int64_t a, int64_t b) { return b ? gcd(b, a % b) : a; }
 
 KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, int num_sms) {
-    KvPlan p;
+    KvPlan p{};
     const int64_t share = q_heads / c.heads, all = b.rows * share;
     p.rows = all <= 8 * (int64_t)b.sequences    ? 8
              : all <= kPromptRows * b.sequences ? 16
@@ -632,8 +632,12 @@ KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, i
     int64_t longest = b.width << c.page_log2;
     if (window > 0 && window < longest - p.rows - 2 * kStep) longest = window + p.rows + 2 * kStep;
     if (p.units < 1) p.units = 1;
-    const int64_t have = (tiles > b.sequences ? tiles : b.sequences) * c.heads, slots = (p.rows == 256 ? 1 : c.bits == 4 && p.rows == 8 ? 3 : 2) * (int64_t)num_sms;
+    const int64_t have = (tiles > b.sequences ? tiles : b.sequences) * c.heads, slots = (p.rows == 256 ? 1 : 2) * (int64_t)num_sms;
     const int64_t most = (longest + kStep - 1) / kStep;
+    if (c.bits == 4 && p.rows != 256) {
+        kv4_few_plan(p, c, have, most, num_sms);
+        return p;
+    }
     int64_t splits;
     if (p.rows == 256) {
         splits = slots / have;
@@ -655,8 +659,15 @@ cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& 
                                 const KvBatch& b, const KvPlan& plan, void* scratch,
                                 unsigned* err, int* launches, cudaStream_t stream) {
     const bool q_vec = (reinterpret_cast<uintptr_t>(Q.p) & 15u) == 0 && Q.row % 8 == 0 && Q.head % 8 == 0;
-    const AttnArgs a{c, Q, O, b, q_heads, (unsigned)(q_heads / c.heads), plan.gap, scale * 1.44269504088896341f, causal,
-                     (int)(window < INT32_MAX ? window : INT32_MAX), plan.splits, q_vec, plan.scratch_bytes, static_cast<float*>(scratch), err};
+    AttnArgs a{c, Q, O, b, q_heads, (unsigned)(q_heads / c.heads), plan.gap, scale * 1.44269504088896341f, causal,
+               (int)(window < INT32_MAX ? window : INT32_MAX), plan.splits, q_vec, plan.scratch_bytes, static_cast<float*>(scratch),
+               nullptr, 0, err};
+    if (plan.ctas > 0) {
+        a.where = static_cast<int2*>(scratch);
+        a.where_bytes = 8 * plan.units * c.heads;
+        a.partial = reinterpret_cast<float*>(a.where + plan.units * c.heads);
+        a.partial_bytes -= a.where_bytes;
+    }
     if (type == ElemType::kBF16)
         return c.dim == 128 ? launch<__nv_bfloat16, 128>(a, plan, launches, stream)
                             : launch<__nv_bfloat16, 64>(a, plan, launches, stream);

@@ -39,7 +39,9 @@ struct AttnArgs {
     int splits;                  // CTAs that share a tile's tokens: a cluster, or with `partial` any number
     bool q_vec;                  // Q in 16-byte loads
     int64_t partial_bytes;
-    float* partial;              // [unit][head][split] x (rows x dim sums, then rows x (max, sum))
+    float* partial;              // [unit][head][split] x (rows x dim sums, then rows x (max, sum)); of 4 bits [CTA][2] x the same
+    int2* where;                 // 4 bits: [unit][head], the CTA that begins it and how many share it
+    int64_t where_bytes;
     unsigned* err;
 };
 
@@ -84,14 +86,20 @@ struct Tile {
             if (check && threadIdx.x == 0) atomicOr(a.err, kErrIndex);
             return false;
         }
+        const int first = (u - unit_of(row0, seq)) * rows;
+        if (first < 0 || first >= count * (int)a.share) return false;
+        const bool bad = length < 0 || length > (a.b.width << a.c.page_log2);
+        if (bad && check && threadIdx.x == 0) atomicOr(a.err, kErrIndex);
+        place(a, seq, row0, count, bad ? 0 : length, first, rows, step);
+        return true;
+    }
+    // The tile of the rows from `first` on of a sequence.
+    __device__ __forceinline__ void place(const AttnArgs& a, int sequence, int row, int count, int length, int first, int rows, int step) {
+        seq = sequence;
+        row0 = row;
         nrows = count * (int)a.share;
-        r0 = (u - unit_of(row0, seq)) * rows;
-        if (r0 < 0 || r0 >= nrows) return false;
+        r0 = first;
         len = length;
-        if (length < 0 || length > (a.b.width << a.c.page_log2)) {
-            if (check && threadIdx.x == 0) atomicOr(a.err, kErrIndex);
-            len = 0;
-        }
         p0 = len - count;
         hi = row_hi(a, min(r0 + rows, nrows) - 1);
         lo = row_lo(a, r0);
@@ -99,7 +107,6 @@ struct Tile {
         steps = hi > tok0 ? (hi - tok0 + step - 1) / step : 0;
         per = max(1, (steps + a.splits - 1) / a.splits);
         active = max(1, (steps + per - 1) / per);
-        return true;
     }
 };
 
@@ -113,7 +120,8 @@ __device__ __forceinline__ T* out_row(const AttnArgs& a, const Tile& tile, int h
 cudaError_t kv_prompt_setup();
 // Few query rows over a cache in 4 bits (kv4_attention.cu): tiles of 8 or 16.
 cudaError_t kv4_attention_setup();
-cudaError_t launch_kv4_few(const AttnArgs& a, ElemType type, const KvPlan& plan, cudaStream_t stream);
+void kv4_few_plan(KvPlan& p, const KvView& c, int64_t have, int64_t most, int num_sms);
+cudaError_t launch_kv4_few(const AttnArgs& a, ElemType type, const KvPlan& plan, int* launches, cudaStream_t stream);
 cudaError_t launch_kv_prompt(const AttnArgs& a, ElemType type, const KvPlan& plan, cudaStream_t stream);
 
 }  // namespace libgemm
