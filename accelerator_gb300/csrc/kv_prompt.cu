@@ -37,7 +37,8 @@
 // 2^12), as binary16 (exact for those over 2^-28 of the largest), the cache's
 // warps multiply codes by them, and what stands outside of the products is that
 // power of two alone, where the 8-bit cache has its page's scale.  Scales of tokens
-// that no row of the tile sees are taken for 0.
+// that no row of the tile sees are taken for 0; a token that reads as NaN gets keys of
+// NaN, which make NaN of the scores of the rows that see it, and values of 0.
 //
 // Every wait is bounded; a role that gives up raises the abort flag, all stop,
 // and the matrix unit is drained before tensor memory is freed.
@@ -65,7 +66,6 @@ constexpr int kSlab = kTile * 128;                           // 128 rows of 64 b
 struct alignas(16) PageData {
     float ks, log_v;
     uint32_t plain;      // 1: there, and reads as numbers; 0: reads as NaN; 2: not there
-    uint32_t nan;        // the tokens that do, of 0 in `plain`
 };
 
 template <int D, int BITS>
@@ -425,32 +425,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                 }
                 const uint32_t part = (uint32_t)(chunk * D * BITS / 8), bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, copies)) * part;
                 // 4 bits: of both operands, this lane's scales as binary16 times 2^(138 - e),
-                // e the largest's biased exponent of 16 tokens; bit i of `nan`: token i of these
-                uint32_t held[2][2] = {}, unit[2] = {}, nan = 0;
+                // e the biased exponent of the largest of 16 tokens' (held so that the power
+                // of two and its inverse are normal)
+                uint32_t held[2][2] = {}, unit[2] = {};
                 bool zero[2] = {};
                 if constexpr (BITS == 4) {
                     const int tok = tok_begin + j * kStep + lane * kTokens;
+                    uint32_t bits[2][4], nan = 0;
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
-                        uint32_t bits[4] = {now.scales[v].x & 0x7FFFu, now.scales[v].x >> 16 & 0x7FFFu, now.scales[v].y & 0x7FFFu, now.scales[v].y >> 16 & 0x7FFFu};
+                        bits[v][0] = now.scales[v].x & 0x7FFFu, bits[v][1] = now.scales[v].x >> 16 & 0x7FFFu;
+                        bits[v][2] = now.scales[v].y & 0x7FFFu, bits[v][3] = now.scales[v].y >> 16 & 0x7FFFu;
                         uint32_t most = 0;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            if (!now.live || tok + i < tile.lo || tok + i >= tile.hi) bits[i] = 0;
-                            if (bits[i] >= 0x7F80u) nan |= 1u << (lane % 4 * 4 + i), bits[i] = 0;
-                            most = max(most, bits[i]);
+                            if (!now.live || tok + i < tile.lo || tok + i >= tile.hi) bits[v][i] = 0;
+                            if (bits[v][i] >= 0x7F80u) nan |= 1u << i, bits[v][i] = 0;
+                            most = max(most, bits[v][i]);
                         }
                         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
                         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-                        const uint32_t e = max(most >> 7, 12u);   // so that the power of two and its inverse are normal
-                        const float by = __uint_as_float((265u - e) << 23);
-                        held[v][0] = pack2<__half>(__uint_as_float(bits[0] << 16) * by, __uint_as_float(bits[1] << 16) * by);
-                        held[v][1] = pack2<__half>(__uint_as_float(bits[2] << 16) * by, __uint_as_float(bits[3] << 16) * by);
-                        unit[v] = e;
+                        unit[v] = max(most >> 7, 12u);
                         zero[v] = most == 0;
                     }
-                    nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, 1);
-                    nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, 2);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const float by = __uint_as_float((265u - unit[v]) << 23);
+                        float s[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            s[i] = __uint_as_float(bits[v][i] << 16) * by;
+                            if (nan >> i & 1u) s[i] = v ? 0.0f : __uint_as_float(0x7FC00000u);
+                        }
+                        held[v][0] = pack2<__half>(s[0], s[1]);
+                        held[v][1] = pack2<__half>(s[2], s[3]);
+                    }
                 }
                 bool ok = true;
 #pragma unroll
@@ -464,10 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                                      : "memory");
                         if (values == 0 && lane % 4 == 0)
                             info[j % kSlots * kSubs + lane / 4] =
-                                PageData{__uint_as_float((unit[0] - 11u) << 23), zero[1] ? kNegInf : (float)((int)unit[1] - 138), !now.live ? 2u : nan ? 0u : 1u, nan};
+                                PageData{__uint_as_float((unit[0] - 11u) << 23), zero[1] ? kNegInf : (float)((int)unit[1] - 138), now.live ? 1u : 2u};
                     } else if (values == 0 && lane < kSubs) {
                         const bool plain = now.live && now.ks == now.ks && now.vs == now.vs;
-                        info[j % kSlots * kSubs + lane] = PageData{now.ks, plain ? log2f(now.vs) : 0.0f, plain ? 1u : now.live ? 0u : 2u, 0xFFFFu};
+                        info[j % kSlots * kSubs + lane] = PageData{now.ks, plain ? log2f(now.vs) : 0.0f, plain ? 1u : now.live ? 0u : 2u};
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(bars + 8 * (kCFull + values), bytes);
@@ -545,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                         for (int e = 0; e < kSub; ++e) {
                             uint32_t& x = v[b / 2][b % 2 * 16 + e];
                             if (kind == 2u) x = 0xFF800000u;
-                            else if (x != 0xFF800000u && (BITS == 8 || page[b].nan >> e & 1u)) x = 0x7FC00000u;
+                            else if (x != 0xFF800000u) x = 0x7FC00000u;
                         }
                     }
                     asm volatile("");
