@@ -33,11 +33,14 @@
 //
 // 4 bits.  A token's keys and values have scales of their own, and a code times its
 // scale, c in [-7, 7] times 8 bits, is exact in binary16's 11.  So the copying warp
-// brings the scales of 16 tokens down by one power of two, the largest into [2^11,
-// 2^12), as binary16 (exact for those over 2^-28 of the largest), the cache's
-// warps multiply codes by them, and what stands outside of the products is that
-// power of two alone, where the 8-bit cache has its page's scale.  Scales of tokens
-// that no row of the tile sees are taken for 0; a token that reads as NaN gets keys of
+// brings the scales of 16 tokens to one power of two, S in [2^15, 2^16) for the
+// largest, as binary16, the cache's warps make c * S * 2^-24 of the codes, and what
+// stands outside of the products is a power of two alone, where the 8-bit cache has
+// its page's scale.  A masked nibble is the number u * 2^-24 (or 2^-20), below
+// binary16's normal range, so that c * S * 2^-24 is one fused multiply-add, exact
+// for scales down to 2^-8 of the largest; blocks that have others take c * S * 2^-4
+// by a subtraction and a product, exact down to 2^-28.  Codes wait in two buffers.
+// Scales of tokens that no row of the tile sees are taken for 0; a token that reads as NaN gets keys of
 // NaN, which make NaN of the scores of the rows that see it, and values of 0.
 //
 // Every wait is bounded; a role that gives up raises the abort flag, all stop,
@@ -49,7 +52,9 @@ namespace {
 
 constexpr int kTile = 128, kRows = 2 * kTile, kStep = 128;   // rows of a tile and a CTA, tokens of a block
 constexpr int kSub = 16, kSubs = kStep / kSub;               // tokens that share a page for certain
-constexpr int kSlots = 4;                                    // blocks whose page data are kept
+// Code buffers of each operand, and blocks whose page data are kept.
+constexpr int code_buffers(int bits) { return bits == 4 ? 2 : 1; }
+constexpr int kept_blocks(int bits) { return bits == 4 ? 5 : 4; }
 constexpr int kSoftWarps = 8, kCacheWarps = 4, kThreads = (kSoftWarps + kCacheWarps + 4) * 32;
 // Registers of a thread: launched with 128, then shared out among the roles
 // (whole warpgroups), whose sum is that of the launch.  Of 4 bits the copying warp
@@ -73,15 +78,18 @@ struct Smem {
     static constexpr int kOperand = D / 64 * kSlab;          // 128 x D binary16
     static constexpr int kQ = 0, kK = 2 * kOperand, kV = kK + 2 * kOperand;
     static constexpr int kCodeBytes = kStep * D * BITS / 8;  // keys' and values' each
-    static constexpr int kCodes = kV + 2 * kOperand, kScales = kCodes + 2 * kCodeBytes;
-    static constexpr int kInfo = kScales + (BITS == 4 ? 2 * kStep * 2 : 0);   // binary16 scales, keys' and values'
+    static constexpr int kBuffers = code_buffers(BITS), kSlots = kept_blocks(BITS);
+    // codes [buffer][keys, values]; of 4 bits binary16 scales, and whether they are far apart, likewise
+    static constexpr int kCodes = kV + 2 * kOperand, kScales = kCodes + 2 * kBuffers * kCodeBytes;
+    static constexpr int kWide = kScales + (BITS == 4 ? 2 * kBuffers * kStep * 2 : 0), kInfo = kWide + (BITS == 4 ? 16 : 0);
     static constexpr int kBars = kInfo + kSlots * kSubs * (int)sizeof(PageData);
-    static constexpr int kBytes = kBars + 256 + 1024;        // and the alignment
+    static constexpr int kBytes = kBars + 208 + 1024;        // and the alignment
+    static_assert(kBytes + 16 <= 227 * 1024, "");
 };
 // Barriers: keys and values full / empty (two buffers), per tile scores full,
 // weights full (of the first and of the last 64 tokens), output done; codes
-// full / empty (keys, values); the drain.
-enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kODone = 14, kCFull = 16, kCEmpty = 18, kDrain = 20 };
+// full / empty (keys, values; buffers); the drain.
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kODone = 14, kCFull = 16, kCEmpty = 20, kDrain = 24 };
 
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -128,11 +136,35 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 // Chunk c (eight binary16) of row r of a 64-wide slab: 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// Nibbles of a word, c = u - 8 as pairs of binary16: bits 0-3 with 16-19, and 4-7 with 20-23.
+// What makes values of a word's codes: of a pair of scales S, c * S * 2^-24, or with
+// WIDE c * S * 2^-4.
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t bits_of(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
-__device__ __forceinline__ __half2 nibbles_low(uint32_t w) { return __hsub2(as_half2((w & 0x000F000Fu) | 0x64006400u), as_half2(0x64086408u)); }    // 1024 + u
-__device__ __forceinline__ __half2 nibbles_high(uint32_t w) { return __hsub2(as_half2((w & 0x00F000F0u) | 0x54005400u), as_half2(0x54805480u)); }   // 64 + u
+struct Factors {
+    bool wide;
+    __half2 low, high, less;
+    __device__ __forceinline__ Factors(uint32_t scales, bool w) : wide(w) {
+        const __half2 s = as_half2(scales), sixteenth = as_half2(0x2C002C00u);
+        high = __hmul2(s, sixteenth);
+        low = wide ? high : s;
+        less = __hmul2(s, as_half2(0x80088008u));   // -8 * 2^-24
+    }
+    // The nibbles of bits 0-3 and 16-19, 4-7 and 20-23, 8-11 and 24-27, and the last ones.
+    __device__ __forceinline__ void four(uint32_t x, uint32_t (&d)[4]) const {
+        const uint32_t y = x >> 8, w[4] = {x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!wide) d[i] = bits_of(__hfma2(as_half2(w[i]), i & 1 ? high : low, less));
+            else if (i & 1) d[i] = bits_of(__hmul2(__hsub2(as_half2(w[i] | 0x54005400u), as_half2(0x54805480u)), low));   // 64 + u
+            else d[i] = bits_of(__hmul2(__hsub2(as_half2(w[i] | 0x64006400u), as_half2(0x64086408u)), low));              // 1024 + u
+        }
+    }
+};
+template <typename F>
+__device__ __forceinline__ void with_values(uint32_t wide, F f) {
+    if (wide) f(std::true_type());
+    else f(std::false_type());
+}
 
 template <typename T, int D, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a, bool o_vec) {
@@ -146,6 +178,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
     const uint32_t bars = base + L::kBars;
     volatile int* abort_flag = &s_abort;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int kSlots = L::kSlots;
+    // The barriers of block j's codes, and the phase in which they are its.
+    auto code_bar = [&](int which, int values, int j) { return bars + 8 * (which + values * L::kBuffers + j % L::kBuffers); };
+    auto code_parity = [&](int j) { return (uint32_t)(j / L::kBuffers) & 1u; };
     // Heads fastest: sequences come one after another, long ones seldom last.
     const int h = blockIdx.x % a.c.heads, split = blockIdx.x / a.c.heads % a.splits, u = blockIdx.x / a.c.heads / a.splits;
     Tile tile;
@@ -168,6 +204,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
             mbar_init(bars + 8 * (kPFull + 2 * i), kTile / 32);
             mbar_init(bars + 8 * (kPFull + 2 * i + 1), kTile / 32);
             mbar_init(bars + 8 * (kODone + i), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(bars + 8 * (kCFull + i), 1);
             mbar_init(bars + 8 * (kCEmpty + i), kCacheWarps);
         }
@@ -238,16 +276,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
         const int piece = D == 128 && BITS == 8 ? ct % 4 + 4 * (ct / 8 % 2) : ct % 4;
         const int sub_row = BITS == 4 ? ct / 32 * 8 + ct / 8 % 4 + 4 * (ct / 4 % 2) : D == 128 ? ct / 16 * 2 + ct / 4 % 2 : ct / 4;
         uint4 w[BITS == 8 ? kPasses : 1];
-        uint32_t words[BITS == 4 ? kPasses : 1][kWords], scales[BITS == 4 ? kPasses : 1];
-        auto get = [&](int values, uint32_t parity) {
-            if (!warp_wait(bars + 8 * (kCFull + values), parity, abort_flag, a.err)) return false;
-            const uint32_t codes = base + L::kCodes + values * L::kCodeBytes;
+        uint32_t words[BITS == 4 ? kPasses : 1][kWords], scales[BITS == 4 ? kPasses : 1], wide = 0;
+        auto get = [&](int values, int j) {
+            if (!warp_wait(code_bar(kCFull, values, j), code_parity(j), abort_flag, a.err)) return false;
+            const int buffer = j % L::kBuffers * 2 + values;
+            const uint32_t codes = base + L::kCodes + buffer * L::kCodeBytes;
             if constexpr (BITS == 8) {
                 const uint32_t from = codes + sub_row * D + 16 * piece;
 #pragma unroll
                 for (int i = 0; i < kPasses; ++i) w[i] = lds128(from + i * kPassRows * D);
             } else {
-                const uint32_t at = base + L::kScales + values * (2 * kStep);
+                const uint32_t at = base + L::kScales + buffer * (2 * kStep);
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(wide) : "r"(base + L::kWide + 4 * buffer));
 #pragma unroll
                 for (int i = 0; i < kPasses; ++i) {
                     // values: warp by warp the eights of tokens, of which a lane has a pair
@@ -282,51 +322,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                 }
             } else if (!values) {   // word e is the chunk of elements 32 e + 8 piece on
                 const uint32_t at = to + sub_row * 128, r = sub_row & 7;
+                with_values(wide, [&](auto values_of) {
 #pragma unroll
-                for (int i = 0; i < kPasses; ++i) {
-                    const __half2 s = as_half2(scales[i]);
+                    for (int i = 0; i < kPasses; ++i) {
+                        const Factors f(scales[i], decltype(values_of)::value);
 #pragma unroll
-                    for (int e = 0; e < kWords; ++e) {
-                        const uint32_t x = words[i][e], y = x >> 8;
-                        st_shared_v4(at + e / 2 * kSlab + i * kPassRows * 128 + (((4 * (e % 2) + piece) ^ r) << 4),
-                                     bits_of(__hmul2(nibbles_low(x), s)), bits_of(__hmul2(nibbles_high(x), s)),
-                                     bits_of(__hmul2(nibbles_low(y), s)), bits_of(__hmul2(nibbles_high(y), s)));
+                        for (int e = 0; e < kWords; ++e) {
+                            uint32_t d[4];
+                            f.four(words[i][e], d);
+                            st_shared_v4(at + e / 2 * kSlab + i * kPassRows * 128 + (((4 * (e % 2) + piece) ^ r) << 4), d[0], d[1], d[2], d[3]);
+                        }
                     }
-                }
+                });
             } else {                // words 2e, 2e + 1 are four elements each of two tokens, chunk g of slab e
                 const int g = ct % 32 / 4, t = ct % 4;
+                with_values(wide, [&](auto values_of) {
 #pragma unroll
-                for (int i = 0; i < kPasses; ++i) {
-                    const uint32_t at = to + (8 * (i * kCacheWarps + ct / 32) + 2 * t) * 128;
-                    const __half2 s = as_half2(scales[i]);
+                    for (int i = 0; i < kPasses; ++i) {
+                        const uint32_t at = to + (8 * (i * kCacheWarps + ct / 32) + 2 * t) * 128;
+                        const Factors f(scales[i], decltype(values_of)::value);
 #pragma unroll
-                    for (int e = 0; e < D / 64; ++e) {
-                        uint32_t even[4], odd[4];
+                        for (int e = 0; e < D / 64; ++e) {
+                            uint32_t even[4], odd[4];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const uint32_t x = words[i][2 * e + q], y = x >> 8;
-                            const uint32_t d0 = bits_of(__hmul2(nibbles_low(x), s)), d1 = bits_of(__hmul2(nibbles_high(x), s));
-                            const uint32_t d2 = bits_of(__hmul2(nibbles_low(y), s)), d3 = bits_of(__hmul2(nibbles_high(y), s));
-                            even[2 * q] = __byte_perm(d0, d1, 0x5410), even[2 * q + 1] = __byte_perm(d2, d3, 0x5410);
-                            odd[2 * q] = __byte_perm(d0, d1, 0x7632), odd[2 * q + 1] = __byte_perm(d2, d3, 0x7632);
+                            for (int q = 0; q < 2; ++q) {
+                                uint32_t d[4];
+                                f.four(words[i][2 * e + q], d);
+                                even[2 * q] = __byte_perm(d[0], d[1], 0x5410), even[2 * q + 1] = __byte_perm(d[2], d[3], 0x5410);
+                                odd[2 * q] = __byte_perm(d[0], d[1], 0x7632), odd[2 * q + 1] = __byte_perm(d[2], d[3], 0x7632);
+                            }
+                            st_shared_v4(at + e * kSlab + ((g ^ (2 * t)) << 4), even[0], even[1], even[2], even[3]);
+                            st_shared_v4(at + e * kSlab + 128 + ((g ^ (2 * t + 1)) << 4), odd[0], odd[1], odd[2], odd[3]);
                         }
-                        st_shared_v4(at + e * kSlab + ((g ^ (2 * t)) << 4), even[0], even[1], even[2], even[3]);
-                        st_shared_v4(at + e * kSlab + 128 + ((g ^ (2 * t + 1)) << 4), odd[0], odd[1], odd[2], odd[3]);
                     }
-                }
+                });
             }
             fence_proxy_async_shared();
         };
         for (int j = 0; j < blocks; ++j) {
             const int buf = j & 1;
             const uint32_t parity = (uint32_t)(j >> 1) & 1u;
-            if (!get(0, (uint32_t)j & 1u)) break;
-            warp_arrive(bars + 8 * kCEmpty);
+            if (!get(0, j)) break;
+            warp_arrive(code_bar(kCEmpty, 0, j));
             if (!warp_wait(bars + 8 * (kKEmpty + buf), parity ^ 1u, abort_flag, a.err)) break;
             put(0, base + L::kK + buf * L::kOperand);
             warp_arrive(bars + 8 * (kKFull + buf));
-            if (!get(1, (uint32_t)j & 1u)) break;
-            warp_arrive(bars + 8 * (kCEmpty + 1));
+            if (!get(1, j)) break;
+            warp_arrive(code_bar(kCEmpty, 1, j));
             if (!warp_wait(bars + 8 * (kVEmpty + buf), parity ^ 1u, abort_flag, a.err)) break;
             put(1, base + L::kV + buf * L::kOperand);
             warp_arrive(bars + 8 * (kVFull + buf));
@@ -424,10 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                     if (copies) copies = GEMM_DBG_OK(a.c.data + now.from, a.c.data, extent, chunk * D);
                 }
                 const uint32_t part = (uint32_t)(chunk * D * BITS / 8), bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, copies)) * part;
-                // 4 bits: of both operands, this lane's scales as binary16 times 2^(138 - e),
+                // 4 bits: of both operands, this lane's scales as binary16 times 2^(142 - e),
                 // e the biased exponent of the largest of 16 tokens' (held so that the power
-                // of two and its inverse are normal)
-                uint32_t held[2][2] = {}, unit[2] = {};
+                // of two is normal); whether any of the block's is far from that
+                uint32_t held[2][2] = {}, unit[2] = {}, wide[2] = {};
                 bool zero[2] = {};
                 if constexpr (BITS == 4) {
                     const int tok = tok_begin + j * kStep + lane * kTokens;
@@ -445,12 +487,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                         }
                         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
                         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-                        unit[v] = max(most >> 7, 12u);
+                        unit[v] = max(most >> 7, 15u);
                         zero[v] = most == 0;
+                        bool far = unit[v] > 245u;   // (2^(e - 118) is normal)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) far |= bits[v][i] != 0 && (bits[v][i] >> 7) + 8 < unit[v];
+                        wide[v] = __any_sync(0xFFFFFFFFu, far);
                     }
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
-                        const float by = __uint_as_float((265u - unit[v]) << 23);
+                        const float by = __uint_as_float((269u - unit[v]) << 23);
                         float s[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -465,25 +511,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
 #pragma unroll
                 for (int values = 0; values < 2; ++values) {
                     // Page data of block j go where those of block j - 4 were: its keys' turn
-                    // comes when the keys of j - 1 are taken, so the values of j - 4 are used up.
-                    if (!(ok = warp_wait(bars + 8 * (kCEmpty + values), ((uint32_t)j & 1u) ^ 1u, abort_flag, a.err))) break;
+                    // comes when the keys of j - 1 are taken, so the values of j - 4 are used up
+                    // (4 bits: of j - 5, j - 2 and j - 5).
+                    if (!(ok = warp_wait(code_bar(kCEmpty, values, j), code_parity(j) ^ 1u, abort_flag, a.err))) break;
                     if constexpr (BITS == 4) {
-                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(base + L::kScales + values * (2 * kStep) + 8 * lane),
+                        const int buffer = j % L::kBuffers * 2 + values;
+                        if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + L::kWide + 4 * buffer), "r"(values ? wide[1] : wide[0]) : "memory");
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(base + L::kScales + buffer * (2 * kStep) + 8 * lane),
                                      "r"(values ? held[1][0] : held[0][0]), "r"(values ? held[1][1] : held[0][1])
                                      : "memory");
                         if (values == 0 && lane % 4 == 0)
                             info[j % kSlots * kSubs + lane / 4] =
-                                PageData{__uint_as_float((unit[0] - 11u) << 23), zero[1] ? kNegInf : (float)((int)unit[1] - 138), now.live ? 1u : 2u};
+                                PageData{__uint_as_float((wide[0] ? unit[0] - 11u : unit[0] + 9u) << 23),
+                                         zero[1] ? kNegInf : (float)((int)unit[1] - (wide[1] ? 138 : 118)), now.live ? 1u : 2u};
                     } else if (values == 0 && lane < kSubs) {
                         const bool plain = now.live && now.ks == now.ks && now.vs == now.vs;
                         info[j % kSlots * kSubs + lane] = PageData{now.ks, plain ? log2f(now.vs) : 0.0f, plain ? 1u : now.live ? 0u : 2u};
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * (kCFull + values), bytes);
+                    if (lane == 0) mbar_arrive_expect_tx(code_bar(kCFull, values, j), bytes);
                     __syncwarp();
                     if (copies) {
                         const uint8_t* from = BITS == 4 ? a.c.data + now.from + values * part : (values ? a.c.v : a.c.k) + now.from;
-                        bulk_load(base + L::kCodes + values * L::kCodeBytes + lane * kTokens * (D * BITS / 8), from, part, bars + 8 * (kCFull + values));
+                        bulk_load(base + L::kCodes + (j % L::kBuffers * 2 + values) * L::kCodeBytes + lane * kTokens * (D * BITS / 8), from, part,
+                                  code_bar(kCFull, values, j));
                     }
                     issued[values] = j + 1;
                 }
@@ -491,9 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const AttnArgs a
                 now = next;
             }
             // Copies in flight land before the CTA may leave.
-            if (lane < 2 && issued[lane] > 0) {
-                drain(bars + 8 * (kCFull + lane), (uint32_t)(issued[lane] - 1) & 1u, a.err);
-            }
+            if (lane < 2)
+                for (int j = max(0, issued[lane] - L::kBuffers); j < issued[lane]; ++j) drain(code_bar(kCFull, lane, j), code_parity(j), a.err);
         }
         __syncwarp();
     } else {
