@@ -7,34 +7,40 @@ namespace libgemm {
 namespace {
 
 // ---- the plan ------------------------------------------------------------------
-// Two launches.  One block sums counts and pages over the sequences, a thread a
-// sequence and 1024 at a time, and writes what is one number a sequence; then a
-// warp takes 256 rows of a sequence, whose positions and slots follow from the
-// sequence's first row and place on the stack alone: the new pages' numbers come off
-// the stack, not out of the table, which the same lanes write.
-constexpr int kScanThreads = 1024, kFillThreads = 128, kFillRows = 256;
+// Sums over the sequences (rows, pages), a thread a sequence, give what is one
+// number a sequence; then a warp takes 256 rows of a sequence, whose positions and
+// slots follow from its first row, its length and its place on the stack alone: the
+// new pages' numbers come off the stack, not out of the table, which the same lanes
+// write.  For up to 1024 sequences every block makes the sums itself, in shared
+// memory, and it is one launch; beyond that, or where lengths are written in place,
+// one block makes them and a second launch reads them.
+constexpr int kScanThreads = 1024, kFillThreads = 256, kFillRows = 256, kOneLaunch = 1024;
 
 __device__ __forceinline__ int pages_of(int64_t tokens, const StepPlan& p) {   // columns of the table, which is all that are held
     const int64_t n = (tokens + (1 << p.page_log2) - 1) >> p.page_log2;
     return (int)(n < p.width ? n : p.width);
 }
 
-__global__ void __launch_bounds__(kScanThreads) plan_scan_kernel(StepPlan p, unsigned* err) {
-    __shared__ int64_t s_rows[kScanThreads / 32], s_pages[kScanThreads / 32];
-    grid_launch_dependents();
+// The sums, by one block: put(b, start, first, height, after) of every sequence,
+// and of b = sequences start and height alone.  True if a number is out of range.
+template <typename F>
+__device__ __forceinline__ bool plan_sums(const StepPlan& p, F put) {
+    __shared__ int64_t s_rows[32], s_pages[32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int top = *p.available;
     const int height = top < 0 ? 0 : top > p.capacity ? (int)p.capacity : top;
     bool bad = height != top;
+    auto row = [&](int64_t n) { return (int)(n < p.tokens ? n : p.tokens); };
+    auto left = [&](int64_t taken) { return (int)(height - taken > INT32_MIN ? height - taken : INT32_MIN); };
     int64_t rows0 = 0, pages0 = 0;   // of the sequences before this round's
     for (int64_t b0 = 0; b0 < p.sequences; b0 += blockDim.x) {
         const int64_t b = b0 + threadIdx.x;
         const bool in = b < p.sequences && GEMM_DBG_OK(p.lengths + b, p.lengths, p.sequences * 4, 4);
         const int length = in ? p.lengths[b] : 0, count = in ? __ldg(p.counts + b) : 0;
         const int held = max(length, 0), added = max(count, 0);
-        const int64_t after = (int64_t)held + added;
+        const int64_t after = (int64_t)held + added, need = pages_of(after, p) - pages_of(held, p);
         bad |= length < 0 || count < 0 || (added > 0 && (after > p.width << p.page_log2 || after > INT32_MAX));
-        int64_t rows = added, pages = pages_of(after, p) - pages_of(held, p);   // sums up to this thread's sequence
+        int64_t rows = added, pages = need;   // sums up to this thread's sequence
         for (int i = 1; i < 32; i *= 2) {
             const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, i), g = __shfl_up_sync(0xFFFFFFFFu, pages, i);
             if (lane >= i) rows += r, pages += g;
@@ -47,40 +53,37 @@ __global__ void __launch_bounds__(kScanThreads) plan_scan_kernel(StepPlan p, uns
             if (w == warp) rows += rows_all, pages += pages_all;
             rows_all += s_rows[w], pages_all += s_pages[w];
         }
-        if (in && GEMM_DBG_OK(p.starts + b, p.starts, (p.sequences + 1) * 4, 4) && GEMM_DBG_OK(p.first + b, p.first, p.sequences * 4, 4)) {
-            const int64_t start = rows0 + rows - added, taken = pages0 + pages - (pages_of(after, p) - pages_of(held, p));
-            bad |= rows0 + rows > p.tokens || (pages0 + pages > height && taken < pages0 + pages);
-            p.starts[b] = (int)(start < p.tokens ? start : p.tokens);
-            p.first[b] = held;
-            p.heights[b] = (int)(height - taken > INT32_MIN ? height - taken : INT32_MIN);
-            p.after[b] = (int)(after < INT32_MAX ? after : INT32_MAX);
+        if (in) {
+            bad |= rows0 + rows > p.tokens || (pages0 + pages > height && need > 0);
+            put(b, row(rows0 + rows - added), held, left(pages0 + pages - need), (int)(after < INT32_MAX ? after : INT32_MAX));
         }
         rows0 += rows_all, pages0 += pages_all;
     }
     __syncthreads();   // every thread has read `available`, which may be `left`
-    if (threadIdx.x == 0) {
-        p.starts[p.sequences] = (int)(rows0 < p.tokens ? rows0 : p.tokens);
-        p.heights[p.sequences] = (int)(height - pages0 > INT32_MIN ? height - pages0 : INT32_MIN);
-        *p.left = (int)(height > pages0 ? height - pages0 : 0);
-    }
-    if (bad) atomicOr(err, kErrIndex);
+    if (threadIdx.x == 0) put(p.sequences, row(rows0), 0, left(pages0), 0);
+    return bad;
 }
 
-__global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(StepPlan p) {
-    grid_dependency_wait();
-    const int lane = threadIdx.x % 32;
-    const int64_t u = (int64_t)blockIdx.x * (kFillThreads / 32) + threadIdx.x / 32;
-    // Sequence b's rows are units floor(starts[b] / 256) + b + j, and those past the
-    // last sequence's the same of one more.
+__device__ __forceinline__ void plan_put(const StepPlan& p, int64_t b, int start, int first, int height, int after) {
+    if (!GEMM_DBG_OK(p.starts + b, p.starts, (p.sequences + 1) * 4, 4) || !GEMM_DBG_OK(p.heights + b, p.heights, (p.sequences + 1) * 4, 4)) return;
+    p.starts[b] = start;
+    p.heights[b] = height;
+    if (b == p.sequences) *p.left = max(height, 0);
+    else if (GEMM_DBG_OK(p.first + b, p.first, p.sequences * 4, 4) && GEMM_DBG_OK(p.after + b, p.after, p.sequences * 4, 4)) p.first[b] = first, p.after[b] = after;
+}
+
+// Unit u of the rows, by one warp: sequence b's are units floor(starts[b] / 256) + b
+// + j, and those past the last sequence's the same of one more.
+template <typename S, typename F, typename H>
+__device__ __forceinline__ void plan_fill(const StepPlan& p, int64_t u, S start, F first_of, H height_of) {
     const int n = (int)p.sequences;
-    auto start = [&](int b) { return (int64_t)p.starts[b]; };
-    const int b = last_not_above(n + 1, u, u, [&](int i) { return start(i) / kFillRows + i; });
+    const int b = last_not_above(n + 1, u, u, [&](int i) { return (int64_t)start(i) / kFillRows + i; });
     const int64_t row0 = start(b), end = b < n ? start(b + 1) : p.tokens;
     const int64_t begin = row0 + (u - row0 / kFillRows - b) * kFillRows;
     if (begin >= end) return;
-    const int first = b < n ? p.first[b] : 0, height = b < n ? p.heights[b] : 0, held = pages_of(first, p);
-    const int32_t* table = p.table + (int64_t)b * p.width;
-    for (int64_t row = begin + lane; row < min(end, begin + kFillRows); row += 32) {
+    const int first = b < n ? first_of(b) : 0, height = b < n ? height_of(b) : 0, held = pages_of(first, p);
+    int32_t* table = p.table + (int64_t)b * p.width;
+    for (int64_t row = begin + threadIdx.x % 32; row < min(end, begin + kFillRows); row += 32) {
         int position = -1;
         int64_t slot = -1;
         if (b < n) {
@@ -88,15 +91,14 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(StepPlan p) {
             position = at <= INT32_MAX ? (int)at : -1;
             const int64_t column = at >> p.page_log2;
             const int in = (int)(at & ((1 << p.page_log2) - 1));
-            if (column < p.width && position >= 0) {
+            if (column < p.width && position >= 0 && GEMM_DBG_OK(table + column, p.table, p.sequences * p.width * 4, 4)) {
                 int page;
                 if (column < held) {
                     page = table[column];
                 } else {   // new, off the stack; its first token writes the table
                     const int64_t from = height - 1 - (column - held);
                     page = from >= 0 && GEMM_DBG_OK(p.free + from, p.free, p.capacity * 4, 4) ? __ldg(p.free + from) : -1;
-                    if (in == 0 && GEMM_DBG_OK(table + column, p.table, p.sequences * p.width * 4, 4))
-                        p.table[(int64_t)b * p.width + column] = page;
+                    if (in == 0) table[column] = page;
                 }
                 if (page >= 0) slot = ((int64_t)page << p.page_log2) + in;
             }
@@ -107,14 +109,39 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(StepPlan p) {
     }
 }
 
+__global__ void __launch_bounds__(kFillThreads) plan_kernel(StepPlan p, unsigned* err) {
+    __shared__ int s_start[kOneLaunch + 1], s_first[kOneLaunch], s_height[kOneLaunch + 1];
+    const bool bad = plan_sums(p, [&](int64_t b, int start, int first, int height, int after) {
+        s_start[b] = start, s_height[b] = height;
+        if (b < p.sequences) s_first[b] = first;
+        if (blockIdx.x == 0) plan_put(p, b, start, first, height, after);
+    });
+    if (bad && blockIdx.x == 0) atomicOr(err, kErrIndex);
+    __syncthreads();
+    const int64_t u = (int64_t)blockIdx.x * (kFillThreads / 32) + threadIdx.x / 32;
+    plan_fill(p, u, [&](int b) { return s_start[b]; }, [&](int b) { return s_first[b]; }, [&](int b) { return s_height[b]; });
+}
+
+__global__ void __launch_bounds__(kScanThreads) plan_scan_kernel(StepPlan p, unsigned* err) {
+    grid_launch_dependents();
+    const bool bad = plan_sums(p, [&](int64_t b, int start, int first, int height, int after) { plan_put(p, b, start, first, height, after); });
+    if (bad) atomicOr(err, kErrIndex);
+}
+
+__global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(StepPlan p) {
+    grid_dependency_wait();
+    const int64_t u = (int64_t)blockIdx.x * (kFillThreads / 32) + threadIdx.x / 32;
+    plan_fill(p, u, [&](int b) { return p.starts[b]; }, [&](int b) { return p.first[b]; }, [&](int b) { return p.heights[b]; });
+}
+
 // ---- rotary positions ------------------------------------------------------------
 // A block has some rows with all heads of both operands.  Its threads first make
 // the rows' sines and cosines, one a pair, in shared memory: the angle is
 // position * turns mod 2^64 in fractions of a turn, one integer product without any
 // loss, of which the upper 32 bits become a binary32 half turn count in [-1, 1).  Then
 // each thread has one place of a head -- PER elements of either half, or PER
-// neighbours -- and goes through rows and heads, so that it reads the sines of a row
-// once.
+// neighbours -- and goes through heads and rows, kAhead of them loaded before the
+// first is used.
 constexpr int kRotaryThreads = 256;
 
 template <typename T>
@@ -127,101 +154,143 @@ __device__ __forceinline__ float as_float(T x) {
 // PER elements as the 16 bytes that hold them, or one.
 template <typename T, int PER>
 struct Piece {
-    float v[PER];
+    uint4 v;
     __device__ __forceinline__ void load(const T* p) {
-        if constexpr (PER == 1) v[0] = as_float(*p);
-        else {
-            const uint4 w = *reinterpret_cast<const uint4*>(p);
-            const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) v[i] = as_float(e[i]);
-        }
+        if constexpr (PER == 1) v.x = __float_as_uint(as_float(*p));
+        else v = *reinterpret_cast<const uint4*>(p);
     }
     __device__ __forceinline__ void store(T* p) const {
-        if constexpr (PER == 1) *p = from_float<T>(v[0]);
-        else if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        else *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+        if constexpr (PER == 1) *p = from_float<T>(__uint_as_float(v.x));
+        else *reinterpret_cast<uint4*>(p) = v;
+    }
+    __device__ __forceinline__ void get(float (&f)[PER]) const {
+        if constexpr (PER == 1) f[0] = __uint_as_float(v.x);
+        else {
+            const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) f[i] = as_float(e[i]);
+        }
+    }
+    __device__ __forceinline__ void put(const float (&f)[PER]) {
+        if constexpr (PER == 1) v.x = __float_as_uint(f[0]);
+        else if constexpr (PER == 4) v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        else v = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
     }
 };
+
+constexpr int kAhead = 2;
 
 template <typename T, int PER, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs a, int rows_each, bool inverse, int turned, int places) {
     extern __shared__ float2 s_by[];   // [rows][pairs]: cosine and sine
+    constexpr bool kTwo = !INTERLEAVED || PER == 1;   // a turned place is two pieces
     const int half = a.part / 2;
     const int64_t row0 = (int64_t)blockIdx.x * rows_each;
     const int rows = (int)(a.rows - row0 < rows_each ? a.rows - row0 : rows_each);
+    // Places of a head: `turned` that turn, then those that are copied.  A team of
+    // threads has all places of one head, in turns if it has fewer threads.
+    const int heads = a.x[0].heads + a.x[1].heads, step = places < kRotaryThreads ? places : kRotaryThreads, teams = kRotaryThreads / step;
+    const int team = threadIdx.x / step;
+
+    struct Item {
+        Piece<T, PER> e, f;
+        T* out;
+        const float2* by;
+        int at, other;               // elements of the head; other < 0: copied
+        bool live;
+    };
+    auto load = [&](Item& it, int r, int head, int place) {
+        const bool second = head >= a.x[0].heads;
+        const RotaryRows& x = a.x[second];
+        const int h = second ? head - a.x[0].heads : head;
+        const T* in = static_cast<const T*>(x.in.p) + (row0 + r) * x.in.row + h * x.in.head;
+        it.out = static_cast<T*>(x.out.p) + (row0 + r) * x.out.row + h * x.out.head;
+        [[maybe_unused]] const int64_t in_bytes = ((a.rows - 1) * x.in.row + (x.heads - 1) * x.in.head + a.dim) * (int64_t)sizeof(T);
+        [[maybe_unused]] const int64_t out_bytes = ((a.rows - 1) * x.out.row + (x.heads - 1) * x.out.head + a.dim) * (int64_t)sizeof(T);
+        const bool copied = place >= turned;
+        it.at = copied ? a.part + (place - turned) * PER : place * PER * (INTERLEAVED && PER == 1 ? 2 : 1);
+        it.other = copied ? -1 : kTwo ? it.at + (INTERLEAVED ? 1 : half) : it.at;
+        it.by = s_by + r * half + (kTwo ? place * PER : it.at / 2);
+        it.live = __ldg(a.positions + row0 + r) >= 0 && !(copied && in == it.out) && GEMM_DBG_OK(in + it.at, x.in.p, in_bytes, PER * sizeof(T)) &&
+                  GEMM_DBG_OK(it.out + it.at, x.out.p, out_bytes, PER * sizeof(T));
+        if (kTwo && it.live && !copied)
+            it.live = GEMM_DBG_OK(in + it.other, x.in.p, in_bytes, PER * sizeof(T)) && GEMM_DBG_OK(it.out + it.other, x.out.p, out_bytes, PER * sizeof(T));
+        if (!it.live) return;
+        it.e.load(in + it.at);
+        if (kTwo && !copied) it.f.load(in + it.other);
+    };
+    auto finish = [&](Item& it) {
+        if (!it.live) return;
+        if (it.other >= 0) {
+            float u[PER], v[PER];
+            it.e.get(u);
+            if constexpr (kTwo) {
+                it.f.get(v);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const float2 w = it.by[j];
+                    const float x = u[j], y = v[j];
+                    u[j] = x * w.x - y * w.y;
+                    v[j] = y * w.x + x * w.y;
+                }
+                it.f.put(v);
+                it.f.store(it.out + it.other);
+            } else {
+#pragma unroll
+                for (int j = 0; j < PER; j += 2) {
+                    const float2 w = it.by[j / 2];
+                    const float x = u[j], y = u[j + 1];
+                    u[j] = x * w.x - y * w.y;
+                    u[j + 1] = y * w.x + x * w.y;
+                }
+            }
+            it.e.put(u);
+        }
+        it.e.store(it.out + it.at);
+    };
+
+    int r = 0, head = team, place = team < teams ? threadIdx.x % step : places;
+    auto next = [&](Item (&item)[kAhead]) {   // false if there was none
+        if (place >= places) return false;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            item[i].live = false;
+            if (r < rows) {
+                load(item[i], r, head, place);
+                head += teams;
+                while (r < rows && head >= heads) head -= heads, ++r;   // on in the next row
+            }
+        }
+        if (r >= rows) r = 0, head = team, place += step;
+        while (r < rows && head >= heads) head -= heads, ++r;
+        if (r >= rows) place = places;   // a team past the last head of the last row
+        return true;
+    };
+    while (r < rows && head >= heads) head -= heads, ++r;
+    if (r >= rows) place = places;
+    Item item[kAhead];
+    bool some = next(item);   // under way while the sines are made
     for (int i = threadIdx.x; i < rows * half; i += kRotaryThreads) {
-        const int r = i / half, pair = i % half;
-        const int position = __ldg(a.positions + row0 + r);
+        const int at = i / half, pair = i % half;
+        const int position = __ldg(a.positions + row0 + at);
         const uint64_t turn = (uint64_t)(uint32_t)position * __ldg(a.turns + pair);
         float s, c;
         sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
         s_by[i] = make_float2(c * a.magnitude, (inverse ? -s : s) * a.magnitude);
     }
     __syncthreads();
-    // Places of a head: `turned` that turn, then those that are copied.
-    const int heads = a.x[0].heads + a.x[1].heads, teams = kRotaryThreads / places > 0 ? kRotaryThreads / places : 1;
-    const int step = kRotaryThreads / teams;   // threads of a team
-    const int team = threadIdx.x / step;
-    if (team >= teams) return;
-    for (int i = team; i < rows * heads; i += teams) {
-        const int r = i / heads, head = i % heads;
-        const bool second = head >= a.x[0].heads;
-        const RotaryRows& x = a.x[second];
-        const int h = second ? head - a.x[0].heads : head;
-        if (__ldg(a.positions + row0 + r) < 0) continue;
-        const T* in = static_cast<const T*>(x.in.p) + (row0 + r) * x.in.row + h * x.in.head;
-        T* out = static_cast<T*>(x.out.p) + (row0 + r) * x.out.row + h * x.out.head;
-        [[maybe_unused]] const int64_t in_bytes = ((a.rows - 1) * x.in.row + (x.heads - 1) * x.in.head + a.dim) * (int64_t)sizeof(T);
-        [[maybe_unused]] const int64_t out_bytes = ((a.rows - 1) * x.out.row + (x.heads - 1) * x.out.head + a.dim) * (int64_t)sizeof(T);
-        for (int place = threadIdx.x % step; place < places; place += step) {
-            const float2* by = s_by + r * half;
-            if (place >= turned) {
-                const int at = a.part + (place - turned) * PER;
-                if (in == out || !GEMM_DBG_OK(in + at, x.in.p, in_bytes, PER * sizeof(T)) || !GEMM_DBG_OK(out + at, x.out.p, out_bytes, PER * sizeof(T))) continue;
-                Piece<T, PER> e;
-                e.load(in + at);
-                e.store(out + at);
-            } else if constexpr (INTERLEAVED && PER > 1) {
-                const int at = place * PER;
-                if (!GEMM_DBG_OK(in + at, x.in.p, in_bytes, PER * sizeof(T)) || !GEMM_DBG_OK(out + at, x.out.p, out_bytes, PER * sizeof(T))) continue;
-                Piece<T, PER> e;
-                e.load(in + at);
+    for (; some; some = next(item))
 #pragma unroll
-                for (int j = 0; j < PER; j += 2) {
-                    const float2 w = by[at / 2 + j / 2];
-                    const float u = e.v[j], v = e.v[j + 1];
-                    e.v[j] = u * w.x - v * w.y;
-                    e.v[j + 1] = v * w.x + u * w.y;
-                }
-                e.store(out + at);
-            } else {
-                const int at = place * PER * (INTERLEAVED ? 2 : 1), other = at + (INTERLEAVED ? 1 : half);
-                if (!GEMM_DBG_OK(in + at, x.in.p, in_bytes, PER * sizeof(T)) || !GEMM_DBG_OK(in + other, x.in.p, in_bytes, PER * sizeof(T)) ||
-                    !GEMM_DBG_OK(out + at, x.out.p, out_bytes, PER * sizeof(T)) || !GEMM_DBG_OK(out + other, x.out.p, out_bytes, PER * sizeof(T)))
-                    continue;
-                Piece<T, PER> e, f;
-                e.load(in + at);
-                f.load(in + other);
-#pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const float2 w = by[place * PER + j];
-                    const float u = e.v[j], v = f.v[j];
-                    e.v[j] = u * w.x - v * w.y;
-                    f.v[j] = v * w.x + u * w.y;
-                }
-                e.store(out + at);
-                f.store(out + other);
-            }
-        }
-    }
+        for (int i = 0; i < kAhead; ++i) finish(item[i]);
 }
 
 template <typename T, int PER, bool INTERLEAVED>
 cudaError_t rotate(const RotaryArgs& a, bool inverse, int num_sms, cudaStream_t stream) {
     const int turned = INTERLEAVED && PER > 1 ? a.part / PER : a.part / 2 / PER, places = turned + (a.dim - a.part) / PER;
-    const int64_t each = a.rows / (8 * num_sms);
-    const int rows = (int)(each < 1 ? 1 : each > 4 ? 4 : each);
+    // About four places a thread, unless that leaves SMs without a block.
+    const int64_t most = a.rows / (4 * num_sms), want = 4 * kRotaryThreads / ((int64_t)(a.x[0].heads + a.x[1].heads) * places);
+    const int64_t each = most < want ? most : want;
+    const int rows = (int)(each < 1 ? 1 : each > 8 ? 8 : each);
     rotary_kernel<T, PER, INTERLEAVED><<<(unsigned)((a.rows + rows - 1) / rows), kRotaryThreads, rows * (a.part / 2) * sizeof(float2), stream>>>(
         a, rows, inverse, turned, places);
     return cudaGetLastError();
@@ -244,14 +313,18 @@ cudaError_t rotate(const RotaryArgs& a, bool interleaved, bool inverse, int num_
 LIBGEMM_DEBUG_READER(sequences_debug_flags)
 
 cudaError_t launch_step_plan(const StepPlan& p, unsigned* err, int* launches, cudaStream_t stream) {
-    const unsigned threads = p.sequences <= 256 ? 256 : kScanThreads;
-    plan_scan_kernel<<<1, threads, 0, stream>>>(p, err);
-    cudaError_t e = cudaGetLastError();
-    *launches = 1;
-    if (e != cudaSuccess || p.tokens == 0) return e;
     const int64_t units = p.tokens / kFillRows + p.sequences + 1;
+    const unsigned blocks = (unsigned)((units + kFillThreads / 32 - 1) / (kFillThreads / 32));
+    *launches = 1;
+    if (p.sequences <= kOneLaunch && p.after != p.lengths && p.left != p.available) {
+        plan_kernel<<<blocks, kFillThreads, 0, stream>>>(p, err);
+        return cudaGetLastError();
+    }
+    plan_scan_kernel<<<1, p.sequences <= 256 ? 256 : kScanThreads, 0, stream>>>(p, err);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.tokens == 0) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((units + kFillThreads / 32 - 1) / (kFillThreads / 32)));
+    cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kFillThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
