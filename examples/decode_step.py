@@ -2,17 +2,19 @@
 """One attention layer decoding on operands held in few bits.
 
 The layer's two weight matrices (queries, keys and values together, and the
-output) are kept in 4 bits, its keys and values in a paged 8-bit cache.  Ragged
-prompts are taken in first -- their many rows go through the weights' bfloat16
-values and the ordinary product --, then every step sends one row of each
+output) are kept in 4 bits, its keys and values in a paged cache of 8 or 4 bits.
+Ragged prompts are taken in first -- their many rows go through the weights'
+bfloat16 values and the ordinary product --, then every step sends one row of each
 sequence through
 
-    gemm_w4 -> kv_append -> kv_attention -> gemm_w4
+    kv_plan -> gemm_w4 -> rotary -> kv_append -> kv_attention -> gemm_w4
 
-recorded once as a CUDA graph.  At the end the last step is computed again in
-float32 from the weights' values and the cache's, read back.
+recorded once as a CUDA graph: the plan takes pages off a stack and moves the
+lengths on, so that a replay goes on where the last one ended.  At the end the last
+step is computed again in float32 from the weights' values and the cache's, read
+back.
 
-    python examples/decode_step.py [--batch 8] [--steps 64]
+    python examples/decode_step.py [--batch 8] [--steps 64] [--bits 8]
 """
 import argparse
 import os
@@ -21,7 +23,7 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from accelerator_gb300 import binding, lowbit  # noqa: E402
+from accelerator_gb300 import binding, lowbit, sequences  # noqa: E402
 
 HIDDEN, Q_HEADS, KV_HEADS, DIM, PAGE = 1024, 16, 4, 64, 32
 
@@ -32,6 +34,7 @@ class Layer:
             return torch.randn(rows, columns, generator=generator, device="cuda") * rows ** -0.5
         self.qkv = lowbit.w4_quantize(weight(HIDDEN, (Q_HEADS + 2 * KV_HEADS) * DIM), group=64)
         self.out = lowbit.w4_quantize(weight(Q_HEADS * DIM, HIDDEN), group=64)
+        self.turn = sequences.Rotary(DIM)
 
     @staticmethod
     def heads(joint):
@@ -39,22 +42,26 @@ class Layer:
         joint = joint.view(joint.shape[0], -1, DIM)
         return joint.split((Q_HEADS, KV_HEADS, KV_HEADS), 1)
 
-    def prompt(self, x, cache, table, starts, first, lengths):
-        joint = binding.gemm(x, lowbit.w4_dequantize(self.qkv), mode="bf16").to(torch.bfloat16)
+    def attend(self, joint, cache, table, plan):
         q, k, v = self.heads(joint)
-        lowbit.kv_append(cache, k, v, table, starts, first)
-        o = lowbit.kv_attention(q, cache, table, starts, lengths)
-        return binding.gemm(o.flatten(1), lowbit.w4_dequantize(self.out), mode="bf16").to(torch.bfloat16)
+        sequences.rotary(q, k, plan.positions, self.turn, out=(q, k))
+        lowbit.kv_append(cache, k, v, table, plan.starts, plan.first)
+        return lowbit.kv_attention(q, cache, table, plan.starts, plan.lengths).flatten(1)
 
-    def step(self, x, cache, table, starts, first, lengths):
-        q, k, v = self.heads(lowbit.gemm_w4(x, self.qkv))
-        lowbit.kv_append(cache, k, v, table, starts, first)
-        o = lowbit.kv_attention(q, cache, table, starts, lengths)
-        return lowbit.gemm_w4(o.flatten(1), self.out)
+    def prompt(self, x, cache, table, plan):
+        joint = binding.gemm(x, lowbit.w4_dequantize(self.qkv), mode="bf16").to(torch.bfloat16)
+        o = self.attend(joint, cache, table, plan)
+        return binding.gemm(o, lowbit.w4_dequantize(self.out), mode="bf16").to(torch.bfloat16)
+
+    def step(self, x, cache, table, plan):
+        return lowbit.gemm_w4(self.attend(lowbit.gemm_w4(x, self.qkv), cache, table, plan), self.out)
 
     def plain_step(self, x, cache, table, lengths):
         """The step in float32, over the tokens that the cache holds."""
         q, _, _ = self.heads((x.float() @ lowbit.w4_dequantize(self.qkv, dtype=torch.float32)).to(torch.bfloat16))
+        angle = (lengths - 1).double()[:, None, None] * torch.tensor(self.turn.frequencies, dtype=torch.float64, device="cuda")
+        u, w = q.double().chunk(2, 2)
+        q = torch.cat([u * angle.cos() - w * angle.sin(), w * angle.cos() + u * angle.sin()], 2).to(torch.bfloat16)
         starts = torch.zeros(len(lengths) + 1, dtype=torch.int32, device="cuda")
         starts[1:] = lengths.cumsum(0)
         k, v = lowbit.kv_read(cache, table, starts, torch.zeros_like(lengths), int(starts[-1]), dtype=torch.float32)
@@ -67,27 +74,30 @@ class Layer:
         return o @ lowbit.w4_dequantize(self.out, dtype=torch.float32)
 
 
-def main(batch=8, steps=64, report=print):
+def main(batch=8, steps=64, report=print, bits=8):
     g = torch.Generator(device="cuda").manual_seed(0)
     layer = Layer(g)
     prompts = [5 + 37 * b % 200 for b in range(batch)]
     width = -(-(max(prompts) + steps) // PAGE)
-    cache = lowbit.KvCache.empty(batch * width, KV_HEADS, DIM, PAGE)
-    table = torch.randperm(batch * width, generator=g, device="cuda").to(torch.int32).view(batch, width)
-    lengths = torch.tensor(prompts, dtype=torch.int32, device="cuda")
-    first = torch.zeros_like(lengths)
-    starts = torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
-    starts[1:] = lengths.cumsum(0)
-    x = torch.randn(sum(prompts), HIDDEN, generator=g, device="cuda", dtype=torch.bfloat16)
-    y = layer.prompt(x, cache, table, starts, first, lengths)
-    x = y[starts[1:].long() - 1].clone()
+    pages = batch * width
+    cache = (lowbit.Kv4Cache if bits == 4 else lowbit.KvCache).empty(pages, KV_HEADS, DIM, PAGE)
+    free = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    available = torch.tensor([pages], dtype=torch.int32, device="cuda")
+    table = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    counts = torch.tensor(prompts, dtype=torch.int32, device="cuda")
 
-    one = torch.arange(batch + 1, dtype=torch.int32, device="cuda")
+    def plan(tokens):
+        return sequences.kv_plan(table, lengths, counts, free, available, PAGE, tokens, update=True)
+
+    x = torch.randn(sum(prompts), HIDDEN, generator=g, device="cuda", dtype=torch.bfloat16)
+    first = plan(sum(prompts))
+    y = layer.prompt(x, cache, table, first)
+    x = y[first.starts[1:].long() - 1].clone()
+    counts.fill_(1)
 
     def step():
-        first.copy_(lengths)
-        lengths.add_(1)
-        return layer.step(x, cache, table, one, first, lengths)
+        return layer.step(x, cache, table, plan(batch))
 
     x.copy_(torch.nn.functional.normalize(step().float(), dim=1) * HIDDEN ** 0.5)      # the first step outside of the graph
     graph = torch.cuda.CUDAGraph()
@@ -115,5 +125,6 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--batch", type=int, default=8)
     ap.add_argument("--steps", type=int, default=64)
+    ap.add_argument("--bits", type=int, default=8, choices=(4, 8))
     a = ap.parse_args()
-    main(a.batch, max(a.steps, 3))
+    main(a.batch, max(a.steps, 3), bits=a.bits)
