@@ -244,3 +244,80 @@ def test_offsets_that_descend_are_reported(libgemm, share):
         assert libgemm.debug_status() == libgemm.OK
         lowbit.kv_attention(p.queries(240, share, torch.float16), p.cache, p.table, ints(starts), ints([300] * 5))
         assert libgemm.debug_status() == libgemm.ERR_INDEX
+
+
+@layouts
+def test_many_sequences_in_one_line(libgemm, dim, kind, page):
+    """More sequences than a block has threads, of none to three rows, of every
+    length around a step's and a page's end, some empty."""
+    n = 400
+    lengths = [(b * 37) % 300 if b % 7 else 128 * (b % 5) for b in range(n)]
+    counts = [b % 4 if b % 5 else 1 for b in range(n)]
+    p = ref.Paged4(n, -(-512 // page), 2, dim, page, seed=3)
+    for share in (1, 4):
+        Q = p.queries(sum(counts), 2 * share, kind)
+        ref.check(libgemm, p, Q, counts, lengths)
+        ref.check(libgemm, p, Q, counts, lengths, window=50)
+        ref.check(libgemm, p, Q, counts, lengths, causal=False)
+
+
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("share", [1, 8])
+def test_bad_indices_in_one_line(libgemm, T, share):
+    """Long sequences, whose steps many blocks share: what is out of range is
+    skipped and reported, and the other sequences have their results."""
+    from accelerator_gb300 import lowbit
+    p = ref.Paged4(3, 700, 1, 64, 16)
+    Q = p.queries(3 * T, share, torch.float16)
+    lengths = [11000, 9000, 10500]
+    want = ref.check(libgemm, p, Q, [T] * 3, lengths)
+    pages = p.codes[0].shape[0]
+
+    def call(table=p.table, starts=(0, T, 2 * T, 3 * T), at=lengths):
+        assert libgemm.debug_status() == libgemm.OK
+        O = lowbit.kv_attention(Q, p.cache, table, ints(starts), ints(at))
+        assert libgemm.debug_status() == libgemm.ERR_INDEX
+        return O
+
+    for bad in (-1, pages, -2 ** 31, 2 ** 31 - 1):
+        table = p.table.clone()
+        table[1, 300] = bad
+        O = call(table=table)
+        assert torch.equal(O[:T], want[:T]) and torch.equal(O[2 * T:], want[2 * T:]) and torch.isfinite(O).all()
+    for bad in (-1, 700 * 16 + 1, 2 ** 31 - 1, -2 ** 31):
+        O = call(at=[11000, bad, 10500])
+        assert torch.equal(O[:T], want[:T]) and torch.equal(O[2 * T:], want[2 * T:]) and (O[T:2 * T] == 0).all()
+    for starts in ((0, 3 * T + 1, 2 * T, 3 * T), (0, -5, 2 * T, 3 * T), (0, 2 * T, T, 3 * T), (1, T, 2 * T, 3 * T), (0, 0, 0, 0)):
+        call(starts=starts)
+
+
+def test_two_graphs_and_two_streams(libgemm):
+    """Graphs of one cache that are replayed in turn and at once, each with its own
+    scratch, and calls on two streams."""
+    p = ref.Paged4(2, 700, 2, 64, 16)
+    calls = [(p.queries(2, 8, torch.float16), [1, 1], [11000, 9000]), (p.queries(140, 8, torch.float16), [70, 70], [3000, 500])]
+    want = [p.attend(*c) for c in calls]
+    from accelerator_gb300 import lowbit
+    from kv_ref import offsets
+    args = [(Q, p.cache, p.table, ints(offsets(n)), ints(length)) for Q, n, length in calls]
+    graphs, got = [], []
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(lowbit.kv_attention(*a))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in args]
+    for _ in range(5):
+        for t in got:
+            t.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for _ in range(5):
+        both = [lowbit.kv_attention(*a, stream=s) for a in args for s in streams]
+        torch.cuda.synchronize()
+        assert all(torch.equal(both[i], want[i // 2]) for i in range(4))
+    assert libgemm.debug_status() == libgemm.OK
