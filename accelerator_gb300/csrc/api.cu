@@ -32,10 +32,13 @@ struct DeviceState {
     // reserved (release threshold: never), so repeated calls reuse memory
     // instead of mapping it afresh after every synchronisation.
     cudaMemPool_t pool = nullptr;
-    // The attention kernels' attributes: at the first attention call, not in
-    // every product's first call, and a failure there is theirs alone.
-    std::atomic<bool> attention_done{false};
-    int attention_status = GEMM_OK;
+    // The attention kernels' attributes: at the first attention call over a cache
+    // of 8 or of 4 bits, not in every product's first call, and a failure there is
+    // theirs alone.
+    struct Attention {
+        std::atomic<bool> done{false};
+        int status = GEMM_OK;
+    } attention[2];
 };
 
 std::mutex g_mu;
@@ -451,19 +454,21 @@ int tc_product(const TcPlan& plan, const void* A, const void* B, float* C, int64
 
 void count_launch() { g_launches++; }
 
-int attention_setup() {
+int attention_setup(int bits) {
     DeviceState* st = nullptr;
     const int rc = device_state(&st);
-    if (rc != GEMM_OK || st->attention_done.load(std::memory_order_acquire)) return rc != GEMM_OK ? rc : st->attention_status;
+    if (rc != GEMM_OK) return rc;
+    DeviceState::Attention& at = st->attention[bits == 4];
+    if (at.done.load(std::memory_order_acquire)) return at.status;
     std::lock_guard<std::mutex> lock(g_mu);
-    if (!st->attention_done.load(std::memory_order_relaxed)) {
-        if (kv_attention_setup() != cudaSuccess) {
-            st->attention_status = GEMM_ERR_CUDA;
+    if (!at.done.load(std::memory_order_relaxed)) {
+        if (kv_attention_setup(bits) != cudaSuccess) {
+            at.status = GEMM_ERR_CUDA;
             cudaGetLastError();
         }
-        st->attention_done.store(true, std::memory_order_release);
+        at.done.store(true, std::memory_order_release);
     }
-    return st->attention_status;
+    return at.status;
 }
 
 void* scratch_alloc(int64_t bytes, cudaStream_t stream) {

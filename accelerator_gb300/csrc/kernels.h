@@ -244,7 +244,7 @@ struct KvPlan {
     int ctas;             // few rows over 4 bits: CTAs that share all tiles' tokens evenly, instead of splits
     int64_t scratch_bytes;
 };
-cudaError_t kv_attention_setup();
+cudaError_t kv_attention_setup(int bits);
 KvPlan kv_plan(const KvView& c, const KvBatch& b, int q_heads, int64_t window, int num_sms);
 cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& O, ElemType type,
                                 int q_heads, float scale, bool causal, int64_t window,
@@ -279,8 +279,9 @@ struct RotaryArgs {
 cudaError_t launch_rotary(const RotaryArgs& a, ElemType type, bool interleaved, bool inverse, int num_sms, cudaStream_t stream);
 
 // ---- host-side hooks of the C ABI (api.cu) ----
-// Set-up of the attention kernels on the current device, once; a gemm_status code.
-int attention_setup();
+// Set-up of the attention kernels over a cache of 8 or 4 bits on the current
+// device, once; a gemm_status code.
+int attention_setup(int bits);
 // Stream-ordered scratch from the current device's pool; nullptr if none is
 // to be had.  Freed with cudaFreeAsync on the same stream.
 void* scratch_alloc(int64_t bytes, cudaStream_t stream);

@@ -65,6 +65,7 @@ __device__ __forceinline__ void load_words(uint32_t addr, uint32_t (&w)[D / 32])
         w[0] = v.x, w[1] = v.y;
     }
 }
+constexpr uint32_t kPlain = 256;
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;   // u * 2^-24, u * 2^-20
 
 template <int D, int NQ>
@@ -91,7 +92,7 @@ template <int D, int NQ>
 struct Stages {
     using R = Ring<D, NQ>;
     uint32_t ring, bars;            // full[stages], empty[stages]
-    uint32_t* live_subs;            // which 16s of a stage are there
+    uint32_t* live_subs;            // which 16s of a stage are there; kPlain: all, and every row sees all of them
     volatile int* abort_flag;
     uint32_t phase = 0;
     int stage = 0;
@@ -123,6 +124,8 @@ __device__ __forceinline__ bool copy_steps(const AttnArgs& a, const Tile& tile, 
     const int lane = threadIdx.x % 32, log2 = a.c.page_log2, record = (D + 4) << log2;
     const int32_t* table = a.b.table + tile.seq * a.b.width;
     [[maybe_unused]] const int64_t extent = a.c.pages * a.c.heads * a.c.record();
+    // tokens that every row of the tile sees
+    const int full_lo = tile.row_lo(a, min(tile.r0 + 8 * NQ, tile.nrows) - 1), full_hi = tile.row_hi(a, tile.r0);
     bool live = false;
     const uint8_t* from = nullptr;
     for (int s = 0; s < steps; ++s) {
@@ -145,7 +148,9 @@ __device__ __forceinline__ bool copy_steps(const AttnArgs& a, const Tile& tile, 
         if (copies) bulk_load(st.at() + (sub * kSub >> log2) * record, from, record, st.bars + 8 * st.stage);
         __syncwarp();
         if (lane == 0) {
-            st.live_subs[st.stage] = there >> (s % 4 * 8);
+            const int tok = tok_begin + s * kStep;
+            const uint32_t subs = there >> (s % 4 * 8);
+            st.live_subs[st.stage] = subs == 255u && tok >= full_lo && tok + kStep <= full_hi ? subs | kPlain : subs;
             mbar_arrive_expect_tx(st.bars + 8 * st.stage, parts * record);
         }
         ++issued;
@@ -189,7 +194,6 @@ struct Attend {
     uint32_t qf[NQ][2 * kWords][2];
     float factor[NQ][2], begin[NQ][4];      // of the rows 8n + 2t, + 1, whose scores a lane gets
     int row_lo[NQ][2], row_hi[NQ][2];
-    int full_lo, full_hi;                   // tokens that every row of the tile sees
     // A row's sums: l of the weights exp2(s_j - m) in binary32, o of those times
     // their token's value scale v_j times up = 2^12 / r as binary16, and ones of these
     // alone, where m and r are the row's own largest s_j and exp2(s_j - m) * v_j so
@@ -213,9 +217,9 @@ struct Attend {
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             // its biased exponent, in the range in which both powers below are normal
-            const int k = top < INFINITY ? max(12, min(249, (int)(__float_as_uint(top) >> 23))) : 127;
+            const int k = top < INFINITY ? max(12, (int)(__float_as_uint(top) >> 23)) : 127;
             const float down = __uint_as_float((uint32_t)(265 - k) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);   // 2^(11 + 127 - k)
-            const float back = __uint_as_float((uint32_t)(k + 5) << 23);   // 2^(k - 127 - 11 + 20 - 4): the codes' 2^-20, 2^4 of it with the key's scale
+            const float back = __uint_as_float((uint32_t)k << 23);   // 2^(k - 127); 2^9 more for the 2^-11 above and the codes' 2^-20
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kWords; ++i)
@@ -232,8 +236,8 @@ struct Attend {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 begin[n][i] = begin[n][2 + i] = -8.0f * 9.5367431640625e-7f * __shfl_sync(0xFFFFFFFFu, sum, 4 * (2 * t + i));   // 2^-20
-                // above 0, so that a hidden token's -inf stays that
-                factor[n][i] = fmaxf(fabsf(a.scale_log2) * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + i)), 1.1754943508222875e-38f);
+                // above 0, so that a hidden token's -inf stays that, and finite
+                factor[n][i] = fminf(fmaxf(fabsf(a.scale_log2) * 512.0f * __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + i)), 1.1754943508222875e-38f), 3.4028235e38f);
                 // rows past the last one see all: they are not stored
                 const int rr = tile.r0 + 8 * n + 2 * t + i;
                 row_lo[n][i] = rr < tile.nrows ? tile.row_lo(a, rr) : 0;
@@ -246,8 +250,6 @@ struct Attend {
             l[n][0] = l[n][1] = 0.0f;
             up[n][0] = up[n][1] = kTopP / kLeastP;
         }
-        full_lo = tile.row_lo(a, min(tile.r0 + kRows, tile.nrows) - 1);
-        full_hi = tile.row_hi(a, tile.r0);
     }
 
     // Where this warp's tokens lie in every stage: the keys' codes of token g of its
@@ -266,7 +268,9 @@ struct Attend {
         to_values = 2 * page_tokens;
     }
 
-    // This warp's 32 tokens of a stage, from token `tok` on; `subs`: which 16s are there.
+    // This warp's 32 tokens of a stage, from token `tok` on; `subs`: which 16s are
+    // there.  MASKED: of some that some row does not see, or that are not there.
+    template <bool MASKED>
     __device__ __forceinline__ void step(uint32_t stage_at, int tok, uint32_t subs) {
         const int lane = threadIdx.x % 32, g = lane / 4;
         // scores of tokens 16b + g and 16b + g + 8 (y) for the rows 2t (.x) and 2t + 1 (.y)
@@ -278,10 +282,9 @@ struct Attend {
             uint32_t w0[kWords], w1[kWords];
             load_words<D>(kat, w0);
             load_words<D>(kat + 8 * (D / 2), w1);
-            const float ks[2] = {lds_bf16(sat) * 16.0f, lds_bf16(sat + 16) * 16.0f};
+            const float ks[2] = {lds_bf16(sat), lds_bf16(sat + 16)};
             vs[b][0] = lds_bf16(sat + to_values), vs[b][1] = lds_bf16(sat + to_values + 16);
-            float part[NQ][2][4];
-            constexpr float kZero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float part[NQ][4];
 #pragma unroll
             for (int i = 0; i < kWords; ++i)
 #pragma unroll
@@ -289,22 +292,20 @@ struct Attend {
                     const uint32_t lo = w0[i] >> (8 * x), hi = w1[i] >> (8 * x);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n)
-                        mma_16816_from(part[n][x], i > 0 ? part[n][x] : x ? kZero : begin[n], lo & kLow, hi & kLow, lo & kHigh, hi & kHigh,
-                                       qf[n][2 * i + x][0], qf[n][2 * i + x][1]);
+                        mma_16816_from(part[n], i + x > 0 ? part[n] : begin[n], lo & kLow, hi & kLow, lo & kHigh, hi & kHigh, qf[n][2 * i + x][0],
+                                       qf[n][2 * i + x][1]);
                 }
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                    sc[b][n][y] = __fmul2_rn(__fadd2_rn(make_float2(part[n][0][2 * y], part[n][0][2 * y + 1]), make_float2(part[n][1][2 * y], part[n][1][2 * y + 1])),
-                                             make_float2(ks[y], ks[y]));
+                    sc[b][n][y] = __fmul2_rn(make_float2(part[n][2 * y], part[n][2 * y + 1]), make_float2(ks[y], ks[y]));
         }
         // Tokens that some row does not see, pages that do not exist.  There a weight
         // of 0 has to stay 0 whatever the token has for a scale, and a scale of NaN
         // makes NaN of the rows alone that see it; elsewhere all rows see all tokens.
-        const bool masked = tok < full_lo || tok + kSubs * kSub > full_hi || (subs & 3u) != 3u;
         uint32_t nan = 0;
-        if (masked) {
+        if constexpr (MASKED) {
 #pragma unroll
             for (int b = 0; b < kSubs; ++b)
 #pragma unroll
@@ -319,7 +320,6 @@ struct Attend {
                     if (vs[b][y] != vs[b][y]) nan |= 1u << (2 * b + y);
                     vs[b][y] = fminf(fabsf(vs[b][y]), 3.3895314e38f);
                 }
-            asm volatile("");   // a branch: few tokens come here
         }
         // A weight, and it with its token's value scale, relative to the row's largest.
         float2 w[kSubs][NQ][2], p[kSubs][NQ][2];
@@ -390,7 +390,7 @@ struct Attend {
             }
             weigh();
         }
-        if (masked && __any_sync(0xFFFFFFFFu, nan != 0)) {
+        if (MASKED && __any_sync(0xFFFFFFFFu, nan != 0)) {
             const float bad = __uint_as_float(0x7FC00000u);
 #pragma unroll
             for (int b = 0; b < kSubs; ++b)
@@ -503,8 +503,10 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_cluster_kernel(con
         rows.start(a, tile, [&](int r, int d) { return query<T, D>(a, tile, h, r, d); });
         for (int s = 0; s < steps; ++s) {
             if (!st.wait_full(a.err)) break;
+            const uint32_t subs = st.live_subs[st.stage];
             const int tok = tok_begin + s * kStep + warp * (kSubs * kSub);
-            if (tok < tile.hi) rows.step(st.at(), tok, st.live_subs[st.stage] >> (warp * kSubs));
+            if (subs & kPlain) rows.template step<false>(st.at(), tok, subs);
+            else if (tok < tile.hi) rows.template step<true>(st.at(), tok, subs >> (warp * kSubs));
             st.release();
             st.next();
         }
@@ -754,8 +756,10 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_line_kernel(const 
         const int tok_begin = tile.tok0 + piece.begin * kStep;
         for (int s = 0; ok && s < piece.steps; ++s) {
             if (!(ok = st.wait_full(a.err))) break;
+            const uint32_t subs = st.live_subs[st.stage];
             const int tok = tok_begin + s * kStep + warp * (kSubs * kSub);
-            if (tok < tile.hi) rows.step(st.at(), tok, st.live_subs[st.stage] >> (warp * kSubs));
+            if (subs & kPlain) rows.template step<false>(st.at(), tok, subs);
+            else if (tok < tile.hi) rows.template step<true>(st.at(), tok, subs >> (warp * kSubs));
             st.release();
             st.next();
         }

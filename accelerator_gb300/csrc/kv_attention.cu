@@ -591,13 +591,17 @@ cudaError_t allow_smem() {
 
 LIBGEMM_DEBUG_READER(kv_attention_debug_flags)
 
-cudaError_t kv_attention_setup() {
-    cudaError_t e = allow_smem<__nv_bfloat16, 64>();
-    if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, 128>();
-    if (e == cudaSuccess) e = allow_smem<__half, 64>();
-    if (e == cudaSuccess) e = allow_smem<__half, 128>();
-    if (e == cudaSuccess) e = kv4_attention_setup();
-    return e == cudaSuccess ? kv_prompt_setup() : e;
+cudaError_t kv_attention_setup(int bits) {
+    cudaError_t e = cudaSuccess;
+    if (bits == 4) {
+        e = kv4_attention_setup();
+    } else {
+        e = allow_smem<__nv_bfloat16, 64>();
+        if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, 128>();
+        if (e == cudaSuccess) e = allow_smem<__half, 64>();
+        if (e == cudaSuccess) e = allow_smem<__half, 128>();
+    }
+    return e == cudaSuccess ? kv_prompt_setup(bits) : e;
 }
 
 // How many rows a tile has follows from the rows of a sequence and cache head,

@@ -117,7 +117,7 @@ __device__ __forceinline__ T* out_row(const AttnArgs& a, const Tile& tile, int h
 }
 
 // Many query rows (kv_prompt.cu): tiles of plan.rows = 256, tokens in steps of 128.
-cudaError_t kv_prompt_setup();
+cudaError_t kv_prompt_setup(int bits);
 // Few query rows over a cache in 4 bits (kv4_attention.cu): tiles of 8 or 16.
 cudaError_t kv4_attention_setup();
 void kv4_few_plan(KvPlan& p, const KvView& c, int64_t have, int64_t most, int num_sms);

@@ -767,15 +767,14 @@ cudaError_t with_kernel(ElemType type, int dim, int bits, F f) {
 
 LIBGEMM_DEBUG_READER(kv_prompt_debug_flags)
 
-cudaError_t kv_prompt_setup() {
+cudaError_t kv_prompt_setup(int bits) {
     for (ElemType type : {ElemType::kBF16, ElemType::kF16})
-        for (int dim : {64, 128})
-            for (int bits : {4, 8}) {
-                const cudaError_t e = with_kernel(type, dim, bits, [](auto t, auto d, auto b) {
-                    return allow_smem<decltype(t), decltype(d)::value, decltype(b)::value>();
-                });
-                if (e != cudaSuccess) return e;
-            }
+        for (int dim : {64, 128}) {
+            const cudaError_t e = with_kernel(type, dim, bits, [](auto t, auto d, auto b) {
+                return allow_smem<decltype(t), decltype(d)::value, decltype(b)::value>();
+            });
+            if (e != cudaSuccess) return e;
+        }
     return cudaSuccess;
 }
 

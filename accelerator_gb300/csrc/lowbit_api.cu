@@ -182,7 +182,7 @@ int kv_attention(const Cache* cache, const void* Q, int64_t q_row_stride, int64_
     unsigned* err = nullptr;
     rc = device_setup(&sms, &err);
     if (rc != GEMM_OK) return rc;
-    if ((rc = attention_setup()) != GEMM_OK) return rc;
+    if ((rc = attention_setup(v.bits)) != GEMM_OK) return rc;
     const KvPlan plan = kv_plan(v, b, q_heads, window, sms);
     void* scratch = nullptr;
     if (plan.scratch_bytes > 0 && !(scratch = scratch_alloc(plan.scratch_bytes, stream))) return GEMM_ERR_NO_MEMORY;

@@ -255,8 +255,8 @@ GEMM_API int gemm_tf32_noalloc(const float* A, const float* B, float* C, int64_t
  *
  * The products of a decoding step, in which one operand is kept in 4 or 8
  * bits with scales: C = X*W with a 4-bit W for a few rows X, and attention
- * (two products with a softmax between them) over a paged cache of 8-bit
- * keys and values.  The rules above hold: device pointers, asynchronous on
+ * (two products with a softmax between them) over a paged cache of keys and
+ * values in 8 or 4 bits.  The rules above hold: device pointers, asynchronous on
  * `stream`, status codes, nothing enqueued on an error, scratch from the
  * library's stream-ordered pool, safe under stream capture after the first
  * call on a device.  Indices that live in device memory (page numbers,
@@ -454,7 +454,13 @@ GEMM_API int gemm_kv4_read(const gemm_kv4_cache* cache, void* K, void* V, int ty
                            const int32_t* first, int64_t tokens, int64_t sequences,
                            struct CUstream_st* stream);
 
-/* As gemm_kv_attention, over a cache of 4 bits. */
+/*
+ * As gemm_kv_attention, over a cache of 4 bits.  A query's row is brought to binary16
+ * by a power of two (exact, but for elements under 2^-14 of the row's largest).  A
+ * weight times its token's value scale, or where a sequence and head has many rows
+ * the largest value scale of its 16 tokens, enters the second product as binary16
+ * relative to the largest such product that the row sees.
+ */
 GEMM_API int gemm_kv4_attention(const gemm_kv4_cache* cache, const void* Q, int64_t q_row_stride,
                                 int64_t q_head_stride, void* O, int64_t o_row_stride,
                                 int64_t o_head_stride, int type, int32_t q_heads, float scale,
@@ -495,7 +501,9 @@ GEMM_API int gemm_kv4_attention(const gemm_kv4_cache* cache, const void* Q, int6
  * is over `tokens` (starts ends there and rows past it are not written), a sequence
  * longer than the table is wide or a stack that runs out (the tokens without a page
  * have -1 in slots, and, inside the table, in page_table), a height over free_capacity.
- * The arrays do not overlap but where said.
+ * The arrays do not overlap but where said.  Calls that take from one stack are one
+ * after another.  A sequence that ends gives its pages back by their numbers written
+ * to free_pages from available[0] on, which then counts them.
  */
 GEMM_API int gemm_kv_plan(int32_t* page_table, int64_t table_width, const int32_t* lengths,
                           const int32_t* counts, const int32_t* free_pages,
