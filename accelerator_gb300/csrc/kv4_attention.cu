@@ -269,9 +269,8 @@ struct Attend {
     }
 
     // This warp's 32 tokens of a stage, from token `tok` on; `subs`: which 16s are
-    // there.  MASKED: of some that some row does not see, or that are not there.
-    template <bool MASKED>
-    __device__ __forceinline__ void step(uint32_t stage_at, int tok, uint32_t subs) {
+    // there.  `masked`: of some that some row does not see, or that are not there.
+    __device__ __forceinline__ void step(uint32_t stage_at, int tok, uint32_t subs, bool masked) {
         const int lane = threadIdx.x % 32, g = lane / 4;
         // scores of tokens 16b + g and 16b + g + 8 (y) for the rows 2t (.x) and 2t + 1 (.y)
         float2 sc[kSubs][NQ][2];
@@ -305,7 +304,7 @@ struct Attend {
         // of 0 has to stay 0 whatever the token has for a scale, and a scale of NaN
         // makes NaN of the rows alone that see it; elsewhere all rows see all tokens.
         uint32_t nan = 0;
-        if constexpr (MASKED) {
+        if (masked) {
 #pragma unroll
             for (int b = 0; b < kSubs; ++b)
 #pragma unroll
@@ -390,7 +389,7 @@ struct Attend {
             }
             weigh();
         }
-        if (MASKED && __any_sync(0xFFFFFFFFu, nan != 0)) {
+        if (masked && __any_sync(0xFFFFFFFFu, nan != 0)) {
             const float bad = __uint_as_float(0x7FC00000u);
 #pragma unroll
             for (int b = 0; b < kSubs; ++b)
@@ -505,8 +504,7 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_cluster_kernel(con
             if (!st.wait_full(a.err)) break;
             const uint32_t subs = st.live_subs[st.stage];
             const int tok = tok_begin + s * kStep + warp * (kSubs * kSub);
-            if (subs & kPlain) rows.template step<false>(st.at(), tok, subs);
-            else if (tok < tile.hi) rows.template step<true>(st.at(), tok, subs >> (warp * kSubs));
+            if (tok < tile.hi) rows.step(st.at(), tok, subs >> (warp * kSubs), !(subs & kPlain));
             st.release();
             st.next();
         }
@@ -758,8 +756,7 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_line_kernel(const 
             if (!(ok = st.wait_full(a.err))) break;
             const uint32_t subs = st.live_subs[st.stage];
             const int tok = tok_begin + s * kStep + warp * (kSubs * kSub);
-            if (subs & kPlain) rows.template step<false>(st.at(), tok, subs);
-            else if (tok < tile.hi) rows.template step<true>(st.at(), tok, subs >> (warp * kSubs));
+            if (tok < tile.hi) rows.step(st.at(), tok, subs >> (warp * kSubs), !(subs & kPlain));
             st.release();
             st.next();
         }
