@@ -179,14 +179,18 @@ struct Piece {
 };
 
 constexpr int kAhead = 2;
+constexpr int kMaxRows = 8;
 
 template <typename T, int PER, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs a, int rows_each, bool inverse, int turned, int places) {
-    extern __shared__ float2 s_by[];   // [rows][pairs]: cosine and sine
-    constexpr bool kTwo = !INTERLEAVED || PER == 1;   // a turned place is two pieces
+    extern __shared__ __align__(16) float s_by[];   // cosines, then sines: [rows][pairs] each
+    __shared__ bool s_off[kMaxRows];                // rows that stay as they are
+    constexpr bool kTwo = !INTERLEAVED || PER == 1; // a turned place is two pieces
+    constexpr int kPairs = kTwo ? PER : PER / 2;    // of a turned place
     const int half = a.part / 2;
     const int64_t row0 = (int64_t)blockIdx.x * rows_each;
     const int rows = (int)(a.rows - row0 < rows_each ? a.rows - row0 : rows_each);
+    const float *s_cos = s_by, *s_sin = s_by + rows_each * half;
     // Places of a head: `turned` that turn, then those that are copied.  A team of
     // threads has all places of one head, in turns if it has fewer threads.
     const int heads = a.x[0].heads + a.x[1].heads, step = places < kRotaryThreads ? places : kRotaryThreads, teams = kRotaryThreads / step;
@@ -195,61 +199,75 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
     struct Item {
         Piece<T, PER> e, f;
         T* out;
-        const float2* by;
-        int at, other;               // elements of the head; other < 0: copied
+        int r, pair;                 // pair < 0: copied
         bool live;
     };
     auto load = [&](Item& it, int r, int head, int place) {
         const bool second = head >= a.x[0].heads;
         const RotaryRows& x = a.x[second];
         const int h = second ? head - a.x[0].heads : head;
-        const T* in = static_cast<const T*>(x.in.p) + (row0 + r) * x.in.row + h * x.in.head;
-        it.out = static_cast<T*>(x.out.p) + (row0 + r) * x.out.row + h * x.out.head;
+        const bool copied = place >= turned;
+        const int at = copied ? a.part + (place - turned) * PER : place * PER * (INTERLEAVED && PER == 1 ? 2 : 1);
+        const T* in = static_cast<const T*>(x.in.p) + (row0 + r) * x.in.row + h * x.in.head + at;
+        it.out = static_cast<T*>(x.out.p) + (row0 + r) * x.out.row + h * x.out.head + at;
+        it.r = r;
+        it.pair = copied ? -1 : place * kPairs;
         [[maybe_unused]] const int64_t in_bytes = ((a.rows - 1) * x.in.row + (x.heads - 1) * x.in.head + a.dim) * (int64_t)sizeof(T);
         [[maybe_unused]] const int64_t out_bytes = ((a.rows - 1) * x.out.row + (x.heads - 1) * x.out.head + a.dim) * (int64_t)sizeof(T);
-        const bool copied = place >= turned;
-        it.at = copied ? a.part + (place - turned) * PER : place * PER * (INTERLEAVED && PER == 1 ? 2 : 1);
-        it.other = copied ? -1 : kTwo ? it.at + (INTERLEAVED ? 1 : half) : it.at;
-        it.by = s_by + r * half + (kTwo ? place * PER : it.at / 2);
-        it.live = __ldg(a.positions + row0 + r) >= 0 && !(copied && in == it.out) && GEMM_DBG_OK(in + it.at, x.in.p, in_bytes, PER * sizeof(T)) &&
-                  GEMM_DBG_OK(it.out + it.at, x.out.p, out_bytes, PER * sizeof(T));
+        const int other = INTERLEAVED ? 1 : half;
+        it.live = !(copied && in == it.out) && GEMM_DBG_OK(in, x.in.p, in_bytes, PER * sizeof(T)) && GEMM_DBG_OK(it.out, x.out.p, out_bytes, PER * sizeof(T));
         if (kTwo && it.live && !copied)
-            it.live = GEMM_DBG_OK(in + it.other, x.in.p, in_bytes, PER * sizeof(T)) && GEMM_DBG_OK(it.out + it.other, x.out.p, out_bytes, PER * sizeof(T));
+            it.live = GEMM_DBG_OK(in + other, x.in.p, in_bytes, PER * sizeof(T)) && GEMM_DBG_OK(it.out + other, x.out.p, out_bytes, PER * sizeof(T));
         if (!it.live) return;
-        it.e.load(in + it.at);
-        if (kTwo && !copied) it.f.load(in + it.other);
+        it.e.load(in);
+        if (kTwo && !copied) it.f.load(in + other);
     };
     auto finish = [&](Item& it) {
-        if (!it.live) return;
-        if (it.other >= 0) {
-            float u[PER], v[PER];
-            it.e.get(u);
+        if (!it.live || s_off[it.r]) return;
+        if (it.pair >= 0) {
+            float u[kPairs], v[kPairs], c[kPairs], n[kPairs];   // the pairs, cosines and sines
             if constexpr (kTwo) {
+                it.e.get(u);
                 it.f.get(v);
+            } else {
+                float both[PER];
+                it.e.get(both);
 #pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const float2 w = it.by[j];
-                    const float x = u[j], y = v[j];
-                    u[j] = x * w.x - y * w.y;
-                    v[j] = y * w.x + x * w.y;
-                }
-                it.f.put(v);
-                it.f.store(it.out + it.other);
+                for (int j = 0; j < kPairs; ++j) u[j] = both[2 * j], v[j] = both[2 * j + 1];
+            }
+            const int at = it.r * half + it.pair;
+            if constexpr (kPairs == 1) {
+                c[0] = s_cos[at], n[0] = s_sin[at];
+                const float x = u[0] * c[0] - v[0] * n[0];
+                v[0] = v[0] * c[0] + u[0] * n[0];
+                u[0] = x;
             } else {
 #pragma unroll
-                for (int j = 0; j < PER; j += 2) {
-                    const float2 w = it.by[j / 2];
-                    const float x = u[j], y = u[j + 1];
-                    u[j] = x * w.x - y * w.y;
-                    u[j + 1] = y * w.x + x * w.y;
+                for (int j = 0; j < kPairs; j += 2) {
+                    const float2 c2 = *reinterpret_cast<const float2*>(s_cos + at + j), n2 = *reinterpret_cast<const float2*>(s_sin + at + j);
+                    const float2 u2 = make_float2(u[j], u[j + 1]), v2 = make_float2(v[j], v[j + 1]), m2 = make_float2(-n2.x, -n2.y);
+                    const float2 x = __ffma2_rn(u2, c2, __fmul2_rn(v2, m2)), y = __ffma2_rn(v2, c2, __fmul2_rn(u2, n2));
+                    u[j] = x.x, u[j + 1] = x.y, v[j] = y.x, v[j + 1] = y.y;
                 }
             }
-            it.e.put(u);
+            if constexpr (kTwo) {
+                it.e.put(u);
+                it.f.put(v);
+                it.f.store(it.out + (INTERLEAVED ? 1 : half));
+            } else {
+                float both[PER];
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) both[2 * j] = u[j], both[2 * j + 1] = v[j];
+                it.e.put(both);
+            }
         }
-        it.e.store(it.out + it.at);
+        it.e.store(it.out);
     };
 
     int r = 0, head = team, place = team < teams ? threadIdx.x % step : places;
+    auto settle = [&] {   // head numbers past the last go on in the next row
+        while (r < rows && head >= heads) head -= heads, ++r;
+    };
     auto next = [&](Item (&item)[kAhead]) {   // false if there was none
         if (place >= places) return false;
 #pragma unroll
@@ -258,26 +276,29 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
             if (r < rows) {
                 load(item[i], r, head, place);
                 head += teams;
-                while (r < rows && head >= heads) head -= heads, ++r;   // on in the next row
+                settle();
             }
         }
-        if (r >= rows) r = 0, head = team, place += step;
-        while (r < rows && head >= heads) head -= heads, ++r;
-        if (r >= rows) place = places;   // a team past the last head of the last row
+        if (r >= rows) {
+            r = 0, head = team, place += step;
+            settle();
+        }
         return true;
     };
-    while (r < rows && head >= heads) head -= heads, ++r;
-    if (r >= rows) place = places;
+    settle();
+    if (r >= rows) place = places;   // a team past the last head of the last row
     Item item[kAhead];
     bool some = next(item);   // under way while the sines are made
     for (int i = threadIdx.x; i < rows * half; i += kRotaryThreads) {
         const int at = i / half, pair = i % half;
         const int position = __ldg(a.positions + row0 + at);
         const uint64_t turn = (uint64_t)(uint32_t)position * __ldg(a.turns + pair);
-        float s, c;
-        sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
-        s_by[i] = make_float2(c * a.magnitude, (inverse ? -s : s) * a.magnitude);
+        float n, c;
+        sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &n, &c);   // 2^-31
+        s_by[i] = c * a.magnitude;
+        s_by[rows_each * half + i] = (inverse ? -n : n) * a.magnitude;
     }
+    if (threadIdx.x < rows) s_off[threadIdx.x] = __ldg(a.positions + row0 + threadIdx.x) < 0;
     __syncthreads();
     for (; some; some = next(item))
 #pragma unroll
@@ -290,7 +311,7 @@ cudaError_t rotate(const RotaryArgs& a, bool inverse, int num_sms, cudaStream_t 
     // About four places a thread, unless that leaves SMs without a block.
     const int64_t most = a.rows / (4 * num_sms), want = 4 * kRotaryThreads / ((int64_t)(a.x[0].heads + a.x[1].heads) * places);
     const int64_t each = most < want ? most : want;
-    const int rows = (int)(each < 1 ? 1 : each > 8 ? 8 : each);
+    const int rows = (int)(each < 1 ? 1 : each > kMaxRows ? kMaxRows : each);
     rotary_kernel<T, PER, INTERLEAVED><<<(unsigned)((a.rows + rows - 1) / rows), kRotaryThreads, rows * (a.part / 2) * sizeof(float2), stream>>>(
         a, rows, inverse, turned, places);
     return cudaGetLastError();
