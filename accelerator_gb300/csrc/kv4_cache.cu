@@ -10,6 +10,13 @@
 // and 2t + 9 those from 8g on of each 64 -- so that rows come in 16-byte loads,
 // all in flight at once, and the largest magnitude of a row is found over 4 or 8
 // lanes.
+//
+// 11000 tokens of 4 prompts, 8 heads of 128, bfloat16 (45 MB one way, 12 the other):
+// 18 us to write and 13 us to read back out of a cold L2, 3.2 and 4.3 TB/s, where
+// the measured copy rate would give 8.4 us each way.  Instructions bound both (10.2
+// and 7.0 million, 2 a cycle and SM): the codes' arithmetic, the exchanges between
+// lanes, and each block's search for its part.  The raising of tiny rows inside the
+// pairs' arithmetic, without a branch around a row's, cost 1.3 us.
 #include "kernels.h"
 #include "kv_part.cuh"
 #include "lowbit.cuh"
@@ -35,7 +42,7 @@ __device__ __forceinline__ Scale scale_of(uint32_t top) {   // the bits of the l
     r.bits = __bfloat16_as_ushort(sb);
     if (top >= 0x7F800000u) r.s = 0.0f, r.bits = 0x7FC0;   // NaN; the codes are those of zeros
     else if (r.s < kTiny) r.s = 0.0f, r.bits = 0;
-    r.inv = r.s == 0.0f ? 0.0f : __fdiv_rn(1.0f, r.s);
+    r.inv = r.s == 0.0f ? 0.0f : __frcp_rn(r.s);
     // (binary16's least s is above that)
     r.up = !std::is_same<T, __half>::value && r.s < 7.9e-31f && r.s > 0.0f;
     if (r.up) r.s *= 18446744073709551616.0f, r.inv *= 5.421010862427522e-20f;   // 2^64, 2^-64
@@ -46,7 +53,17 @@ __device__ __forceinline__ Scale scale_of(uint32_t top) {   // the bits of the l
 // nearest integer, ties to even.  The quotient has to be the correctly rounded
 // one, for it is often halfway between two integers: from q = x * (1 / s) the
 // residual x - q * s (exact in one fused multiply-add) gives it (Markstein 1990)
-// as long as nothing underflows, hence `up`.  |x / s| stays under 7.04.
+// as long as nothing underflows, hence `up` and `raise` (which is exact: a change
+// of exponent, of values under 2^-96).  |x / s| stays under 7.04.
+template <typename T>
+__device__ __forceinline__ void raise(Eight<T>& x, const Scale& r) {
+    if constexpr (!std::is_same<T, __half>::value) {
+        if (r.up)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x.put(e, x.at(e) * 18446744073709551616.0f);
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t nibbles_of(const Eight<T>& x, const Scale& r) {
     const float2 inv = make_float2(r.inv, r.inv), minus = make_float2(-r.s, -r.s);
@@ -54,8 +71,7 @@ __device__ __forceinline__ uint32_t nibbles_of(const Eight<T>& x, const Scale& r
     float2 u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float2 v = make_float2(x.at(2 * i), x.at(2 * i + 1));
-        if (r.up) v.x *= 18446744073709551616.0f, v.y *= 18446744073709551616.0f;
+        const float2 v = make_float2(x.at(2 * i), x.at(2 * i + 1));
         const float2 q = __fmul2_rn(v, inv);
         u[i] = __fadd2_rn(__ffma2_rn(__ffma2_rn(q, minus, v), inv, q), to_nibble);
     }
@@ -152,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(KvView c, KvRows K
             const int tok = 8 * r + g;
             uint32_t w[kWords];
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) w[i] = nibbles_of(held[r][i], s);
+            for (int i = 0; i < kWords; ++i) raise(held[r][i], s), w[i] = nibbles_of(held[r][i], s);
             uint8_t* to = at.codes + tok * (D / 2) + t * kChunk;
             if (here(tok) && GEMM_DBG_OK(to, c.data, at.extent, kChunk)) store_chunk<kChunk>(to, w);
             if (t == 0) put_scale(tok, s.bits);
@@ -178,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(KvView c, KvRows K
                 for (int m = 4; m < 32; m *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
                 const Scale s = scale_of<T>(top);
 #pragma unroll
-                for (int i = 0; i < D / 64; ++i) own[o][i] = nibbles_of(held[r][o][i], s);
+                for (int i = 0; i < D / 64; ++i) raise(held[r][o][i], s), own[o][i] = nibbles_of(held[r][o][i], s);
                 if (g == 0) put_scale(8 * r + 2 * t + o, s.bits);
             }
             // four dimensions of both tokens to a word
