@@ -40,8 +40,12 @@
 // binary16's normal range, so that c * S * 2^-24 is one fused multiply-add, exact
 // for scales down to 2^-8 of the largest; blocks that have others take c * S * 2^-4
 // by a subtraction and a product, exact down to 2^-28.  Codes wait in two buffers.
-// Scales of tokens that no row of the tile sees are taken for 0; a token that reads as NaN gets keys of
-// NaN, which make NaN of the scores of the rows that see it, and values of 0.
+// Scales of tokens that no row of the tile sees are taken for 0; a token that reads
+// as NaN gets keys of NaN, which make NaN of the scores of the rows that see it, and
+// values of 0.  The example above takes 468 us over 4 bits, 550 TFLOP/s, and 402 with
+// the arithmetic on the codes left out: the chain of a tile, as above, then the cache's
+// warps.  One buffer of codes and a product after a subtraction for all blocks took
+// 499 us, NaN looked for with each score 585 (registers spilled).
 //
 // Every wait is bounded; a role that gives up raises the abort flag, all stop,
 // and the matrix unit is drained before tensor memory is freed.
