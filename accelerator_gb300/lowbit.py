@@ -325,9 +325,10 @@ def kv_append(cache, K, V, page_table, starts, first, stream=None):
         raise TypeError(f"K and V must have {cache.heads} heads")
     if rows != v_rows:
         raise ValueError(f"{rows} keys and {v_rows} values")
-    rc = getattr(binding.lib(), cache._append)(cache._ref, K.data_ptr() or None, kr, kh, V.data_ptr() or None, vr, vh, kind,
-                                      page_table.data_ptr() or None, width, starts.data_ptr(),
-                                      first.data_ptr() or None, rows, sequences, _stream(stream, cache.index))
+    call = getattr(binding.lib(), cache._append)
+    rc = call(cache._ref, K.data_ptr() or None, kr, kh, V.data_ptr() or None, vr, vh, kind,
+              page_table.data_ptr() or None, width, starts.data_ptr(),
+              first.data_ptr() or None, rows, sequences, _stream(stream, cache.index))
     if rc:
         raise GemmError(rc, cache._append)
 
@@ -343,9 +344,10 @@ def kv_read(cache, page_table, starts, first, tokens, dtype=torch.bfloat16, stre
     shape = (tokens, cache.heads, cache.head_dim)
     K = _empty(shape, dtype, cache.device, stream)
     V = _empty(shape, dtype, cache.device, stream)
-    rc = getattr(binding.lib(), cache._read)(cache._ref, K.data_ptr() or None, V.data_ptr() or None, kind,
-                                    page_table.data_ptr() or None, width, starts.data_ptr(),
-                                    first.data_ptr() or None, tokens, sequences, _stream(stream, cache.index))
+    call = getattr(binding.lib(), cache._read)
+    rc = call(cache._ref, K.data_ptr() or None, V.data_ptr() or None, kind,
+              page_table.data_ptr() or None, width, starts.data_ptr(),
+              first.data_ptr() or None, tokens, sequences, _stream(stream, cache.index))
     if rc:
         raise GemmError(rc, cache._read)
     return K, V
@@ -376,10 +378,11 @@ def kv_attention(Q, cache, page_table, starts, lengths, scale=None, causal=True,
         scale = cache.head_dim ** -0.5
     if window >= 1 << 63:       # as good as none, but ctypes would take its low 64 bits
         window = (1 << 63) - 1
-    rc = getattr(binding.lib(), cache._attention)(cache._ref, Q.data_ptr() or None, qr, qh, out.data_ptr() or None, orow, oh,
-                                         _TYPES[kind], heads, scale, causal, window, page_table.data_ptr() or None,
-                                         width, starts.data_ptr(), lengths.data_ptr() or None, rows, sequences,
-                                         _stream(stream, cache.index))
+    call = getattr(binding.lib(), cache._attention)
+    rc = call(cache._ref, Q.data_ptr() or None, qr, qh, out.data_ptr() or None, orow, oh,
+              _TYPES[kind], heads, scale, causal, window, page_table.data_ptr() or None,
+              width, starts.data_ptr(), lengths.data_ptr() or None, rows, sequences,
+              _stream(stream, cache.index))
     if rc:
         raise GemmError(rc, cache._attention)
     return out

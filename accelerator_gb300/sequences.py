@@ -30,7 +30,8 @@ def kv_plan(page_table, lengths, counts, free, available, page_tokens, tokens, u
     """The plan of a step in which sequence b, with lengths[b] tokens in the cache,
     gets counts[b] more (0: it rests).  `free` is a stack of free pages of which the
     first available[0] are on it, `tokens` (a host number) the rows of the step: the
-    sum of the counts, or more (the rows behind get position and slot -1).
+    sum of the counts, or more (the rows behind get position and slot -1; ``rotary``
+    and the calls on a cache leave such rows as they were, the latter with ERR_INDEX).
 
     Writes the pages that the new tokens begin into page_table and returns a Plan:
     starts and first as kv_append takes them, lengths after the step as
@@ -53,6 +54,8 @@ def kv_plan(page_table, lengths, counts, free, available, page_tokens, tokens, u
         raise ValueError(f"{n} page table rows, {lengths.shape[0]} lengths and {counts.shape[0]} counts do not fit together")
     if tokens < 0:
         raise ValueError("tokens must not be negative")
+    if abs(page_tokens) >= 1 << 31:     # not one, but ctypes would take its low 32 bits
+        page_tokens = 0
     device = page_table.device
     slots = _empty((tokens,), torch.int64, device, stream)
     parts = [n + 1, n + 1, n, tokens] if update else [n + 1, n + 1, n, tokens, n, 1]
@@ -112,7 +115,8 @@ class Rotary(_Handle):
                 raise ValueError("frequencies are taken as they are: no scaling")
         if given is not None:
             magnitude = float(given)
-        if len(frequencies) != half or not all(math.isfinite(f) for f in frequencies) or not math.isfinite(magnitude):
+        if (len(frequencies) != half or not all(math.isfinite(f) for f in frequencies)
+                or not abs(magnitude) <= torch.finfo(torch.float32).max):
             raise ValueError(f"{half} finite frequencies and a finite magnitude are wanted")
         # in turns times 2^64, modulo 2^64, as signed numbers
         turns = [round(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for f in frequencies]

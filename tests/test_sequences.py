@@ -179,7 +179,7 @@ def test_plan_refusals_of_the_binding(libgemm, monkeypatch):
         sequences.kv_plan(table, L[:1], C, F, A, 16, 2)
     with pytest.raises(ValueError):
         sequences.kv_plan(table, L, C, F, A, 16, -1)
-    for page in (0, 3, -16, 1 << 21):
+    for page in (0, 3, -16, 1 << 21, (1 << 32) + 16, 16 - (1 << 32)):
         with pytest.raises(libgemm.GemmError):
             sequences.kv_plan(table, L, C, F, A, page, 2)
     with pytest.raises(libgemm.GemmError):
@@ -281,7 +281,8 @@ def test_tables_that_are_refused():
         with pytest.raises(ValueError):
             sequences.Rotary(part, device="cpu")
     for kw in (dict(layout="other"), dict(scaling="other"), dict(base=0.0), dict(factor=-1.0), dict(scaling="yarn"), dict(frequencies=[1.0]),
-               dict(frequencies=[1.0] * 31 + [float("nan")]), dict(magnitude=float("inf")), dict(frequencies=[1.0] * 32, scaling="linear")):
+               dict(frequencies=[1.0] * 31 + [float("nan")]), dict(magnitude=float("inf")), dict(magnitude=1e39),
+               dict(frequencies=[1.0] * 32, scaling="linear")):
         with pytest.raises(ValueError):
             sequences.Rotary(64, device="cpu", **kw)
 
@@ -460,6 +461,43 @@ def test_steps_of_everything_together(libgemm, bits):
             want = torch.einsum("thgn,nhd->thgd", a.masked_fill(hide[:, None, None], -float("inf")).softmax(-1), v[mine].double())
             assert ((O[rows] - want.reshape(-1, 8, dim)).abs() <= 0.01 * v[mine].abs().max()).all() if counts[b] else True
     assert available.item() == 40 - sum(-(-t // page) for t in total)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("counts", [[1, 0, 1], [300, 0, 41]])
+def test_rows_behind_the_last_sequence(libgemm, bits, counts):
+    """A step with room for more rows than it has: the calls on a cache leave the
+    rows behind as they were (and report the offsets that end before them), and the
+    others get what they get alone."""
+    from accelerator_gb300 import lowbit, sequences
+    page, heads, dim, rows, spare = 16, 2, 64, sum(counts), 3
+    turn = sequences.Rotary(dim)
+    Q, K, V = [torch.randn(rows + spare, n, dim, device="cuda").to(torch.bfloat16) for n in (8, heads, heads)]
+    Q[rows:] = K[rows:] = V[rows:] = float("nan")
+    got = []
+    for room in (0, spare):
+        cache = (lowbit.Kv4Cache if bits == 4 else lowbit.KvCache).empty(40, heads, dim, page)
+        for x in ([cache.data] if bits == 4 else [cache.k_codes, cache.v_codes]):
+            x.zero_()
+        table = torch.full((3, 20), -1, dtype=torch.int32, device="cuda")
+        p = sequences.kv_plan(table, ints([0, 0, 0]), ints(counts), ints(range(40)), ints([40]), page, rows + room)
+        assert p.positions[rows:].tolist() == p.slots[rows:].tolist() == [-1] * room
+        q, k = [torch.full_like(x[:rows + room], 7.0) for x in (Q, K)]
+        sequences.rotary(Q[:rows + room], K[:rows + room], p.positions, turn, out=(q, k))
+        assert (q[rows:] == 7).all() and (k[rows:] == 7).all()
+        assert libgemm.debug_status() == libgemm.OK
+        status = libgemm.ERR_INDEX if room else libgemm.OK
+        lowbit.kv_append(cache, k, V[:rows + room], table, p.starts, p.first)
+        assert libgemm.debug_status() == status
+        O = torch.full_like(q, 7.0)
+        lowbit.kv_attention(q, cache, table, p.starts, p.lengths, out=O)
+        assert libgemm.debug_status() == status
+        assert (O[rows:] == 7).all()
+        got.append((q[:rows], k[:rows], O[:rows], *([cache.data] if bits == 4 else [cache.k_codes, cache.v_codes, cache.k_scales])))
+    assert got[0][2].isfinite().all()
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
 
 
 # ---- without a GPU ---------------------------------------------------------------
