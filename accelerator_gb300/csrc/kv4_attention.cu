@@ -461,17 +461,31 @@ struct Attend {
             }
         }
     }
-    // Element d of row r (0 .. 7) of what the warps have put: maximum, sum of weights, result so far.
-    static __device__ __forceinline__ void joined(const float* s_o, const float* s_m, const float* s_l, int r, int d, float& top, float& sum, float& acc) {
+    // Elements d .. d + 3 of row r (0 .. 7) of what the warps have put: maximum, sum of weights, results so far.
+    static __device__ __forceinline__ void joined(const float* s_o, const float* s_m, const float* s_l, int r, int d, float& top, float& sum, float4& acc) {
         top = s_m[r];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w * 8 + r]);
-        sum = acc = 0.0f;
+        sum = 0.0f;
+        acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = exp2_approx(s_m[w * 8 + r] - top);
+            const float4 x = *reinterpret_cast<const float4*>(s_o + (w * 8 + r) * kLd + d);
             sum = fmaf(f, s_l[w * 8 + r], sum);
-            acc = fmaf(f, s_o[(w * 8 + r) * kLd + d], acc);
+            acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y), acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+        }
+    }
+    static __device__ __forceinline__ void store(T* to, const float4& acc, float sum) {
+        const float x[4] = {acc.x, acc.y, acc.z, acc.w};
+        uint32_t y[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) y[i] = pack2<T>(sum == 0.0f ? 0.0f : x[2 * i] / sum, sum == 0.0f ? 0.0f : x[2 * i + 1] / sum);
+        if ((reinterpret_cast<uintptr_t>(to) & 7u) == 0) {
+            *reinterpret_cast<uint2*>(to) = make_uint2(y[0], y[1]);
+        } else {
+            const T* e = reinterpret_cast<const T*>(y);
+            to[0] = e[0], to[1] = e[1], to[2] = e[2], to[3] = e[3];
         }
     }
 };
@@ -530,15 +544,16 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_cluster_kernel(con
         ((a.b.rows - 1) * a.O.row + (a.q_heads - 1) * a.O.head + D) * (int64_t)sizeof(T);
     const int rows = min(tile.nrows - tile.r0, kRows);
     auto place = [&](int r, int d) { return s_o + r / 8 * kGroup + r % 8 * A::kLd + d; };   // warp 0's
-    for (int i = threadIdx.x; i < rows * D; i += kThreads) {
+    for (int i = 4 * threadIdx.x; i < rows * D; i += 4 * kThreads) {
         const int r = i / D, d = i % D;
-        float top, sum, acc;
+        float top, sum;
+        float4 acc;
         A::joined(s_o + r / 8 * kGroup, s_m + r / 8 * kWarps * 8, s_l + r / 8 * kWarps * 8, r % 8, d, top, sum, acc);
         if (a.splits == 1) {
             T* dst = out_row<T>(a, tile, h, tile.r0 + r) + d;
-            if (GEMM_DBG_OK(dst, a.O.p, o_bytes, sizeof(T))) *dst = from_float<T>(sum == 0.0f ? 0.0f : acc / sum);
+            if (GEMM_DBG_OK(dst, a.O.p, o_bytes, 4 * sizeof(T))) A::store(dst, acc, sum);
         } else {
-            *place(r, d) = acc;   // read by this thread alone so far
+            *reinterpret_cast<float4*>(place(r, d)) = acc;   // read by this thread alone so far
             if (d == 0) s_joined[2 * r] = top, s_joined[2 * r + 1] = sum;
         }
     }
@@ -577,12 +592,15 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_cluster_kernel(con
 // heads and steps, and each CTA of one round takes an equal piece of it: its first
 // and its last tile may be others' too, and a second launch joins those.  (A
 // sequence's tiles count as many steps each as its longest can have: a walk needs
-// lengths and row counts alone.)
+// lengths and row counts alone.)  What a tile's beginning and end take counts as
+// kOpening steps at its head; where a piece would begin or end among these, it
+// does so before them.
+constexpr int kOpening = 3;
 struct Walk {
     int seq;
     int64_t at, left;                  // place among the sequence's steps; steps still to go
     int row0, count, len, tiles;
-    int64_t weight;                    // steps of each of its tiles and heads
+    int64_t weight;                    // steps of each of its tiles and heads, and kOpening
 
     // Sequence q's numbers; `report`: one thread of the launch says what is out of range.
     __device__ __forceinline__ void look(const AttnArgs& a, int q, int rows, bool report) {
@@ -603,7 +621,7 @@ struct Walk {
             const int64_t seen = ((int64_t)a.window + rows / a.share + 1 + 2 * (kStep - 1)) / kStep;
             weight = weight < seen ? weight : seen;
         }
-        if (weight < 1) weight = 1;
+        weight = (weight < 1 ? 1 : weight) + kOpening;
     }
     __device__ __forceinline__ int64_t steps(const AttnArgs& a) const { return (int64_t)tiles * a.c.heads * weight; }
 };
@@ -628,11 +646,13 @@ __device__ __forceinline__ bool next_piece(const AttnArgs& a, Walk& w, int rows,
     const int64_t which = w.at / w.weight, k = w.at - which * w.weight;
     const int j = (int)(which / a.c.heads);
     const int64_t n = w.weight - k < w.left ? w.weight - k : w.left;
+    if (k == 0 && n <= kOpening) return false;   // the next CTA's
+    const int64_t begin = k == 0 ? 0 : k - kOpening, end = k + n - kOpening;
     piece.h = (int)(which - (int64_t)j * a.c.heads);
     tile.place(a, w.seq, w.row0, w.count, w.len, j * rows, rows, kStep);
     piece.unit = (int)(((int64_t)w.row0 * a.share + (int64_t)w.seq * a.gap) / rows) + j;
-    piece.begin = (int)(k < tile.steps ? k : tile.steps);
-    piece.steps = (int)(k + n < tile.steps ? k + n : tile.steps) - piece.begin;
+    piece.begin = (int)(begin < tile.steps ? begin : tile.steps);
+    piece.steps = (int)(end < tile.steps ? end : tile.steps) - piece.begin;
     piece.first = k == 0;
     piece.whole = k == 0 && n == w.weight;
     piece.pieces = 1 + (int)((w.weight - n + per - 1) / per);
@@ -705,8 +725,9 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_line_kernel(const 
             if (at < walk.steps(a)) break;
             at -= walk.steps(a);
         }
-        walk.at = at;
-        walk.left = per < all - lo ? per : all - lo;
+        const int64_t k = at % walk.weight, back = k <= kOpening ? k : 0;
+        walk.at = at - back;
+        walk.left = (per < all - lo ? per : all - lo) + back;
         s_walk = walk;
     }
     __syncthreads();
@@ -786,16 +807,20 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_line_kernel(const 
             if (ok) rows.put(n, s_o, s_m, s_l);
             if (!(ok = warps_agree(ok))) break;
             const int live = min(tile.nrows - tile.r0 - 8 * n, 8);
-            for (int i = threadIdx.x; i < live * D; i += kWarps * 32) {
+            for (int i = 4 * threadIdx.x; i < live * D; i += 4 * kWarps * 32) {
                 const int r = i / D, d = i % D;
-                float top, sum, acc;
+                float top, sum;
+                float4 acc;
                 A::joined(s_o, s_m, s_l, r, d, top, sum, acc);
                 if (piece.whole) {
                     T* dst = out_row<T>(a, tile, piece.h, tile.r0 + 8 * n + r) + d;
-                    if (GEMM_DBG_OK(dst, a.O.p, o_bytes, sizeof(T))) *dst = from_float<T>(sum == 0.0f ? 0.0f : acc / sum);
+                    if (GEMM_DBG_OK(dst, a.O.p, o_bytes, 4 * sizeof(T))) A::store(dst, acc, sum);
                 } else {
                     float *to = slot + (8 * n + r) * D + d, *ml = slot + kRows * D + 2 * (8 * n + r);
-                    if (GEMM_DBG_OK(to, a.partial, a.partial_bytes, 4)) *to = acc;
+                    if (GEMM_DBG_OK(to, a.partial, a.partial_bytes, 16)) {   // 8-byte aligned
+                        reinterpret_cast<float2*>(to)[0] = make_float2(acc.x, acc.y);
+                        reinterpret_cast<float2*>(to)[1] = make_float2(acc.z, acc.w);
+                    }
                     if (d == 0 && GEMM_DBG_OK(ml, a.partial, a.partial_bytes, 8)) ml[0] = top, ml[1] = sum;
                 }
             }
@@ -951,7 +976,8 @@ void kv4_few_plan(KvPlan& p, const KvView& c, int64_t have, int64_t most, int nu
         return;
     }
     p.splits = 1;
-    p.ctas = (int)(have * most < slots ? have * most : slots);
+    const int64_t line = have * (most + kOpening);
+    p.ctas = (int)(line < slots ? line : slots);
     p.scratch_bytes = 8 * p.units * c.heads + (int64_t)p.ctas * 2 * (p.rows * (c.dim + 2) * 4);
 }
 
