@@ -196,7 +196,7 @@ __device__ __forceinline__ Eight<T> query(const AttnArgs& a, const Tile& tile, i
 // P^T, for which the weights are turned over in registers.
 template <typename T, int D, int NQ>
 struct Attend {
-    static constexpr int kRows = 8 * NQ, kLd = D + 4, kWords = D / 32;
+    static constexpr int kLd = D + 4, kWords = D / 32;
     static constexpr int MT = D / 16;   // row tiles of O^T: row g of tile 2i + x is d = 64 (i / 2) + 8g + 4 (i % 2) + 2x, row g + 8 the next
     // Query row 8n + g as the column g of B.  A lane's part of a row is 8
     // neighbours of each 32: elements e and e + 4 a word's two halves hold
@@ -630,12 +630,12 @@ struct Walk {
 // at the head of a stage, the queries behind it.
 struct alignas(16) Piece {
     Tile tile;
-    int unit, h, begin, steps, pieces;   // pieces: CTAs that share the tile, known where it begins
-    bool first, whole, end;              // end: there is none
+    int h, begin, steps;
+    bool first, whole, end;              // it has the tile's first token, all of them; end: there is none
 };
 
 // False at the end.
-__device__ __forceinline__ bool next_piece(const AttnArgs& a, Walk& w, int rows, int64_t per, Piece& piece) {
+__device__ __forceinline__ bool next_piece(const AttnArgs& a, Walk& w, int rows, Piece& piece) {
     Tile& tile = piece.tile;
     if (w.left <= 0) return false;
     while (w.at >= w.steps(a)) {
@@ -650,12 +650,10 @@ __device__ __forceinline__ bool next_piece(const AttnArgs& a, Walk& w, int rows,
     const int64_t begin = k == 0 ? 0 : k - kOpening, end = k + n - kOpening;
     piece.h = (int)(which - (int64_t)j * a.c.heads);
     tile.place(a, w.seq, w.row0, w.count, w.len, j * rows, rows, kStep);
-    piece.unit = (int)(((int64_t)w.row0 * a.share + (int64_t)w.seq * a.gap) / rows) + j;
     piece.begin = (int)(begin < tile.steps ? begin : tile.steps);
     piece.steps = (int)(end < tile.steps ? end : tile.steps) - piece.begin;
     piece.first = k == 0;
     piece.whole = k == 0 && n == w.weight;
-    piece.pieces = 1 + (int)((w.weight - n + per - 1) / per);
     w.at += n;
     w.left -= n;
     return true;
@@ -738,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_line_kernel(const 
         int issued = 0;
         Piece piece;
         for (bool ok = true; ok;) {
-            piece.end = !next_piece(a, walk, kRows, per, piece);
+            piece.end = !next_piece(a, walk, kRows, piece);
             if (!(ok = st.wait_empty(a.err))) break;
             uint8_t* at = smem + st.stage * R::kStageBytes;
             if (lane == 0) *reinterpret_cast<Piece*>(at) = piece;
@@ -793,10 +791,6 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_line_kernel(const 
             st.release();
             st.next();
         }
-        if (ok && threadIdx.x == 0 && piece.first) {
-            int2* to = a.where + (int64_t)piece.unit * a.c.heads + piece.h;
-            if (GEMM_DBG_OK(to, a.where, a.where_bytes, 8)) *to = make_int2(blockIdx.x, piece.whole ? 1 : piece.pieces);
-        }
         // A slot for the tile that others began, one for that which others go on with.
         float* slot = a.partial + ((int64_t)blockIdx.x * 2 + (piece.first ? 1 : 0)) * (kRows * (D + 2));
 #pragma unroll
@@ -817,10 +811,7 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_line_kernel(const 
                     if (GEMM_DBG_OK(dst, a.O.p, o_bytes, 4 * sizeof(T))) A::store(dst, acc, sum);
                 } else {
                     float *to = slot + (8 * n + r) * D + d, *ml = slot + kRows * D + 2 * (8 * n + r);
-                    if (GEMM_DBG_OK(to, a.partial, a.partial_bytes, 16)) {   // 8-byte aligned
-                        reinterpret_cast<float2*>(to)[0] = make_float2(acc.x, acc.y);
-                        reinterpret_cast<float2*>(to)[1] = make_float2(acc.z, acc.w);
-                    }
+                    if (GEMM_DBG_OK(to, a.partial, a.partial_bytes, 16)) *reinterpret_cast<float4*>(to) = acc;
                     if (d == 0 && GEMM_DBG_OK(ml, a.partial, a.partial_bytes, 8)) ml[0] = top, ml[1] = sum;
                 }
             }
@@ -833,41 +824,80 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_line_kernel(const 
 
 // Joins the tiles that were shared, in the order of their tokens: a warp a row
 // (TEAM = 1), or eight warps one where few tiles are shared by many CTAs each, so that
-// all parts' loads are under way at once.
+// all parts' loads are under way at once.  Which CTAs have a tile follows from the
+// lengths, and is found before the parts are there.
 template <typename T, int D, int NQ, int TEAM>
 __global__ void __launch_bounds__(256) kv4_line_join_kernel(const AttnArgs a) {
-    constexpr int kRows = 8 * NQ, kEach = D / 32;
+    constexpr int kRows = 8 * NQ, kEach = D / 32, kBatch = 4;
     __shared__ float s_acc[TEAM][D], s_sum[TEAM];
+    __shared__ int64_t s_before[8], s_all[8];
     const int u = blockIdx.x, h = blockIdx.y, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     Tile tile;
-    const bool found = tile.find(a, u, kRows, kStep, false);
+    if (!tile.find(a, u, kRows, kStep, false)) return;
+    int64_t before = 0, all = 0;
+    Walk walk;
+    for (int q = threadIdx.x; q < a.b.sequences; q += 256) {
+        walk.look(a, q, kRows, false);
+        const int64_t steps = walk.steps(a);
+        all += steps;
+        if (q < tile.seq) before += steps;
+    }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) {
+        before += __shfl_xor_sync(0xFFFFFFFFu, before, i);
+        all += __shfl_xor_sync(0xFFFFFFFFu, all, i);
+    }
+    if (lane == 0) s_before[warp] = before, s_all[warp] = all;
+    __syncthreads();
+    before = all = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) before += s_before[w], all += s_all[w];
+    walk.look(a, tile.seq, kRows, false);
+    const int64_t ctas = a.partial_bytes / (2 * kRows * (D + 2) * 4), per = (all + ctas - 1) / ctas;
+    before += ((int64_t)(tile.r0 / kRows) * a.c.heads + h) * walk.weight;
+    const int64_t from = (before + kOpening) / per, n = per * (from + 1) - before;   // the CTA that begins it, and as much of it
+    const int first = (int)from, pieces = n >= walk.weight ? 1 : 1 + (int)((walk.weight - n + per - 1) / per);
     grid_dependency_wait();   // launched while the parts are still being made
-    if (!found) return;
-    const int2* at = a.where + (int64_t)u * a.c.heads + h;
-    if (!GEMM_DBG_OK(at, a.where, a.where_bytes, 8)) return;
-    const int first = at->x, pieces = at->y, ctas = (int)(a.partial_bytes / (2 * kRows * (D + 2) * 4));
-    if (pieces <= 1 || first < 0 || pieces > ctas - first) return;   // (also if the wait of a part gave up)
+    if (pieces <= 1 || pieces > ctas - first) return;
     [[maybe_unused]] const int64_t o_bytes =
         ((a.b.rows - 1) * a.O.row + (a.q_heads - 1) * a.O.head + D) * (int64_t)sizeof(T);
     const int member = warp % TEAM, r = blockIdx.z * (8 / TEAM) + warp / TEAM;
     if (TEAM == 1 ? tile.r0 + r >= tile.nrows : tile.r0 + (int)blockIdx.z >= tile.nrows) return;   // of a team all or none
     auto part = [&](int i) { return a.partial + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * (kRows * (D + 2)); };
+    const int share = (pieces + TEAM - 1) / TEAM, end = min(pieces, (member + 1) * share);
     float top = kLowest, sum = 0.0f, acc[kEach] = {};
+    float m[kBatch], l[kBatch], x[kBatch][kEach];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            m[b] = kLowest, l[b] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) x[b][e] = 0.0f;
+            if (i0 + b >= end) continue;
+            const float *at = part(i0 + b), *ml = at + kRows * D + 2 * r;
+            if (!GEMM_DBG_OK(ml, a.partial, a.partial_bytes, 8)) continue;
+            m[b] = ml[0], l[b] = ml[1];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) x[b][e] = at[r * D + lane + 32 * e];
+        }
+    };
+    load(member * share);   // under way together with the maxima
     for (int i = lane; i < pieces; i += 32) {
         const float* ml = part(i) + kRows * D + 2 * r;
         if (GEMM_DBG_OK(ml, a.partial, a.partial_bytes, 8)) top = fmaxf(top, ml[0]);
     }
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-    const int share = (pieces + TEAM - 1) / TEAM;
-#pragma unroll 8
-    for (int i = member * share; i < min(pieces, (member + 1) * share); ++i) {
-        const float *from = part(i), *ml = from + kRows * D + 2 * r;
-        if (!GEMM_DBG_OK(ml, a.partial, a.partial_bytes, 8)) continue;
-        const float f = exp2_approx(ml[0] - top);
-        sum = fmaf(f, ml[1], sum);
+    for (int i = member * share; i < end; i += kBatch) {
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) acc[e] = fmaf(f, from[r * D + lane + 32 * e], acc[e]);
+        for (int b = 0; b < kBatch; ++b) {
+            if (i + b >= end) break;
+            const float f = exp2_approx(m[b] - top);
+            sum = fmaf(f, l[b], sum);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) acc[e] = fmaf(f, x[b][e], acc[e]);
+        }
+        if (i + kBatch < end) load(i + kBatch);
     }
     if constexpr (TEAM > 1) {
 #pragma unroll
@@ -978,7 +1008,7 @@ void kv4_few_plan(KvPlan& p, const KvView& c, int64_t have, int64_t most, int nu
     p.splits = 1;
     const int64_t line = have * (most + kOpening);
     p.ctas = (int)(line < slots ? line : slots);
-    p.scratch_bytes = 8 * p.units * c.heads + (int64_t)p.ctas * 2 * (p.rows * (c.dim + 2) * 4);
+    p.scratch_bytes = (int64_t)p.ctas * 2 * (p.rows * (c.dim + 2) * 4);
 }
 
 }  // namespace libgemm

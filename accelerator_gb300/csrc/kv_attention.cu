@@ -665,13 +665,7 @@ cudaError_t launch_kv_attention(const KvView& c, const KvRows& Q, const KvRows& 
     const bool q_vec = (reinterpret_cast<uintptr_t>(Q.p) & 15u) == 0 && Q.row % 8 == 0 && Q.head % 8 == 0;
     AttnArgs a{c, Q, O, b, q_heads, (unsigned)(q_heads / c.heads), plan.gap, scale * 1.44269504088896341f, causal,
                (int)(window < INT32_MAX ? window : INT32_MAX), plan.splits, q_vec, plan.scratch_bytes, static_cast<float*>(scratch),
-               nullptr, 0, err};
-    if (plan.ctas > 0) {
-        a.where = static_cast<int2*>(scratch);
-        a.where_bytes = 8 * plan.units * c.heads;
-        a.partial = reinterpret_cast<float*>(a.where + plan.units * c.heads);
-        a.partial_bytes -= a.where_bytes;
-    }
+               err};
     if (type == ElemType::kBF16)
         return c.dim == 128 ? launch<__nv_bfloat16, 128>(a, plan, launches, stream)
                             : launch<__nv_bfloat16, 64>(a, plan, launches, stream);

@@ -40,8 +40,6 @@ struct AttnArgs {
     bool q_vec;                  // Q in 16-byte loads
     int64_t partial_bytes;
     float* partial;              // [unit][head][split] x (rows x dim sums, then rows x (max, sum)); of 4 bits [CTA][2] x the same
-    int2* where;                 // 4 bits: [unit][head], the CTA that begins it and how many share it
-    int64_t where_bytes;
     unsigned* err;
 };
 
