@@ -18,17 +18,21 @@
 // Every token has its own scales.  A page and head's codes and scales lie in one
 // piece, and one bulk copy brings them.
 //
-// 64 sequences of up to 8192 tokens, 64 heads over 8 of 128: 318 MB in 78 us, 4.1
-// TB/s or 60 % of the measured copy rate (over 8 bits 617 MB in 123 us).  Instructions
-// bound it, 212 of a warp for 16 tokens and a head (117 of them on the ALU pipe)
-// at 2.1 a cycle and SM: 16 sequences take 30 us from memory and 28 from L2.
+// 64 sequences of up to 8192 tokens, 64 heads over 8 of 128: 318 MB in 67 us, 4.8
+// TB/s or 70 % of the measured copy rate (over 8 bits 617 MB in 123 us).  Between a
+// CTA's first stage and its last that is 6.3 TB/s; the rest is its beginning (6.5 us:
+// 2.1 to find its piece, 2.3 to look its tile and queries up, 2 for the first copies,
+// which all ask for at once), the parting of the CTAs' ends (57 to 64 us) and the
+// joining launch (2.8).  Up to 32768 tokens take 211 us, 89 %.  A warp has 212
+// instructions for 16 tokens, 117 of them on the ALU pipe.
 // Three CTAs an SM, as 128 registers allow, of four computing warps and a copying
 // one each.  With two an SM, and a cluster a tile, 110 us; with three, and sums that
 // change their reference seldom, 92; all steps in one line 82, flags of the stages
-// that every row sees whole 80.  Left: four CTAs an SM without a copying warp 108;
-// most of the line shared out and the rest in small pieces for SMs done first 86;
-// two or three times as many pieces 94 and 100; values' codes loaded before the
-// weights are made 83.
+// that every row sees whole 80, tiles' openings counted 70, results joined four at a
+// time 67.5.  Left: four CTAs an SM without a copying warp 108 (when it was 92), or
+// with 96 registers 97 (78); two or three times as many pieces 94 and 100 (93);
+// values' codes loaded before the weights are made 83 (82); the first copies before
+// the queries 69 (67.5: the queries wait behind them).
 #include "kv_attention.cuh"
 
 namespace libgemm {
@@ -595,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, resident(NQ)) kv4_cluster_kernel(con
 // lengths and row counts alone.)  What a tile's beginning and end take counts as
 // kOpening steps at its head; where a piece would begin or end among these, it
 // does so before them.
-constexpr int kOpening = 3;
+constexpr int kOpening = 3;   // 8192 tokens: 2 69.8 us, 3 67.5, 4 67.5, 5 69.4; 0 78
 struct Walk {
     int seq;
     int64_t at, left;                  // place among the sequence's steps; steps still to go
@@ -940,8 +944,8 @@ cudaError_t launch(const AttnArgs& a, const KvPlan& plan, int* launches, cudaStr
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_line_kernel<T, D, NQ>, a);
     if (e != cudaSuccess) return e;
     *launches = 2;
-    // 8 heads over 32768 and 200000 tokens: 23.2 and 55.2 us with a team of warps a
-    // row, 30.7 and 64.6 with one warp; 64 sequences of up to 8192: 83.7 and 77.2.
+    // 8 heads over 32768 and 200000 tokens: 18.7 and 48.4 us with a team of warps a
+    // row, 23.2 and 53.5 with one warp; 64 sequences of up to 8192: 84 and 67.
     const bool team = plan.ctas > 8 * plan.units * a.c.heads;
     cfg.gridDim = dim3((unsigned)plan.units, (unsigned)a.c.heads, team ? plan.rows : NQ);
     cfg.blockDim = dim3(256);
@@ -992,10 +996,10 @@ cudaError_t launch_kv4_few(const AttnArgs& a, ElemType type, const KvPlan& plan,
 
 // The host's part of launch_kv4_few: how few rows' tokens are shared.  A cluster a
 // tile is one launch, and no CTA has to find its piece: 8 heads over up to 1000
-// tokens take 7.2 us for one sequence (in a line 11.1) and 9.1 for 6 (12.7), over up
-// to 8192 tokens 12.5 for one (14.9) and 17.4 for 6 (22.2).  But clusters of eight do
+// tokens take 6.7 us for one sequence (in a line 8.9) and 8.4 for 6 (11.5), over up
+// to 8192 tokens 12.3 for one (12.0) and 16.7 for 6 (17.2).  But clusters of eight do
 // not find the last of the GPU's slots: with 448 CTAs for 456 slots, 7 sequences,
-// 1000 tokens take 14.0 us (12.6), hence seven eighths.
+// 1000 tokens take 13.2 us (11.6), hence seven eighths.
 void kv4_few_plan(KvPlan& p, const KvView& c, int64_t have, int64_t most, int num_sms) {
     const int64_t slots = (int64_t)resident(p.rows / 8) * num_sms;
     p.ctas = 0;
