@@ -837,7 +837,10 @@ __global__ void __launch_bounds__(256) kv4_line_join_kernel(const AttnArgs a) {
     __shared__ int64_t s_before[8], s_all[8];
     const int u = blockIdx.x, h = blockIdx.y, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     Tile tile;
-    if (!tile.find(a, u, kRows, kStep, false)) return;
+    if (!tile.find(a, u, kRows, kStep, false)) {
+        grid_dependency_wait();   // this launch does not end before the one that makes the parts
+        return;
+    }
     int64_t before = 0, all = 0;
     Walk walk;
     for (int q = threadIdx.x; q < a.b.sequences; q += 256) {
