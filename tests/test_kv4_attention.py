@@ -261,6 +261,19 @@ def test_many_sequences_in_one_line(libgemm, dim, kind, page):
         ref.check(libgemm, p, Q, counts, lengths, causal=False)
 
 
+@pytest.mark.parametrize("n", [1, 2, 7, 40, 113, 150, 229, 300, 520])
+def test_pieces_of_every_size(libgemm, n):
+    """From less than a tile's opening to some tiles for each block: pieces that
+    begin and end inside openings, blocks that get none, tiles in many pieces."""
+    dim, page = 64, 128
+    lengths = [(b * 331 + n) % 520 if b % 11 else (b * 97) % 8300 for b in range(n)]
+    lengths[-1] = 8290
+    p = ref.Paged4(min(n, 20), 65, 1, dim, page, seed=n)     # a table too wide for a cluster a tile
+    p.table = p.table[torch.arange(n, device="cuda") % 20].contiguous()
+    for share in (1, 3):
+        ref.check(libgemm, p, p.queries(n, share, torch.bfloat16), [1] * n, lengths)
+
+
 @pytest.mark.parametrize("T", [1, 3])
 @pytest.mark.parametrize("share", [1, 8])
 def test_bad_indices_in_one_line(libgemm, T, share):
