@@ -16,7 +16,8 @@
 // the measured copy rate would give 8.4 us each way.  Instructions bound both (10.2
 // and 7.0 million, 2 a cycle and SM): the codes' arithmetic, the exchanges between
 // lanes, and each block's search for its part.  The raising of tiny rows inside the
-// pairs' arithmetic, without a branch around a row's, cost 1.3 us.
+// pairs' arithmetic, without a branch around a row's, cost 1.3 us; a block that goes
+// through all heads of its part saves searches and has fewer warps: 21.9 and 14.7 us.
 #include "kernels.h"
 #include "kv_part.cuh"
 #include "lowbit.cuh"
