@@ -232,8 +232,9 @@ struct Attend {
                 for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i].at(e)));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            // its biased exponent, in the range in which both powers below are normal
-            const int k = top < INFINITY ? max(12, (int)(__float_as_uint(top) >> 23)) : 127;
+            // its biased exponent, in the range in which the powers below, and 16 times the
+            // first, are finite and normal: rows of zeros stay zeros
+            const int k = top < INFINITY ? max(15, (int)(__float_as_uint(top) >> 23)) : 127;
             const float down = __uint_as_float((uint32_t)(265 - k) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);   // 2^(11 + 127 - k)
             const float back = __uint_as_float((uint32_t)k << 23);   // 2^(k - 127); 2^9 more for the 2^-11 above and the codes' 2^-20
             float sum = 0.0f;
