@@ -32,37 +32,48 @@ __device__ __forceinline__ bool plan_sums(const StepPlan& p, F put) {
     const int top = *p.available;
     const int height = top < 0 ? 0 : top > p.capacity ? (int)p.capacity : top;
     bool bad = height != top;
-    auto row = [&](int64_t n) { return (int)(n < p.tokens ? n : p.tokens); };
     auto left = [&](int64_t taken) { return (int)(height - taken > INT32_MIN ? height - taken : INT32_MIN); };
     int64_t rows0 = 0, pages0 = 0;   // of the sequences before this round's
     for (int64_t b0 = 0; b0 < p.sequences; b0 += blockDim.x) {
         const int64_t b = b0 + threadIdx.x;
         const bool in = b < p.sequences && GEMM_DBG_OK(p.lengths + b, p.lengths, p.sequences * 4, 4);
         const int length = in ? p.lengths[b] : 0, count = in ? __ldg(p.counts + b) : 0;
-        const int held = max(length, 0), added = max(count, 0);
-        const int64_t after = (int64_t)held + added, need = pages_of(after, p) - pages_of(held, p);
+        const int held = max(length, 0);
+        int added = max(count, 0);
+        int64_t after = (int64_t)held + added, need = pages_of(after, p) - pages_of(held, p);
         bad |= length < 0 || count < 0 || (added > 0 && (after > p.width << p.page_log2 || after > INT32_MAX));
-        int64_t rows = added, pages = need;   // sums up to this thread's sequence
-        for (int i = 1; i < 32; i *= 2) {
-            const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, i), g = __shfl_up_sync(0xFFFFFFFFu, pages, i);
-            if (lane >= i) rows += r, pages += g;
-        }
-        __syncthreads();   // the last round's sums have been read
-        if (lane == 31) s_rows[warp] = rows, s_pages[warp] = pages;
-        __syncthreads();
-        int64_t rows_all = 0, pages_all = 0;
-        for (int w = 0; w < warps; ++w) {
-            if (w == warp) rows += rows_all, pages += pages_all;
-            rows_all += s_rows[w], pages_all += s_pages[w];
+        int64_t rows, pages, rows_all, pages_all;   // sums up to this thread's sequence, and of all
+        auto sum = [&] {
+            rows = added, pages = need;
+            for (int i = 1; i < 32; i *= 2) {
+                const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, i), g = __shfl_up_sync(0xFFFFFFFFu, pages, i);
+                if (lane >= i) rows += r, pages += g;
+            }
+            __syncthreads();   // the last sums have been read
+            if (lane == 31) s_rows[warp] = rows, s_pages[warp] = pages;
+            __syncthreads();
+            rows_all = pages_all = 0;
+            for (int w = 0; w < warps; ++w) {
+                if (w == warp) rows += rows_all, pages += pages_all;
+                rows_all += s_rows[w], pages_all += s_pages[w];
+            }
+        };
+        sum();
+        if (rows0 + rows_all > p.tokens) {   // (all threads or none) a sequence gets what the rows have room for, and pages for that
+            bad = true;
+            const int64_t room = p.tokens - rows0 - (rows - added);
+            if (added > room) added = room > 0 ? (int)room : 0;
+            after = (int64_t)held + added, need = pages_of(after, p) - pages_of(held, p);
+            sum();
         }
         if (in) {
-            bad |= rows0 + rows > p.tokens || (pages0 + pages > height && need > 0);
-            put(b, row(rows0 + rows - added), held, left(pages0 + pages - need), (int)(after < INT32_MAX ? after : INT32_MAX));
+            bad |= pages0 + pages > height && need > 0;
+            put(b, (int)(rows0 + rows - added), held, left(pages0 + pages - need), (int)(after < INT32_MAX ? after : INT32_MAX));
         }
         rows0 += rows_all, pages0 += pages_all;
     }
     __syncthreads();   // every thread has read `available`, which may be `left`
-    if (threadIdx.x == 0) put(p.sequences, row(rows0), 0, left(pages0), 0);
+    if (threadIdx.x == 0) put(p.sequences, (int)rows0, 0, left(pages0), 0);
     return bad;
 }
 

@@ -39,7 +39,8 @@ def kv_plan(page_table, lengths, counts, free, available, page_tokens, tokens, u
     place in it) of the rows, what is then available, and the stack's heights
     before each sequence and after the last.  With `update`, lengths and
     available are written in place (a step recorded in a graph goes on where the
-    last replay ended).  Bad numbers and pages that run out are reported by
+    last replay ended).  Bad numbers, counts past `tokens` (sequences get what there
+    is room for, in their order) and pages that run out are reported by
     ``binding.debug_status()`` as ERR_INDEX; the tokens without a page have slot -1."""
     index = page_table.get_device()
     if not (page_table.dtype is lengths.dtype is counts.dtype is free.dtype is available.dtype is _I32 and page_table.is_cuda

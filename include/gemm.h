@@ -499,8 +499,9 @@ GEMM_API int gemm_kv4_attention(const gemm_kv4_cache* cache, const void* Q, int6
  * get -1 in both (gemm_rotary leaves such rows as they are; so do the calls on a
  * cache, which report offsets that end before the last row).  page_tokens is a
  * power of 2 up to 2^20.  Reported as GEMM_ERR_INDEX: a negative length or count
- * (taken for 0), counts whose sum is over `tokens` (starts ends there and rows past
- * it are not written), a sequence longer than the table is wide or a stack that runs
+ * (taken for 0), counts whose sum is over `tokens` (sequences get the rows that
+ * there is room for, in their order, and starts, lengths and pages go by those
+ * alone), a sequence longer than the table is wide or a stack that runs
  * out (the tokens without a page have -1 in slots, and, inside the table, in
  * page_table), a height over free_capacity.
  * The arrays do not overlap but where said.  Calls that take from one stack are one
