@@ -535,8 +535,10 @@ enum gemm_rotary_layout { GEMM_ROTARY_HALF = 0, GEMM_ROTARY_INTERLEAVED = 1 };
  *   positions int32[rows], on the device
  *   turns     uint64[rotary_dim / 2], on the device: frequency i in turns
  *             (radians / 2 pi) a position, times 2^64, rounded.  The angle is the
- *             product's fraction of a turn, exact for every position.
- * Sines and cosines, products and sums are binary32; a result is rounded once.
+ *             product's fraction of a turn, exact for every position; what it is past
+ *             the nearest quarter turn is rounded to binary32.
+ * Sines and cosines (to some 2^-24 of themselves, next to their zeros too), products
+ * and sums are binary32; a result is rounded once.
  */
 GEMM_API int gemm_rotary(const void* Q, int64_t q_row_stride, int64_t q_head_stride, void* Q_out,
                          int64_t q_out_row_stride, int64_t q_out_head_stride, int32_t q_heads,
