@@ -149,11 +149,17 @@ def rotary(Q, K, positions, table: Rotary, inverse=False, out=None, stream=None)
     head strides; K may be None) with every head turned by its row's position (int32,
     as kv_plan gives them), or, with `inverse`, turned back: the gradient's way.
     Returns (Q, K) anew, or in `out`, a pair that may be (Q, K) itself.  Rows with a
-    negative position are not written."""
+    negative position are not written.  Autograd does not see this call: where it
+    records (not under torch.no_grad or in a Function's forward), tensors that
+    require a gradient are refused."""
     kind, index = Q.dtype, table.index
     number = _TYPES.get(kind)
     if number is None:
         raise TypeError("Q must be float32, bfloat16 or float16")
+    if torch.is_grad_enabled() and (Q.requires_grad or (K is not None and K.requires_grad)
+                                    or (out is not None and any(t is not None and t.requires_grad for t in out))):
+        raise TypeError("autograd does not see rotary: its results would have no gradient (the way back is inverse=True, of the "
+                        "results' gradients)")
     qr, qh = _rows(Q, "Q", kind, index)
     rows, q_heads, dim = Q.shape
     if not (positions.dtype is _I32 and positions.get_device() == index and positions.dim() == 1 and positions.is_contiguous()):
