@@ -57,21 +57,11 @@ constexpr float kTopP = 4096.0f;
 constexpr float kLeastP = 3.1554436e-30f;   // 2^-98
 constexpr int kMaxCluster = 8;
 
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
-}
 // A bfloat16 in shared memory.
 __device__ __forceinline__ float lds_bf16(uint32_t addr) {
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
     return __uint_as_float((uint32_t)v << 16);
-}
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
 }
 // D / 8 bytes.
 template <int D>
@@ -97,14 +87,6 @@ struct Ring {
     static constexpr int kAbortAt = kBarsAt + 16 * kStages;
     static constexpr int kBytes = kAbortAt + 16;
 };
-
-// The 8 x 8 binary16 matrix that a warp holds in fragments (lane 4 g + t has
-// row g, columns 2t and 2t + 1), transposed.
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
 
 // The ring's place in shared memory, and where a warp is in its rounds.
 template <int D, int NQ>

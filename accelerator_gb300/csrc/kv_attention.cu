@@ -18,16 +18,6 @@ constexpr int kSubs = 2;         // a warp takes this many times 16 tokens at on
 constexpr int kStep = kWarps * kSubs * kSub;   // tokens of a stage
 constexpr int kRingBytes = 96 * 1024;  // two CTAs of an SM keep 192 KB in flight
 constexpr int kMaxCluster = 8;
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
 
 // What the copying warp tells the others about 16 tokens of a stage.
 struct SubInfo {
@@ -46,14 +36,6 @@ struct Ring {
     static constexpr int kAbortAt = kBarsAt + 16 * kStages;
     static constexpr int kBytes = kAbortAt + 16;
 };
-
-// The 8 x 8 binary16 matrix that a warp holds in fragments (lane 4 g + t has
-// row g, columns 2t and 2t + 1), transposed.
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
 
 // Few query rows: a tile of 8 * NQ rows over a share of its tokens.  One warp
 // copies whole pages' parts into a ring of stages of 128 tokens (their codes

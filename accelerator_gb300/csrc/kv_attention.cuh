@@ -26,6 +26,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// The 8 x 8 binary16 matrix that a warp holds in fragments (lane 4 g + t has
+// row g, columns 2t and 2t + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 struct AttnArgs {
     KvView c;
     KvRows Q, O;

@@ -329,11 +329,6 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {   // streamed past 
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
 
 // A cluster of CTAs computes 32 * WN columns of C for 8 * MT rows: each CTA a
 // range of the blocks of 64 rows of W, in which each of its warps takes every
