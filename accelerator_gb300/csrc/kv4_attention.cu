@@ -21,13 +21,20 @@
 // Every token has its own scales.  A page and head's codes and scales lie in one
 // piece, and one bulk copy brings them.
 //
-// 64 sequences of up to 8192 tokens, 64 heads over 8 of 128: 318 MB in 67 us, 4.8
-// TB/s or 70 % of the measured copy rate (over 8 bits 617 MB in 123 us).  Between a
+// Weights, times their token's value scale, are binary16 in the second product: with
+// more bits it would have to be made twice.  Results are 1.74e-3 of their size from 64
+// bits in bfloat16 and 2.9e-4 in binary16, where rounding them is 1.73e-3 and 2.1e-4
+// (8192 tokens, normal queries and values).
+//
+// 64 sequences of up to 8192 tokens, 64 heads over 8 of 128: 318 MB in 67.5 us, 4.7
+// TB/s or 69 % of the measured copy rate (over 8 bits 617 MB in 123 us).  Between a
 // CTA's first stage and its last that is 6.3 TB/s; the rest is its beginning (6.5 us:
 // 2.1 to find its piece, 2.3 to look its tile and queries up, 2 for the first copies,
 // which all ask for at once), the parting of the CTAs' ends (57 to 64 us) and the
-// joining launch (2.8).  Up to 32768 tokens take 211 us, 89 %.  A warp has 212
-// instructions for 16 tokens, 117 of them on the ALU pipe.
+// joining launch (2.8).  Up to 32768 tokens take 214 us, 88 %.  A warp had 212
+// instructions for 16 tokens, 117 of them on the ALU pipe, before the 8 of the codes
+// came off in every step, for which 8 more (66.5 us then, and 211).
+// Tiles of 16 rows, two CTAs an SM: the same with two queries a sequence takes 145 us.
 // Three CTAs an SM, as 128 registers allow, of four computing warps and a copying
 // one each.  With two an SM, and a cluster a tile, 110 us; with three, and sums that
 // change their reference seldom, 92; all steps in one line 82, flags of the stages

@@ -13,11 +13,14 @@
 //
 // 11000 tokens of 4 prompts, 8 heads of 128, bfloat16 (45 MB one way, 12 the other):
 // 18 us to write and 13 us to read back out of a cold L2, 3.2 and 4.3 TB/s, where
-// the measured copy rate would give 8.4 us each way.  Instructions bound both (10.2
-// and 7.0 million, 2 a cycle and SM): the codes' arithmetic, the exchanges between
-// lanes, and each block's search for its part.  The raising of tiny rows inside the
-// pairs' arithmetic, without a branch around a row's, cost 1.3 us; a block that goes
-// through all heads of its part saves searches and has fewer warps: 21.9 and 14.7 us.
+// the measured copy rate would give 8.4 us each way.  Neither instructions nor memory
+// are at their limit: SMs are at work for 77 and 70 % of the time (1.8 and 1.5 rounds
+// of blocks), and then issue 0.61 instructions a cycle and scheduler (10.2 and 7.0 million
+// in all) at half of their warps' places; of a warp's waits 28 and 31 % are for its
+// loads, which come behind the search for its part, then for the ALU pipe.  The
+// raising of tiny rows inside the pairs' arithmetic, without a branch around a row's,
+// cost 1.3 us; a block that goes through all heads of its part saves searches and has
+// fewer warps: 21.9 and 14.7 us.
 #include "kernels.h"
 #include "kv_part.cuh"
 #include "lowbit.cuh"

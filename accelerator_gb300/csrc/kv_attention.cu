@@ -593,8 +593,14 @@ cudaError_t kv_attention_setup(int bits) {
 // again.  4 sequences over 4000 tokens of 8 heads of 128, two query heads to each:
 // of 31 queries 77 us in tiles of 16 and 49 in one of 256, of 17 queries 63 and
 // 47, of 16 queries 46 in two tiles of 16.  (With 2 cache heads, too few tiles to
-// fill the GPU, 17 and 31 queries take 28 us in tiles of 16 and 38 in one of 256,
-// and batches that mix prompts and single tokens take one kernel for both.)
+// fill the GPU, 17 and 31 queries take 28 us in tiles of 16 and 38 in one of 256.)
+// The border is that of 8 bits.  Over 4 the same batch, recorded, takes in tiles of 16
+// and in one of 256: 5 queries 16 and 38 us, 16 27 and 41, 17 33 and 41, 31 38 and 43;
+// with 2 cache heads 13 and 27, 17 and 29, 17 and 29, 17 and 30.
+//
+// A batch that mixes prompts and single tokens takes one kernel for both: 60 single
+// tokens over up to 8192, 64 heads over 8, recorded, 63 us over 4 bits (119 over 8), a prompt of
+// 1000 over 8192 474 (421), together 850 (745); with a prompt of 100 258 (346).
 //
 // Few rows: tiles that fill an eighth of the GPU's CTA slots or more, or whose
 // tokens are few, have their tokens shared over a cluster (joined through

@@ -15,7 +15,10 @@ namespace {
 // memory, and it is one launch; beyond that, or where lengths are written in place,
 // one block makes them and a second launch reads them.  Latency bounds it: a plan of 64
 // sequences takes 4.6 us of the GPU in one launch and 4.1 and 4.3 in two, one of 1000
-// sequences of up to 512 rows 11.6 (3.1 MB of positions and slots written).
+// sequences of up to 512 rows 11.6 (3.1 MB of positions and slots written).  Recorded
+// one after another, one launch and two (with lengths in place): 64 sequences of one row
+// 2.8 and 3.1 us, 512 of up to 64 rows 4.5 and 7.2, 1000 of one row 5.6 and 6.7, 1024 5.8
+// and 6.9; in two launches 1025 take 11.0, as the sums go through two rounds, 2000 11.2.
 constexpr int kScanThreads = 1024, kFillThreads = 256, kFillRows = 256, kOneLaunch = 1024;
 
 __device__ __forceinline__ int pages_of(int64_t tokens, const StepPlan& p) {   // columns of the table, which is all that are held
@@ -160,6 +163,10 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(StepPlan p) {
 // packed, one place ahead took 41.6 us, two 42.9 and four 45.9 (74 registers), and two
 // the least for few rows.  A row a team with its sines kept in registers takes 39.5
 // and, for 2000 rows of 24 heads that turn 32 of 128 dimensions, 10.7 where this takes 8.5.
+// (All of these with 32 bits of the angle; with 64, recorded: 40.1 -> 40.6 us, 6.2 -> 6.5
+// for that part.)  9700 rows of 20 heads of 64, 50 MB: 13.8 us out of a cold L2, where the
+// copy rate would give 7.4: the SMs are at work for 69 % of it, the rest is the launch's
+// beginning and end, and then issue 0.58 instructions a cycle and scheduler.
 constexpr int kRotaryThreads = 256;
 
 template <typename T>
@@ -197,6 +204,9 @@ struct Piece {
 };
 
 constexpr int kAhead = 2;
+// Rows of a block: the rule at the launch would take more for very few heads, whose
+// threads then have nothing to turn.  100000 rows of 64 dimensions: 16 + 4 heads 91 us
+// (5.6 TB/s), 8 + 2 59 (4.3), 4 + 1 46, 2 + 1 42, 1 + 1 40 (1.3).
 constexpr int kMaxRows = 8;
 
 template <typename T, int PER, bool INTERLEAVED>
@@ -347,6 +357,9 @@ cudaError_t rotate(const RotaryArgs& a, bool interleaved, bool inverse, int num_
     auto by16 = [](const KvRows& r) {
         return (reinterpret_cast<uintptr_t>(r.p) & 15u) == 0 && r.row * sizeof(T) % 16 == 0 && r.head * sizeof(T) % 16 == 0;
     };
+    // Pieces of 16 bytes where all of them fit, one element else.  11000 rows of 20 heads
+    // of bfloat16, recorded: halves of 80 of 80 dimensions 14 us, 40 of 80 60 (neighbours:
+    // 15), 32 of 96 19 and 24 of 96 72; 40 heads of 128 41, one element off 16 bytes 127.
     bool vec = a.part % (interleaved ? kPer : 2 * kPer) == 0 && a.dim % kPer == 0;
     for (const RotaryRows& x : a.x) vec = vec && (x.heads == 0 || (by16(x.in) && by16(x.out)));
     if (vec) return interleaved ? rotate<T, kPer, true>(a, inverse, num_sms, stream) : rotate<T, kPer, false>(a, inverse, num_sms, stream);

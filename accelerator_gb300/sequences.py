@@ -81,8 +81,9 @@ class Rotary(_Handle):
       "ntk"     base * factor ** (rotary_dim / (rotary_dim - 2)) for base
       "yarn"    with r = original * f / (2 pi) turns in the original context
                 and k = (r - 1) / 31 held to [0, 1]: k f + (1 - k) f / factor,
-                and results times 0.1 ln(factor) + 1
-    or give `frequencies` (and `magnitude`) as they are."""
+                and results times 0.1 ln(factor) + 1 (under 1 for a factor under 1)
+    or give `frequencies` (and `magnitude`) as they are: for models whose code has its
+    ramp over the pairs' numbers, or three bands of them."""
 
     __slots__ = ("rotary_dim", "layout", "frequencies", "magnitude", "turns", "device", "index", "_ptr", "_layout")
 
